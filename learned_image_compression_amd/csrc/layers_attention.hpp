@@ -1,0 +1,465 @@
+// layers_attention.hpp -- what the attention kernels share: arguments, the
+// tiles in LDS, matrix fragments, and which keys a query sees.
+//
+// Matrix layout.  All products use 32 x 32 accumulators (64 lanes, 16 values
+// each): lane l holds column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4.  An
+// operand fragment is 8 values a lane: row (or column) l % 32 and eight of the
+// sixteen summed indexes.  Which eight is free as long as both operands agree:
+//
+// * "row" fragments (the summed index runs along a tile's row): 8 h .. 8 h + 7
+//   of each 16, h = l / 32: one 16-byte read.
+// * "column" fragments (it runs down the tile's rows): 4 h .. 4 h + 3 and
+//   8 + 4 h .. 8 + 4 h + 3, which is how an accumulator holds its rows.  So the
+//   probabilities of one product are the operand of the next as they stand, with
+//   no exchange between lanes, and the transposed reads of 4 rows x 16 columns
+//   (ds_read_b64_tr_b16) give the other operand.
+//
+// That is why scores are formed transposed wherever a query's row is reduced: a
+// lane then holds one query and half of a tile's keys.
+//
+// 32-bit tiles use eight 32x32x2 products where 16-bit ones use one 32x32x16.
+#pragma once
+
+#include <cmath>
+
+#include "layers_common.hpp"
+
+namespace lic {
+
+using float16v = float __attribute__((ext_vector_type(16)));
+using short4v = short __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    lic_attention_args p;
+    float scale_log2;   // scale * log2 e: exponentials are base 2
+    float *part;        // split rows: unnormalised sums [split][row][tile dim], then m, l
+    float *delta;       // backward: dout . out of each row [batch][heads][queries]
+    int splits;
+    int group;          // heads that share a kv head
+    uint32_t blocks;    // of the launch's real work
+};
+
+// smaller and larger of two whole numbers (the mixed overloads of min and max may go
+// through double)
+__device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ int64_t most(int64_t a, int64_t b) { return a > b ? a : b; }
+
+template <typename T>
+struct Frag;
+template <>
+struct Frag<bf16> {
+    using V = bf16 __attribute__((ext_vector_type(8)));
+};
+template <>
+struct Frag<f16> {
+    using V = f16 __attribute__((ext_vector_type(8)));
+};
+template <>
+struct Frag<float> {
+    using V = float __attribute__((ext_vector_type(8)));
+};
+template <typename T>
+using FragV = typename Frag<T>::V;
+
+__device__ __forceinline__ float16v mma(FragV<bf16> a, FragV<bf16> b, float16v c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float16v mma(FragV<f16> a, FragV<f16> b, float16v c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float16v mma(FragV<float> a, FragV<float> b, float16v c)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+}
+
+// row of an accumulator that a lane's value i is
+__device__ __forceinline__ constexpr int acc_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// Eight of an accumulator's values (half 0 or 1 of them) as a column operand.
+template <typename T>
+__device__ __forceinline__ FragV<T> operand(const float16v &p, int half)
+{
+    FragV<T> r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = (T)p[half * 8 + i];
+    return r;
+}
+
+__device__ __forceinline__ float16v zero16()
+{
+    float16v z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        z[i] = 0.0f;
+    return z;
+}
+
+// the larger (sum) of a lane's value and of its partner's 32 lanes away
+__device__ __forceinline__ float pair_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// A tile of ROWS rows of DT values in LDS: blocks of 32 columns, each ROWS rows of
+// 64 (16-bit) or 128 bytes whose 16-byte pieces are permuted by the row, so that
+// 16 rows' pieces of a row fragment, and 4 rows x 32 columns of a transposed read,
+// fall into all banks once.
+template <typename T, int ROWS, int DT>
+struct Tile {
+    static constexpr int kPiece = 16 / sizeof(T);             // values of a piece
+    static constexpr int kPieces = 32 / kPiece;               // pieces of a block's row
+    static constexpr int kRowBytes = 32 * sizeof(T);
+    static constexpr int kBytes = ROWS * DT * sizeof(T);
+
+    static __device__ __forceinline__ int swizzle(int row)
+    {
+        return sizeof(T) == 2 ? (row >> 2) & 3 : (row >> 1) & 7;
+    }
+    static __device__ __forceinline__ int at(int row, int block, int piece)
+    {
+        return (block * ROWS + row) * kRowBytes + ((piece ^ swizzle(row)) << 4);
+    }
+
+    // values 16 kk + 8 h .. + 7 of `row`
+    static __device__ __forceinline__ FragV<T> row_frag(const uint8_t *lds, int row, int kk, int h)
+    {
+        FragV<T> f;
+        const int block = kk >> 1;
+        if constexpr (sizeof(T) == 2) {
+            f = *reinterpret_cast<const FragV<T> *>(lds + at(row, block, (kk & 1) * 2 + h));
+        } else {
+            using Q = float __attribute__((ext_vector_type(4)));
+            const Q a = *reinterpret_cast<const Q *>(lds + at(row, block, (kk & 1) * 4 + 2 * h));
+            const Q b = *reinterpret_cast<const Q *>(lds + at(row, block, (kk & 1) * 4 + 2 * h + 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i] = a[i];
+                f[4 + i] = b[i];
+            }
+        }
+        return f;
+    }
+
+    // column 32 block + l % 32, rows row0 + {4 h .., 8 + 4 h ..}
+    static __device__ __forceinline__ FragV<T> col_frag(const uint8_t *lds, int row0, int block, int lane)
+    {
+        FragV<T> f;
+        const int h = lane >> 5;
+        if constexpr (sizeof(T) == 2) {
+            // a lane's address: 4 columns of one of the 4 rows; its result: its column's 4 rows
+            const int j = lane & 15;
+            const int row = row0 + 4 * h + (j >> 2);
+            const int piece = ((lane >> 4) & 1) * 2 + ((j & 3) >> 1);
+            using Lds = __attribute__((address_space(3))) short4v;
+            const auto read = [&](int r) {
+                const uint8_t *p = lds + at(r, block, piece) + (j & 1) * 8;
+                return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (Lds *)(__attribute__((address_space(3))) void *)p);
+            };
+            union {
+                short4v s[2];
+                FragV<T> f;
+            } u;
+            u.s[0] = read(row);
+            u.s[1] = read(row + 8);
+            f = u.f;
+        } else {
+            const int c = lane & 31;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = row0 + acc_row(i, h);
+                f[i] = *reinterpret_cast<const float *>(lds + at(row, block, c >> 2) + (c & 3) * 4);
+            }
+        }
+        return f;
+    }
+};
+
+// ROWS rows on their way from memory to a tile, through the registers of THREADS threads.
+// VEC: heads, strides and addresses allow 16-byte loads.
+template <typename T, int ROWS, int DT, int THREADS, bool VEC>
+struct Stage {
+    using TileT = Tile<T, ROWS, DT>;
+    static constexpr int kEach = ROWS * DT / TileT::kPiece / THREADS;
+    static_assert(kEach * THREADS * TileT::kPiece == ROWS * DT, "tile and threads");
+    uint4 r[kEach];
+
+    static __device__ __forceinline__ void place(int i, int t, int &row, int &block, int &piece)
+    {
+        const int e = i * THREADS + t;
+        piece = e % TileT::kPieces;
+        const int rest = e / TileT::kPieces;
+        row = rest % ROWS;
+        block = rest / ROWS;
+    }
+
+    // rows [0, rows) of base exist; the others and columns from dim on become 0
+    __device__ __forceinline__ void fetch(const T *base, int64_t stride, int rows, int dim, int t)
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            int row, block, piece;
+            place(i, t, row, block, piece);
+            const int d = block * 32 + piece * TileT::kPiece;
+            const T *p = base + (int64_t)row * stride + d;
+            r[i] = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (VEC) {
+                if (row < rows && d < dim)
+                    r[i] = *reinterpret_cast<const uint4 *>(p);
+            } else {
+                Vec<T, TileT::kPiece> v;
+#pragma unroll
+                for (int e = 0; e < TileT::kPiece; ++e)
+                    v.v[e] = row < rows && d + e < dim ? p[e] : (T)0.0f;
+                r[i] = *reinterpret_cast<const uint4 *>(&v);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(uint8_t *lds, int t) const
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            int row, block, piece;
+            place(i, t, row, block, piece);
+            *reinterpret_cast<uint4 *>(lds + TileT::at(row, block, piece)) = r[i];
+        }
+    }
+};
+
+// One row's values 16 kk + 8 h .. + 7 straight from memory (0 beyond dim or without a row).
+template <typename T, bool VEC>
+__device__ __forceinline__ FragV<T> row_from_memory(const T *row, bool there, int kk, int h, int dim)
+{
+    FragV<T> f;
+    const int d = 16 * kk + 8 * h;
+    if constexpr (VEC) {
+        constexpr int P = 16 / sizeof(T);
+        using Q = T __attribute__((ext_vector_type(P)));
+#pragma unroll
+        for (int i = 0; i < 8; i += P) {
+            Q q;
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+                q[e] = (T)0.0f;
+            if (there && d + i < dim)
+                q = *reinterpret_cast<const Q *>(row + d + i);
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+                f[i + e] = q[e];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = there && d + i < dim ? row[d + i] : (T)0.0f;
+    }
+    return f;
+}
+
+// The keys that one query may see by lengths and windows, or the queries that may see
+// one key: [first, first + count).
+struct Range {
+    int first;
+    uint32_t count;
+
+    __device__ __forceinline__ void set(int64_t lo, int64_t hi, int64_t end)
+    {
+        first = (int)least(lo, end);
+        count = hi > lo ? (uint32_t)(hi - lo) : 0u;
+    }
+    __device__ __forceinline__ bool holds(int x) const { return (uint32_t)(x - first) < count; }
+    // whether all (none) of [x0, x0 + n) are in it
+    __device__ __forceinline__ bool covers(int x0, int n) const
+    {
+        return x0 >= first && (int64_t)x0 + n <= (int64_t)first + count;
+    }
+    __device__ __forceinline__ bool misses(int x0, int n) const
+    {
+        return count == 0u || (int64_t)x0 + n <= first || x0 >= (int64_t)first + count;
+    }
+};
+
+// Keys that any of the queries [q0, q1) may see: [lo, hi).
+__device__ __forceinline__ void key_range(const AttnArgs &a, int len, int q0, int q1, int &lo, int &hi)
+{
+    const int64_t t0 = (int64_t)q0 + len - a.p.queries, t1 = (int64_t)q1 - 1 + len - a.p.queries;
+    const int64_t l = a.p.window_left < 0 ? 0 : most(0, t0 - a.p.window_left);
+    const int64_t h = a.p.window_right < 0 ? len : least(len, t1 + a.p.window_right + 1);
+    lo = (int)least(l, len);
+    hi = (int)most(h, lo);
+}
+
+// Queries that may see any of the keys [k0, k1): [lo, hi).
+__device__ __forceinline__ void query_range(const AttnArgs &a, int len, int k0, int k1, int &lo, int &hi)
+{
+    const int64_t back = (int64_t)len - a.p.queries; // position - query
+    const int64_t l = a.p.window_right < 0 ? 0 : most(0, (int64_t)k0 - a.p.window_right - back);
+    const int64_t h = a.p.window_left < 0 ? a.p.queries : least(a.p.queries, (int64_t)k1 + a.p.window_left - back);
+    lo = (int)least(l, a.p.queries);
+    hi = (int)most(h, lo);
+}
+
+__device__ __forceinline__ Range keys_of(const AttnArgs &a, int len, int query)
+{
+    Range r;
+    int lo, hi;
+    key_range(a, len, query, query + 1, lo, hi);
+    r.set(lo, query < a.p.queries ? hi : lo, len);
+    return r;
+}
+
+__device__ __forceinline__ Range queries_of(const AttnArgs &a, int len, int key)
+{
+    Range r;
+    int lo, hi;
+    query_range(a, len, key, key + 1, lo, hi);
+    r.set(lo, key < len ? hi : lo, a.p.queries);
+    return r;
+}
+
+__device__ __forceinline__ int key_length(const AttnArgs &a, int b)
+{
+    const int keys = (int)a.p.keys;
+    return a.p.key_lengths ? min(max(a.p.key_lengths[b], 0), keys) : keys;
+}
+
+__device__ __forceinline__ const uint8_t *mask_row(const AttnArgs &a, int b, int head, int query)
+{
+    return a.p.mask + b * a.p.mask_stride[0] + head * a.p.mask_stride[1] +
+           (int64_t)query * a.p.mask_stride[2];
+}
+
+template <typename T>
+__device__ __forceinline__ const T *head_row(const void *p, const int64_t *stride, int b, int64_t row, int head)
+{
+    return static_cast<const T *>(p) + b * stride[0] + row * stride[1] + head * stride[2];
+}
+template <typename T>
+__device__ __forceinline__ T *head_row(void *p, const int64_t *stride, int b, int64_t row, int head)
+{
+    return static_cast<T *>(p) + b * stride[0] + row * stride[1] + head * stride[2];
+}
+
+// Blocks are handed to the 8 XCDs in turn; neighbours in this order share an XCD and
+// so its L2, which lets the blocks of one head read its keys from there.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t block, uint32_t blocks)
+{
+    const uint32_t each = (blocks + 7) / 8;
+    return (block & 7) * each + (block >> 3); // may be >= blocks: no work
+}
+inline uint32_t xcd_grid(uint32_t blocks) { return (blocks + 7) / 8 * 8; }
+
+// Orders a wave's own LDS writes before its other lanes' reads.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.402823466e38f); }
+
+// The rows (a lane's l % 32) where either of a row's two lanes says so.
+__device__ __forceinline__ uint64_t rows_of(bool flag)
+{
+    const uint64_t f = __builtin_amdgcn_ballot_w64(flag);
+    return (f | (f >> 32)) & 0xffffffffull;
+}
+
+// A lane's part of an accumulator's column, times f, to columns 32 block .. of a row.
+template <typename T, bool VEC>
+__device__ __forceinline__ void put_column(T *out, const float16v &v, float f, int block, int h, int dim)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+        const int d = block * 32 + acc_row(i, h);
+        Vec<T, 4> w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w.v[e] = down<T>(v[i + e] * f);
+        if constexpr (VEC) {
+            if (d < dim)
+                *reinterpret_cast<Vec<T, 4> *>(out + d) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < dim)
+                    out[d + e] = w.v[e];
+        }
+    }
+}
+
+// Per element type; defined in one translation unit each (layers_attention_<type>.hip).
+template <typename T>
+struct Attention {
+    static int forward(AttnArgs a, hipStream_t s);
+    static int backward(AttnArgs a, hipStream_t s);
+};
+
+// A kernel of more than 64 KiB of LDS says so once.
+template <typename K>
+inline void allow_lds(K kernel, int bytes)
+{
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Splits of the key axis that the rows kernel takes: enough blocks for two a CU, at least
+// 256 keys each, at most 64.
+inline int row_splits(const lic_attention_args &p)
+{
+    const int64_t rows = p.queries * (p.heads / p.kv_heads);
+    const int64_t blocks = (rows + 31) / 32 * p.batch * p.kv_heads;
+    int64_t n = (512 + blocks - 1) / blocks;
+    const int64_t most = (p.keys + 255) / 256;
+    n = n < most ? n : most;
+    n = n < 64 ? n : 64;
+    return n < 1 ? 1 : (int)n;
+}
+
+// Few rows for the keys: the rows kernel, which splits the key axis over waves and
+// blocks; else the tiles kernel, whose blocks hold 128 queries of one head.
+inline bool few_rows(const lic_attention_args &p)
+{
+    const int64_t rows = p.queries * (p.heads / p.kv_heads);
+    const int64_t tiles = (p.queries + 127) / 128 * p.batch * p.heads;
+    return rows <= 64 || tiles < 128;
+}
+
+// Splits of the backward kernels' loops, where their blocks alone would not fill the CUs:
+// over the query tiles of all heads that share a kv head, and over key tiles.
+inline int backward_splits(int64_t blocks, int64_t steps)
+{
+    int64_t n = blocks > 0 ? 512 / blocks : 1;
+    const int64_t most = steps / 4; // a split takes at least four tiles
+    n = n < most ? n : most;
+    n = n < 16 ? n : 16;
+    return n < 1 ? 1 : (int)n;
+}
+inline int keys_splits(const lic_attention_args &p)
+{
+    return backward_splits((p.keys + 127) / 128 * p.batch * p.kv_heads,
+                           (p.queries + 31) / 32 * (p.heads / p.kv_heads));
+}
+inline int queries_splits(const lic_attention_args &p)
+{
+    return backward_splits((p.queries + 127) / 128 * p.batch * p.heads, (p.keys + 63) / 64);
+}
+
+inline int tile_dim(int64_t dim, bool vec) { return vec ? (int)((dim + 31) / 32 * 32) : LIC_MAX_HEAD_DIM; }
+
+}  // namespace lic

@@ -1,0 +1,603 @@
+// layers_attention_backward.hpp -- attention's backward kernels (included by the
+// translation unit of each element type).
+//
+//   p_ij = exp(scale q_i . k_j - lse_i),  D_i = dout_i . out_i
+//   dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i . v_j - D_i)
+//   dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+//
+// The probabilities are formed again rather than kept: two kernels walk the pairs, one with
+// keys held (dk, dv) and one with queries held (dq), so every sum stays in the registers
+// of one wave and no atomic decides an order.  That is seven products where five would do
+// if one kernel's waves added into another's rows.
+//
+// Rounding: p and ds pass to their second product in the inputs' type, like any
+// operand; sums, D and the scores stay in 32 bits.  p is rounded as 2^10 p, which costs
+// nothing (the power goes into lse, its inverse into D and the last scaling): among
+// thousands of keys most p lie below float16's normal numbers.
+#pragma once
+
+#include "layers_attention.hpp"
+
+namespace lic {
+namespace {
+
+// D of each row: 16 lanes a row.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void attention_delta(AttnArgs a)
+{
+    const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
+    const int64_t line = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int lane = threadIdx.x & 15, dim = (int)a.p.dim;
+    float sum = 0.0f;
+    if (line < lines) {
+        const int64_t bh = line / a.p.queries;
+        const int64_t query = line - bh * a.p.queries;
+        const int head = (int)(bh % a.p.heads), b = (int)(bh / a.p.heads);
+        const T *o = head_row<T>(static_cast<const void *>(a.p.out), a.p.out_stride, b, query, head);
+        const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
+        if constexpr (VEC) {
+            constexpr int P = 16 / sizeof(T);
+            for (int d = lane * P; d < dim; d += 16 * P) {
+                const Vec<T, P> x = *reinterpret_cast<const Vec<T, P> *>(o + d);
+                const Vec<T, P> y = *reinterpret_cast<const Vec<T, P> *>(g + d);
+#pragma unroll
+                for (int e = 0; e < P; ++e)
+                    sum = fmaf(up(x.v[e]), up(y.v[e]), sum);
+            }
+        } else {
+            for (int d = lane; d < dim; d += 16)
+                sum = fmaf(up(o[d]), up(g[d]), sum);
+        }
+    }
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1)
+        sum += __shfl_xor(sum, x);
+    if (line < lines && lane == 0)
+        a.delta[line] = sum;
+}
+
+constexpr float kLift = 10.0f, kLower = 1.0f / 1024.0f; // 2^10 and its inverse
+
+// lse in powers of two; a row that sees nothing gets p = 0 everywhere
+__device__ __forceinline__ float lse_log2(float lse)
+{
+    return lse == -INFINITY ? INFINITY : lse * kLog2e;
+}
+
+// Which of an accumulator's pairs are visible, a bit each.  `other` runs along its rows;
+// mask: the lane's own entry, `step` to the next of the others.
+__device__ __forceinline__ uint32_t visible(const Range &range, const uint8_t *mask, int64_t step, int other0, int h)
+{
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int x = other0 + acc_row(i, h);
+        bool seen = range.holds(x);
+        if (mask && seen)
+            seen = mask[x * step] != 0;
+        bits |= (uint32_t)seen << i;
+    }
+    return bits;
+}
+
+// One query's gradient with the keys it sees alone (see careful_row of the forward call).
+template <typename T>
+__device__ void careful_dq(const AttnArgs &a, int b, int head, int query, int len, int lo, int hi, float (&dq)[2])
+{
+    const int lane = threadIdx.x & 63, dim = (int)a.p.dim, kv = head / a.group;
+    const Range range = keys_of(a, len, query);
+    const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
+    const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
+    const uint8_t *mask = a.p.mask ? mask_row(a, b, head, query) : nullptr;
+    const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
+    const float lse = lse_log2(a.p.lse[line]), delta = a.delta[line];
+    dq[0] = dq[1] = 0.0f;
+    for (int k0 = lo; k0 < hi; k0 += 64) {
+        const int key = k0 + lane;
+        const bool seen = key < hi && range.holds(key) && (!mask || mask[key * a.p.mask_stride[3]] != 0);
+        float ds = 0.0f;
+        if (seen) {
+            const T *k = head_row<T>(a.p.k, a.p.k_stride, b, key, kv);
+            const T *v = head_row<T>(a.p.v, a.p.v_stride, b, key, kv);
+            float s = 0.0f, dp = 0.0f;
+            for (int d = 0; d < dim; ++d) {
+                s = fmaf(up(q[d]), up(k[d]), s);
+                dp = fmaf(up(g[d]), up(v[d]), dp);
+            }
+            ds = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -lse)) * (dp - delta);
+        }
+        for (uint64_t left = __builtin_amdgcn_ballot_w64(seen); left; left &= left - 1) {
+            const int j = __builtin_ctzll(left);
+            const float x = __shfl(ds, j);
+            const T *k = head_row<T>(a.p.k, a.p.k_stride, b, k0 + j, kv);
+            if (lane < dim)
+                dq[0] = fmaf(x, up(k[lane]), dq[0]);
+            if (lane + 64 < dim)
+                dq[1] = fmaf(x, up(k[lane + 64]), dq[1]);
+        }
+    }
+}
+
+// One key's gradients from the queries [lo, hi) of a head that see it alone, added to dk, dv.
+template <typename T>
+__device__ void careful_dkv(const AttnArgs &a, int b, int head, int key, int len, int lo, int hi, float (&dk)[2],
+                            float (&dv)[2])
+{
+    const int lane = threadIdx.x & 63, dim = (int)a.p.dim, kv = head / a.group;
+    const Range range = queries_of(a, len, key);
+    const T *k = head_row<T>(a.p.k, a.p.k_stride, b, key, kv);
+    const T *v = head_row<T>(a.p.v, a.p.v_stride, b, key, kv);
+    const int64_t line0 = ((int64_t)b * a.p.heads + head) * a.p.queries;
+    for (int q0 = lo; q0 < hi; q0 += 64) {
+        const int query = q0 + lane;
+        const bool seen = query < hi && range.holds(query) &&
+                          (!a.p.mask || mask_row(a, b, head, query)[key * a.p.mask_stride[3]] != 0);
+        float p = 0.0f, ds = 0.0f;
+        if (seen) {
+            const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
+            const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
+            float s = 0.0f, dp = 0.0f;
+            for (int d = 0; d < dim; ++d) {
+                s = fmaf(up(q[d]), up(k[d]), s);
+                dp = fmaf(up(g[d]), up(v[d]), dp);
+            }
+            p = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -lse_log2(a.p.lse[line0 + query])));
+            ds = p * (dp - a.delta[line0 + query]);
+        }
+        for (uint64_t left = __builtin_amdgcn_ballot_w64(seen); left; left &= left - 1) {
+            const int j = __builtin_ctzll(left);
+            const float pj = __shfl(p, j), dj = __shfl(ds, j);
+            const T *q = head_row<T>(a.p.q, a.p.q_stride, b, q0 + j, head);
+            const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, q0 + j, head);
+            if (lane < dim) {
+                dk[0] = fmaf(dj, up(q[lane]), dk[0]);
+                dv[0] = fmaf(pj, up(g[lane]), dv[0]);
+            }
+            if (lane + 64 < dim) {
+                dk[1] = fmaf(dj, up(q[lane + 64]), dk[1]);
+                dv[1] = fmaf(pj, up(g[lane + 64]), dv[1]);
+            }
+        }
+    }
+}
+
+// ---- dk, dv ------------------------------------------------------------------
+//
+// A block of four waves holds 128 keys of one kv head, 32 a wave; the queries of
+// the heads that share it pass through LDS in tiles of 32 or 64 with their dout, lse and D.
+// Scores have queries along the accumulator's rows and keys across the lanes.
+template <typename T, int DT>
+struct KeysBackward {
+    static constexpr int kQueries = sizeof(T) == 4 || DT == 128 ? 32 : 64;
+    using TileT = Tile<T, kQueries, DT>;
+    static constexpr int kStats = 4 * TileT::kBytes;         // two buffers of lse, D
+    static constexpr int kLds = kStats + 2 * 2 * kQueries * 4;
+};
+
+template <typename T, int DT, bool VEC>
+__global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
+{
+    using G = KeysBackward<T, DT>;
+    using TileT = typename G::TileT;
+    constexpr int KK = DT / 16, ND = DT / 32, NQ = G::kQueries;
+    extern __shared__ __align__(16) uint8_t lds[];
+
+    const uint32_t block = xcd_order(blockIdx.x, a.blocks);
+    if (block >= a.blocks)
+        return;
+    const uint32_t k_blocks = (uint32_t)((a.p.keys + 127) / 128);
+    const int key0 = (int)(block % k_blocks) * 128; // the first keys are seen by the most queries
+    const uint32_t rest = block / k_blocks;
+    const int split = (int)(rest % (uint32_t)a.splits);
+    const uint32_t bk = rest / (uint32_t)a.splits;
+    const int kv = (int)(bk % (uint32_t)a.p.kv_heads), b = (int)(bk / (uint32_t)a.p.kv_heads);
+
+    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5;
+    const int key = key0 + wave * 32 + (lane & 31);
+    const int dim = (int)a.p.dim, len = key_length(a, b);
+    const Range range = queries_of(a, len, key);
+
+    FragV<T> kf[KK], vf[KK];
+    {
+        const T *k = head_row<T>(a.p.k, a.p.k_stride, b, key, kv);
+        const T *v = head_row<T>(a.p.v, a.p.v_stride, b, key, kv);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            kf[kk] = row_from_memory<T, VEC>(k, key < len, kk, h, dim);
+            vf[kk] = row_from_memory<T, VEC>(v, key < len, kk, h, dim);
+        }
+    }
+    float16v dk[ND], dv[ND];
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+        dk[n] = dv[n] = zero16();
+
+    // tiles of all heads in one row: this split takes an even share of them
+    int lo = 0, hi = 0;
+    if (key0 < len)
+        query_range(a, len, key0, min(key0 + 128, len), lo, hi);
+    lo &= ~(NQ - 1);
+    const int tiles = (hi - lo + NQ - 1) / NQ, all = tiles * a.group;
+    const int share = (all + a.splits - 1) / a.splits;
+    const int first = min(all, split * share), end = min(all, first + share);
+
+    Stage<T, NQ, DT, 256, VEC> qst, gst;
+    float stat = 0.0f; // the first NQ threads: lse, the next: D
+    const auto fetch = [&](int i) {
+        const int head = kv * a.group + i / tiles, q0 = lo + (i % tiles) * NQ;
+        const int rows = (int)a.p.queries - q0;
+        qst.fetch(head_row<T>(a.p.q, a.p.q_stride, b, q0, head), a.p.q_stride[1], rows, dim, t);
+        gst.fetch(head_row<T>(a.p.dout, a.p.dout_stride, b, q0, head), a.p.dout_stride[1], rows, dim, t);
+        if (t < 2 * NQ) {
+            const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + q0;
+            const int r = t % NQ;
+            if (t < NQ)
+                stat = r < rows ? lse_log2(a.p.lse[line + r]) - kLift : INFINITY;
+            else
+                stat = r < rows ? a.delta[line + r] * kLower : 0.0f;
+        }
+    };
+    const auto store = [&](int buf) {
+        qst.store(lds + buf * TileT::kBytes, t);
+        gst.store(lds + (2 + buf) * TileT::kBytes, t);
+        if (t < 2 * NQ)
+            reinterpret_cast<float *>(lds + G::kStats)[buf * 2 * NQ + t] = stat;
+    };
+    if (first < end) {
+        fetch(first);
+        store(0);
+    }
+    int buf = 0;
+    for (int i = first; i < end; ++i, buf ^= 1) {
+        __syncthreads();
+        if (i + 1 < end)
+            fetch(i + 1);
+        const int head = kv * a.group + i / tiles, q0 = lo + (i % tiles) * NQ;
+#pragma unroll
+        for (int n32 = 0; n32 < NQ; n32 += 32) {
+            const int qn = q0 + n32;
+            if (__all(range.misses(qn, 32)))
+                continue;
+            const uint8_t *ql = lds + buf * TileT::kBytes, *gl = lds + (2 + buf) * TileT::kBytes;
+            const float *lse = reinterpret_cast<const float *>(lds + G::kStats) + buf * 2 * NQ + n32;
+            const float *delta = lse + NQ;
+            float16v s = zero16(), dp = zero16();
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                s = mma(TileT::row_frag(ql, n32 + (lane & 31), kk, h), kf[kk], s);
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                dp = mma(TileT::row_frag(gl, n32 + (lane & 31), kk, h), vf[kk], dp);
+            uint32_t seen = 0xffffu;
+            // rows beyond the queries have p = 0 by their lse; lanes beyond the keys are not stored
+            const bool part = a.p.mask || !__all(key >= len || range.covers(qn, min(32, (int)a.p.queries - qn)));
+            if (part) {
+                const uint8_t *mask =
+                    a.p.mask ? mask_row(a, b, head, 0) + min(key, (int)a.p.keys - 1) * a.p.mask_stride[3] : nullptr;
+                seen = visible(range, mask, a.p.mask_stride[2], qn, h);
+            }
+#pragma unroll
+            for (int i4 = 0; i4 < 16; i4 += 4) {
+                const float4 ls = *reinterpret_cast<const float4 *>(lse + acc_row(i4, h));
+                const float4 de = *reinterpret_cast<const float4 *>(delta + acc_row(i4, h));
+                const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = i4 + e;
+                    s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -l4[e]));
+                    dp[r] = s[r] * fmaf(dp[r], kLower, -d4[e]);
+                }
+            }
+            if (part) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    s[r] = (seen >> r) & 1 ? s[r] : 0.0f;
+                    dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const FragV<T> p = operand<T>(s, half), ds = operand<T>(dp, half);
+#pragma unroll
+                for (int n = 0; n < ND; ++n) {
+                    dv[n] = mma(TileT::col_frag(gl, n32 + half * 16, n, lane), p, dv[n]);
+                    dk[n] = mma(TileT::col_frag(ql, n32 + half * 16, n, lane), ds, dk[n]);
+                }
+            }
+        }
+        if (i + 1 < end)
+            store(buf ^ 1);
+    }
+
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            bad |= not_finite(dk[n][i]) || not_finite(dv[n][i]);
+    uint64_t redo = rows_of(bad && key < len);
+    const bool again = (redo >> (lane & 31)) & 1;
+    const float scale = (float)a.p.scale;
+    const int64_t keys_all = a.p.batch * a.p.kv_heads * a.p.keys;
+    const auto part_row = [&](int k) { // [split][dk, dv][batch, kv head, key][DT]
+        return a.part + ((int64_t)split * 2 * keys_all + ((int64_t)b * a.p.kv_heads + kv) * a.p.keys + k) * DT;
+    };
+    if (key < a.p.keys && !again) {
+#pragma unroll
+        for (int n = 0; n < ND; ++n) {
+            if (key >= len) {
+                dk[n] = zero16();
+                dv[n] = zero16();
+            }
+            if (a.splits == 1) {
+                put_column<T, VEC>(head_row<T>(a.p.dk, a.p.dk_stride, b, key, kv), dk[n], scale, n, h, dim);
+                put_column<T, VEC>(head_row<T>(a.p.dv, a.p.dv_stride, b, key, kv), dv[n], kLower, n, h, dim);
+            } else {
+                put_column<float, true>(part_row(key), dk[n], scale, n, h, DT);
+                put_column<float, true>(part_row(key) + keys_all * DT, dv[n], kLower, n, h, DT);
+            }
+        }
+    }
+    for (; redo; redo &= redo - 1) {
+        const int k = key0 + wave * 32 + __builtin_ctzll(redo);
+        float ck[2] = {0.0f, 0.0f}, cv[2] = {0.0f, 0.0f};
+        for (int i = first; i < end; ++i) {
+            const int q0 = lo + (i % tiles) * NQ;
+            careful_dkv<T>(a, b, kv * a.group + i / tiles, k, len, q0, min(q0 + NQ, (int)a.p.queries), ck, cv);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int d = lane + 64 * c;
+            if (a.splits == 1) {
+                if (d < dim) {
+                    head_row<T>(a.p.dk, a.p.dk_stride, b, k, kv)[d] = down<T>(ck[c] * scale);
+                    head_row<T>(a.p.dv, a.p.dv_stride, b, k, kv)[d] = down<T>(cv[c]);
+                }
+            } else if (d < DT) {
+                part_row(k)[d] = ck[c] * scale;
+                part_row(k)[keys_all * DT + d] = cv[c];
+            }
+        }
+    }
+}
+
+// ---- dq ------------------------------------------------------------------------
+//
+// As the forward kernel of many queries: 128 queries of one head in a block, keys and
+// values through LDS in tiles of 64 taken as two halves, scores with keys along the rows.
+template <typename T, int DT>
+struct QueriesBackward {
+    static constexpr int kKeys = 64;
+    using TileT = Tile<T, kKeys, DT>;
+    static constexpr int kLds = 4 * TileT::kBytes;
+};
+
+template <typename T, int DT, bool VEC>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries_backward(AttnArgs a)
+{
+    using G = QueriesBackward<T, DT>;
+    using TileT = typename G::TileT;
+    constexpr int KK = DT / 16, ND = DT / 32;
+    extern __shared__ __align__(16) uint8_t lds[];
+
+    const uint32_t block = xcd_order(blockIdx.x, a.blocks);
+    if (block >= a.blocks)
+        return;
+    const uint32_t q_blocks = (uint32_t)((a.p.queries + 127) / 128);
+    const int q0 = (int)(q_blocks - 1 - block % q_blocks) * 128;
+    const uint32_t rest = block / q_blocks;
+    const int split = (int)(rest % (uint32_t)a.splits);
+    const uint32_t bh = rest / (uint32_t)a.splits;
+    const int head = (int)(bh % (uint32_t)a.p.heads), b = (int)(bh / (uint32_t)a.p.heads);
+    const int kv = head / a.group;
+
+    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5;
+    const int query = q0 + wave * 32 + (lane & 31);
+    const bool there = query < a.p.queries;
+    const int dim = (int)a.p.dim, len = key_length(a, b);
+    const Range range = keys_of(a, len, query);
+    const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
+    const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
+    const float lse = there ? lse_log2(a.p.lse[line]) : INFINITY;
+    const float delta = there ? a.delta[line] : 0.0f;
+
+    FragV<T> qf[KK], gf[KK];
+    {
+        const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
+        const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            qf[kk] = row_from_memory<T, VEC>(q, there, kk, h, dim);
+            gf[kk] = row_from_memory<T, VEC>(g, there, kk, h, dim);
+        }
+    }
+    float16v dq[ND];
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+        dq[n] = zero16();
+
+    int lo, hi;
+    key_range(a, len, q0, min(q0 + 128, (int)a.p.queries), lo, hi);
+    lo &= ~(G::kKeys - 1);
+    if (a.splits > 1) {
+        const int64_t share = ((hi - lo + a.splits - 1) / a.splits + G::kKeys - 1) / G::kKeys * G::kKeys;
+        const int64_t first = least(hi, lo + share * split);
+        hi = (int)least(hi, first + share);
+        lo = (int)first;
+    }
+    const T *kbase = head_row<T>(a.p.k, a.p.k_stride, b, 0, kv);
+    const T *vbase = head_row<T>(a.p.v, a.p.v_stride, b, 0, kv);
+    const int64_t ks = a.p.k_stride[1], vs = a.p.v_stride[1];
+
+    Stage<T, G::kKeys, DT, 256, VEC> kst, vst;
+    if (lo < hi) {
+        kst.fetch(kbase + lo * ks, ks, len - lo, dim, t);
+        vst.fetch(vbase + lo * vs, vs, len - lo, dim, t);
+        kst.store(lds, t);
+        vst.store(lds + 2 * TileT::kBytes, t);
+    }
+    int buf = 0;
+    for (int k0 = lo; k0 < hi; k0 += G::kKeys, buf ^= 1) {
+        __syncthreads();
+        const int64_t next = (int64_t)k0 + G::kKeys;
+        if (next < hi) {
+            kst.fetch(kbase + next * ks, ks, (int)(len - next), dim, t);
+            vst.fetch(vbase + next * vs, vs, (int)(len - next), dim, t);
+        }
+        const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int kn = k0 + n * 32;
+            if (__all(range.misses(kn, 32)))
+                continue;
+            float16v s = zero16(), dp = zero16();
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                s = mma(TileT::row_frag(kl, n * 32 + (lane & 31), kk, h), qf[kk], s);
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk)
+                dp = mma(TileT::row_frag(vl, n * 32 + (lane & 31), kk, h), gf[kk], dp);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * (dp[r] - delta);
+            if (mask || !__all(!there || range.covers(kn, 32))) {
+                const uint32_t seen = visible(range, mask, a.p.mask_stride[3], kn, h);
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const FragV<T> ds = operand<T>(dp, half);
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+                    dq[d] = mma(TileT::col_frag(kl, n * 32 + half * 16, d, lane), ds, dq[d]);
+            }
+        }
+        if (next < hi) {
+            kst.store(lds + (buf ^ 1) * TileT::kBytes, t);
+            vst.store(lds + (2 + (buf ^ 1)) * TileT::kBytes, t);
+        }
+    }
+
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            bad |= not_finite(dq[n][i]);
+    uint64_t redo = rows_of(bad && there);
+    const float scale = (float)a.p.scale;
+    const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
+    if (there && !((redo >> (lane & 31)) & 1)) {
+#pragma unroll
+        for (int n = 0; n < ND; ++n) {
+            if (a.splits == 1)
+                put_column<T, VEC>(head_row<T>(a.p.dq, a.p.dq_stride, b, query, head), dq[n], scale, n, h, dim);
+            else
+                put_column<float, true>(a.part + (split * lines + line) * DT, dq[n], scale, n, h, DT);
+        }
+    }
+    for (; redo; redo &= redo - 1) {
+        const int qi = q0 + wave * 32 + __builtin_ctzll(redo);
+        float c[2];
+        careful_dq<T>(a, b, head, qi, len, lo, hi, c);
+        for (int e = 0; e < 2; ++e) {
+            const int d = lane + 64 * e;
+            if (a.splits == 1) {
+                if (d < dim)
+                    head_row<T>(a.p.dq, a.p.dq_stride, b, qi, head)[d] = down<T>(c[e] * scale);
+            } else if (d < DT) {
+                const int64_t ln = ((int64_t)b * a.p.heads + head) * a.p.queries + qi;
+                a.part[(split * lines + ln) * DT + d] = c[e] * scale;
+            }
+        }
+    }
+}
+
+// The splits' parts summed in their order: four columns of a row a thread.
+struct JoinArgs {
+    const float *part;
+    void *out;
+    int64_t stride[3]; // batch, row, head
+    int64_t step;      // from a split's part to the next's
+    int64_t lines, rows, heads;
+    int splits, dim;
+};
+
+template <typename T, int DT>
+__global__ __launch_bounds__(256) void attention_join(JoinArgs a)
+{
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t line = id / (DT / 4);
+    const int d = (int)(id % (DT / 4)) * 4;
+    if (line >= a.lines || d >= a.dim)
+        return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < a.splits; ++i) {
+        const float4 p = *reinterpret_cast<const float4 *>(a.part + i * a.step + line * DT + d);
+        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    const int64_t bh = line / a.rows;
+    T *out = head_row<T>(a.out, a.stride, (int)(bh / a.heads), line - bh * a.rows, (int)(bh % a.heads));
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    for (int e = 0; e < 4; ++e)
+        if (d + e < a.dim)
+            out[d + e] = down<T>(v[e]);
+}
+
+template <typename T, int DT>
+void join(const float *part, void *out, const int64_t *stride, int64_t step, int64_t batch, int64_t rows,
+          int64_t heads, int splits, int64_t dim, hipStream_t s)
+{
+    JoinArgs j{part, out, {stride[0], stride[1], stride[2]}, step, batch * rows * heads, rows, heads, splits, (int)dim};
+    const int64_t threads = j.lines * (DT / 4);
+    attention_join<T, DT><<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(j);
+}
+
+template <typename T, int DT, bool VEC>
+int run_backward(AttnArgs a, hipStream_t s)
+{
+    const lic_attention_args &p = a.p;
+    float *parts = a.part;
+    if (p.queries > 0) {
+        const int64_t lines = p.batch * p.heads * p.queries;
+        attention_delta<T, VEC><<<(uint32_t)((lines + 15) / 16), 256, 0, s>>>(a);
+    }
+    if (p.keys > 0) {
+        using G = KeysBackward<T, DT>;
+        static const bool once = (allow_lds(attention_keys_backward<T, DT, VEC>, G::kLds), true);
+        (void)once;
+        a.splits = keys_splits(p);
+        a.part = parts;
+        const int64_t blocks = (p.keys + 127) / 128 * p.batch * p.kv_heads * a.splits;
+        if (blocks > 0x7fffff00)
+            return RANS_E_ARG;
+        a.blocks = (uint32_t)blocks;
+        attention_keys_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
+        if (a.splits > 1) {
+            const int64_t all = p.batch * p.kv_heads * p.keys * DT;
+            join<T, DT>(parts, p.dk, p.dk_stride, 2 * all, p.batch, p.keys, p.kv_heads, a.splits, p.dim, s);
+            join<T, DT>(parts + all, p.dv, p.dv_stride, 2 * all, p.batch, p.keys, p.kv_heads, a.splits, p.dim, s);
+        }
+    }
+    if (p.queries > 0) {
+        using G = QueriesBackward<T, DT>;
+        static const bool once = (allow_lds(attention_queries_backward<T, DT, VEC>, G::kLds), true);
+        (void)once;
+        a.splits = queries_splits(p);
+        a.part = parts; // dk and dv are joined by now, in this stream's order
+        const int64_t blocks = (p.queries + 127) / 128 * p.batch * p.heads * a.splits;
+        if (blocks > 0x7fffff00)
+            return RANS_E_ARG;
+        a.blocks = (uint32_t)blocks;
+        attention_queries_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
+        if (a.splits > 1)
+            join<T, DT>(parts, p.dq, p.dq_stride, p.batch * p.heads * p.queries * DT, p.batch, p.queries, p.heads,
+                        a.splits, p.dim, s);
+    }
+    return launched();
+}
+
+}  // namespace
+}  // namespace lic

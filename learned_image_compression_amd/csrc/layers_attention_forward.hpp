@@ -1,0 +1,526 @@
+// layers_attention_forward.hpp -- attention's forward kernels (included by the
+// translation unit of each element type).
+//
+// One pass over the keys with a running maximum m and sum l of each row.  The
+// maximum is only raised when a tile exceeds it by more than 2^8: below that the
+// probabilities stay under 256, which 32-bit sums and both 16-bit types hold, and the
+// accumulators need no scaling in most tiles.
+#pragma once
+
+#include "layers_attention.hpp"
+
+namespace lic {
+namespace {
+
+constexpr float kSlack = 8.0f; // in powers of two
+
+// Scores of one accumulator (keys along its rows) that a query does not see become -inf.
+__device__ __forceinline__ void hide(float16v &s, const AttnArgs &a, const Range &range, const uint8_t *mask,
+                                     int key0, int h)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int key = key0 + acc_row(i, h);
+        bool seen = range.holds(key);
+        if (mask && seen)
+            seen = mask[key * a.p.mask_stride[3]] != 0;
+        s[i] = seen ? s[i] : -INFINITY;
+    }
+}
+
+// The running softmax of a lane's query over N accumulators of scores, which become
+// probabilities relative to the running maximum.
+template <int N, int ACC>
+__device__ __forceinline__ void soften(float16v (&s)[N], float scale, float &m, float &l, float16v (&o)[ACC])
+{
+    float top = s[0][0];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            top = fmaxf(top, s[n][i]);
+    top = pair_max(top) * scale;
+    if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+        const float next = fmaxf(m, top);
+        const float shrink = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+        m = next;
+        l *= shrink;
+#pragma unroll
+        for (int n = 0; n < ACC; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[n][i] *= shrink;
+    }
+    const float base = m == -INFINITY ? 0.0f : m; // nothing seen yet: exp(-inf) below
+    float sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], scale, -base));
+            sum += s[n][i];
+        }
+    l += sum;
+}
+
+// A row that came out not finite, again and with the keys that it sees alone: a NaN or
+// an infinity of a key it does not see is multiplied by its probability 0 above.
+// Lane l takes key l of each 64, then column l (and l + 64) of the sum.
+template <typename T>
+__device__ void careful_row(const AttnArgs &a, int b, int head, int query, int len, int lo, int hi, float &m,
+                            float &l, float (&o)[2])
+{
+    const int lane = threadIdx.x & 63, dim = (int)a.p.dim, kv = head / a.group;
+    const Range range = keys_of(a, len, query);
+    const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
+    const uint8_t *mask = a.p.mask ? mask_row(a, b, head, query) : nullptr;
+    m = -INFINITY, l = 0.0f, o[0] = o[1] = 0.0f;
+    for (int k0 = lo; k0 < hi; k0 += 64) {
+        const int key = k0 + lane;
+        const bool seen = key < hi && range.holds(key) && (!mask || mask[key * a.p.mask_stride[3]] != 0);
+        float s = -INFINITY;
+        if (seen) {
+            const T *k = head_row<T>(a.p.k, a.p.k_stride, b, key, kv);
+            float dot = 0.0f;
+            for (int d = 0; d < dim; ++d)
+                dot = fmaf(up(q[d]), up(k[d]), dot);
+            s = dot * a.scale_log2;
+        }
+        float top = s;
+        for (int x = 32; x > 0; x >>= 1)
+            top = fmaxf(top, __shfl_xor(top, x));
+        const float next = fmaxf(m, top);
+        const float shrink = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+        const float p = seen ? __builtin_amdgcn_exp2f(s - (next == -INFINITY ? 0.0f : next)) : 0.0f;
+        m = next;
+        float sum = p;
+        for (int x = 32; x > 0; x >>= 1)
+            sum += __shfl_xor(sum, x);
+        l = l * shrink + sum;
+        o[0] *= shrink, o[1] *= shrink;
+        for (uint64_t left = __builtin_amdgcn_ballot_w64(seen); left; left &= left - 1) {
+            const int j = __builtin_ctzll(left);
+            const float pj = __shfl(p, j);
+            const T *v = head_row<T>(a.p.v, a.p.v_stride, b, k0 + j, kv);
+            if (lane < dim)
+                o[0] = fmaf(pj, up(v[lane]), o[0]);
+            if (lane + 64 < dim)
+                o[1] = fmaf(pj, up(v[lane + 64]), o[1]);
+        }
+    }
+}
+
+__device__ __forceinline__ float log_sum(float m, float l)
+{
+    return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// ---- many queries ----------------------------------------------------------
+//
+// A block of four waves holds 128 queries of one head, 32 a wave, in registers; keys
+// and values pass through LDS in tiles of 64, two buffers, so one barrier a tile.
+// A key tile serves four waves and costs each 1 LDS byte per 2 dim flops.
+template <typename T, int DT, bool VEC>
+struct TilesForward {
+    static constexpr int kKeys = 64;
+    using TileT = Tile<T, kKeys, DT>;
+    using StageT = Stage<T, kKeys, DT, 256, VEC>;
+    static constexpr int kLds = 4 * TileT::kBytes;
+};
+
+template <typename T, int DT, bool VEC>
+__global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void attention_tiles_forward(AttnArgs a)
+{
+    using G = TilesForward<T, DT, VEC>;
+    using TileT = typename G::TileT;
+    constexpr int KK = DT / 16, ND = DT / 32;
+    extern __shared__ __align__(16) uint8_t lds[];
+
+    const uint32_t block = xcd_order(blockIdx.x, a.blocks);
+    if (block >= a.blocks)
+        return;
+    const uint32_t q_blocks = (uint32_t)((a.p.queries + 127) / 128);
+    const uint32_t bh = block / q_blocks;
+    const int head = (int)(bh % (uint32_t)a.p.heads), b = (int)(bh / (uint32_t)a.p.heads);
+    const int kv = head / a.group;
+    // the last queries see the most keys: they start first
+    const int q0 = (int)(q_blocks - 1 - block % q_blocks) * 128;
+
+    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5;
+    const int query = q0 + wave * 32 + (lane & 31);
+    const int dim = (int)a.p.dim, len = key_length(a, b);
+    const Range range = keys_of(a, len, query);
+    const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
+
+    FragV<T> qf[KK];
+    {
+        const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+            qf[kk] = row_from_memory<T, VEC>(q, query < a.p.queries, kk, h, dim);
+    }
+    float16v o[ND];
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+        o[n] = zero16();
+    float m = -INFINITY, l = 0.0f;
+
+    int lo, hi;
+    key_range(a, len, q0, min(q0 + 128, (int)a.p.queries), lo, hi);
+    lo &= ~(G::kKeys - 1);
+    const T *kbase = head_row<T>(a.p.k, a.p.k_stride, b, 0, kv);
+    const T *vbase = head_row<T>(a.p.v, a.p.v_stride, b, 0, kv);
+    const int64_t ks = a.p.k_stride[1], vs = a.p.v_stride[1];
+
+    typename G::StageT kst, vst;
+    if (lo < hi) {
+        kst.fetch(kbase + lo * ks, ks, len - lo, dim, t);
+        vst.fetch(vbase + lo * vs, vs, len - lo, dim, t);
+        kst.store(lds, t);
+        vst.store(lds + 2 * TileT::kBytes, t);
+    }
+    int buf = 0;
+    for (int k0 = lo; k0 < hi; k0 += G::kKeys, buf ^= 1) {
+        __syncthreads();
+        const int64_t next = (int64_t)k0 + G::kKeys;
+        if (next < hi) {
+            kst.fetch(kbase + next * ks, ks, (int)(len - next), dim, t);
+            vst.fetch(vbase + next * vs, vs, (int)(len - next), dim, t);
+        }
+        if (!__all(range.misses(k0, G::kKeys))) {
+            const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
+            float16v s[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                s[n] = zero16();
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+                    s[n] = mma(TileT::row_frag(kl, n * 32 + (lane & 31), kk, h), qf[kk], s[n]);
+            }
+            if (mask || !__all(query >= a.p.queries || range.covers(k0, G::kKeys))) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    hide(s[n], a, range, mask, k0 + n * 32, h);
+            }
+            soften(s, a.scale_log2, m, l, o);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const FragV<T> p = operand<T>(s[n], half);
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+                        o[d] = mma(TileT::col_frag(vl, n * 32 + half * 16, d, lane), p, o[d]);
+                }
+        }
+        if (next < hi) {
+            kst.store(lds + (buf ^ 1) * TileT::kBytes, t);
+            vst.store(lds + (2 + (buf ^ 1)) * TileT::kBytes, t);
+        }
+    }
+
+    const float total = pair_sum(l);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            bad |= not_finite(o[n][i]);
+    uint64_t redo = rows_of(bad && query < a.p.queries);
+    if (query < a.p.queries && !((redo >> (lane & 31)) & 1)) {
+        T *out = head_row<T>(a.p.out, a.p.out_stride, b, query, head);
+#pragma unroll
+        for (int n = 0; n < ND; ++n)
+            put_column<T, VEC>(out, o[n], inv, n, h, dim);
+        if (h == 0)
+            a.p.lse[((int64_t)b * a.p.heads + head) * a.p.queries + query] = log_sum(m, total);
+    }
+    for (; redo; redo &= redo - 1) {
+        const int qi = q0 + wave * 32 + __builtin_ctzll(redo);
+        float cm, cl, co[2];
+        careful_row<T>(a, b, head, qi, len, lo, hi, cm, cl, co);
+        const float ci = cl == 0.0f ? 0.0f : 1.0f / cl;
+        T *out = head_row<T>(a.p.out, a.p.out_stride, b, qi, head);
+        if (lane < dim)
+            out[lane] = down<T>(co[0] * ci);
+        if (lane + 64 < dim)
+            out[lane + 64] = down<T>(co[1] * ci);
+        if (lane == 0)
+            a.p.lse[((int64_t)b * a.p.heads + head) * a.p.queries + qi] = log_sum(cm, cl);
+    }
+}
+
+// ---- few queries -------------------------------------------------------------
+//
+// The queries of all heads that share a kv head are packed into tiles of 32 rows
+// (row r: query r / group, head r % group of them), so keys and values are read once
+// for all of them; the key axis is split over blocks, and over a block's four waves,
+// which take tiles of 32 keys in turn, each with its own LDS and no barrier.  Memory
+// bounds it: with a single row 31 of 32 columns of the products are idle, and the
+// matrix units still need less time than the keys' way from HBM.
+// The waves' parts are joined in LDS, the blocks' by attention_rows_join.
+template <typename T, int DT, bool VEC>
+struct RowsForward {
+    static constexpr int kKeys = 32;
+    using TileT = Tile<T, kKeys, DT>;
+    using StageT = Stage<T, kKeys, DT, 64, VEC>;
+    static constexpr int kWave = 2 * TileT::kBytes;       // keys, values
+    static constexpr int kSums = 32 * DT * 4;             // a wave's part at the end
+    static constexpr int kLds = 4 * (kWave > kSums ? kWave : kSums) + 4 * 32 * 2 * 4;
+};
+
+// place of a sum: columns rotated by the row, so 32 rows of one column fall into all banks
+template <int DT>
+__device__ __forceinline__ int sum_at(int row, int d)
+{
+    return row * DT + (d + row < DT ? d + row : d + row - DT);
+}
+
+template <typename T, int DT, bool VEC>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_forward(AttnArgs a)
+{
+    using G = RowsForward<T, DT, VEC>;
+    using TileT = typename G::TileT;
+    constexpr int KK = DT / 16, ND = DT / 32, kRegion = G::kWave > G::kSums ? G::kWave : G::kSums;
+    extern __shared__ __align__(16) uint8_t lds[];
+
+    const int rows = (int)a.p.queries * a.group, row_tiles = (rows + 31) / 32;
+    const uint32_t block = blockIdx.x;
+    const int split = (int)(block % (uint32_t)a.splits);
+    const uint32_t rest = block / (uint32_t)a.splits;
+    const int row_tile = (int)(rest % (uint32_t)row_tiles);
+    const uint32_t bk = rest / (uint32_t)row_tiles;
+    const int kv = (int)(bk % (uint32_t)a.p.kv_heads), b = (int)(bk / (uint32_t)a.p.kv_heads);
+
+    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5;
+    const int row = row_tile * 32 + (lane & 31);
+    const int query = row / a.group, head = kv * a.group + row % a.group;
+    const int dim = (int)a.p.dim, len = key_length(a, b);
+    const Range range = keys_of(a, len, query);
+    const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
+
+    FragV<T> qf[KK];
+    {
+        const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+            qf[kk] = row_from_memory<T, VEC>(q, row < rows, kk, h, dim);
+    }
+    float16v o[ND];
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+        o[n] = zero16();
+    float m = -INFINITY, l = 0.0f;
+
+    // this split's keys: an even share in whole tiles of the four waves
+    int lo, hi;
+    key_range(a, len, row_tile * 32 / a.group, min((row_tile * 32 + 31) / a.group + 1, (int)a.p.queries), lo, hi);
+    const int share = ((hi - lo + a.splits - 1) / a.splits + 127) / 128 * 128;
+    const int64_t first = (int64_t)lo + (int64_t)share * split;
+    const int end = (int)least(hi, first + share);
+
+    const T *kbase = head_row<T>(a.p.k, a.p.k_stride, b, 0, kv);
+    const T *vbase = head_row<T>(a.p.v, a.p.v_stride, b, 0, kv);
+    const int64_t ks = a.p.k_stride[1], vs = a.p.v_stride[1];
+    uint8_t *kl = lds + wave * kRegion, *vl = kl + TileT::kBytes;
+
+    typename G::StageT kst, vst;
+    int64_t k0 = first + wave * 32;
+    if (k0 < end) {
+        kst.fetch(kbase + k0 * ks, ks, (int)(end - k0), dim, lane);
+        vst.fetch(vbase + k0 * vs, vs, (int)(end - k0), dim, lane);
+    }
+    for (; k0 < end; k0 += 128) {
+        wave_fence();
+        kst.store(kl, lane);
+        vst.store(vl, lane);
+        wave_fence();
+        const int64_t next = k0 + 128;
+        if (next < end) {
+            kst.fetch(kbase + next * ks, ks, (int)(end - next), dim, lane);
+            vst.fetch(vbase + next * vs, vs, (int)(end - next), dim, lane);
+        }
+        float16v s[1] = {zero16()};
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk)
+            s[0] = mma(TileT::row_frag(kl, lane & 31, kk, h), qf[kk], s[0]);
+        // the tile may pass the split's end: those keys are the next split's
+        const bool whole = k0 + 32 <= end;
+        if (mask || !whole || !__all(row >= rows || range.covers((int)k0, 32))) {
+            hide(s[0], a, range, mask, (int)k0, h);
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (k0 + acc_row(i, h) >= end)
+                        s[0][i] = -INFINITY;
+            }
+        }
+        soften(s, a.scale_log2, m, l, o);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const FragV<T> p = operand<T>(s[0], half);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                o[d] = mma(TileT::col_frag(vl, half * 16, d, lane), p, o[d]);
+        }
+    }
+
+    // a wave's part: sums [32][DT], then m and l
+    l = pair_sum(l);
+    bool bad = false;
+    float *sums = reinterpret_cast<float *>(lds + wave * kRegion);
+    float2 *stats = reinterpret_cast<float2 *>(lds + 4 * kRegion);
+    wave_fence();
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            bad |= not_finite(o[n][i]);
+            sums[sum_at<DT>(lane & 31, n * 32 + acc_row(i, h))] = o[n][i];
+        }
+    if (h == 0)
+        stats[wave * 32 + lane] = make_float2(m, l);
+    wave_fence();
+    for (uint64_t redo = rows_of(bad && row < rows); redo; redo &= redo - 1) {
+        const int j = __builtin_ctzll(redo);
+        const int r = row_tile * 32 + j;
+        float cm = -INFINITY, cl = 0.0f, co[2] = {0.0f, 0.0f};
+        // this wave's tiles, each joined to the ones before
+        for (int64_t c0 = first + wave * 32; c0 < end; c0 += 128) {
+            float tm, tl, to[2];
+            careful_row<T>(a, b, kv * a.group + r % a.group, r / a.group, len, (int)c0,
+                           (int)least(c0 + 32, end), tm, tl, to);
+            const float next = fmaxf(cm, tm);
+            if (next == -INFINITY && tl == 0.0f)
+                continue;
+            const float wc = cl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(cm - next);
+            const float wt = tl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(tm - next);
+            cl = cl * wc + tl * wt;
+            co[0] = (cl == 0.0f ? 0.0f : co[0] * wc) + (tl == 0.0f ? 0.0f : to[0] * wt);
+            co[1] = (cl == 0.0f ? 0.0f : co[1] * wc) + (tl == 0.0f ? 0.0f : to[1] * wt);
+            cm = next;
+        }
+        if (lane < DT)
+            sums[sum_at<DT>(j, lane)] = co[0];
+        if (lane + 64 < DT)
+            sums[sum_at<DT>(j, lane + 64)] = co[1];
+        if (lane == 0)
+            stats[wave * 32 + j] = make_float2(cm, cl);
+    }
+    __syncthreads();
+
+    const float *all = reinterpret_cast<const float *>(lds);
+    for (int e = t; e < 32 * DT; e += 256) {
+        const int j = e / DT, d = e % DT, r = row_tile * 32 + j;
+        if (r >= rows)
+            break;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            top = fmaxf(top, stats[w * 32 + j].x);
+        float sum = 0.0f, total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float2 st = stats[w * 32 + j];
+            if (st.y != 0.0f) { // NaN counts
+                const float f = __builtin_amdgcn_exp2f(st.x - top);
+                sum += f * all[w * (kRegion / 4) + sum_at<DT>(j, d)];
+                total += f * st.y;
+            }
+        }
+        const int qi = r / a.group, hd = kv * a.group + r % a.group;
+        const int64_t line = ((int64_t)b * a.p.heads + hd) * a.p.queries + qi;
+        if (a.splits == 1) {
+            if (d < dim)
+                head_row<T>(a.p.out, a.p.out_stride, b, qi, hd)[d] = down<T>(total == 0.0f ? 0.0f : sum / total);
+            if (d == 0)
+                a.p.lse[line] = log_sum(top, total);
+        } else {
+            const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
+            float *part = a.part + (split * lines + line) * (DT + 2);
+            part[2 + d] = sum;
+            if (d == 0) {
+                part[0] = top;
+                part[1] = total;
+            }
+        }
+    }
+}
+
+// The splits' parts of each row joined: a wave a row.
+template <typename T, int DT>
+__global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a)
+{
+    const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
+    const int64_t line = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (line >= lines)
+        return;
+    const int lane = threadIdx.x & 63;
+    const float *part = a.part + line * (DT + 2);
+    const int64_t step = lines * (DT + 2);
+    float top = -INFINITY;
+    for (int s = lane; s < a.splits; s += 64)
+        top = fmaxf(top, part[s * step]);
+    for (int x = 32; x > 0; x >>= 1)
+        top = fmaxf(top, __shfl_xor(top, x));
+    float sum[2] = {0.0f, 0.0f}, total = 0.0f;
+    for (int s = 0; s < a.splits; ++s) {
+        const float *p = part + s * step;
+        const float pm = p[0], pl = p[1];
+        if (pl == 0.0f)
+            continue;
+        const float f = __builtin_amdgcn_exp2f(pm - top);
+        total += f * pl;
+        if (lane < DT)
+            sum[0] += f * p[2 + lane];
+        if (lane + 64 < DT)
+            sum[1] += f * p[2 + lane + 64];
+    }
+    const int query = (int)(line % a.p.queries);
+    const int64_t bh = line / a.p.queries;
+    const int head = (int)(bh % a.p.heads), b = (int)(bh / a.p.heads);
+    T *out = head_row<T>(a.p.out, a.p.out_stride, b, query, head);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    if (lane < a.p.dim)
+        out[lane] = down<T>(sum[0] * inv);
+    if (lane + 64 < a.p.dim)
+        out[lane + 64] = down<T>(sum[1] * inv);
+    if (lane == 0)
+        a.p.lse[line] = log_sum(top, total);
+}
+
+// ---- host ----------------------------------------------------------------------
+
+template <typename T, int DT, bool VEC>
+int run_forward(AttnArgs a, hipStream_t s)
+{
+    if (few_rows(a.p)) {
+        using G = RowsForward<T, DT, VEC>;
+        static const bool once = (allow_lds(attention_rows_forward<T, DT, VEC>, G::kLds), true);
+        (void)once;
+        a.splits = row_splits(a.p);
+        const int64_t rows = a.p.queries * a.group;
+        const int64_t blocks = (rows + 31) / 32 * a.p.batch * a.p.kv_heads * a.splits;
+        if (blocks > 0x7fffffff)
+            return RANS_E_ARG;
+        attention_rows_forward<T, DT, VEC><<<(uint32_t)blocks, 256, G::kLds, s>>>(a);
+        if (a.splits > 1) {
+            const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
+            attention_rows_join<T, DT><<<(uint32_t)((lines + 3) / 4), 256, 0, s>>>(a);
+        }
+        return launched();
+    }
+    using G = TilesForward<T, DT, VEC>;
+    static const bool once = (allow_lds(attention_tiles_forward<T, DT, VEC>, G::kLds), true);
+    (void)once;
+    const int64_t blocks = (a.p.queries + 127) / 128 * a.p.batch * a.p.heads;
+    if (blocks > 0x7fffff00)
+        return RANS_E_ARG;
+    a.blocks = (uint32_t)blocks;
+    attention_tiles_forward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
+    return launched();
+}
+
+}  // namespace
+}  // namespace lic

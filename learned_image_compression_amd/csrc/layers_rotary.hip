@@ -1,0 +1,238 @@
+// layers_rotary.hip -- rotary positions: the tables of cosines and sines, and
+// the rotation of queries and keys (its inverse is the gradient).
+//
+// The rotation is bound by HBM: q and k are read and written once, the tables
+// are a small part (a row serves all heads of a token).  A thread turns V pairs
+// of one head (two 16-byte loads of 16-bit values, four of 32-bit ones with V = 8
+// and V = 4) or copies 2 V of the head's other values; neighbouring threads take
+// the units of a head, then the heads of a token, so a token's table row is read
+// from L1 by all heads but the first.  q and k share one launch.
+#include "layers_common.hpp"
+
+namespace lic {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RotaryArgs {
+    lic_rotary_args p;
+    uint32_t turn_units, units; // units of a head: turning, then copying
+    uint32_t all_heads;
+    uint64_t total;
+};
+
+template <typename T, int V, bool INTER>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
+{
+    using VT = Vec<T, V>;
+    const lic_rotary_args &p = a.p;
+    const uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= a.total)
+        return;
+    const uint64_t row = id / a.units; // (batch, token, head)
+    const uint32_t unit = (uint32_t)(id - row * a.units);
+    const uint64_t bs = row / a.all_heads;
+    uint32_t head = (uint32_t)(row - bs * a.all_heads);
+    const uint64_t b = bs / (uint64_t)p.tokens, s = bs - b * (uint64_t)p.tokens;
+
+    const bool is_q = head < (uint32_t)p.heads;
+    if (!is_q)
+        head -= (uint32_t)p.heads;
+    const int64_t *si = is_q ? p.q_stride : p.k_stride;
+    const int64_t *so = is_q ? p.q_out_stride : p.k_out_stride;
+    const T *in = static_cast<const T *>(is_q ? p.q : p.k) + b * si[0] + s * si[1] + head * si[2];
+    T *out = static_cast<T *>(is_q ? p.q_out : p.k_out) + b * so[0] + s * so[1] + head * so[2];
+
+    const int half = (int)p.rotary_dim / 2;
+    if (unit >= a.turn_units) { // values beyond the rotated part
+        const int d0 = (int)p.rotary_dim + (int)(unit - a.turn_units) * 2 * V;
+        if (in != out) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (d0 + h * V < p.dim)
+                    *reinterpret_cast<VT *>(out + d0 + h * V) =
+                        *reinterpret_cast<const VT *>(in + d0 + h * V);
+        }
+        return;
+    }
+    const int j = (int)unit * V;
+    const int at0 = INTER ? 2 * j : j, at1 = INTER ? 2 * j + V : half + j;
+    const VT x0 = *reinterpret_cast<const VT *>(in + at0);
+    const VT x1 = *reinterpret_cast<const VT *>(in + at1);
+    const int64_t pos = p.positions ? p.positions[b * p.pos_batch + s] : (int64_t)s;
+    float c[V], n[V];
+    if ((uint64_t)pos < (uint64_t)p.table_rows) {
+        constexpr int W = V < 4 ? V : 4;
+        const float *ct = p.cos + pos * half + j, *st = p.sin + pos * half + j;
+#pragma unroll
+        for (int i = 0; i < V; i += W) {
+            const Vec<float, W> cv = *reinterpret_cast<const Vec<float, W> *>(ct + i);
+            const Vec<float, W> sv = *reinterpret_cast<const Vec<float, W> *>(st + i);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                c[i + w] = cv.v[w];
+                n[i + w] = p.inverse ? -sv.v[w] : sv.v[w];
+            }
+        }
+    } else {
+        if (p.status)
+            *p.status = RANS_E_INDEX;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            c[i] = n[i] = __builtin_nanf("");
+    }
+    VT y0, y1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        // pair i: neighbours (interleaved: element 2 i of the 2 V that x0 and x1 hold), or
+        // the same place of the two halves
+        const int e = 2 * i;
+        const float u = up(INTER ? (e < V ? x0.v[e % V] : x1.v[e % V]) : x0.v[i]);
+        const float w = up(INTER ? (e + 1 < V ? x0.v[(e + 1) % V] : x1.v[(e + 1) % V]) : x1.v[i]);
+        const T t0 = down<T>(u * c[i] - w * n[i]), t1 = down<T>(u * n[i] + w * c[i]);
+        if constexpr (INTER) {
+            (e < V ? y0 : y1).v[e % V] = t0;
+            (e + 1 < V ? y0 : y1).v[(e + 1) % V] = t1;
+        } else {
+            y0.v[i] = t0;
+            y1.v[i] = t1;
+        }
+    }
+    *reinterpret_cast<VT *>(out + at0) = y0;
+    *reinterpret_cast<VT *>(out + at1) = y1;
+}
+
+struct TableArgs {
+    const double *coords;
+    float *cos, *sin;
+    double base, factor, low, high, original, amplitude;
+    uint64_t total;
+    int axes, pairs;
+};
+
+// One thread an angle.  Once for a model, so double precision costs nothing.
+__global__ __launch_bounds__(kThreads) void rotary_table_kernel(TableArgs a)
+{
+    const uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (id >= a.total)
+        return;
+    const uint64_t row = id / (uint32_t)a.pairs;
+    const int pair = (int)(id - row * (uint32_t)a.pairs);
+    const int n = a.pairs / a.axes, axis = pair / n, j = pair - axis * n;
+    double freq = pow(a.base, -(double)j / n);
+    if (a.factor != 1.0) {
+        double keep = 0.0;
+        if (a.high > a.low) {
+            const double turns = a.original * freq / 6.283185307179586;
+            keep = fmin(1.0, fmax(0.0, (turns - a.low) / (a.high - a.low)));
+        }
+        freq *= keep + (1.0 - keep) / a.factor;
+    }
+    double s, c;
+    sincos(a.coords[row * (uint32_t)a.axes + axis] * freq, &s, &c);
+    a.cos[id] = (float)(c * a.amplitude);
+    a.sin[id] = (float)(s * a.amplitude);
+}
+
+template <typename T, int V>
+int run_rotary(RotaryArgs a, hipStream_t s)
+{
+    const lic_rotary_args &p = a.p;
+    a.turn_units = (uint32_t)(p.rotary_dim / 2 / V);
+    a.units = a.turn_units + (uint32_t)((p.dim - p.rotary_dim + 2 * V - 1) / (2 * V));
+    a.all_heads = (uint32_t)(p.heads + p.kv_heads);
+    a.total = (uint64_t)p.batch * p.tokens * a.all_heads * a.units;
+    const uint64_t blocks = (a.total + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffull)
+        return RANS_E_ARG;
+    if (p.interleaved)
+        rotary_kernel<T, V, true><<<(uint32_t)blocks, kThreads, 0, s>>>(a);
+    else
+        rotary_kernel<T, V, false><<<(uint32_t)blocks, kThreads, 0, s>>>(a);
+    return launched();
+}
+
+// Whether heads, strides and addresses let V values be read at once.
+template <typename T>
+bool fits(const lic_rotary_args &p, int V)
+{
+    const uint64_t bytes = V * sizeof(T);
+    // the table is read by at most four values at once
+    const int w = V < 4 ? V : 4;
+    if ((p.rotary_dim / 2) % V || p.dim % V || !aligned_to(p.cos, 4 * w) ||
+        !aligned_to(p.sin, 4 * w))
+        return false;
+    const auto ok = [&](const void *x, const int64_t *st, int64_t heads) {
+        return aligned_to(x, bytes) && (p.batch == 1 || st[0] % V == 0) &&
+               (p.tokens == 1 || st[1] % V == 0) && (heads == 1 || st[2] % V == 0);
+    };
+    return ok(p.q, p.q_stride, p.heads) && ok(p.q_out, p.q_out_stride, p.heads) &&
+           (p.kv_heads == 0 || (ok(p.k, p.k_stride, p.kv_heads) &&
+                                ok(p.k_out, p.k_out_stride, p.kv_heads)));
+}
+
+bool extent(int64_t v, int64_t least, int64_t most) { return v >= least && v <= most; }
+
+}  // namespace
+}  // namespace lic
+
+using namespace lic;
+
+extern "C" int lic_rotary_table(const double *coords, int64_t rows, int32_t axes,
+                                int32_t rotary_dim, double base, double factor, double low,
+                                double high, double original, double amplitude, float *cos,
+                                float *sin, hipStream_t hstream)
+{
+    const auto finite = [](double v) { return v - v == 0.0; };
+    if (!extent(rows, 0, 1ll << 31) || axes < 1 || axes > 8 || rotary_dim < 2 ||
+        rotary_dim > 65536 || rotary_dim % 2 || (rotary_dim / 2) % axes || !(base > 0.0) ||
+        !finite(base) || !(factor > 0.0) || !finite(factor) || !finite(low) || !finite(high) ||
+        !(original >= 0.0) || !finite(original) || !finite(amplitude))
+        return RANS_E_ARG;
+    if (rows == 0)
+        return RANS_OK;
+    if (!coords || !cos || !sin)
+        return RANS_E_ARG;
+    TableArgs a{coords, cos, sin, base, factor, low, high, original, amplitude,
+                (uint64_t)rows * (uint64_t)(rotary_dim / 2), axes, rotary_dim / 2};
+    const uint64_t blocks = (a.total + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffull)
+        return RANS_E_ARG;
+    rotary_table_kernel<<<(uint32_t)blocks, kThreads, 0, hstream>>>(a);
+    return launched();
+}
+
+extern "C" int lic_rotary(const lic_rotary_args *args, hipStream_t hstream)
+{
+    if (!args)
+        return RANS_E_ARG;
+    const lic_rotary_args &p = *args;
+    if (!valid_dtype(p.dtype) || !extent(p.batch, 0, 1ll << 31) || !extent(p.tokens, 0, 1ll << 31) ||
+        !extent(p.heads, 1, 65536) || !extent(p.kv_heads, 0, 65536) || !extent(p.dim, 2, 65536) ||
+        !extent(p.rotary_dim, 2, p.dim) || p.rotary_dim % 2 || !extent(p.table_rows, 0, 1ll << 40) ||
+        p.pos_batch < 0)
+        return RANS_E_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (p.q_stride[i] < 0 || p.k_stride[i] < 0 || p.q_out_stride[i] < 0 ||
+            p.k_out_stride[i] < 0)
+            return RANS_E_ARG;
+    if (p.batch == 0 || p.tokens == 0)
+        return RANS_OK;
+    if (!p.q || !p.q_out || (p.kv_heads && (!p.k || !p.k_out)) || !p.cos || !p.sin ||
+        (!p.positions && p.table_rows < p.tokens) ||
+        p.batch > (1ll << 40) / p.tokens)
+        return RANS_E_ARG;
+    RotaryArgs a{};
+    a.p = p;
+    return with_dtype(p.dtype, [&](auto t) {
+        using T = decltype(t);
+        constexpr int V = 16 / sizeof(T);
+        if (fits<T>(p, V))
+            return run_rotary<T, V>(a, hstream);
+        if (fits<T>(p, 4)) // 16-bit heads of 24, 40, 72: 8 bytes at once
+            return run_rotary<T, 4>(a, hstream);
+        return run_rotary<T, 1>(a, hstream);
+    });
+}
+
+extern "C" const char *lic_layers_target(void) { return "gfx950"; }

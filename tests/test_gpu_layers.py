@@ -1,0 +1,573 @@
+"""The network operators on the GPU against plain 64-bit forms (`layers_ref`, where the
+bounds are derived), at the sizes, masks, strides and values where they can go wrong."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import layers_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+ALL = (F32, F16, BF16)
+
+
+@pytest.fixture(scope="module")
+def L():
+    from learned_image_compression_amd import layers
+    layers.load()
+    return layers
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(g, *shape, dtype=F32):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def passes(got, want, bound, what):
+    w = R.worst(got, want, bound)
+    print(f"{what}: {w:.3f} of the bound", flush=True)
+    assert w <= 1.0, (what, w)
+
+
+# ---- group norm ----------------------------------------------------------------
+
+NORM = [
+    # N, C, spatial, groups, activation, parameters, dtype
+    (1, 192, (17, 30), 32, "silu", F32, F32),
+    (1, 192, (17, 30), 32, "silu", F32, BF16),
+    (2, 64, (33, 65), 8, "gelu", F16, F16),
+    (3, 30, (7, 5), 5, "relu", None, F32),        # vectors of two
+    (2, 31, (9, 11), 31, "silu", F32, BF16),      # one channel a group, odd
+    (2, 31, (9, 11), 1, "gelu", BF16, BF16),
+    (5, 320, (40, 41), 32, "silu", F32, F16),     # ten channels a group
+    (1, 8, (1, 1), 2, "none", F32, F32),          # four values a group
+    (1, 4, (1,), 4, "silu", F32, F32),            # one value a group
+    (4, 1300, (6,), 13, "silu", F32, BF16),       # tokens; a row wider than a block
+    (1, 4100, (3, 3), 4, "none", F32, F32),
+    (64, 16, (3, 3), 4, "silu", F32, BF16),       # many samples
+    (1, 16, (300, 301), 2, "gelu", F32, F32),     # many chunks
+    (2, 96, (4, 5, 6), 8, "silu", F32, F16),      # three axes
+]
+
+
+@pytest.mark.parametrize("n,c,space,groups,kind,params,dtype", NORM)
+def test_group_norm(L, n, c, space, groups, kind, params, dtype):
+    g = gen(c + n)
+    x = normal(g, n, *space, c).mul_(1.5).add_(normal(g, c)).to(dtype).movedim(-1, 1)
+    dy = normal(g, n, *space, c, dtype=dtype).movedim(-1, 1)
+    w = b = None
+    if params is not None:
+        w, b = (1 + 0.3 * normal(g, c)).to(params), (0.3 * normal(g, c)).to(params)
+    y, mean, rstd = L.group_norm_forward(x, groups, w, b, eps=1e-5, activation=kind)
+    assert y.dtype == dtype and y.shape == x.shape and y.stride() == x.stride()
+    # relu's slope jumps at 0: where u is within rounding of it, dy is set to 0
+    r = R.group_norm(x, groups, w, b, 1e-5, kind)
+    if kind == "relu":
+        dy.masked_fill_(r["u"].abs() < 1e-4, 0.0)
+    r = R.group_norm(x, groups, w, b, 1e-5, kind, dy)
+    u = R.UNIT[dtype]
+    passes(y, r["y"], u * r["y"].abs() + R.F32 * (1 + r["u"].abs()), "y")
+    passes(mean, r["mean"], R.F32 * (1 + r["mean"].abs()), "mean")
+    passes(rstd, r["rstd"], R.F32 * r["rstd"], "rstd")
+    dx, dw, db = L.group_norm_backward(dy, x, groups, w, b, mean, rstd, activation=kind)
+    assert dx.stride() == x.stride() and dw.dtype == (params or F32)
+    pu = R.UNIT[params or F32]
+    passes(dx, r["dx"], u * r["dx"].abs() + R.F32 * r["dx_abs"], "dx")
+    passes(dw, r["dw"], pu * r["dw"].abs() + R.F32 * (r["dw_abs"] + r["db_abs"]), "dw")
+    passes(db, r["db"], pu * r["db"].abs() + R.F32 * r["db_abs"], "db")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("where", ["rows", "samples", "odd address", "nchw view"])
+def test_group_norm_strides(L, dtype, where):
+    g = gen(7)
+    n, c, h, w = 2, 24, 9, 13
+    if where == "rows":          # channels cut out of a wider tensor
+        x = normal(g, n, h, w, c + 8, dtype=dtype)[..., 8:].movedim(-1, 1)
+    elif where == "samples":
+        x = normal(g, n + 2, h, w, c, dtype=dtype)[::2].movedim(-1, 1)
+    elif where == "odd address":
+        x = normal(g, n * h * w * c + 1, dtype=dtype)[1:].view(n, h, w, c).movedim(-1, 1)
+    else:                        # a padded image's inner columns: not evenly spaced
+        x = normal(g, n, h, w + 2, c, dtype=dtype)[:, :, 1:-1].movedim(-1, 1)
+        with pytest.raises(ValueError, match="evenly spaced"):
+            L.group_norm_forward(x, 4)
+        return
+    y, mean, rstd = L.group_norm_forward(x, 4, activation="silu")
+    r = R.group_norm(x, 4, None, None, 1e-5, "silu")
+    passes(y, r["y"], R.UNIT[dtype] * r["y"].abs() + R.F32 * (1 + r["u"].abs()), where)
+    out = torch.full((n, h, w, c + 8), 7.0, dtype=dtype, device="cuda")
+    L.group_norm_forward(x, 4, activation="silu", out=out[..., 4:4 + c].movedim(-1, 1))
+    assert torch.equal(out[..., 4:4 + c], y.movedim(1, -1))
+    assert bool((out[..., :4] == 7).all()) and bool((out[..., 4 + c:] == 7).all())
+
+
+def test_group_norm_large_mean(L):
+    """Mean 1000 deviations from 0, and a first value 1000 deviations from the others."""
+    g = gen(3)
+    x = normal(g, 2, 50, 60, 32).add_(1000.0)
+    x[0, 0, 0] = 2000.0
+    x = x.movedim(-1, 1)
+    y, _, _ = L.group_norm_forward(x, 4)
+    r = R.group_norm(x, 4, None, None, 1e-5, "none")
+    # the mean itself is held to 2^-24 of 1000, a few times over
+    passes(y, r["y"], R.F32 * (1 + r["y"].abs()) + 8 * 2.0 ** -24 * 1000, "y")
+
+
+def test_group_norm_infinities_stay_in_their_group(L):
+    g = gen(4)
+    x = normal(g, 2, 10, 10, 32)
+    x[0, 3, 3, 1] = math.inf
+    x[1, 3, 3, 31] = math.nan
+    x = x.movedim(-1, 1)
+    y, _, _ = L.group_norm_forward(x, 8, activation="silu")
+    bad = torch.zeros(2, 32, dtype=torch.bool, device="cuda")
+    bad[0, :4], bad[1, 28:] = True, True
+    assert bool(torch.isfinite(y.movedim(1, -1)[~bad[:, None, None, :].expand(2, 10, 10, 32)]).all())
+    assert not bool(torch.isfinite(y[bad.nonzero(as_tuple=True)]).any())
+
+
+def test_group_norm_empty(L):
+    x = torch.empty(0, 8, 4, 4, device="cuda").to(memory_format=torch.channels_last)
+    assert L.group_norm_forward(x, 2)[0].shape == x.shape
+    x = torch.empty(2, 0, 8, device="cuda").transpose(1, 2)
+    y, mean, rstd = L.group_norm_forward(x, 2)
+    dx, dw, db = L.group_norm_backward(x, x, 2, None, None, mean, rstd)
+    assert y.shape == dx.shape == x.shape and bool((dw == 0).all()) and bool((db == 0).all())
+
+
+def test_group_norm_autograd_and_differences(L):
+    """Against the formula through autograd's layouts, and against differences of the forward."""
+    g = gen(5)
+    x = normal(g, 2, 12, 7, 9).to(memory_format=torch.channels_last).requires_grad_()
+    w, b = (1 + 0.2 * normal(g, 12)).requires_grad_(), normal(g, 12).requires_grad_()
+    dy = normal(g, 2, 12, 7, 9)  # channels first
+    got = torch.autograd.grad(L.group_norm(x, 3, w, b, activation="gelu"), (x, w, b), dy)
+    r = R.group_norm(x.detach(), 3, w.detach(), b.detach(), 1e-5, "gelu", dy)
+    for a, k in zip(got, ("dx", "dw", "db")):
+        passes(a, r[k], R.F32 * (r[k].abs() + r[k + "_abs"].max()), k)
+    # central differences along a random direction: off by h^2 and by the outputs' 2^-24 / h
+    h = 2.0 ** -6
+    for i, t in enumerate((x, w, b)):
+        d = normal(g, *t.shape)
+        d = d.to(memory_format=torch.channels_last) if t.dim() == 4 else d
+        ends = []
+        for s in (h, -h):
+            args = [p.detach() for p in (x, w, b)]
+            args[i] = args[i] + s * d
+            ends.append((L.group_norm(args[0], 3, args[1], args[2], activation="gelu").double() * dy).sum())
+        want, have = float((ends[0] - ends[1]) / (2 * h)), float((got[i].double() * d).sum())
+        size = float((got[i].double() * d).abs().sum())
+        assert abs(want - have) <= 4 * h * h * size, (i, want, have)
+
+
+# ---- rotary -----------------------------------------------------------------------
+
+
+def tables(rows, pairs, g):
+    a = torch.rand(rows, pairs, generator=g, device="cuda", dtype=torch.float64) * 2 * math.pi
+    return a.cos().float(), a.sin().float()
+
+
+ROTARY = [
+    # B, S, heads, kv heads, dim, rotary dim
+    (1, 1, 1, 1, 2, 2),
+    (16, 1, 16, 4, 64, 64),
+    (2, 7, 3, 0, 32, 32),
+    (2, 33, 6, 2, 40, 20),
+    (1, 50, 5, 5, 72, 36),
+    (3, 9, 2, 1, 128, 64),
+    (2, 5, 3, 3, 11, 6),
+    (1, 257, 2, 2, 96, 96),
+]
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("b,s,h,kv,d,r", ROTARY)
+def test_rotary(L, b, s, h, kv, d, r, interleaved, dtype):
+    g = gen(d + s)
+    cos, sin = tables(s + 40, r // 2, g)
+    q = normal(g, b, s, h, d, dtype=dtype)
+    k = normal(g, b, s, kv, d, dtype=dtype) if kv else None
+    for positions in (None, torch.randint(0, s + 40, (s,), generator=g, device="cuda", dtype=torch.int32),
+                      torch.randint(0, s + 40, (b, s), generator=g, device="cuda", dtype=torch.int32)):
+        for inverse in (False, True):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            got = L.rotary(q, k, cos, sin, positions=positions, interleaved=interleaved, inverse=inverse,
+                           status=status)
+            for x, y in zip((q, k), got):
+                if x is None:
+                    assert y is None
+                    continue
+                want = R.turn(x, cos, sin, positions, interleaved, inverse)
+                passes(y, want, R.UNIT[dtype] * want.abs() + 4 * 2.0 ** -24 * x.double().abs().max(), "turned")
+                assert torch.equal(y[..., r:], x[..., r:])
+            assert int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", ALL)
+def test_rotary_strides_and_in_place(L, dtype):
+    g = gen(1)
+    cos, sin = tables(20, 16, g)
+    qkv = normal(g, 2, 20, 9, 48, dtype=dtype)
+    q, k = qkv[:, :, :6, :40], qkv[:, :, 6:, 1:41]        # k misaligned
+    want = R.turn(q, cos, sin, None, False), R.turn(k, cos, sin, None, False)
+    before = qkv.clone()
+    a, b = L.rotary(q, k, cos, sin)
+    for x, w in zip((a, b), want):
+        passes(x, w, R.UNIT[dtype] * w.abs() + 2e-6, "strided")
+    L.rotary(q, k, cos, sin, out=(q, k))
+    assert torch.equal(q, a) and torch.equal(k, b)
+    assert torch.equal(qkv[:, :, :6, 40:], before[:, :, :6, 40:]) and torch.equal(qkv[:, :, 6:, 0], before[:, :, 6:, 0])
+    heads_first = normal(g, 2, 6, 20, 32, dtype=dtype).transpose(1, 2)
+    x, _ = L.rotary(heads_first, None, cos, sin)
+    w = R.turn(heads_first, cos, sin, None, False)
+    passes(x, w, R.UNIT[dtype] * w.abs() + 2e-6, "heads first")
+
+
+def test_rotary_positions_outside_the_tables(L):
+    g = gen(2)
+    cos, sin = tables(10, 8, g)
+    q = normal(g, 1, 4, 2, 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, -1, 9, 10], dtype=torch.int32, device="cuda")
+    y, _ = L.rotary(q, None, cos, sin, positions=at, status=status)
+    assert int(status) == -3
+    assert bool(torch.isnan(y[:, [1, 3]]).all()) and bool(torch.isfinite(y[:, [0, 2]]).all())
+
+
+def test_rotary_autograd(L):
+    g = gen(6)
+    cos, sin = tables(12, 6, g)
+    q, k = normal(g, 2, 12, 4, 16).requires_grad_(), normal(g, 2, 12, 2, 16).requires_grad_()
+    dq, dk = normal(g, 2, 12, 16, 4).transpose(2, 3), normal(g, 2, 12, 2, 16)
+    a, b = L.rotary(q, k, cos, sin, interleaved=True)
+    got = torch.autograd.grad((a, b), (q, k), (dq, dk))
+    for x, d in zip(got, (dq, dk)):
+        w = R.turn(d, cos, sin, None, True, inverse=True)
+        passes(x, w, 2e-6 * (1 + w.abs()), "gradient")
+    # the rotation is linear, so differences give it exactly: <dq, R v> = <R^T dq, v>
+    v = normal(g, 2, 12, 4, 16)
+    turned, _ = L.rotary(v, None, cos, sin, interleaved=True)
+    left, right = (dq.double() * turned).sum(), (got[0].double() * v).sum()
+    assert abs(float(left - right)) <= 1e-5 * float((dq.double() * turned).abs().sum())
+
+
+@pytest.mark.parametrize("scaling,more", [
+    ("none", {}), ("linear", {"factor": 8.0}), ("base", {"factor": 4.0}),
+    ("ramp", {"factor": 16.0, "original": 4096}), ("ramp", {"factor": 2.0, "original": 512, "amplitude": 1.0}),
+])
+@pytest.mark.parametrize("axes", [1, 2])
+def test_rotary_table(L, scaling, more, axes):
+    rows = torch.tensor([0, 1, 2, 1000, 131071, 1048576], dtype=torch.float64, device="cuda")
+    coords = rows if axes == 1 else torch.stack((rows, rows.flip(0)), dim=1).contiguous()
+    cos, sin = L.rotary_table(coords, 64, base=10000.0, scaling=scaling, **more)
+    n = 32 // axes
+    f = 10000.0 ** (-torch.arange(n, dtype=torch.float64) / n)
+    gain, factor = more.get("amplitude", 1.0), more.get("factor", 1.0)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "base":
+        f = (10000.0 * factor ** (n / (n - 1))) ** (-torch.arange(n, dtype=torch.float64) / n)
+        assert abs(float(f[-1]) * factor / 10000.0 ** (-(n - 1) / n) - 1) < 1e-12
+    elif scaling == "ramp":
+        keep = ((more["original"] * f / (2 * math.pi) - 1) / 31).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+        gain = more.get("amplitude", 0.1 * math.log(factor) + 1)
+    c = coords.cpu().view(-1, axes)
+    angle = torch.cat([c[:, a:a + 1] * f for a in range(axes)], dim=1)
+    # a 64-bit angle of a million is off by 1e-10; then one rounding to 32 bits
+    for got, want in ((cos, angle.cos() * gain), (sin, angle.sin() * gain)):
+        assert float((got.cpu().double() - want).abs().max()) <= 2.0 ** -24 * 2 + 1e-9
+
+
+# ---- attention ----------------------------------------------------------------------
+
+CASES = [
+    # B, Q, S, H, K, D, options
+    (1, 1, 1, 1, 1, 8, {}),
+    (2, 1, 5000, 4, 1, 64, {}),                          # a single token, split keys
+    (3, 1, 700, 8, 2, 128, {"lengths": [700, 1, 0]}),
+    (2, 3, 333, 6, 6, 40, {"causal": True}),
+    (1, 17, 600, 40, 1, 32, {"causal": True}),           # 680 rows a kv head
+    (2, 130, 130, 2, 2, 32, {"causal": True}),
+    (40, 150, 150, 4, 2, 64, {"causal": True}),          # tiles
+    (33, 129, 65, 4, 4, 96, {}),
+    (30, 256, 190, 5, 5, 72, {"lengths": "ragged"}),
+    (32, 200, 200, 4, 4, 16, {"window": (13, 0)}),
+    (32, 200, 200, 4, 4, 24, {"window": (5, 9)}),
+    (32, 140, 260, 4, 2, 128, {"window": (None, 3)}),
+    (32, 300, 100, 4, 4, 64, {"causal": True}),          # more queries than keys: 200 see nothing
+    (32, 129, 129, 4, 4, 32, {"mask": "slices"}),        # the first slice sees nothing
+    (8, 100, 77, 2, 1, 64, {"mask": "slices"}),
+    (4, 70, 90, 2, 2, 32, {"mask": "full"}),
+    (32, 150, 133, 4, 2, 64, {"mask": "keys", "causal": True}),
+    (1, 600, 600, 2, 1, 128, {"causal": True}),          # few blocks: split sums
+    (2, 64, 64, 2, 2, 20, {"causal": True}),             # no 16-byte rows in 16 bits
+    (33, 130, 70, 4, 2, 7, {"lengths": "ragged"}),
+    (2, 5, 9, 1, 1, 1, {}),
+    (32, 129, 131, 4, 4, 100, {"scale": 0.3}),
+]
+
+
+def attention_case(b, q, s, h, kv, d, options, dtype, seed=0):
+    g = gen(seed + q + s)
+    options = dict(options)
+    t = [normal(g, b, q, h, d, dtype=dtype), normal(g, b, s, kv, d, dtype=dtype), normal(g, b, s, kv, d, dtype=dtype),
+         normal(g, b, q, h, d, dtype=dtype)]
+    lengths = options.pop("lengths", None)
+    if lengths is not None:
+        if lengths == "ragged":
+            lengths = [(s - 11 * i) % (s + 1) for i in range(b)]
+        options["key_lengths"] = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    mask = options.pop("mask", None)
+    if mask == "slices":
+        options["mask"] = torch.arange(s, device="cuda")[None, :] % 4 < torch.arange(q, device="cuda")[:, None] % 4
+    elif mask == "keys":
+        options["mask"] = torch.rand(b, 1, 1, s, generator=g, device="cuda") < 0.7
+    elif mask == "full":
+        options["mask"] = (torch.rand(b, h, q, s, generator=g, device="cuda") < 0.3).to(torch.uint8)
+    return t, options
+
+
+def attention_passes(L, t, options, dtype, what=""):
+    q, k, v, dout = t
+    out, lse = L.attention_forward(q, k, v, **options)
+    r = R.attention(q, k, v, dout, **options)
+    u, e = R.UNIT[dtype], R.F32 + r["slack"]
+    passes(out, r["out"], (2 * u + e) * r["out_abs"], what + "out")
+    passes(lse, r["lse"], R.F32 * (1 + torch.nan_to_num(r["lse"], neginf=0.0).abs()) + r["slack"], what + "lse")
+    assert bool((out[(lse == -math.inf).transpose(1, 2)] == 0).all())
+    grads = L.attention_backward(dout, q, k, v, out, lse, **options)
+    for x, name, n in zip(grads, ("dq", "dk", "dv"), (3, 3, 2)):
+        least = R.STEP[dtype] * (1 + r.get(name + "_ones", 0.0))
+        passes(x, r[name], (n * u + 2 * e) * r[name + "_abs"] + least, what + name)
+    return (out, lse, *grads), r
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention(L, case, dtype):
+    b, q, s, h, kv, d, options = CASES[case]
+    print(CASES[case], dtype, flush=True)
+    t, options = attention_case(b, q, s, h, kv, d, options, dtype)
+    attention_passes(L, t, options, dtype)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("layout", ["packed", "heads first", "odd address", "odd stride", "shared"])
+@pytest.mark.parametrize("b,n", [(1, 40), (32, 140)])
+def test_attention_strides(L, layout, b, n, dtype):
+    g = gen(9)
+    h, d = 4, 32
+    if layout == "packed":
+        q, k, v = normal(g, b, n, 3, h, d, dtype=dtype).unbind(2)
+    elif layout == "heads first":
+        q, k, v = (normal(g, b, h, n, d, dtype=dtype).transpose(1, 2) for _ in range(3))
+    elif layout == "odd address":
+        q, k, v = (normal(g, b * n * h * d + 1, dtype=dtype)[1:].view(b, n, h, d) for _ in range(3))
+    elif layout == "odd stride":
+        q, k, v = (normal(g, b, n, h, d + 1, dtype=dtype)[..., :d] for _ in range(3))
+    else:  # one set of keys for the whole batch
+        q = normal(g, b, n, h, d, dtype=dtype)
+        k, v = (normal(g, 1, n, h, d, dtype=dtype).expand(b, n, h, d) for _ in range(2))
+    dout = normal(g, b, h, n, d, dtype=dtype).transpose(1, 2)
+    attention_passes(L, (q, k, v, dout), {"causal": True}, dtype)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("b,n,s", [(2, 1, 300), (2, 30, 300), (32, 140, 200)])
+def test_attention_keeps_masked_values_out(L, b, n, s, dtype):
+    """NaN and infinities in places that some queries, or none, see."""
+    t, options = attention_case(b, n, s, 4, 2, 64, {"mask": "slices"}, dtype)
+    q, k, v, dout = t
+    mask = options["mask"].clone()
+    mask[:, 40:60] = False       # nobody sees these
+    mask[:, 8] = False
+    mask[n // 2, 8] = True       # one query sees this one
+    options["mask"] = mask
+    k[:, 41], v[:, 42] = math.nan, math.inf
+    k[:, 45, :, 3] = -math.inf
+    v[:, 8] = math.nan
+    clean = [x.clone() for x in t]
+    for x in clean[1:3]:
+        x[~torch.isfinite(x)] = 0.0
+    r = R.attention(*clean, **options)
+    out, lse = L.attention_forward(q, k, v, **options)
+    u, e = R.UNIT[dtype], R.F32 + r["slack"]
+    hit = torch.zeros(n, dtype=torch.bool, device="cuda")
+    hit[n // 2] = True
+    assert bool(torch.isnan(out[:, hit]).all())
+    passes(out[:, ~hit], r["out"][:, ~hit], (2 * u + e) * r["out_abs"][:, ~hit], "out")
+    passes(lse, r["lse"], R.F32 * (1 + torch.nan_to_num(r["lse"], neginf=0.0).abs()) + r["slack"], "lse")
+    # gradients: only what the query that saw a NaN takes part in is lost
+    dq, dk, dv = L.attention_backward(dout, q, k, v, out, lse, **options)
+    passes(dq[:, ~hit], r["dq"][:, ~hit], (3 * u + 2 * e) * r["dq_abs"][:, ~hit], "dq")
+    untouched = ~mask[n // 2]
+    for x, name, f in ((dk, "dk", 3), (dv, "dv", 2)):
+        passes(x[:, untouched], r[name][:, untouched], (f * u + 2 * e) * r[name + "_abs"][:, untouched], name)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("b,n", [(2, 20), (32, 140)])
+def test_attention_nan_queries_stay_in_their_rows(L, b, n, dtype):
+    t, options = attention_case(b, n, n, 4, 2, 32, {"causal": True}, dtype)
+    q, k, v, dout = t
+    bad = n // 3
+    q[:, bad] = math.nan
+    clean = [x.clone() for x in t]
+    clean[0][:, bad] = 0.0
+    r = R.attention(*clean, **options)
+    out, lse = L.attention_forward(q, k, v, **options)
+    keep = torch.arange(n, device="cuda") != bad
+    assert bool(torch.isnan(out[:, bad]).all())
+    u, e = R.UNIT[dtype], R.F32 + r["slack"]
+    passes(out[:, keep], r["out"][:, keep], (2 * u + e) * r["out_abs"][:, keep], "out")
+    dq, dk, dv = L.attention_backward(dout, q, k, v, out, lse, **options)
+    passes(dq[:, keep], r["dq"][:, keep], (3 * u + 2 * e) * r["dq_abs"][:, keep], "dq")
+    # keys after the bad query are not seen by it
+    passes(dk[:, bad + 1:], r["dk"][:, bad + 1:], (3 * u + 2 * e) * r["dk_abs"][:, bad + 1:], "dk")
+    passes(dv[:, bad + 1:], r["dv"][:, bad + 1:], (2 * u + 2 * e) * r["dv_abs"][:, bad + 1:], "dv")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("b,n", [(1, 1), (2, 40), (32, 140)])
+def test_attention_large_scores(L, b, n, dtype):
+    """Scores that rise by hundreds along the keys: the running maximum is raised again and again."""
+    t, options = attention_case(b, n, 400, 4, 4, 32, {}, dtype)
+    q, k, v, dout = t
+    q.fill_(1.0)
+    k.copy_((torch.arange(400, device="cuda") / 4)[None, :, None, None].to(dtype).expand_as(k))
+    attention_passes(L, (q, k, v, dout), {"scale": 0.25}, dtype)
+
+
+def test_attention_long_cache_offsets(L):
+    """Keys whose offsets pass 2^31 elements (and 2^32 bytes)."""
+    g = gen(11)
+    s, step = 9000, 300000
+    store = torch.empty(s * step, dtype=BF16, device="cuda")
+    rows = store.view(1, s, 1, step)
+    k, v = rows[..., :64], rows[..., 64:128]
+    k.copy_(normal(g, 1, s, 1, 64, dtype=BF16))
+    v.copy_(normal(g, 1, s, 1, 64, dtype=BF16))
+    for n in (1, 200):
+        q, dout = normal(g, 1, n, 2, 64, dtype=BF16), normal(g, 1, n, 2, 64, dtype=BF16)
+        attention_passes(L, (q, k, v, dout), {"causal": True}, BF16)
+
+
+def test_attention_autograd_and_differences(L):
+    g = gen(12)
+    q, k, v = (normal(g, 2, 30, h, 16).requires_grad_() for h in (4, 2, 2))
+    dout = normal(g, 2, 30, 16, 4).transpose(2, 3)
+    mask = torch.rand(30, 30, generator=g, device="cuda") < 0.6
+    got = torch.autograd.grad(L.attention(q, k, v, mask=mask), (q, k, v), dout)
+    r = R.attention(q.detach(), k.detach(), v.detach(), dout, mask=mask)
+    for x, name in zip(got, ("dq", "dk", "dv")):
+        passes(x, r[name], 3 * R.F32 * r[name + "_abs"], name)
+    h = 2.0 ** -7
+    for i in range(3):
+        d = normal(g, *(q, k, v)[i].shape)
+        ends = []
+        for s in (h, -h):
+            args = [p.detach() for p in (q, k, v)]
+            args[i] = args[i] + s * d
+            ends.append((L.attention(*args, mask=mask).double() * dout).sum())
+        want, have = float((ends[0] - ends[1]) / (2 * h)), float((got[i].double() * d).sum())
+        size = float((got[i].double() * d).abs().sum())
+        assert abs(want - have) <= 16 * h * h * size, (i, want, have)
+
+
+def test_results_do_not_depend_on_timing(L):
+    """The same bits again, with the GPU busy, on another stream and from a graph's replays."""
+    t, options = attention_case(2, 1, 3000, 8, 2, 64, {"lengths": [3000, 1777]}, BF16)
+    big, _ = attention_case(1, 500, 500, 4, 2, 64, {}, BF16)
+    x = normal(gen(1), 2, 40, 50, 64, dtype=BF16).movedim(-1, 1)
+
+    def call():
+        a = L.attention_forward(*t[:3], **options)
+        b = L.attention_forward(*big[:3], causal=True)
+        y = L.group_norm_forward(x, 8, activation="silu")
+        return (*a, *b, *L.attention_backward(big[3], *big[:3], *b, causal=True), *y,
+                *L.group_norm_backward(x, x, 8, None, None, y[1], y[2], activation="silu"))
+
+    first = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = call()
+    third = call()
+    torch.cuda.synchronize()
+    for a, b, c in zip(first, second, third):
+        assert torch.equal(a, b) and torch.equal(a, c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call()
+    for _ in range(3):
+        for h in held:
+            h.zero_()
+        graph.replay()
+        again = call()
+        torch.cuda.synchronize()
+        for a, b, c in zip(first, held, again):
+            assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_refusals(L):
+    q = torch.zeros(2, 4, 4, 16, device="cuda")
+    k = torch.zeros(2, 6, 2, 16, device="cuda")
+    ok = L.attention_forward(q, k, k)
+    for bad, kw in (((q, k.half(), k), {}), ((q.cpu(), k, k), {}), ((q, k, k.transpose(1, 2)), {}),
+                    ((q[..., :8], k, k), {}), ((q[:, :, :3], k, k), {}), ((q.double(), k, k), {}),
+                    ((q.transpose(2, 3), k, k), {}), ((q, k, k), {"scale": 0.0}), ((q, k, k), {"scale": math.nan}),
+                    ((q, k, k), {"window": (-2, 0)}), ((q, k, k), {"mask": torch.ones(5, 6, device="cuda") > 0}),
+                    ((q, k, k), {"mask": torch.ones(4, 6, device="cuda")}),
+                    ((q, k, k), {"key_lengths": torch.ones(2, device="cuda")}),
+                    ((q, k, k), {"key_lengths": torch.ones(3, dtype=torch.int32, device="cuda")}),
+                    ((torch.zeros(1, 1, 1, 129, device="cuda"),) + (torch.zeros(1, 1, 1, 129, device="cuda"),) * 2, {})):
+        with pytest.raises((TypeError, ValueError)):
+            L.attention_forward(*bad, **kw)
+    with pytest.raises(ValueError):
+        L.attention_backward(q[:1], q, k, k, *ok)
+    x = torch.zeros(2, 8, 4, 4, device="cuda").to(memory_format=torch.channels_last)
+    for bad, kw in (((x.contiguous(), 2), {}), ((x, 3), {}), ((x, 0), {}), ((x, 2, torch.ones(7, device="cuda")), {}),
+                    ((x, 2), {"activation": "tanh"}), ((x.double(), 2), {}), ((x.cpu(), 2), {}),
+                    ((x, 2, torch.ones(8, device="cuda"), torch.ones(8, device="cuda").half()), {})):
+        with pytest.raises((TypeError, ValueError)):
+            L.group_norm_forward(*bad, **kw)
+    c = torch.zeros(4, 8, device="cuda")
+    for bad, kw in (((q, None, c[:3], c[:3]), {}), ((q, None, c.half(), c), {}), ((q, None, c, c[:, :4]), {}),
+                    ((q, k, c, c), {}), ((q[..., :8], None, c, c), {}),
+                    ((q, None, c, c), {"positions": torch.zeros(4, dtype=torch.int64, device="cuda")}),
+                    ((q, None, c, c), {"positions": torch.zeros(5, dtype=torch.int32, device="cuda")})):
+        with pytest.raises((TypeError, ValueError)):
+            L.rotary(*bad, **kw)
+    for kw in ({"rotary_dim": 7}, {"rotary_dim": 6, "scaling": "twist"}, {"rotary_dim": 6, "scaling": "ramp"},
+               {"rotary_dim": 6, "factor": 0.0}):
+        with pytest.raises(ValueError):
+            L.rotary_table(torch.zeros(4, dtype=torch.float64, device="cuda"), **kw)
+
+
+def test_empty_calls(L):
+    q = torch.zeros(2, 3, 4, 16, device="cuda")
+    k = torch.zeros(2, 0, 2, 16, device="cuda")
+    out, lse = L.attention_forward(q, k, k)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    dq, dk, dv = L.attention_backward(q, q, k, k, out, lse)
+    assert bool((dq == 0).all()) and dk.shape == k.shape
+    k = torch.ones(2, 5, 2, 16, device="cuda")
+    out, lse = L.attention_forward(q[:, :0], k, k)
+    dq, dk, dv = L.attention_backward(q[:, :0], q[:, :0], k, k, out, lse)
+    assert out.shape == (2, 0, 4, 16) and bool((dk == 0).all()) and bool((dv == 0).all())
+    out, lse = L.attention_forward(q[:0], k[:0], k[:0])
+    assert out.shape == (0, 3, 4, 16)
+    c = torch.zeros(0, 8, device="cuda")
+    assert L.rotary(q[:, :0], None, c, c)[0].shape == (2, 0, 4, 16)
