@@ -34,7 +34,7 @@ bool valid_call(const lic_attention_args &p, bool backward)
 
 uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-uint64_t delta_bytes(const lic_attention_args &p) { return round256((uint64_t)p.batch * p.heads * p.queries * 4); }
+uint64_t row_bytes(const lic_attention_args &p) { return round256((uint64_t)p.batch * p.heads * p.queries * sizeof(float2)); }
 
 // Parts of split sums are as wide as the widest tile the call may take.
 uint64_t part_bytes(const lic_attention_args &p, bool backward)
@@ -57,7 +57,7 @@ uint64_t workspace(const lic_attention_args &p, bool backward)
 {
     if (p.batch == 0 || (p.queries == 0 && !backward))
         return 0;
-    return (backward ? delta_bytes(p) : 0) + round256(part_bytes(p, backward));
+    return (backward ? row_bytes(p) : 0) + round256(part_bytes(p, backward));
 }
 
 int call(const lic_attention_args *args, void *ws, uint64_t ws_bytes, hipStream_t s, bool backward)
@@ -77,8 +77,8 @@ int call(const lic_attention_args *args, void *ws, uint64_t ws_bytes, hipStream_
     a.group = (int)(args->heads / args->kv_heads);
     a.splits = 1;
     if (backward) {
-        a.delta = static_cast<float *>(ws);
-        a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + delta_bytes(*args));
+        a.rows = static_cast<float2 *>(ws);
+        a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + row_bytes(*args));
     } else {
         a.part = static_cast<float *>(ws);
     }

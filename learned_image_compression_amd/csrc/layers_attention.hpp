@@ -36,7 +36,7 @@ struct AttnArgs {
     lic_attention_args p;
     float scale_log2;   // scale * log2 e: exponentials are base 2
     float *part;        // split rows: unnormalised sums [split][row][tile dim], then m, l
-    float *delta;       // backward: dout . out of each row [batch][heads][queries]
+    float2 *rows;       // backward: lse in powers of two, dout . out [batch][heads][queries]
     int splits;
     int group;          // heads that share a kv head
     uint32_t blocks;    // of the launch's real work
@@ -78,6 +78,22 @@ __device__ __forceinline__ float16v mma(FragV<float> a, FragV<float> b, float16v
     for (int i = 0; i < 8; ++i)
         c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
     return c;
+}
+
+// Waits until the products issued so far are in their registers (at most 18 issue slots
+// for 32-bit products, 11 for 16-bit ones).  The hardware leaves that wait to the program and the
+// compiler puts it in, but where a branch stands between a product and the first arithmetic on its
+// result it may count along the longer path only (seen with hipcc 7.2: 4 slots of 18 on the path
+// around an if).  So results are settled before such a branch; arithmetic would wait anyhow.
+template <typename T>
+__device__ __forceinline__ void settle()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (sizeof(T) == 4)
+        asm volatile("s_nop 15\n\ts_nop 2");
+    else
+        asm volatile("s_nop 11");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // row of an accumulator that a lane's value i is
@@ -188,6 +204,44 @@ struct Tile {
         }
         return f;
     }
+};
+
+// N products whose LDS operands are read a batch of B ahead of the products that take
+// them.  Left to itself the compiler reads, waits and multiplies one fragment after another,
+// which costs an LDS latency a product; the scheduling barriers hold only memory and matrix
+// instructions in their batches.  start() may stand well before run().
+template <typename T, int N, int B>
+struct Pipe {
+    static constexpr int kAhead = B < N ? B : N;
+    static_assert(N % kAhead == 0, "whole batches");
+    FragV<T> f[2][kAhead];
+
+    template <typename Read>
+    __device__ __forceinline__ void start(Read &&read)
+    {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            f[0][i] = read(i);
+        __builtin_amdgcn_sched_barrier(kLet);
+    }
+    template <typename Read, typename Use>
+    __device__ __forceinline__ void run(Read &&read, Use &&use)
+    {
+#pragma unroll
+        for (int b = 0; b < N / kAhead; ++b) {
+            if ((b + 1) * kAhead < N) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    f[(b + 1) & 1][i] = read((b + 1) * kAhead + i);
+                __builtin_amdgcn_sched_barrier(kLet);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                use(b * kAhead + i, f[b & 1][i]);
+            __builtin_amdgcn_sched_barrier(kLet);
+        }
+    }
+    static constexpr int kLet = 0x6; // vector and scalar arithmetic may pass
 };
 
 // ROWS rows on their way from memory to a tile, through the registers of THREADS threads.
@@ -342,6 +396,32 @@ __device__ __forceinline__ const uint8_t *mask_row(const AttnArgs &a, int b, int
 {
     return a.p.mask + b * a.p.mask_stride[0] + head * a.p.mask_stride[1] +
            (int64_t)query * a.p.mask_stride[2];
+}
+
+// Which of an accumulator's 16 pairs are visible, a bit each.  x0 + its row is what range
+// limits; mask: the entry of 0 there, `step` to the next.  All bytes are asked for before the
+// first is looked at; a pair outside the range reads one inside instead.
+__device__ __forceinline__ uint32_t visible(const Range &range, const uint8_t *mask, int64_t step, int x0, int h)
+{
+    uint32_t bits = 0;
+    if (mask) {
+        uint8_t byte[16];
+        if (range.count) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int x = x0 + acc_row(i, h);
+                byte[i] = mask[(range.holds(x) ? x : range.first) * step];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                bits |= (uint32_t)(range.holds(x0 + acc_row(i, h)) && byte[i] != 0) << i;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            bits |= (uint32_t)range.holds(x0 + acc_row(i, h)) << i;
+    }
+    return bits;
 }
 
 template <typename T>

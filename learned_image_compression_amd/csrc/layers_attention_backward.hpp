@@ -21,9 +21,15 @@
 namespace lic {
 namespace {
 
-// D of each row: 16 lanes a row.
+// lse in powers of two; a row that sees nothing gets p = 0 everywhere
+__device__ __forceinline__ float lse_log2(float lse)
+{
+    return lse == -INFINITY ? INFINITY : lse * kLog2e;
+}
+
+// What the backward kernels need of each row, lse in powers of two and D: 16 lanes a row.
 template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void attention_delta(AttnArgs a)
+__global__ __launch_bounds__(256) void attention_row_stats(AttnArgs a)
 {
     const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
     const int64_t line = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -53,32 +59,10 @@ __global__ __launch_bounds__(256) void attention_delta(AttnArgs a)
     for (int x = 8; x > 0; x >>= 1)
         sum += __shfl_xor(sum, x);
     if (line < lines && lane == 0)
-        a.delta[line] = sum;
+        a.rows[line] = make_float2(lse_log2(a.p.lse[line]), sum);
 }
 
 constexpr float kLift = 10.0f, kLower = 1.0f / 1024.0f; // 2^10 and its inverse
-
-// lse in powers of two; a row that sees nothing gets p = 0 everywhere
-__device__ __forceinline__ float lse_log2(float lse)
-{
-    return lse == -INFINITY ? INFINITY : lse * kLog2e;
-}
-
-// Which of an accumulator's pairs are visible, a bit each.  `other` runs along its rows;
-// mask: the lane's own entry, `step` to the next of the others.
-__device__ __forceinline__ uint32_t visible(const Range &range, const uint8_t *mask, int64_t step, int other0, int h)
-{
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int x = other0 + acc_row(i, h);
-        bool seen = range.holds(x);
-        if (mask && seen)
-            seen = mask[x * step] != 0;
-        bits |= (uint32_t)seen << i;
-    }
-    return bits;
-}
 
 // One query's gradient with the keys it sees alone (see careful_row of the forward call).
 template <typename T>
@@ -90,7 +74,7 @@ __device__ void careful_dq(const AttnArgs &a, int b, int head, int query, int le
     const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
     const uint8_t *mask = a.p.mask ? mask_row(a, b, head, query) : nullptr;
     const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
-    const float lse = lse_log2(a.p.lse[line]), delta = a.delta[line];
+    const float lse = a.rows[line].x, delta = a.rows[line].y;
     dq[0] = dq[1] = 0.0f;
     for (int k0 = lo; k0 < hi; k0 += 64) {
         const int key = k0 + lane;
@@ -141,8 +125,9 @@ __device__ void careful_dkv(const AttnArgs &a, int b, int head, int key, int len
                 s = fmaf(up(q[d]), up(k[d]), s);
                 dp = fmaf(up(g[d]), up(v[d]), dp);
             }
-            p = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -lse_log2(a.p.lse[line0 + query])));
-            ds = p * (dp - a.delta[line0 + query]);
+            const float2 row = a.rows[line0 + query];
+            p = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -row.x));
+            ds = p * (dp - row.y);
         }
         for (uint64_t left = __builtin_amdgcn_ballot_w64(seen); left; left &= left - 1) {
             const int j = __builtin_ctzll(left);
@@ -168,7 +153,7 @@ __device__ void careful_dkv(const AttnArgs &a, int b, int head, int key, int len
 // Scores have queries along the accumulator's rows and keys across the lanes.
 template <typename T, int DT>
 struct KeysBackward {
-    static constexpr int kQueries = sizeof(T) == 4 || DT == 128 ? 32 : 64;
+    static constexpr int kQueries = sizeof(T) == 4 ? 32 : 64;
     using TileT = Tile<T, kQueries, DT>;
     static constexpr int kStats = 4 * TileT::kBytes;         // two buffers of lse, D
     static constexpr int kLds = kStats + 2 * 2 * kQueries * 4;
@@ -222,26 +207,24 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
     const int first = min(all, split * share), end = min(all, first + share);
 
     Stage<T, NQ, DT, 256, VEC> qst, gst;
-    float stat = 0.0f; // the first NQ threads: lse, the next: D
+    float2 stat = make_float2(INFINITY, 0.0f); // of the first NQ threads' rows
     const auto fetch = [&](int i) {
         const int head = kv * a.group + i / tiles, q0 = lo + (i % tiles) * NQ;
         const int rows = (int)a.p.queries - q0;
         qst.fetch(head_row<T>(a.p.q, a.p.q_stride, b, q0, head), a.p.q_stride[1], rows, dim, t);
         gst.fetch(head_row<T>(a.p.dout, a.p.dout_stride, b, q0, head), a.p.dout_stride[1], rows, dim, t);
-        if (t < 2 * NQ) {
-            const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + q0;
-            const int r = t % NQ;
-            if (t < NQ)
-                stat = r < rows ? lse_log2(a.p.lse[line + r]) - kLift : INFINITY;
-            else
-                stat = r < rows ? a.delta[line + r] * kLower : 0.0f;
-        }
+        stat = make_float2(INFINITY, 0.0f);
+        if (t < min(NQ, rows))
+            stat = a.rows[((int64_t)b * a.p.heads + head) * a.p.queries + q0 + t];
     };
     const auto store = [&](int buf) {
         qst.store(lds + buf * TileT::kBytes, t);
         gst.store(lds + (2 + buf) * TileT::kBytes, t);
-        if (t < 2 * NQ)
-            reinterpret_cast<float *>(lds + G::kStats)[buf * 2 * NQ + t] = stat;
+        if (t < NQ) {
+            float *s = reinterpret_cast<float *>(lds + G::kStats) + buf * 2 * NQ;
+            s[t] = stat.x - kLift;
+            s[NQ + t] = stat.y * kLower;
+        }
     };
     if (first < end) {
         fetch(first);
@@ -262,12 +245,26 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
             const float *lse = reinterpret_cast<const float *>(lds + G::kStats) + buf * 2 * NQ + n32;
             const float *delta = lse + NQ;
             float16v s = zero16(), dp = zero16();
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                s = mma(TileT::row_frag(ql, n32 + (lane & 31), kk, h), kf[kk], s);
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                dp = mma(TileT::row_frag(gl, n32 + (lane & 31), kk, h), vf[kk], dp);
+            {
+                Pipe<T, 2 * KK, 4> pipe;
+                const auto read = [&](int i) {
+                    return TileT::row_frag(i < KK ? ql : gl, n32 + (lane & 31), i % KK, h);
+                };
+                pipe.start(read);
+                pipe.run(read, [&](int i, const FragV<T> &f) {
+                    if (i < KK)
+                        s = mma(f, kf[i % KK], s);
+                    else
+                        dp = mma(f, vf[i % KK], dp);
+                });
+            }
+            settle<T>();
+            // operands of the second products: (half, dout then q, block of columns)
+            const auto read = [&](int i) {
+                return TileT::col_frag(i / ND % 2 ? ql : gl, n32 + i / (2 * ND) * 16, i % ND, lane);
+            };
+            Pipe<T, 4 * ND, 4> pipe;
+            pipe.start(read);
             uint32_t seen = 0xffffu;
             // rows beyond the queries have p = 0 by their lse; lanes beyond the keys are not stored
             const bool part = a.p.mask || !__all(key >= len || range.covers(qn, min(32, (int)a.p.queries - qn)));
@@ -295,20 +292,21 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
                     dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
                 }
             }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const FragV<T> p = operand<T>(s, half), ds = operand<T>(dp, half);
-#pragma unroll
-                for (int n = 0; n < ND; ++n) {
-                    dv[n] = mma(TileT::col_frag(gl, n32 + half * 16, n, lane), p, dv[n]);
-                    dk[n] = mma(TileT::col_frag(ql, n32 + half * 16, n, lane), ds, dk[n]);
-                }
-            }
+            const FragV<T> p[2] = {operand<T>(s, 0), operand<T>(s, 1)};
+            const FragV<T> ds[2] = {operand<T>(dp, 0), operand<T>(dp, 1)};
+            pipe.run(read, [&](int i, const FragV<T> &f) {
+                const int half = i / (2 * ND), n = i % ND;
+                if (i / ND % 2)
+                    dk[n] = mma(f, ds[half], dk[n]);
+                else
+                    dv[n] = mma(f, p[half], dv[n]);
+            });
         }
         if (i + 1 < end)
             store(buf ^ 1);
     }
 
+    settle<T>();
     bool bad = false;
 #pragma unroll
     for (int n = 0; n < ND; ++n)
@@ -398,8 +396,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
     const Range range = keys_of(a, len, query);
     const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
     const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
-    const float lse = there ? lse_log2(a.p.lse[line]) : INFINITY;
-    const float delta = there ? a.delta[line] : 0.0f;
+    const float2 row = there ? a.rows[line] : make_float2(INFINITY, 0.0f);
+    const float lse = row.x, delta = row.y;
 
     FragV<T> qf[KK], gf[KK];
     {
@@ -451,12 +449,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
             if (__all(range.misses(kn, 32)))
                 continue;
             float16v s = zero16(), dp = zero16();
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                s = mma(TileT::row_frag(kl, n * 32 + (lane & 31), kk, h), qf[kk], s);
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk)
-                dp = mma(TileT::row_frag(vl, n * 32 + (lane & 31), kk, h), gf[kk], dp);
+            {
+                Pipe<T, 2 * KK, 4> pipe;
+                const auto read = [&](int i) {
+                    return TileT::row_frag(i < KK ? kl : vl, n * 32 + (lane & 31), i % KK, h);
+                };
+                pipe.start(read);
+                pipe.run(read, [&](int i, const FragV<T> &f) {
+                    if (i < KK)
+                        s = mma(f, qf[i % KK], s);
+                    else
+                        dp = mma(f, gf[i % KK], dp);
+                });
+            }
+            settle<T>();
+            const auto read = [&](int i) {
+                return TileT::col_frag(kl, n * 32 + i / ND * 16, i % ND, lane);
+            };
+            Pipe<T, 2 * ND, ND == 3 ? 3 : 4> pipe;
+            pipe.start(read);
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * (dp[r] - delta);
@@ -466,13 +477,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
                 for (int r = 0; r < 16; ++r)
                     dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
             }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const FragV<T> ds = operand<T>(dp, half);
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-                    dq[d] = mma(TileT::col_frag(kl, n * 32 + half * 16, d, lane), ds, dq[d]);
-            }
+            const FragV<T> ds[2] = {operand<T>(dp, 0), operand<T>(dp, 1)};
+            pipe.run(read, [&](int i, const FragV<T> &f) { dq[i % ND] = mma(f, ds[i / ND], dq[i % ND]); });
         }
         if (next < hi) {
             kst.store(lds + (buf ^ 1) * TileT::kBytes, t);
@@ -480,6 +486,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
         }
     }
 
+    settle<T>();
     bool bad = false;
 #pragma unroll
     for (int n = 0; n < ND; ++n)
@@ -562,7 +569,7 @@ int run_backward(AttnArgs a, hipStream_t s)
     float *parts = a.part;
     if (p.queries > 0) {
         const int64_t lines = p.batch * p.heads * p.queries;
-        attention_delta<T, VEC><<<(uint32_t)((lines + 15) / 16), 256, 0, s>>>(a);
+        attention_row_stats<T, VEC><<<(uint32_t)((lines + 15) / 16), 256, 0, s>>>(a);
     }
     if (p.keys > 0) {
         using G = KeysBackward<T, DT>;

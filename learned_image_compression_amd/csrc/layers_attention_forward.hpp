@@ -18,14 +18,10 @@ constexpr float kSlack = 8.0f; // in powers of two
 __device__ __forceinline__ void hide(float16v &s, const AttnArgs &a, const Range &range, const uint8_t *mask,
                                      int key0, int h)
 {
+    const uint32_t seen = visible(range, mask, a.p.mask_stride[3], key0, h);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int key = key0 + acc_row(i, h);
-        bool seen = range.holds(key);
-        if (mask && seen)
-            seen = mask[key * a.p.mask_stride[3]] != 0;
-        s[i] = seen ? s[i] : -INFINITY;
-    }
+    for (int i = 0; i < 16; ++i)
+        s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
 }
 
 // The running softmax of a lane's query over N accumulators of scores, which become
@@ -189,29 +185,28 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         }
         if (!__all(range.misses(k0, G::kKeys))) {
             const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
-            float16v s[2];
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                s[n] = zero16();
-#pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
-                    s[n] = mma(TileT::row_frag(kl, n * 32 + (lane & 31), kk, h), qf[kk], s[n]);
+            float16v s[2] = {zero16(), zero16()};
+            {
+                Pipe<T, 2 * KK, 4> pipe;
+                const auto read = [&](int i) {
+                    return TileT::row_frag(kl, i / KK * 32 + (lane & 31), i % KK, h);
+                };
+                pipe.start(read);
+                pipe.run(read, [&](int i, const FragV<T> &f) { s[i / KK] = mma(f, qf[i % KK], s[i / KK]); });
             }
+            settle<T>();
+            const auto read = [&](int i) { return TileT::col_frag(vl, i / ND * 16, i % ND, lane); };
+            Pipe<T, 4 * ND, 4> pipe;
+            pipe.start(read);
             if (mask || !__all(query >= a.p.queries || range.covers(k0, G::kKeys))) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
                     hide(s[n], a, range, mask, k0 + n * 32, h);
             }
             soften(s, a.scale_log2, m, l, o);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const FragV<T> p = operand<T>(s[n], half);
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-                        o[d] = mma(TileT::col_frag(vl, n * 32 + half * 16, d, lane), p, o[d]);
-                }
+            const FragV<T> p[4] = {operand<T>(s[0], 0), operand<T>(s[0], 1), operand<T>(s[1], 0),
+                                   operand<T>(s[1], 1)};
+            pipe.run(read, [&](int i, const FragV<T> &f) { o[i % ND] = mma(f, p[i / ND], o[i % ND]); });
         }
         if (next < hi) {
             kst.store(lds + (buf ^ 1) * TileT::kBytes, t);
@@ -219,6 +214,7 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         }
     }
 
+    settle<T>();
     const float total = pair_sum(l);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     bool bad = false;
@@ -345,6 +341,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk)
             s[0] = mma(TileT::row_frag(kl, lane & 31, kk, h), qf[kk], s[0]);
+        settle<T>();
         // the tile may pass the split's end: those keys are the next split's
         const bool whole = k0 + 32 <= end;
         if (mask || !whole || !__all(row >= rows || range.covers((int)k0, 32))) {
@@ -367,6 +364,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
     }
 
     // a wave's part: sums [32][DT], then m and l
+    settle<T>();
     l = pair_sum(l);
     bool bad = false;
     float *sums = reinterpret_cast<float *>(lds + wave * kRegion);
