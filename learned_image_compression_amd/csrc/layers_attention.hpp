@@ -24,6 +24,9 @@
 
 #include "layers_common.hpp"
 
+// m0 is named in a clobber list although the compiler reserves it
+#pragma clang diagnostic ignored "-Winline-asm"
+
 namespace lic {
 
 using float16v = float __attribute__((ext_vector_type(16)));
@@ -244,10 +247,104 @@ struct Pipe {
     static constexpr int kLet = 0x6; // vector and scalar arithmetic may pass
 };
 
-// ROWS rows on their way from memory to a tile, through the registers of THREADS threads.
-// VEC: heads, strides and addresses allow 16-byte loads.
+// All loads of the wave so far are done.  Said with the builtin, so the compiler knows: it would
+// wait in each turn of a loop for what was loaded before it.
+__device__ __forceinline__ void loads_done()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70); // vmcnt 0
+    asm volatile("" ::: "memory");
+}
+
+// ROWS rows on their way from memory to a tile, by THREADS threads.
+//
+// With VEC (sizes, strides and addresses allow 16-byte loads) the memory system writes them to
+// LDS by itself: no register is held while they are under way, and store() only waits.  A
+// wave's 64 pieces land next to each other, so the permutation is in which piece a lane
+// asks for.  The load is written out: for the builtin the compiler waits at the next transposed
+// read, which cannot be of the same buffer.  store() waits instead, before the barrier.  Rows past the last repeat it (their scores are hidden); pieces past the head's
+// size are never written, and clear() made them 0.
+// Without VEC values pass through registers one by one, rows and columns past the end as 0.
 template <typename T, int ROWS, int DT, int THREADS, bool VEC>
 struct Stage {
+    using TileT = Tile<T, ROWS, DT>;
+    static constexpr int kEach = ROWS * DT / TileT::kPiece / THREADS;
+    static_assert(kEach * THREADS * TileT::kPiece == ROWS * DT, "tile and threads");
+    uint4 r[VEC ? 1 : kEach];
+
+    // which row, block of columns and piece the i-th 16 bytes of thread t are in LDS
+    static __device__ __forceinline__ void place(int i, int t, int &row, int &block, int &piece)
+    {
+        const int e = i * THREADS + t;
+        piece = e % TileT::kPieces;
+        const int rest = e / TileT::kPieces;
+        row = rest % ROWS;
+        block = rest / ROWS;
+        if constexpr (VEC)
+            piece ^= TileT::swizzle(row);
+    }
+
+    static __device__ __forceinline__ void clear(uint8_t *lds, int dim, int t)
+    {
+        if (VEC && dim < DT) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                int row, block, piece;
+                place(i, t, row, block, piece);
+                if (block * 32 + piece * TileT::kPiece >= dim)
+                    *reinterpret_cast<uint4 *>(lds + TileT::at(row, block, piece)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void fetch(uint8_t *lds, const T *base, int64_t stride, int rows, int dim, int t)
+    {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            int row, block, piece;
+            place(i, t, row, block, piece);
+            const int d = block * 32 + piece * TileT::kPiece;
+            if constexpr (VEC) {
+                const uint32_t at = (uint32_t)min(row, rows - 1) * (uint32_t)(stride * sizeof(T)) + d * sizeof(T);
+                // the wave's first piece; lane l's lands 16 l bytes on
+                const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds +
+                                    (i * THREADS + (t & ~63)) * 16;
+                if (dim == DT || d < dim)
+                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                                 :
+                                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(base)
+                                 : "memory", "m0");
+            } else {
+                const T *p = base + (int64_t)row * stride + d;
+                Vec<T, TileT::kPiece> v;
+#pragma unroll
+                for (int e = 0; e < TileT::kPiece; ++e)
+                    v.v[e] = row < rows && d + e < dim ? p[e] : (T)0.0f;
+                r[i] = *reinterpret_cast<const uint4 *>(&v);
+            }
+        }
+    }
+
+    // what fetch() asked for is in LDS (after this and a barrier)
+    __device__ __forceinline__ void store(uint8_t *lds, int t) const
+    {
+        if constexpr (VEC) {
+            loads_done();
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                int row, block, piece;
+                place(i, t, row, block, piece);
+                *reinterpret_cast<uint4 *>(lds + TileT::at(row, block, piece)) = r[i];
+            }
+        }
+    }
+};
+
+// The same through registers always: a wave that loads for itself alone holds the next rows
+// while it works on these, and needs LDS for one tile only.
+template <typename T, int ROWS, int DT, int THREADS, bool VEC>
+struct HeldStage {
     using TileT = Tile<T, ROWS, DT>;
     static constexpr int kEach = ROWS * DT / TileT::kPiece / THREADS;
     static_assert(kEach * THREADS * TileT::kPiece == ROWS * DT, "tile and threads");

@@ -148,19 +148,31 @@ __device__ void careful_dkv(const AttnArgs &a, int b, int head, int key, int len
 
 // ---- dk, dv ------------------------------------------------------------------
 //
-// A block of four waves holds 128 keys of one kv head, 32 a wave; the queries of
-// the heads that share it pass through LDS in tiles of 32 or 64 with their dout, lse and D.
-// Scores have queries along the accumulator's rows and keys across the lanes.
+// A block holds 128 keys of one kv head, 32 a wave; the queries of the heads that share it
+// pass through LDS in tiles of 32 or 64 with their dout, lse and D.  Scores have queries along
+// the accumulator's rows and keys across the lanes.
+//
+// Four waves hold their keys' and values' fragments in registers.  With heads of 128 in 16
+// bits those and the accumulators (192 registers) leave no room for a second wave on
+// a SIMD, and one wave cannot overlap its exponentials with its products.  There keys and
+// values stay in LDS, half as many reads again, and eight waves work on a block: the upper
+// four take the second half of each query tile and their sums are added at the end.
 template <typename T, int DT>
 struct KeysBackward {
+    static constexpr bool kWide = sizeof(T) == 2 && DT == 128;
+    static constexpr int kThreads = kWide ? 512 : 256;
     static constexpr int kQueries = sizeof(T) == 4 ? 32 : 64;
     using TileT = Tile<T, kQueries, DT>;
-    static constexpr int kStats = 4 * TileT::kBytes;         // two buffers of lse, D
+    using KeysT = Tile<T, 128, DT>;
+    static constexpr int kKeys = 4 * TileT::kBytes;          // after two buffers of q and dout: keys, values
+    static constexpr int kStats = kKeys + (kWide ? 2 * KeysT::kBytes : 0); // two buffers of lse, D
     static constexpr int kLds = kStats + 2 * 2 * kQueries * 4;
+    static constexpr int kWaves = sizeof(T) == 2 ? 2 : 1;    // of a SIMD
 };
 
 template <typename T, int DT, bool VEC>
-__global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
+__global__ __launch_bounds__((KeysBackward<T, DT>::kThreads), (KeysBackward<T, DT>::kWaves)) void
+attention_keys_backward(AttnArgs a)
 {
     using G = KeysBackward<T, DT>;
     using TileT = typename G::TileT;
@@ -177,13 +189,28 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
     const uint32_t bk = rest / (uint32_t)a.splits;
     const int kv = (int)(bk % (uint32_t)a.p.kv_heads), b = (int)(bk / (uint32_t)a.p.kv_heads);
 
-    const int t = (int)threadIdx.x, lane = t & 63, wave = t >> 6, h = lane >> 5;
+    const int t = (int)threadIdx.x, lane = t & 63, wave = (t >> 6) & 3, upper = t >> 8, h = lane >> 5;
     const int key = key0 + wave * 32 + (lane & 31);
     const int dim = (int)a.p.dim, len = key_length(a, b);
     const Range range = queries_of(a, len, key);
 
-    FragV<T> kf[KK], vf[KK];
-    {
+    // fragments of the wave's keys and values: held, or read from LDS each time
+    FragV<T> kf[G::kWide ? 1 : KK], vf[G::kWide ? 1 : KK];
+    const uint8_t *kl = lds + G::kKeys, *vl = kl + G::KeysT::kBytes;
+    if constexpr (G::kWide) {
+        using WholeT = Stage<T, 128, DT, G::kThreads, VEC>;
+        WholeT ks, vs;
+        ks.clear(lds + G::kKeys, dim, t);
+        vs.clear(lds + G::kKeys + G::KeysT::kBytes, dim, t);
+        if (key0 < len) {
+            ks.fetch(lds + G::kKeys, head_row<T>(a.p.k, a.p.k_stride, b, key0, kv), a.p.k_stride[1], len - key0, dim,
+                     t);
+            vs.fetch(lds + G::kKeys + G::KeysT::kBytes, head_row<T>(a.p.v, a.p.v_stride, b, key0, kv),
+                     a.p.v_stride[1], len - key0, dim, t);
+            ks.store(lds + G::kKeys, t);
+            vs.store(lds + G::kKeys + G::KeysT::kBytes, t);
+        }
+    } else {
         const T *k = head_row<T>(a.p.k, a.p.k_stride, b, key, kv);
         const T *v = head_row<T>(a.p.v, a.p.v_stride, b, key, kv);
 #pragma unroll
@@ -206,13 +233,14 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
     const int share = (all + a.splits - 1) / a.splits;
     const int first = min(all, split * share), end = min(all, first + share);
 
-    Stage<T, NQ, DT, 256, VEC> qst, gst;
+    using StageT = Stage<T, NQ, DT, G::kThreads, VEC>;
+    StageT qst, gst;
     float2 stat = make_float2(INFINITY, 0.0f); // of the first NQ threads' rows
-    const auto fetch = [&](int i) {
+    const auto fetch = [&](int i, int buf) {
         const int head = kv * a.group + i / tiles, q0 = lo + (i % tiles) * NQ;
         const int rows = (int)a.p.queries - q0;
-        qst.fetch(head_row<T>(a.p.q, a.p.q_stride, b, q0, head), a.p.q_stride[1], rows, dim, t);
-        gst.fetch(head_row<T>(a.p.dout, a.p.dout_stride, b, q0, head), a.p.dout_stride[1], rows, dim, t);
+        qst.fetch(lds + buf * TileT::kBytes, head_row<T>(a.p.q, a.p.q_stride, b, q0, head), a.p.q_stride[1], rows, dim, t);
+        gst.fetch(lds + (2 + buf) * TileT::kBytes, head_row<T>(a.p.dout, a.p.dout_stride, b, q0, head), a.p.dout_stride[1], rows, dim, t);
         stat = make_float2(INFINITY, 0.0f);
         if (t < min(NQ, rows))
             stat = a.rows[((int64_t)b * a.p.heads + head) * a.p.queries + q0 + t];
@@ -226,18 +254,23 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
             s[NQ + t] = stat.y * kLower;
         }
     };
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        StageT::clear(lds + i * TileT::kBytes, dim, t);
     if (first < end) {
-        fetch(first);
+        fetch(first, 0);
         store(0);
     }
+    loads_done();
     int buf = 0;
     for (int i = first; i < end; ++i, buf ^= 1) {
         __syncthreads();
         if (i + 1 < end)
-            fetch(i + 1);
+            fetch(i + 1, buf ^ 1);
         const int head = kv * a.group + i / tiles, q0 = lo + (i % tiles) * NQ;
 #pragma unroll
-        for (int n32 = 0; n32 < NQ; n32 += 32) {
+        for (int half_tile = 0; half_tile < (G::kWide ? 1 : NQ / 32); ++half_tile) {
+            const int n32 = (G::kWide ? upper : half_tile) * 32;
             const int qn = q0 + n32;
             if (__all(range.misses(qn, 32)))
                 continue;
@@ -245,7 +278,26 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
             const float *lse = reinterpret_cast<const float *>(lds + G::kStats) + buf * 2 * NQ + n32;
             const float *delta = lse + NQ;
             float16v s = zero16(), dp = zero16();
-            {
+            if constexpr (G::kWide) {
+                // q and keys in turn, then dout and values
+                const auto read = [&](int i) {
+                    const int kk = i / 2 % KK;
+                    if (i % 2)
+                        return G::KeysT::row_frag(i < 2 * KK ? kl : vl, wave * 32 + (lane & 31), kk, h);
+                    return TileT::row_frag(i < 2 * KK ? ql : gl, n32 + (lane & 31), kk, h);
+                };
+                Pipe<T, 4 * KK, 4> pipe;
+                FragV<T> left;
+                pipe.start(read);
+                pipe.run(read, [&](int i, const FragV<T> &f) {
+                    if (i % 2 == 0)
+                        left = f;
+                    else if (i < 2 * KK)
+                        s = mma(left, f, s);
+                    else
+                        dp = mma(left, f, dp);
+                });
+            } else {
                 Pipe<T, 2 * KK, 4> pipe;
                 const auto read = [&](int i) {
                     return TileT::row_frag(i < KK ? ql : gl, n32 + (lane & 31), i % KK, h);
@@ -253,9 +305,9 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
                 pipe.start(read);
                 pipe.run(read, [&](int i, const FragV<T> &f) {
                     if (i < KK)
-                        s = mma(f, kf[i % KK], s);
+                        s = mma(f, kf[G::kWide ? 0 : i % KK], s);
                     else
-                        dp = mma(f, vf[i % KK], dp);
+                        dp = mma(f, vf[G::kWide ? 0 : i % KK], dp);
                 });
             }
             settle<T>();
@@ -307,6 +359,29 @@ __global__ __launch_bounds__(256, 1) void attention_keys_backward(AttnArgs a)
     }
 
     settle<T>();
+    if constexpr (G::kWide) {
+        float *sums = reinterpret_cast<float *>(lds) + wave * (2 * ND * 16 * 64) + lane;
+        __syncthreads();
+        if (upper) {
+#pragma unroll
+            for (int n = 0; n < ND; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sums[(n * 16 + i) * 64] = dk[n][i];
+                    sums[((ND + n) * 16 + i) * 64] = dv[n][i];
+                }
+        }
+        __syncthreads();
+        if (upper)
+            return;
+#pragma unroll
+        for (int n = 0; n < ND; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                dk[n][i] += sums[(n * 16 + i) * 64];
+                dv[n][i] += sums[((ND + n) * 16 + i) * 64];
+            }
+    }
     bool bad = false;
 #pragma unroll
     for (int n = 0; n < ND; ++n)
@@ -427,20 +502,25 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
     const T *vbase = head_row<T>(a.p.v, a.p.v_stride, b, 0, kv);
     const int64_t ks = a.p.k_stride[1], vs = a.p.v_stride[1];
 
-    Stage<T, G::kKeys, DT, 256, VEC> kst, vst;
+    using StageT = Stage<T, G::kKeys, DT, 256, VEC>;
+    StageT kst, vst;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        StageT::clear(lds + i * TileT::kBytes, dim, t);
     if (lo < hi) {
-        kst.fetch(kbase + lo * ks, ks, len - lo, dim, t);
-        vst.fetch(vbase + lo * vs, vs, len - lo, dim, t);
+        kst.fetch(lds, kbase + lo * ks, ks, len - lo, dim, t);
+        vst.fetch(lds + 2 * TileT::kBytes, vbase + lo * vs, vs, len - lo, dim, t);
         kst.store(lds, t);
         vst.store(lds + 2 * TileT::kBytes, t);
     }
+    loads_done();
     int buf = 0;
     for (int k0 = lo; k0 < hi; k0 += G::kKeys, buf ^= 1) {
         __syncthreads();
         const int64_t next = (int64_t)k0 + G::kKeys;
         if (next < hi) {
-            kst.fetch(kbase + next * ks, ks, (int)(len - next), dim, t);
-            vst.fetch(vbase + next * vs, vs, (int)(len - next), dim, t);
+            kst.fetch(lds + (buf ^ 1) * TileT::kBytes, kbase + next * ks, ks, (int)(len - next), dim, t);
+            vst.fetch(lds + (2 + (buf ^ 1)) * TileT::kBytes, vbase + next * vs, vs, (int)(len - next), dim, t);
         }
         const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
 #pragma unroll
@@ -581,7 +661,7 @@ int run_backward(AttnArgs a, hipStream_t s)
         if (blocks > 0x7fffff00)
             return RANS_E_ARG;
         a.blocks = (uint32_t)blocks;
-        attention_keys_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
+        attention_keys_backward<T, DT, VEC><<<xcd_grid(a.blocks), G::kThreads, G::kLds, s>>>(a);
         if (a.splits > 1) {
             const int64_t all = p.batch * p.kv_heads * p.keys * DT;
             join<T, DT>(parts, p.dk, p.dk_stride, 2 * all, p.batch, p.keys, p.kv_heads, a.splits, p.dim, s);

@@ -169,19 +169,23 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
     const int64_t ks = a.p.k_stride[1], vs = a.p.v_stride[1];
 
     typename G::StageT kst, vst;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        G::StageT::clear(lds + i * TileT::kBytes, dim, t);
     if (lo < hi) {
-        kst.fetch(kbase + lo * ks, ks, len - lo, dim, t);
-        vst.fetch(vbase + lo * vs, vs, len - lo, dim, t);
+        kst.fetch(lds, kbase + lo * ks, ks, len - lo, dim, t);
+        vst.fetch(lds + 2 * TileT::kBytes, vbase + lo * vs, vs, len - lo, dim, t);
         kst.store(lds, t);
         vst.store(lds + 2 * TileT::kBytes, t);
     }
+    loads_done();
     int buf = 0;
     for (int k0 = lo; k0 < hi; k0 += G::kKeys, buf ^= 1) {
         __syncthreads();
         const int64_t next = (int64_t)k0 + G::kKeys;
         if (next < hi) {
-            kst.fetch(kbase + next * ks, ks, (int)(len - next), dim, t);
-            vst.fetch(vbase + next * vs, vs, (int)(len - next), dim, t);
+            kst.fetch(lds + (buf ^ 1) * TileT::kBytes, kbase + next * ks, ks, (int)(len - next), dim, t);
+            vst.fetch(lds + (2 + (buf ^ 1)) * TileT::kBytes, vbase + next * vs, vs, (int)(len - next), dim, t);
         }
         if (!__all(range.misses(k0, G::kKeys))) {
             const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
@@ -260,7 +264,7 @@ template <typename T, int DT, bool VEC>
 struct RowsForward {
     static constexpr int kKeys = 32;
     using TileT = Tile<T, kKeys, DT>;
-    using StageT = Stage<T, kKeys, DT, 64, VEC>;
+    using StageT = HeldStage<T, kKeys, DT, 64, VEC>;
     static constexpr int kWave = 2 * TileT::kBytes;       // keys, values
     static constexpr int kSums = 32 * DT * 4;             // a wave's part at the end
     static constexpr int kLds = 4 * (kWave > kSums ? kWave : kSums) + 4 * 32 * 2 * 4;

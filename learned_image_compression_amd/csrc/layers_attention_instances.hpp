@@ -23,12 +23,14 @@ int with_tile(int64_t dim, bool vec, F &&f)
     }
 }
 
-// Whether a head's row can be read and written 16 bytes at a time.
+// Whether a head's row can be read and written 16 bytes at a time.  (A tile's loads count
+// bytes from its first row in 32 bits: 64 rows of less than 2^24 values.)
 template <typename T>
 bool vector_rows(const lic_attention_args &p, const void *x, const int64_t *stride, int64_t rows, int64_t heads)
 {
     constexpr int n = 16 / sizeof(T);
     return !x || (aligned_to(x, 16) && (p.batch == 1 || stride[0] % n == 0) && (rows == 1 || stride[1] % n == 0) &&
+                  stride[1] < (1 << 24) &&
                   (heads == 1 || stride[2] % n == 0));
 }
 
