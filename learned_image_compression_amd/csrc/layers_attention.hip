@@ -34,7 +34,7 @@ bool valid_call(const lic_attention_args &p, bool backward)
 
 uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-uint64_t row_bytes(const lic_attention_args &p) { return round256((uint64_t)p.batch * p.heads * p.queries * sizeof(float2)); }
+uint64_t row_bytes(const lic_attention_args &p) { return round256((uint64_t)p.batch * p.heads * p.queries * 2 * sizeof(float)); }
 
 // Parts of split sums are as wide as the widest tile the call may take.
 uint64_t part_bytes(const lic_attention_args &p, bool backward)
@@ -77,7 +77,8 @@ int call(const lic_attention_args *args, void *ws, uint64_t ws_bytes, hipStream_
     a.group = (int)(args->heads / args->kv_heads);
     a.splits = 1;
     if (backward) {
-        a.rows = static_cast<float2 *>(ws);
+        a.row_lse = static_cast<float *>(ws);
+        a.row_delta = a.row_lse + args->batch * args->heads * args->queries;
         a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + row_bytes(*args));
     } else {
         a.part = static_cast<float *>(ws);

@@ -39,7 +39,8 @@ struct AttnArgs {
     lic_attention_args p;
     float scale_log2;   // scale * log2 e: exponentials are base 2
     float *part;        // split rows: unnormalised sums [split][row][tile dim], then m, l
-    float2 *rows;       // backward: lse in powers of two, dout . out [batch][heads][queries]
+    float *row_lse;     // backward, [batch][heads][queries] each: lse in powers of two, less 10,
+    float *row_delta;   // and dout . out / 2^10
     int splits;
     int group;          // heads that share a kv head
     uint32_t blocks;    // of the launch's real work
@@ -247,6 +248,22 @@ struct Pipe {
     static constexpr int kLet = 0x6; // vector and scalar arithmetic may pass
 };
 
+// Each active lane's N bytes at base + at to LDS, at address `to` + N times its lane.
+template <int N>
+__device__ __forceinline__ void load_lds(uint32_t to, const void *base, uint32_t at)
+{
+    if constexpr (N == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(to), "v"(at), "s"(base)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                     :
+                     : "s"(to), "v"(at), "s"(base)
+                     : "memory", "m0");
+}
+
 // All loads of the wave so far are done.  Said with the builtin, so the compiler knows: it would
 // wait in each turn of a loop for what was loaded before it.
 __device__ __forceinline__ void loads_done()
@@ -297,24 +314,20 @@ struct Stage {
         }
     }
 
+    // Rows from `base` (the same for the whole block), `rows` of them exist.
     __device__ __forceinline__ void fetch(uint8_t *lds, const T *base, int64_t stride, int rows, int dim, int t)
     {
+        if constexpr (VEC) {
+            if (dim == DT)
+                ask<true>(lds, base, stride, rows, dim, t);
+            else
+                ask<false>(lds, base, stride, rows, dim, t);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            int row, block, piece;
-            place(i, t, row, block, piece);
-            const int d = block * 32 + piece * TileT::kPiece;
-            if constexpr (VEC) {
-                const uint32_t at = (uint32_t)min(row, rows - 1) * (uint32_t)(stride * sizeof(T)) + d * sizeof(T);
-                // the wave's first piece; lane l's lands 16 l bytes on
-                const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds +
-                                    (i * THREADS + (t & ~63)) * 16;
-                if (dim == DT || d < dim)
-                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                                 :
-                                 : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(at), "s"(base)
-                                 : "memory", "m0");
-            } else {
+            for (int i = 0; i < kEach; ++i) {
+                int row, block, piece;
+                place(i, t, row, block, piece);
+                const int d = block * 32 + piece * TileT::kPiece;
                 const T *p = base + (int64_t)row * stride + d;
                 Vec<T, TileT::kPiece> v;
 #pragma unroll
@@ -322,6 +335,23 @@ struct Stage {
                     v.v[e] = row < rows && d + e < dim ? p[e] : (T)0.0f;
                 r[i] = *reinterpret_cast<const uint4 *>(&v);
             }
+        }
+    }
+
+    template <bool WHOLE>
+    static __device__ __forceinline__ void ask(uint8_t *lds, const T *base, int64_t stride, int rows, int dim, int t)
+    {
+        // the wave's first piece; lane l's lands 16 l bytes on
+        const uint32_t first = __builtin_amdgcn_readfirstlane(
+            (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + (t & ~63) * 16);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            int row, block, piece;
+            place(i, t, row, block, piece);
+            const int d = block * 32 + piece * TileT::kPiece;
+            const uint32_t at = (uint32_t)min(row, rows - 1) * (uint32_t)(stride * sizeof(T)) + d * sizeof(T);
+            if (WHOLE || d < dim)
+                load_lds<16>(first + i * THREADS * 16, base, at);
         }
     }
 

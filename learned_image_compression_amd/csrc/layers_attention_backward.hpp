@@ -21,13 +21,10 @@
 namespace lic {
 namespace {
 
-// lse in powers of two; a row that sees nothing gets p = 0 everywhere
-__device__ __forceinline__ float lse_log2(float lse)
-{
-    return lse == -INFINITY ? INFINITY : lse * kLog2e;
-}
+constexpr float kLift = 10.0f, kLower = 1.0f / 1024.0f; // 2^10 and its inverse
 
-// What the backward kernels need of each row, lse in powers of two and D: 16 lanes a row.
+// What the backward kernels need of each row, lse in powers of two (a row that sees nothing: p = 0
+// everywhere) and D, as they take them: 16 lanes a row.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void attention_row_stats(AttnArgs a)
 {
@@ -59,10 +56,12 @@ __global__ __launch_bounds__(256) void attention_row_stats(AttnArgs a)
     for (int x = 8; x > 0; x >>= 1)
         sum += __shfl_xor(sum, x);
     if (line < lines && lane == 0)
-        a.rows[line] = make_float2(lse_log2(a.p.lse[line]), sum);
+    {
+        const float lse = a.p.lse[line];
+        a.row_lse[line] = lse == -INFINITY ? INFINITY : lse * kLog2e - kLift;
+        a.row_delta[line] = sum * kLower;
+    }
 }
-
-constexpr float kLift = 10.0f, kLower = 1.0f / 1024.0f; // 2^10 and its inverse
 
 // One query's gradient with the keys it sees alone (see careful_row of the forward call).
 template <typename T>
@@ -74,7 +73,7 @@ __device__ void careful_dq(const AttnArgs &a, int b, int head, int query, int le
     const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
     const uint8_t *mask = a.p.mask ? mask_row(a, b, head, query) : nullptr;
     const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
-    const float lse = a.rows[line].x, delta = a.rows[line].y;
+    const float lse = a.row_lse[line], delta = a.row_delta[line];
     dq[0] = dq[1] = 0.0f;
     for (int k0 = lo; k0 < hi; k0 += 64) {
         const int key = k0 + lane;
@@ -88,7 +87,7 @@ __device__ void careful_dq(const AttnArgs &a, int b, int head, int query, int le
                 s = fmaf(up(q[d]), up(k[d]), s);
                 dp = fmaf(up(g[d]), up(v[d]), dp);
             }
-            ds = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -lse)) * (dp - delta);
+            ds = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -lse)) * fmaf(dp, kLower, -delta);
         }
         for (uint64_t left = __builtin_amdgcn_ballot_w64(seen); left; left &= left - 1) {
             const int j = __builtin_ctzll(left);
@@ -102,7 +101,8 @@ __device__ void careful_dq(const AttnArgs &a, int b, int head, int query, int le
     }
 }
 
-// One key's gradients from the queries [lo, hi) of a head that see it alone, added to dk, dv.
+// One key's gradients from the queries [lo, hi) of a head that see it alone, added to dk and (2^10
+// times) dv.
 template <typename T>
 __device__ void careful_dkv(const AttnArgs &a, int b, int head, int key, int len, int lo, int hi, float (&dk)[2],
                             float (&dv)[2])
@@ -125,9 +125,8 @@ __device__ void careful_dkv(const AttnArgs &a, int b, int head, int key, int len
                 s = fmaf(up(q[d]), up(k[d]), s);
                 dp = fmaf(up(g[d]), up(v[d]), dp);
             }
-            const float2 row = a.rows[line0 + query];
-            p = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -row.x));
-            ds = p * (dp - row.y);
+            p = __builtin_amdgcn_exp2f(fmaf(s, a.scale_log2, -a.row_lse[line0 + query]));
+            ds = p * fmaf(dp, kLower, -a.row_delta[line0 + query]);
         }
         for (uint64_t left = __builtin_amdgcn_ballot_w64(seen); left; left &= left - 1) {
             const int j = __builtin_ctzll(left);
@@ -235,39 +234,59 @@ attention_keys_backward(AttnArgs a)
 
     using StageT = Stage<T, NQ, DT, G::kThreads, VEC>;
     StageT qst, gst;
-    float2 stat = make_float2(INFINITY, 0.0f); // of the first NQ threads' rows
-    const auto fetch = [&](int i, int buf) {
-        const int head = kv * a.group + i / tiles, q0 = lo + (i % tiles) * NQ;
-        const int rows = (int)a.p.queries - q0;
-        qst.fetch(lds + buf * TileT::kBytes, head_row<T>(a.p.q, a.p.q_stride, b, q0, head), a.p.q_stride[1], rows, dim, t);
-        gst.fetch(lds + (2 + buf) * TileT::kBytes, head_row<T>(a.p.dout, a.p.dout_stride, b, q0, head), a.p.dout_stride[1], rows, dim, t);
-        stat = make_float2(INFINITY, 0.0f);
-        if (t < min(NQ, rows))
-            stat = a.rows[((int64_t)b * a.p.heads + head) * a.p.queries + q0 + t];
+    // the tile that is loaded next: its head, first query, and where its rows begin
+    int head = kv * a.group + (tiles ? first / tiles : 0), q_next = lo + (tiles ? first % tiles : 0) * NQ;
+    const int64_t qs = a.p.q_stride[1] * NQ, gs = a.p.dout_stride[1] * NQ;
+    const T *qp = nullptr, *gp = nullptr;
+    const float *lp = nullptr, *dp_row = nullptr;
+    const auto enter = [&]() {
+        qp = head_row<T>(a.p.q, a.p.q_stride, b, q_next, head);
+        gp = head_row<T>(a.p.dout, a.p.dout_stride, b, q_next, head);
+        const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + q_next;
+        lp = a.row_lse + line;
+        dp_row = a.row_delta + line;
+    };
+    const auto fetch = [&](int buf) {
+        const int rows = (int)a.p.queries - q_next;
+        qst.fetch(lds + buf * TileT::kBytes, qp, a.p.q_stride[1], rows, dim, t);
+        gst.fetch(lds + (2 + buf) * TileT::kBytes, gp, a.p.dout_stride[1], rows, dim, t);
+        // the first wave brings the tile's lse, the second its D
+        const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + G::kStats +
+                            buf * 2 * NQ * 4;
+        const int turn = __builtin_amdgcn_readfirstlane(t >> 6);
+        if (turn < 2 && lane < NQ)
+            load_lds<4>(to + turn * NQ * 4, turn ? dp_row : lp, min(lane, rows - 1) * 4);
+        q_next += NQ, qp += qs, gp += gs, lp += NQ, dp_row += NQ;
+        if (q_next >= lo + tiles * NQ) {
+            q_next = lo;
+            ++head;
+            if (head < (kv + 1) * a.group)
+                enter();
+        }
     };
     const auto store = [&](int buf) {
         qst.store(lds + buf * TileT::kBytes, t);
         gst.store(lds + (2 + buf) * TileT::kBytes, t);
-        if (t < NQ) {
-            float *s = reinterpret_cast<float *>(lds + G::kStats) + buf * 2 * NQ;
-            s[t] = stat.x - kLift;
-            s[NQ + t] = stat.y * kLower;
-        }
+        loads_done();
     };
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         StageT::clear(lds + i * TileT::kBytes, dim, t);
+    int q_cur = q_next, head_cur = head; // the tile worked on
     if (first < end) {
-        fetch(first, 0);
+        enter();
+        fetch(0);
         store(0);
     }
     loads_done();
     int buf = 0;
     for (int i = first; i < end; ++i, buf ^= 1) {
         __syncthreads();
-        if (i + 1 < end)
-            fetch(i + 1, buf ^ 1);
-        const int head = kv * a.group + i / tiles, q0 = lo + (i % tiles) * NQ;
+        const int q0 = q_cur, q_head = head_cur;
+        if (i + 1 < end) {
+            q_cur = q_next, head_cur = head;
+            fetch(buf ^ 1);
+        }
 #pragma unroll
         for (int half_tile = 0; half_tile < (G::kWide ? 1 : NQ / 32); ++half_tile) {
             const int n32 = (G::kWide ? upper : half_tile) * 32;
@@ -318,11 +337,11 @@ attention_keys_backward(AttnArgs a)
             Pipe<T, 4 * ND, 4> pipe;
             pipe.start(read);
             uint32_t seen = 0xffffu;
-            // rows beyond the queries have p = 0 by their lse; lanes beyond the keys are not stored
-            const bool part = a.p.mask || !__all(key >= len || range.covers(qn, min(32, (int)a.p.queries - qn)));
+            // lanes beyond the keys are not stored
+            const bool part = a.p.mask || !__all(key >= len || range.covers(qn, 32));
             if (part) {
                 const uint8_t *mask =
-                    a.p.mask ? mask_row(a, b, head, 0) + min(key, (int)a.p.keys - 1) * a.p.mask_stride[3] : nullptr;
+                    a.p.mask ? mask_row(a, b, q_head, 0) + min(key, (int)a.p.keys - 1) * a.p.mask_stride[3] : nullptr;
                 seen = visible(range, mask, a.p.mask_stride[2], qn, h);
             }
 #pragma unroll
@@ -424,11 +443,11 @@ attention_keys_backward(AttnArgs a)
             if (a.splits == 1) {
                 if (d < dim) {
                     head_row<T>(a.p.dk, a.p.dk_stride, b, k, kv)[d] = down<T>(ck[c] * scale);
-                    head_row<T>(a.p.dv, a.p.dv_stride, b, k, kv)[d] = down<T>(cv[c]);
+                    head_row<T>(a.p.dv, a.p.dv_stride, b, k, kv)[d] = down<T>(cv[c] * kLower);
                 }
             } else if (d < DT) {
                 part_row(k)[d] = ck[c] * scale;
-                part_row(k)[keys_all * DT + d] = cv[c];
+                part_row(k)[keys_all * DT + d] = cv[c] * kLower;
             }
         }
     }
@@ -471,8 +490,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
     const Range range = keys_of(a, len, query);
     const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
     const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
-    const float2 row = there ? a.rows[line] : make_float2(INFINITY, 0.0f);
-    const float lse = row.x, delta = row.y;
+    const float lse = there ? a.row_lse[line] : INFINITY;
+    const float delta = there ? a.row_delta[line] : 0.0f;
 
     FragV<T> qf[KK], gf[KK];
     {
@@ -507,21 +526,27 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         StageT::clear(lds + i * TileT::kBytes, dim, t);
+    const T *kp = kbase + lo * ks, *vp = vbase + lo * vs; // the next tile
+    const auto fetch = [&](int buf, int rows) {
+        kst.fetch(lds + buf * TileT::kBytes, kp, ks, rows, dim, t);
+        vst.fetch(lds + (2 + buf) * TileT::kBytes, vp, vs, rows, dim, t);
+        kp += ks * G::kKeys, vp += vs * G::kKeys;
+    };
+    const auto store = [&](int buf) {
+        kst.store(lds + buf * TileT::kBytes, t);
+        vst.store(lds + (2 + buf) * TileT::kBytes, t);
+    };
     if (lo < hi) {
-        kst.fetch(lds, kbase + lo * ks, ks, len - lo, dim, t);
-        vst.fetch(lds + 2 * TileT::kBytes, vbase + lo * vs, vs, len - lo, dim, t);
-        kst.store(lds, t);
-        vst.store(lds + 2 * TileT::kBytes, t);
+        fetch(0, len - lo);
+        store(0);
     }
     loads_done();
     int buf = 0;
     for (int k0 = lo; k0 < hi; k0 += G::kKeys, buf ^= 1) {
         __syncthreads();
-        const int64_t next = (int64_t)k0 + G::kKeys;
-        if (next < hi) {
-            kst.fetch(lds + (buf ^ 1) * TileT::kBytes, kbase + next * ks, ks, (int)(len - next), dim, t);
-            vst.fetch(lds + (2 + (buf ^ 1)) * TileT::kBytes, vbase + next * vs, vs, (int)(len - next), dim, t);
-        }
+        const bool more = k0 + G::kKeys < hi;
+        if (more)
+            fetch(buf ^ 1, len - k0 - G::kKeys);
         const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -550,7 +575,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
             pipe.start(read);
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * (dp[r] - delta);
+                dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * fmaf(dp[r], kLower, -delta);
             if (mask || !__all(!there || range.covers(kn, 32))) {
                 const uint32_t seen = visible(range, mask, a.p.mask_stride[3], kn, h);
 #pragma unroll
@@ -560,10 +585,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
             const FragV<T> ds[2] = {operand<T>(dp, 0), operand<T>(dp, 1)};
             pipe.run(read, [&](int i, const FragV<T> &f) { dq[i % ND] = mma(f, ds[i / ND], dq[i % ND]); });
         }
-        if (next < hi) {
-            kst.store(lds + (buf ^ 1) * TileT::kBytes, t);
-            vst.store(lds + (2 + (buf ^ 1)) * TileT::kBytes, t);
-        }
+        if (more)
+            store(buf ^ 1);
     }
 
     settle<T>();

@@ -172,21 +172,27 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         G::StageT::clear(lds + i * TileT::kBytes, dim, t);
+    const T *kp = kbase + lo * ks, *vp = vbase + lo * vs; // the next tile
+    const auto fetch = [&](int buf, int rows) {
+        kst.fetch(lds + buf * TileT::kBytes, kp, ks, rows, dim, t);
+        vst.fetch(lds + (2 + buf) * TileT::kBytes, vp, vs, rows, dim, t);
+        kp += ks * G::kKeys, vp += vs * G::kKeys;
+    };
+    const auto store = [&](int buf) {
+        kst.store(lds + buf * TileT::kBytes, t);
+        vst.store(lds + (2 + buf) * TileT::kBytes, t);
+    };
     if (lo < hi) {
-        kst.fetch(lds, kbase + lo * ks, ks, len - lo, dim, t);
-        vst.fetch(lds + 2 * TileT::kBytes, vbase + lo * vs, vs, len - lo, dim, t);
-        kst.store(lds, t);
-        vst.store(lds + 2 * TileT::kBytes, t);
+        fetch(0, len - lo);
+        store(0);
     }
     loads_done();
     int buf = 0;
     for (int k0 = lo; k0 < hi; k0 += G::kKeys, buf ^= 1) {
         __syncthreads();
-        const int64_t next = (int64_t)k0 + G::kKeys;
-        if (next < hi) {
-            kst.fetch(lds + (buf ^ 1) * TileT::kBytes, kbase + next * ks, ks, (int)(len - next), dim, t);
-            vst.fetch(lds + (2 + (buf ^ 1)) * TileT::kBytes, vbase + next * vs, vs, (int)(len - next), dim, t);
-        }
+        const bool more = k0 + G::kKeys < hi;
+        if (more)
+            fetch(buf ^ 1, len - k0 - G::kKeys);
         if (!__all(range.misses(k0, G::kKeys))) {
             const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
             float16v s[2] = {zero16(), zero16()};
@@ -212,10 +218,8 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
                                    operand<T>(s[1], 1)};
             pipe.run(read, [&](int i, const FragV<T> &f) { o[i % ND] = mma(f, p[i / ND], o[i % ND]); });
         }
-        if (next < hi) {
-            kst.store(lds + (buf ^ 1) * TileT::kBytes, t);
-            vst.store(lds + (2 + (buf ^ 1)) * TileT::kBytes, t);
-        }
+        if (more)
+            store(buf ^ 1);
     }
 
     settle<T>();
