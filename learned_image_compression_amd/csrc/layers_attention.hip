@@ -48,9 +48,7 @@ uint64_t part_bytes(const lic_attention_args &p, bool backward)
         return n > 1 ? n * q_lines * (LIC_MAX_HEAD_DIM + 2) * 4 : 0;
     }
     const int nk = keys_splits(p), nq = queries_splits(p);
-    const uint64_t keys = nk > 1 ? 2 * nk * k_lines * LIC_MAX_HEAD_DIM * 4 : 0;
-    const uint64_t queries = nq > 1 ? nq * q_lines * LIC_MAX_HEAD_DIM * 4 : 0;
-    return keys > queries ? keys : queries;
+    return (nk > 1 ? 2 * nk * k_lines * LIC_MAX_HEAD_DIM * 4 : 0) + (nq > 1 ? nq * q_lines * LIC_MAX_HEAD_DIM * 4 : 0);
 }
 
 uint64_t workspace(const lic_attention_args &p, bool backward)

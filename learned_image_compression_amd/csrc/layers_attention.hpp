@@ -51,6 +51,16 @@ struct AttnArgs {
 __device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 __device__ __forceinline__ int64_t most(int64_t a, int64_t b) { return a > b ? a : b; }
 
+// The kernel's arguments (its first and only parameter) read again where they are used: what
+// only a rare path needs would otherwise be held in scalar registers through the whole
+// kernel, and there are too few of them.
+__device__ __forceinline__ const AttnArgs &rare_args()
+{
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *(const AttnArgs *)p;
+}
+
 template <typename T>
 struct Frag;
 template <>
@@ -273,6 +283,16 @@ __device__ __forceinline__ void loads_done()
     asm volatile("" ::: "memory");
 }
 
+// The same for all but the last N loads.
+template <int N>
+__device__ __forceinline__ void loads_done_but()
+{
+    static_assert(N < 64, "what the counter holds");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+}
+
 // ROWS rows on their way from memory to a tile, by THREADS threads.
 //
 // With VEC (sizes, strides and addresses allow 16-byte loads) the memory system writes them to
@@ -367,58 +387,6 @@ struct Stage {
                 place(i, t, row, block, piece);
                 *reinterpret_cast<uint4 *>(lds + TileT::at(row, block, piece)) = r[i];
             }
-        }
-    }
-};
-
-// The same through registers always: a wave that loads for itself alone holds the next rows
-// while it works on these, and needs LDS for one tile only.
-template <typename T, int ROWS, int DT, int THREADS, bool VEC>
-struct HeldStage {
-    using TileT = Tile<T, ROWS, DT>;
-    static constexpr int kEach = ROWS * DT / TileT::kPiece / THREADS;
-    static_assert(kEach * THREADS * TileT::kPiece == ROWS * DT, "tile and threads");
-    uint4 r[kEach];
-
-    static __device__ __forceinline__ void place(int i, int t, int &row, int &block, int &piece)
-    {
-        const int e = i * THREADS + t;
-        piece = e % TileT::kPieces;
-        const int rest = e / TileT::kPieces;
-        row = rest % ROWS;
-        block = rest / ROWS;
-    }
-
-    // rows [0, rows) of base exist; the others and columns from dim on become 0
-    __device__ __forceinline__ void fetch(const T *base, int64_t stride, int rows, int dim, int t)
-    {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            int row, block, piece;
-            place(i, t, row, block, piece);
-            const int d = block * 32 + piece * TileT::kPiece;
-            const T *p = base + (int64_t)row * stride + d;
-            r[i] = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (VEC) {
-                if (row < rows && d < dim)
-                    r[i] = *reinterpret_cast<const uint4 *>(p);
-            } else {
-                Vec<T, TileT::kPiece> v;
-#pragma unroll
-                for (int e = 0; e < TileT::kPiece; ++e)
-                    v.v[e] = row < rows && d + e < dim ? p[e] : (T)0.0f;
-                r[i] = *reinterpret_cast<const uint4 *>(&v);
-            }
-        }
-    }
-
-    __device__ __forceinline__ void store(uint8_t *lds, int t) const
-    {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            int row, block, piece;
-            place(i, t, row, block, piece);
-            *reinterpret_cast<uint4 *>(lds + TileT::at(row, block, piece)) = r[i];
         }
     }
 };
@@ -638,13 +606,21 @@ inline int row_splits(const lic_attention_args &p)
     return n < 1 ? 1 : (int)n;
 }
 
-// Few rows for the keys: the rows kernel, which splits the key axis over waves and
-// blocks; else the tiles kernel, whose blocks hold 128 queries of one head.
+// Which forward kernel: the one of few queries (32 rows of all heads that share keys a block, the
+// key axis split over waves and blocks) or the one of many (128 queries of one head a block).
+// Both costs in units of what the second takes for 64 keys (about 1 us in 16 bits, 2.6 to 8.6
+// in 32): its blocks run 512 at once, two a CU; the first gets through 1400 tiles of 32 x 32
+// in that time and pays for joining, more where splits are joined by a second launch.
+// Measured (us, few / many), bfloat16, dim 64: 8160 x 8160, 1 head 51 / 123; 1000 x 1000, 8
+// heads 17 / 20; 510 x 510, 24 heads 22 / 13; 70 x 70, 128 heads 7.0 / 6.5; 40 x 500, 128 heads
+// 15.6 / 11.9; 8 x 1000, 256 heads on 32 11 / 19.
 inline bool few_rows(const lic_attention_args &p)
 {
-    const int64_t rows = p.queries * (p.heads / p.kv_heads);
-    const int64_t tiles = (p.queries + 127) / 128 * p.batch * p.heads;
-    return rows <= 64 || tiles < 128;
+    const int64_t shared = p.batch * p.kv_heads;
+    const double row_tiles = (double)((p.queries * (p.heads / p.kv_heads) + 31) / 32 * shared);
+    const double rounds = (double)(((p.queries + 127) / 128 * p.batch * p.heads + 511) / 512);
+    const double fixed = (row_splits(p) > 1 ? 5.0 : 1.0) * (p.dtype == LIC_F32 ? 0.4 : 1.0);
+    return row_tiles * (double)((p.keys + 31) / 32) / 1400.0 + fixed < rounds * (double)((p.keys + 63) / 64);
 }
 
 // Splits of the backward kernels' loops, where their blocks alone would not fill the CUs:

@@ -23,57 +23,16 @@ namespace {
 
 constexpr float kLift = 10.0f, kLower = 1.0f / 1024.0f; // 2^10 and its inverse
 
-// What the backward kernels need of each row, lse in powers of two (a row that sees nothing: p = 0
-// everywhere) and D, as they take them: 16 lanes a row.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void attention_row_stats(AttnArgs a)
-{
-    const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
-    const int64_t line = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int lane = threadIdx.x & 15, dim = (int)a.p.dim;
-    float sum = 0.0f;
-    if (line < lines) {
-        const int64_t bh = line / a.p.queries;
-        const int64_t query = line - bh * a.p.queries;
-        const int head = (int)(bh % a.p.heads), b = (int)(bh / a.p.heads);
-        const T *o = head_row<T>(static_cast<const void *>(a.p.out), a.p.out_stride, b, query, head);
-        const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
-        if constexpr (VEC) {
-            constexpr int P = 16 / sizeof(T);
-            for (int d = lane * P; d < dim; d += 16 * P) {
-                const Vec<T, P> x = *reinterpret_cast<const Vec<T, P> *>(o + d);
-                const Vec<T, P> y = *reinterpret_cast<const Vec<T, P> *>(g + d);
-#pragma unroll
-                for (int e = 0; e < P; ++e)
-                    sum = fmaf(up(x.v[e]), up(y.v[e]), sum);
-            }
-        } else {
-            for (int d = lane; d < dim; d += 16)
-                sum = fmaf(up(o[d]), up(g[d]), sum);
-        }
-    }
-#pragma unroll
-    for (int x = 8; x > 0; x >>= 1)
-        sum += __shfl_xor(sum, x);
-    if (line < lines && lane == 0)
-    {
-        const float lse = a.p.lse[line];
-        a.row_lse[line] = lse == -INFINITY ? INFINITY : lse * kLog2e - kLift;
-        a.row_delta[line] = sum * kLower;
-    }
-}
-
 // One query's gradient with the keys it sees alone (see careful_row of the forward call).
 template <typename T>
-__device__ void careful_dq(const AttnArgs &a, int b, int head, int query, int len, int lo, int hi, float (&dq)[2])
+__device__ void careful_dq(const AttnArgs &a, int b, int head, int query, int len, int lo, int hi, float lse,
+                           float delta, float (&dq)[2])
 {
     const int lane = threadIdx.x & 63, dim = (int)a.p.dim, kv = head / a.group;
     const Range range = keys_of(a, len, query);
     const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
     const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
     const uint8_t *mask = a.p.mask ? mask_row(a, b, head, query) : nullptr;
-    const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
-    const float lse = a.row_lse[line], delta = a.row_delta[line];
     dq[0] = dq[1] = 0.0f;
     for (int k0 = lo; k0 < hi; k0 += 64) {
         const int key = k0 + lane;
@@ -431,6 +390,7 @@ attention_keys_backward(AttnArgs a)
         }
     }
     for (; redo; redo &= redo - 1) {
+        const AttnArgs &a = rare_args();
         const int k = key0 + wave * 32 + __builtin_ctzll(redo);
         float ck[2] = {0.0f, 0.0f}, cv[2] = {0.0f, 0.0f};
         for (int i = first; i < end; ++i) {
@@ -455,7 +415,7 @@ attention_keys_backward(AttnArgs a)
 
 // ---- dq ------------------------------------------------------------------------
 //
-// As the forward kernel of many queries: 128 queries of one head in a block, keys and
+// It runs first.  As the forward kernel of many queries: 128 queries of one head in a block, keys and
 // values through LDS in tiles of 64 taken as two halves, scores with keys along the rows.
 template <typename T, int DT>
 struct QueriesBackward {
@@ -490,17 +450,32 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
     const Range range = keys_of(a, len, query);
     const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
     const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
-    const float lse = there ? a.row_lse[line] : INFINITY;
-    const float delta = there ? a.row_delta[line] : 0.0f;
 
     FragV<T> qf[KK], gf[KK];
+    // a row's lse in powers of two (a row that sees nothing: p = 0 everywhere) and D, as the products
+    // take them; kept for the keys' kernel, which runs after this one
+    float lse = INFINITY, delta = 0.0f;
     {
         const T *q = head_row<T>(a.p.q, a.p.q_stride, b, query, head);
         const T *g = head_row<T>(a.p.dout, a.p.dout_stride, b, query, head);
+        const T *o = head_row<T>(static_cast<const void *>(a.p.out), a.p.out_stride, b, query, head);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             qf[kk] = row_from_memory<T, VEC>(q, there, kk, h, dim);
             gf[kk] = row_from_memory<T, VEC>(g, there, kk, h, dim);
+            const FragV<T> of = row_from_memory<T, VEC>(o, there, kk, h, dim);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                delta = fmaf(up(gf[kk][e]), up(of[e]), delta);
+        }
+        delta = pair_sum(delta) * kLower;
+        if (there) {
+            const float own = a.p.lse[line];
+            lse = own == -INFINITY ? INFINITY : own * kLog2e - kLift;
+            if (h == 0 && split == 0) {
+                a.row_lse[line] = lse;
+                a.row_delta[line] = delta;
+            }
         }
     }
     float16v dq[ND];
@@ -609,9 +584,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
         }
     }
     for (; redo; redo &= redo - 1) {
-        const int qi = q0 + wave * 32 + __builtin_ctzll(redo);
+        const AttnArgs &a = rare_args();
+        const int j = __builtin_ctzll(redo), qi = q0 + wave * 32 + j;
         float c[2];
-        careful_dq<T>(a, b, head, qi, len, lo, hi, c);
+        careful_dq<T>(a, b, head, qi, len, lo, hi, __shfl(lse, j), __shfl(delta, j), c);
         for (int e = 0; e < 2; ++e) {
             const int d = lane + 64 * e;
             if (a.splits == 1) {
@@ -625,44 +601,53 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
     }
 }
 
-// The splits' parts summed in their order: four columns of a row a thread.
+// The splits' parts summed in their order, of dq, dk and dv in one launch: four columns of a row a
+// thread.
 struct JoinArgs {
-    const float *part;
-    void *out;
-    int64_t stride[3]; // batch, row, head
-    int64_t step;      // from a split's part to the next's
-    int64_t lines, rows, heads;
-    int splits, dim;
+    struct One {
+        const float *part;
+        void *out;
+        int64_t stride[3]; // batch, row, head
+        int64_t step;      // from a split's part to the next's
+        int64_t lines, rows, heads;
+        int splits;
+    } one[3];
+    int count, dim;
 };
 
 template <typename T, int DT>
-__global__ __launch_bounds__(256) void attention_join(JoinArgs a)
+__global__ __launch_bounds__(256) void attention_join(JoinArgs j)
 {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t line = id / (DT / 4);
+    int64_t line = id / (DT / 4);
     const int d = (int)(id % (DT / 4)) * 4;
-    if (line >= a.lines || d >= a.dim)
+    for (int k = 0; k < j.count; ++k) {
+        const JoinArgs::One &a = j.one[k];
+        if (line >= a.lines) {
+            line -= a.lines;
+            continue;
+        }
+        if (d >= j.dim)
+            return;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i0 = 0; i0 < a.splits; i0 += 4) {
+            float4 p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                p[u] = *reinterpret_cast<const float4 *>(a.part + min(i0 + u, a.splits - 1) * a.step + line * DT + d);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u < a.splits)
+                    s.x += p[u].x, s.y += p[u].y, s.z += p[u].z, s.w += p[u].w;
+        }
+        const int64_t bh = line / a.rows;
+        T *out = head_row<T>(a.out, a.stride, (int)(bh / a.heads), line - bh * a.rows, (int)(bh % a.heads));
+        const float v[4] = {s.x, s.y, s.z, s.w};
+        for (int e = 0; e < 4; ++e)
+            if (d + e < j.dim)
+                out[d + e] = down<T>(v[e]);
         return;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < a.splits; ++i) {
-        const float4 p = *reinterpret_cast<const float4 *>(a.part + i * a.step + line * DT + d);
-        s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
     }
-    const int64_t bh = line / a.rows;
-    T *out = head_row<T>(a.out, a.stride, (int)(bh / a.heads), line - bh * a.rows, (int)(bh % a.heads));
-    const float v[4] = {s.x, s.y, s.z, s.w};
-    for (int e = 0; e < 4; ++e)
-        if (d + e < a.dim)
-            out[d + e] = down<T>(v[e]);
-}
-
-template <typename T, int DT>
-void join(const float *part, void *out, const int64_t *stride, int64_t step, int64_t batch, int64_t rows,
-          int64_t heads, int splits, int64_t dim, hipStream_t s)
-{
-    JoinArgs j{part, out, {stride[0], stride[1], stride[2]}, step, batch * rows * heads, rows, heads, splits, (int)dim};
-    const int64_t threads = j.lines * (DT / 4);
-    attention_join<T, DT><<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(j);
 }
 
 template <typename T, int DT, bool VEC>
@@ -670,41 +655,55 @@ int run_backward(AttnArgs a, hipStream_t s)
 {
     const lic_attention_args &p = a.p;
     float *parts = a.part;
+    JoinArgs j{};
+    j.dim = (int)p.dim;
+    const auto joined = [&](const float *part, void *out, const int64_t *stride, int64_t step, int64_t rows,
+                            int64_t heads, int splits) {
+        j.one[j.count++] = {part, out, {stride[0], stride[1], stride[2]}, step, p.batch * rows * heads, rows, heads,
+                            splits};
+    };
     if (p.queries > 0) {
+        using G = QueriesBackward<T, DT>;
+        static const bool once = (allow_lds(attention_queries_backward<T, DT, VEC>, G::kLds), true);
+        (void)once;
+        a.splits = queries_splits(p);
         const int64_t lines = p.batch * p.heads * p.queries;
-        attention_row_stats<T, VEC><<<(uint32_t)((lines + 15) / 16), 256, 0, s>>>(a);
+        const int64_t blocks = (p.queries + 127) / 128 * p.batch * p.heads * a.splits;
+        if (blocks > 0x7fffff00)
+            return RANS_E_ARG;
+        a.blocks = (uint32_t)blocks;
+        a.part = parts;
+        attention_queries_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
+        if (a.splits > 1) {
+            joined(parts, p.dq, p.dq_stride, lines * DT, p.queries, p.heads, a.splits);
+            parts += a.splits * lines * DT;
+        }
     }
     if (p.keys > 0) {
         using G = KeysBackward<T, DT>;
         static const bool once = (allow_lds(attention_keys_backward<T, DT, VEC>, G::kLds), true);
         (void)once;
         a.splits = keys_splits(p);
-        a.part = parts;
         const int64_t blocks = (p.keys + 127) / 128 * p.batch * p.kv_heads * a.splits;
         if (blocks > 0x7fffff00)
             return RANS_E_ARG;
         a.blocks = (uint32_t)blocks;
+        a.part = parts;
         attention_keys_backward<T, DT, VEC><<<xcd_grid(a.blocks), G::kThreads, G::kLds, s>>>(a);
         if (a.splits > 1) {
             const int64_t all = p.batch * p.kv_heads * p.keys * DT;
-            join<T, DT>(parts, p.dk, p.dk_stride, 2 * all, p.batch, p.keys, p.kv_heads, a.splits, p.dim, s);
-            join<T, DT>(parts + all, p.dv, p.dv_stride, 2 * all, p.batch, p.keys, p.kv_heads, a.splits, p.dim, s);
+            joined(parts, p.dk, p.dk_stride, 2 * all, p.keys, p.kv_heads, a.splits);
+            joined(parts + all, p.dv, p.dv_stride, 2 * all, p.keys, p.kv_heads, a.splits);
         }
     }
-    if (p.queries > 0) {
-        using G = QueriesBackward<T, DT>;
-        static const bool once = (allow_lds(attention_queries_backward<T, DT, VEC>, G::kLds), true);
-        (void)once;
-        a.splits = queries_splits(p);
-        a.part = parts; // dk and dv are joined by now, in this stream's order
-        const int64_t blocks = (p.queries + 127) / 128 * p.batch * p.heads * a.splits;
-        if (blocks > 0x7fffff00)
+    if (j.count) {
+        int64_t lines = 0;
+        for (int k = 0; k < j.count; ++k)
+            lines += j.one[k].lines;
+        const int64_t blocks = (lines * (DT / 4) + 255) / 256;
+        if (blocks > 0x7fffffff)
             return RANS_E_ARG;
-        a.blocks = (uint32_t)blocks;
-        attention_queries_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
-        if (a.splits > 1)
-            join<T, DT>(parts, p.dq, p.dq_stride, p.batch * p.heads * p.queries * DT, p.batch, p.queries, p.heads,
-                        a.splits, p.dim, s);
+        attention_join<T, DT><<<(uint32_t)blocks, 256, 0, s>>>(j);
     }
     return launched();
 }

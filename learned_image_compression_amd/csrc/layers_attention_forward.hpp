@@ -241,6 +241,7 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
             a.p.lse[((int64_t)b * a.p.heads + head) * a.p.queries + query] = log_sum(m, total);
     }
     for (; redo; redo &= redo - 1) {
+        const AttnArgs &a = rare_args();
         const int qi = q0 + wave * 32 + __builtin_ctzll(redo);
         float cm, cl, co[2];
         careful_row<T>(a, b, head, qi, len, lo, hi, cm, cl, co);
@@ -260,25 +261,28 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
 // The queries of all heads that share a kv head are packed into tiles of 32 rows
 // (row r: query r / group, head r % group of them), so keys and values are read once
 // for all of them; the key axis is split over blocks, and over a block's four waves,
-// which take tiles of 32 keys in turn, each with its own LDS and no barrier.  Memory
-// bounds it: with a single row 31 of 32 columns of the products are idle, and the
-// matrix units still need less time than the keys' way from HBM.
-// The waves' parts are joined in LDS, the blocks' by attention_rows_join.
+// which take tiles of 32 keys in turn, each in its own LDS and with no barrier: the next
+// tile is asked for before this one is waited for.  Memory bounds it: with a single row 31 of
+// 32 columns of the products are idle, and the matrix units still need less time than the
+// keys' way from HBM.  The waves' parts are joined in LDS, the blocks' by attention_rows_join.
 template <typename T, int DT, bool VEC>
 struct RowsForward {
     static constexpr int kKeys = 32;
     using TileT = Tile<T, kKeys, DT>;
-    using StageT = HeldStage<T, kKeys, DT, 64, VEC>;
-    static constexpr int kWave = 2 * TileT::kBytes;       // keys, values
+    using StageT = Stage<T, kKeys, DT, 64, VEC>;
+    static constexpr int kPair = 2 * TileT::kBytes;       // keys, values
+    static constexpr int kBuffers = 8 * kPair <= 128 * 1024 ? 2 : 1;
     static constexpr int kSums = 32 * DT * 4;             // a wave's part at the end
-    static constexpr int kLds = 4 * (kWave > kSums ? kWave : kSums) + 4 * 32 * 2 * 4;
+    static constexpr int kRegion = kBuffers * kPair > kSums ? kBuffers * kPair : kSums;
+    static constexpr int kLds = 4 * kRegion + 4 * 32 * 2 * 4;  // and m, l of each wave and row
 };
 
-// place of a sum: columns rotated by the row, so 32 rows of one column fall into all banks
+// place of a sum: a row's columns rotated by four for each row, so that eight rows' four columns
+// fall into different banks
 template <int DT>
 __device__ __forceinline__ int sum_at(int row, int d)
 {
-    return row * DT + (d + row < DT ? d + row : d + row - DT);
+    return row * DT + (d + 4 * row) % DT;
 }
 
 template <typename T, int DT, bool VEC>
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
 {
     using G = RowsForward<T, DT, VEC>;
     using TileT = typename G::TileT;
-    constexpr int KK = DT / 16, ND = DT / 32, kRegion = G::kWave > G::kSums ? G::kWave : G::kSums;
+    constexpr int KK = DT / 16, ND = DT / 32, kRegion = G::kRegion;
     extern __shared__ __align__(16) uint8_t lds[];
 
     const int rows = (int)a.p.queries * a.group, row_tiles = (rows + 31) / 32;
@@ -327,28 +331,46 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
     const T *kbase = head_row<T>(a.p.k, a.p.k_stride, b, 0, kv);
     const T *vbase = head_row<T>(a.p.v, a.p.v_stride, b, 0, kv);
     const int64_t ks = a.p.k_stride[1], vs = a.p.v_stride[1];
-    uint8_t *kl = lds + wave * kRegion, *vl = kl + TileT::kBytes;
+    uint8_t *mine = lds + wave * kRegion; // buffers of keys, values
 
     typename G::StageT kst, vst;
-    int64_t k0 = first + wave * 32;
-    if (k0 < end) {
-        kst.fetch(kbase + k0 * ks, ks, (int)(end - k0), dim, lane);
-        vst.fetch(vbase + k0 * vs, vs, (int)(end - k0), dim, lane);
-    }
-    for (; k0 < end; k0 += 128) {
-        wave_fence();
-        kst.store(kl, lane);
-        vst.store(vl, lane);
-        wave_fence();
-        const int64_t next = k0 + 128;
-        if (next < end) {
-            kst.fetch(kbase + next * ks, ks, (int)(end - next), dim, lane);
-            vst.fetch(vbase + next * vs, vs, (int)(end - next), dim, lane);
-        }
-        float16v s[1] = {zero16()};
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
-            s[0] = mma(TileT::row_frag(kl, lane & 31, kk, h), qf[kk], s[0]);
+    for (int i = 0; i < 2 * G::kBuffers; ++i)
+        G::StageT::clear(mine + i * TileT::kBytes, dim, lane);
+    wave_fence();
+    const auto fetch = [&](int64_t k, int buf) {
+        kst.fetch(mine + buf * G::kPair, kbase + k * ks, ks, (int)(end - k), dim, lane);
+        vst.fetch(mine + buf * G::kPair + TileT::kBytes, vbase + k * vs, vs, (int)(end - k), dim, lane);
+    };
+    loads_done();
+    int64_t k0 = first + __builtin_amdgcn_readfirstlane(wave) * 32;
+    int buf = 0;
+    if (VEC && G::kBuffers == 2 && k0 < end)
+        fetch(k0, 0);
+    for (; k0 < end; k0 += 128) {
+        uint8_t *kl = mine + buf * G::kPair, *vl = kl + TileT::kBytes;
+        wave_fence();
+        if (VEC && G::kBuffers == 2) {
+            if (k0 + 128 < end) {
+                fetch(k0 + 128, buf ^ 1);
+                loads_done_but<2 * G::StageT::kEach>();
+            } else {
+                loads_done();
+            }
+            buf ^= 1;
+        } else {
+            fetch(k0, 0);
+            kst.store(kl, lane);
+            vst.store(vl, lane);
+        }
+        wave_fence();
+        float16v s[1] = {zero16()};
+        {
+            Pipe<T, KK, KK % 4 ? 2 : 4> pipe;
+            const auto read = [&](int i) { return TileT::row_frag(kl, lane & 31, i, h); };
+            pipe.start(read);
+            pipe.run(read, [&](int i, const FragV<T> &f) { s[0] = mma(f, qf[i], s[0]); });
+        }
         settle<T>();
         // the tile may pass the split's end: those keys are the next split's
         const bool whole = k0 + 32 <= end;
@@ -362,13 +384,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
             }
         }
         soften(s, a.scale_log2, m, l, o);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const FragV<T> p = operand<T>(s[0], half);
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-                o[d] = mma(TileT::col_frag(vl, half * 16, d, lane), p, o[d]);
-        }
+        const FragV<T> p[2] = {operand<T>(s[0], 0), operand<T>(s[0], 1)};
+        const auto read = [&](int i) { return TileT::col_frag(vl, i / ND * 16, i % ND, lane); };
+        Pipe<T, 2 * ND, ND == 3 ? 3 : ND == 1 ? 2 : 4> pipe;
+        pipe.start(read);
+        pipe.run(read, [&](int i, const FragV<T> &f) { o[i % ND] = mma(f, p[i / ND], o[i % ND]); });
     }
 
     // a wave's part: sums [32][DT], then m and l
@@ -381,14 +401,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
 #pragma unroll
     for (int n = 0; n < ND; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            bad |= not_finite(o[n][i]);
-            sums[sum_at<DT>(lane & 31, n * 32 + acc_row(i, h))] = o[n][i];
+        for (int i = 0; i < 16; i += 4) {
+            bad |= not_finite(o[n][i]) || not_finite(o[n][i + 1]) || not_finite(o[n][i + 2]) || not_finite(o[n][i + 3]);
+            *reinterpret_cast<float4 *>(sums + sum_at<DT>(lane & 31, n * 32 + acc_row(i, h))) =
+                make_float4(o[n][i], o[n][i + 1], o[n][i + 2], o[n][i + 3]);
         }
     if (h == 0)
         stats[wave * 32 + lane] = make_float2(m, l);
     wave_fence();
     for (uint64_t redo = rows_of(bad && row < rows); redo; redo &= redo - 1) {
+        const AttnArgs &a = rare_args();
         const int j = __builtin_ctzll(redo);
         const int r = row_tile * 32 + j;
         float cm = -INFINITY, cl = 0.0f, co[2] = {0.0f, 0.0f};
@@ -416,45 +438,71 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
     }
     __syncthreads();
 
-    const float *all = reinterpret_cast<const float *>(lds);
-    for (int e = t; e < 32 * DT; e += 256) {
-        const int j = e / DT, d = e % DT, r = row_tile * 32 + j;
-        if (r >= rows)
-            break;
-        float top = -INFINITY;
+    // (m, l) of the waves become their weights, and of the first wave's the row's own in `whole`
+    __shared__ float2 whole[32];
+    if (t < 32) {
+        float top = -INFINITY, total = 0.0f;
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-            top = fmaxf(top, stats[w * 32 + j].x);
-        float sum = 0.0f, total = 0.0f;
+            top = fmaxf(top, stats[w * 32 + t].x);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float2 st = stats[w * 32 + j];
-            if (st.y != 0.0f) { // NaN counts
-                const float f = __builtin_amdgcn_exp2f(st.x - top);
-                sum += f * all[w * (kRegion / 4) + sum_at<DT>(j, d)];
-                total += f * st.y;
-            }
+            const float2 st = stats[w * 32 + t];
+            // a wave that saw nothing has sums of 0 and no weight (a NaN has one)
+            const float f = st.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(st.x - top);
+            total += f * st.y;
+            stats[w * 32 + t].x = f;
         }
-        const int qi = r / a.group, hd = kv * a.group + r % a.group;
+        whole[t] = make_float2(top, total);
+    }
+    __syncthreads();
+    const float *all = reinterpret_cast<const float *>(lds);
+    const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
+    for (int e = t; e < 8 * DT; e += 256) { // 32 rows of DT / 4
+        const int j = e / (DT / 4), d = e % (DT / 4) * 4, r = row_tile * 32 + j;
+        if (r >= rows)
+            break;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float f = stats[w * 32 + j].x;
+            const float4 v = *reinterpret_cast<const float4 *>(all + w * (kRegion / 4) + sum_at<DT>(j, d));
+            sum.x += f * v.x, sum.y += f * v.y, sum.z += f * v.z, sum.w += f * v.w;
+        }
+        const float top = whole[j].x, total = whole[j].y;
+        const int qi = r / a.group, hd = kv * a.group + r - qi * a.group;
         const int64_t line = ((int64_t)b * a.p.heads + hd) * a.p.queries + qi;
         if (a.splits == 1) {
-            if (d < dim)
-                head_row<T>(a.p.out, a.p.out_stride, b, qi, hd)[d] = down<T>(total == 0.0f ? 0.0f : sum / total);
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            T *out = head_row<T>(a.p.out, a.p.out_stride, b, qi, hd) + d;
+            const float v[4] = {sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv};
+            if constexpr (VEC) {
+                Vec<T, 4> w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w.v[i] = down<T>(v[i]);
+                if (d < dim)
+                    *reinterpret_cast<Vec<T, 4> *>(out) = w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (d + i < dim)
+                        out[i] = down<T>(v[i]);
+            }
             if (d == 0)
                 a.p.lse[line] = log_sum(top, total);
         } else {
-            const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
-            float *part = a.part + (split * lines + line) * (DT + 2);
-            part[2 + d] = sum;
-            if (d == 0) {
-                part[0] = top;
-                part[1] = total;
-            }
+            // sums [split][line][DT], then top and total [split][line]
+            *reinterpret_cast<float4 *>(a.part + (split * lines + line) * DT + d) = sum;
+            if (d == 0)
+                reinterpret_cast<float2 *>(a.part + a.splits * lines * DT)[split * lines + line] =
+                    make_float2(top, total);
         }
     }
 }
 
-// The splits' parts of each row joined: a wave a row.
+// The splits' parts of each row joined, a wave a row: lane s weighs split s, then all splits'
+// sums are read at once.
 template <typename T, int DT>
 __global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a)
 {
@@ -463,25 +511,36 @@ __global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a)
     if (line >= lines)
         return;
     const int lane = threadIdx.x & 63;
-    const float *part = a.part + line * (DT + 2);
-    const int64_t step = lines * (DT + 2);
-    float top = -INFINITY;
-    for (int s = lane; s < a.splits; s += 64)
-        top = fmaxf(top, part[s * step]);
+    const float *part = a.part + line * DT;
+    const int64_t step = lines * DT;
+    float2 stat = make_float2(-INFINITY, 0.0f);
+    if (lane < a.splits)
+        stat = reinterpret_cast<const float2 *>(a.part + a.splits * step)[lane * lines + line];
+    float top = stat.x;
     for (int x = 32; x > 0; x >>= 1)
         top = fmaxf(top, __shfl_xor(top, x));
-    float sum[2] = {0.0f, 0.0f}, total = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-        const float *p = part + s * step;
-        const float pm = p[0], pl = p[1];
-        if (pl == 0.0f)
-            continue;
-        const float f = __builtin_amdgcn_exp2f(pm - top);
-        total += f * pl;
-        if (lane < DT)
-            sum[0] += f * p[2 + lane];
-        if (lane + 64 < DT)
-            sum[1] += f * p[2 + lane + 64];
+    // a split that saw nothing has sums of 0 and no weight
+    const float weight = stat.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(stat.x - top);
+    float total = weight * stat.y;
+    for (int x = 32; x > 0; x >>= 1)
+        total += __shfl_xor(total, x);
+    float sum[2] = {0.0f, 0.0f};
+    const int d0 = min(lane, DT - 1), d1 = min(lane + 64, DT - 1);
+    for (int s0 = 0; s0 < a.splits; s0 += 8) {
+        float v[2][8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const float *p = part + min(s0 + u, a.splits - 1) * step;
+            v[0][u] = p[d0];
+            v[1][u] = DT > 64 ? p[d1] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            // lanes past the splits have no weight
+            const float f = __shfl(weight, min(s0 + u, 63));
+            sum[0] = fmaf(f, s0 + u < a.splits ? v[0][u] : 0.0f, sum[0]);
+            sum[1] = fmaf(f, s0 + u < a.splits ? v[1][u] : 0.0f, sum[1]);
+        }
     }
     const int query = (int)(line % a.p.queries);
     const int64_t bh = line / a.p.queries;
