@@ -301,7 +301,7 @@ attention_keys_backward(AttnArgs a)
             if (part) {
                 const uint8_t *mask =
                     a.p.mask ? mask_row(a, b, q_head, 0) + min(key, (int)a.p.keys - 1) * a.p.mask_stride[3] : nullptr;
-                seen = visible(range, mask, a.p.mask_stride[2], qn, h);
+                seen = visible(range, mask, a.p.mask_stride[2], (int)a.p.queries, qn, h);
             }
 #pragma unroll
             for (int i4 = 0; i4 < 16; i4 += 4) {
@@ -552,7 +552,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
             for (int r = 0; r < 16; ++r)
                 dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * fmaf(dp[r], kLower, -delta);
             if (mask || !__all(!there || range.covers(kn, 32))) {
-                const uint32_t seen = visible(range, mask, a.p.mask_stride[3], kn, h);
+                const uint32_t seen = visible(range, mask, a.p.mask_stride[3], (int)a.p.keys, kn, h);
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
                     dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;

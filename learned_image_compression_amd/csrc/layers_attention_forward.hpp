@@ -18,7 +18,7 @@ constexpr float kSlack = 8.0f; // in powers of two
 __device__ __forceinline__ void hide(float16v &s, const AttnArgs &a, const Range &range, const uint8_t *mask,
                                      int key0, int h)
 {
-    const uint32_t seen = visible(range, mask, a.p.mask_stride[3], key0, h);
+    const uint32_t seen = visible(range, mask, a.p.mask_stride[3], (int)a.p.keys, key0, h);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;

@@ -12,11 +12,34 @@ namespace lic {
 using bf16 = __bf16;
 using f16 = _Float16;
 
+// smaller and larger of two whole numbers (the mixed overloads of min and max may go
+// through double)
+__device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ int64_t most(int64_t a, int64_t b) { return a > b ? a : b; }
+
 // N elements of T as one load or store of at most 16 bytes
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Vec {
     T v[N];
 };
+
+// A store that the caches need not keep.  For outputs that would push the inputs out of the 256
+// MB last-level cache between two readings of them (kCacheBytes), or out of it for the next reader.
+constexpr int64_t kCacheBytes = 256ll << 20;
+template <typename V>
+__device__ __forceinline__ void store_past(V *p, const V &v, bool past)
+{
+    if constexpr (sizeof(V) == 16) {
+        using W = uint32_t __attribute__((ext_vector_type(4)));
+        if (past) {
+            W w;
+            __builtin_memcpy(&w, &v, 16);
+            __builtin_nontemporal_store(w, reinterpret_cast<W *>(p));
+            return;
+        }
+    }
+    *p = v;
+}
 
 // rounding to 16 bits is to nearest, ties to even, in both types
 template <typename T>

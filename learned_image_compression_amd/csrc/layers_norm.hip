@@ -5,6 +5,7 @@
 //   du = dy f'(u),  S1_c = sum du,  S2_c = sum du xh   (over positions)
 //   A_g = sum_c w_c S1_c / m,  B_g = sum_c w_c S2_c / m
 //   dx = rstd_g (w_c du - A_g - xh B_g),  db = sum_n S1,  dw = sum_n S2
+//      = gain_c du - rstd A - d rstd^2 B  with d = x - mean, gain = w rstd: as it is computed
 //
 // HBM bounds all of it.  A group's statistics need all of its values before the
 // first output, so x (backward: x and dy) is read twice unless a sample's group
@@ -34,7 +35,10 @@ namespace lic {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4; // rows in flight of a thread: 64 bytes of loads
+constexpr int kResident = 512; // threads of a resident block
+constexpr int kUnroll = 4;    // vectors in flight of a thread: 64 bytes of loads
+constexpr int kJoinAhead = 8; // chunks that a join asks for at once
+constexpr int kBlocks = 1024; // of a chunked launch: four a CU
 
 struct NormArgs {
     const void *x, *dy;
@@ -50,7 +54,8 @@ struct NormArgs {
     float eps;
     int samples, channels, groups, per_group, param_dtype, act;
     int vecs, tile_vecs, tiles, chunks; // 16-byte vectors of a row, of a tile; tiles of a row
-    int bundle;                         // resident: groups of a block
+    bool past;                          // forward outputs pass the caches
+    uint32_t blocks;                    // resident: samples * groups
 };
 
 __device__ __forceinline__ float param(const void *p, int dtype, int c, float none)
@@ -83,14 +88,14 @@ __device__ __forceinline__ float fast_exp(float x)
 // most 1.5e-7), so value and slope share one exponential.
 __device__ __forceinline__ void normal_cdf(float u, float &phi, float &e)
 {
-    const float z = fabsf(u) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * z);
-    e = fast_exp(-z * z);
-    const float poly =
-        t * (0.254829592f +
-             t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-    const float tail = 0.5f * poly * e;
-    phi = u < 0.0f ? tail : 1.0f - tail;
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(u), 0.3275911f * 0.70710678118654752f, 1.0f));
+    e = __builtin_amdgcn_exp2f(u * u * (-0.5f * 1.4426950408889634f));
+    // half the polynomial
+    const float poly = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f),
+                                                0.5f * 1.421413741f),
+                                        -0.5f * 0.284496736f),
+                                0.5f * 0.254829592f);
+    phi = 0.5f + copysignf(fmaf(-poly, e, 0.5f), u);
 }
 
 template <int ACT>
@@ -115,12 +120,12 @@ __device__ __forceinline__ float act_slope(float u)
         return u > 0.0f ? 1.0f : 0.0f;
     if constexpr (ACT == LIC_ACT_SILU) {
         const float s = __builtin_amdgcn_rcpf(1.0f + fast_exp(-u));
-        return s + u * s * (1.0f - s);
+        return s * fmaf(u, 1.0f - s, 1.0f);
     }
     if constexpr (ACT == LIC_ACT_GELU) {
         float phi, e;
         normal_cdf(u, phi, e);
-        return phi + u * e * 0.3989422804014327f;
+        return fmaf(u * 0.3989422804014327f, e, phi);
     }
     return 1.0f;
 }
@@ -147,6 +152,31 @@ struct Place {
         row_end = min(a.positions, row + a.rows);
     }
 };
+
+// f(vector of each array, row) for a thread's rows: U rows of all arrays are asked for before the
+// first is worked on, also at the end of a chunk, where a row a time would cost a memory
+// latency each.
+template <int U, int ARRAYS, typename V, typename F>
+__device__ __forceinline__ void walk(const Place &at, const V *const (&array)[ARRAYS], const int64_t (&row)[ARRAYS],
+                                     F &&f)
+{
+    const int64_t step = at.rows_at_once;
+    for (int64_t p = at.row + at.lane_row; p < at.row_end; p += U * step) {
+        V v[U][ARRAYS];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (p + u * step < at.row_end) {
+#pragma unroll
+                for (int k = 0; k < ARRAYS; ++k)
+                    v[u][k] = *reinterpret_cast<const V *>(reinterpret_cast<const uint8_t *>(array[k]) +
+                                                           (p + u * step) * row[k]);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (p + u * step < at.row_end)
+                f(v[u], p + u * step);
+    }
+}
 
 // Adds up `mine` over the threads that share channels and leaves each
 // channel's sum with f(channel in the tile's first .., sum).
@@ -216,31 +246,16 @@ __global__ __launch_bounds__(kThreads) void norm_partial_forward(NormArgs a)
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
             shift[i] = up(first.v[i]);
-        const int64_t step = at.rows_at_once;
-        int64_t p = at.row + at.lane_row;
-        for (; p + (kUnroll - 1) * step < at.row_end; p += kUnroll * step) {
-            V v[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                v[u] = *reinterpret_cast<const V *>(x + (p + u * step) * a.x_row);
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float d = up(v[u].v[i]) - shift[i];
-                    s[i].x += d;
-                    s[i].y += d * d;
-                }
-        }
-        for (; p < at.row_end; p += step) {
-            const V v = *reinterpret_cast<const V *>(x + p * a.x_row);
+        const V *const arrays[] = {reinterpret_cast<const V *>(x)};
+        const int64_t rows[] = {a.x_row * (int64_t)sizeof(T)};
+        walk<kUnroll>(at, arrays, rows, [&](const V(&v)[1], int64_t) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float d = up(v.v[i]) - shift[i];
+                const float d = up(v[0].v[i]) - shift[i];
                 s[i].x += d;
                 s[i].y += d * d;
             }
-        }
+        });
     }
     const float count = (float)(at.row_end - at.row);
     const int c_tile = (int)(blockIdx.x % a.tiles) * a.tile_vecs * VEC;
@@ -263,13 +278,22 @@ __global__ __launch_bounds__(kThreads) void norm_join_forward(NormArgs a)
     const float about = part[0].x;
     const int64_t entries = (int64_t)a.chunks * a.per_group;
     float2 s = make_float2(0.0f, 0.0f);
-    for (int64_t e = threadIdx.x; e < entries; e += kThreads) {
-        const int64_t chunk = e / a.per_group;
-        const float2 p = part[chunk * a.channels + (e - chunk * a.per_group)];
-        const float count = (float)min(a.rows, a.positions - chunk * a.rows);
-        const float d = p.x - about;
-        s.x += count * d;
-        s.y += p.y + count * d * d;
+    for (int64_t e0 = threadIdx.x; e0 < entries; e0 += kJoinAhead * kThreads) {
+        float2 p[kJoinAhead];
+        float count[kJoinAhead];
+#pragma unroll
+        for (int u = 0; u < kJoinAhead; ++u) {
+            const int64_t e = least(e0 + u * kThreads, entries - 1), chunk = e / a.per_group;
+            p[u] = part[chunk * a.channels + (e - chunk * a.per_group)];
+            count[u] = e0 + u * kThreads < entries ? (float)least(a.rows, a.positions - chunk * a.rows) : 0.0f;
+            p[u].y = e0 + u * kThreads < entries ? p[u].y : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kJoinAhead; ++u) {
+            const float d = p[u].x - about;
+            s.x += count[u] * d;
+            s.y += p[u].y + count[u] * d * d;
+        }
     }
     s = block_sum<kThreads>(s);
     if (threadIdx.x == 0) {
@@ -299,32 +323,21 @@ __global__ __launch_bounds__(kThreads) void norm_output_forward(NormArgs a)
     }
     const T *x = static_cast<const T *>(a.x) + at.n * a.x_sample + at.c0;
     T *y = static_cast<T *>(a.out) + at.n * a.out_sample + at.c0;
-    const int64_t step = at.rows_at_once;
-    const auto put = [&](const V &v, int64_t p) {
+    const V *const arrays[] = {reinterpret_cast<const V *>(x)};
+    const int64_t rows[] = {a.x_row * (int64_t)sizeof(T)};
+    walk<kUnroll>(at, arrays, rows, [&](const V(&v)[1], int64_t p) {
         V o;
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            o.v[i] = down<T>(act_value<ACT>((up(v.v[i]) - mean[i]) * gain[i] + bias[i]));
-        *reinterpret_cast<V *>(y + p * a.out_row) = o;
-    };
-    int64_t p = at.row + at.lane_row;
-    for (; p + (kUnroll - 1) * step < at.row_end; p += kUnroll * step) {
-        V v[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            v[u] = *reinterpret_cast<const V *>(x + (p + u * step) * a.x_row);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            put(v[u], p + u * step);
-    }
-    for (; p < at.row_end; p += step)
-        put(*reinterpret_cast<const V *>(x + p * a.x_row), p);
+            o.v[i] = down<T>(act_value<ACT>((up(v[0].v[i]) - mean[i]) * gain[i] + bias[i]));
+        store_past(reinterpret_cast<V *>(y + p * a.out_row), o, a.past);
+    });
 }
 
-// Constants of a thread's channels in the backward kernels.
+// Constants of a thread's channels in the backward kernels: u = gain d + bias with d = x - mean.
 template <int VEC>
 struct Channels {
-    float mean[VEC], rstd[VEC], weight[VEC], bias[VEC];
+    float mean[VEC], gain[VEC], bias[VEC];
 
     __device__ Channels(const NormArgs &a, int n, int c0)
     {
@@ -332,14 +345,13 @@ struct Channels {
         for (int i = 0; i < VEC; ++i) {
             const int64_t g = (int64_t)n * a.groups + (c0 + i) / a.per_group;
             mean[i] = a.mean[g];
-            rstd[i] = a.rstd[g];
-            weight[i] = param(a.weight, a.param_dtype, c0 + i, 1.0f);
+            gain[i] = a.rstd[g] * param(a.weight, a.param_dtype, c0 + i, 1.0f);
             bias[i] = param(a.bias, a.param_dtype, c0 + i, 0.0f);
         }
     }
 };
 
-// Backward: a channel's sums of du and du xh over one chunk.
+// Backward: a channel's sums of du and du d over one chunk.
 template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_partial_backward(NormArgs a)
 {
@@ -353,32 +365,17 @@ __global__ __launch_bounds__(kThreads) void norm_partial_backward(NormArgs a)
         const Channels<VEC> ch(a, at.n, at.c0);
         const T *x = static_cast<const T *>(a.x) + at.n * a.x_sample + at.c0;
         const T *dy = static_cast<const T *>(a.dy) + at.n * a.dy_sample + at.c0;
-        const int64_t step = at.rows_at_once;
-        const auto add = [&](const V &v, const V &d) {
+        const V *const arrays[] = {reinterpret_cast<const V *>(x), reinterpret_cast<const V *>(dy)};
+        const int64_t rows[] = {a.x_row * (int64_t)sizeof(T), a.dy_row * (int64_t)sizeof(T)};
+        walk<kUnroll / 2>(at, arrays, rows, [&](const V(&v)[2], int64_t) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float xh = (up(v.v[i]) - ch.mean[i]) * ch.rstd[i];
-                const float du = up(d.v[i]) * act_slope<ACT>(ch.weight[i] * xh + ch.bias[i]);
+                const float d = up(v[0].v[i]) - ch.mean[i];
+                const float du = up(v[1].v[i]) * act_slope<ACT>(fmaf(d, ch.gain[i], ch.bias[i]));
                 s[i].x += du;
-                s[i].y += du * xh;
+                s[i].y = fmaf(du, d, s[i].y);
             }
-        };
-        constexpr int U = kUnroll / 2; // two arrays are read
-        int64_t p = at.row + at.lane_row;
-        for (; p + (U - 1) * step < at.row_end; p += U * step) {
-            V v[U], d[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                v[u] = *reinterpret_cast<const V *>(x + (p + u * step) * a.x_row);
-                d[u] = *reinterpret_cast<const V *>(dy + (p + u * step) * a.dy_row);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                add(v[u], d[u]);
-        }
-        for (; p < at.row_end; p += step)
-            add(*reinterpret_cast<const V *>(x + p * a.x_row),
-                *reinterpret_cast<const V *>(dy + p * a.dy_row));
+        });
     }
     const int c_tile = (int)(blockIdx.x % a.tiles) * a.tile_vecs * VEC;
     float2 *part = a.part + ((int64_t)at.n * a.chunks + at.chunk) * a.channels;
@@ -397,16 +394,24 @@ __global__ __launch_bounds__(kThreads) void norm_join_backward(NormArgs a)
     const int width = min(a.per_group, kThreads), ways = kThreads / width;
     const int lane = t % width, way = t / width;
     const float2 *part = a.part + (int64_t)n * a.chunks * a.channels;
+    const float rstd = a.rstd[(int64_t)n * a.groups + g];
     float2 slope = make_float2(0.0f, 0.0f);
     for (int first = 0; first < a.per_group; first += width) {
         const int c = g * a.per_group + first + lane;
         const bool mine = first + lane < a.per_group;
         float2 s = make_float2(0.0f, 0.0f);
         if (mine && way < ways)
-            for (int64_t k = way; k < a.chunks; k += ways) {
-                const float2 p = part[k * a.channels + c];
-                s.x += p.x;
-                s.y += p.y;
+            for (int64_t k0 = way; k0 < a.chunks; k0 += kJoinAhead * ways) {
+                float2 p[kJoinAhead];
+#pragma unroll
+                for (int u = 0; u < kJoinAhead; ++u)
+                    p[u] = part[least(k0 + u * ways, a.chunks - 1) * a.channels + c];
+#pragma unroll
+                for (int u = 0; u < kJoinAhead; ++u)
+                    if (k0 + u * ways < a.chunks) {
+                        s.x += p[u].x;
+                        s.y += p[u].y;
+                    }
             }
         __syncthreads();
         red[t] = s;
@@ -416,6 +421,7 @@ __global__ __launch_bounds__(kThreads) void norm_join_backward(NormArgs a)
                 s.x += red[w * width + lane].x;
                 s.y += red[w * width + lane].y;
             }
+            s.y *= rstd; // xh = d rstd
             a.totals[(int64_t)n * a.channels + c] = s;
             const float w = param(a.weight, a.param_dtype, c, 1.0f);
             slope.x += w * s.x;
@@ -424,8 +430,9 @@ __global__ __launch_bounds__(kThreads) void norm_join_backward(NormArgs a)
     }
     slope = block_sum<kThreads>(slope);
     if (t == 0) {
+        // as the outputs take them: rstd A and rstd^2 B
         const float m = (float)((double)a.positions * a.per_group);
-        a.slopes[(int64_t)n * a.groups + g] = make_float2(slope.x / m, slope.y / m);
+        a.slopes[(int64_t)n * a.groups + g] = make_float2(rstd * slope.x / m, rstd * rstd * slope.y / m);
     }
 }
 
@@ -475,34 +482,189 @@ __global__ __launch_bounds__(kThreads) void norm_output_backward(NormArgs a)
     const T *x = static_cast<const T *>(a.x) + at.n * a.x_sample + at.c0;
     const T *dy = static_cast<const T *>(a.dy) + at.n * a.dy_sample + at.c0;
     T *dx = static_cast<T *>(a.out) + at.n * a.out_sample + at.c0;
-    const int64_t step = at.rows_at_once;
-    const auto put = [&](const V &v, const V &d, int64_t p) {
+    const V *const arrays[] = {reinterpret_cast<const V *>(x), reinterpret_cast<const V *>(dy)};
+    const int64_t rows[] = {a.x_row * (int64_t)sizeof(T), a.dy_row * (int64_t)sizeof(T)};
+    walk<kUnroll / 2>(at, arrays, rows, [&](const V(&v)[2], int64_t p) {
         V o;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const float xh = (up(v.v[i]) - ch.mean[i]) * ch.rstd[i];
-            const float du = up(d.v[i]) * act_slope<ACT>(ch.weight[i] * xh + ch.bias[i]);
-            o.v[i] = down<T>(ch.rstd[i] * (ch.weight[i] * du - slope[i].x - xh * slope[i].y));
+            const float d = up(v[0].v[i]) - ch.mean[i];
+            const float du = up(v[1].v[i]) * act_slope<ACT>(fmaf(d, ch.gain[i], ch.bias[i]));
+            o.v[i] = down<T>(fmaf(ch.gain[i], du, fmaf(-d, slope[i].y, -slope[i].x)));
         }
         *reinterpret_cast<V *>(dx + p * a.out_row) = o;
-    };
-    constexpr int U = kUnroll / 2;
-    int64_t p = at.row + at.lane_row;
-    for (; p + (U - 1) * step < at.row_end; p += U * step) {
-        V v[U], d[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            v[u] = *reinterpret_cast<const V *>(x + (p + u * step) * a.x_row);
-            d[u] = *reinterpret_cast<const V *>(dy + (p + u * step) * a.dy_row);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            put(v[u], d[u], p + u * step);
-    }
-    for (; p < at.row_end; p += step)
-        put(*reinterpret_cast<const V *>(x + p * a.x_row),
-            *reinterpret_cast<const V *>(dy + p * a.dy_row), p);
+    });
 }
+
+// ---- one launch ------------------------------------------------------------
+//
+// A block keeps one group of one sample in LDS, each thread its own vectors (of channels of
+// the one group) of every rows_at_once-th row.  The blocks of a sample's groups run on one XCD: they
+// share its cache lines where a group's channels do not fill one.
+
+struct Resident {
+    int n, g, lane_row, rows_at_once, c0, slots;
+    bool active;
+
+    __device__ Resident(const NormArgs &a, int vec)
+    {
+        const uint32_t each = (a.blocks + 7) / 8, block = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
+        active = block < a.blocks;
+        n = (int)(block / (uint32_t)a.groups);
+        g = (int)(block - (uint32_t)n * a.groups);
+        const int t = (int)threadIdx.x, width = a.per_group / vec;
+        lane_row = t / width;
+        rows_at_once = kResident / width;
+        c0 = g * a.per_group + (t - lane_row * width) * vec;
+        slots = lane_row < rows_at_once && lane_row < a.positions
+                    ? (int)((a.positions - lane_row + rows_at_once - 1) / rows_at_once)
+                    : 0;
+    }
+};
+
+template <typename T, int VEC, int ACT>
+__global__ __launch_bounds__(kResident) void norm_resident_forward(NormArgs a)
+{
+    using V = Vec<T, VEC>;
+    extern __shared__ __align__(16) uint8_t lds[];
+    V *held = reinterpret_cast<V *>(lds) + threadIdx.x;
+    const Resident at(a, VEC);
+    if (!at.active)
+        return;
+    const T *x = static_cast<const T *>(a.x) + at.n * a.x_sample;
+    const float shift = up(x[at.g * a.per_group]); // a value of the group
+    x += at.c0 + at.lane_row * a.x_row;
+    const int64_t step = at.rows_at_once * a.x_row;
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < at.slots; ++i) {
+        const V v = *reinterpret_cast<const V *>(x + i * step);
+        held[i * kResident] = v;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            s.x += up(v.v[e]) - shift;
+    }
+    const float m = (float)((double)a.positions * a.per_group);
+    const float mean = shift + block_sum<kResident>(s).x / m;
+    for (int i = 0; i < at.slots; ++i) {
+        const V v = held[i * kResident];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float d = up(v.v[e]) - mean;
+            s.y += d * d;
+        }
+    }
+    const float rstd = 1.0f / sqrtf(block_sum<kResident>(s).y / m + a.eps);
+    if (threadIdx.x == 0) {
+        a.mean[(int64_t)at.n * a.groups + at.g] = mean;
+        a.rstd[(int64_t)at.n * a.groups + at.g] = rstd;
+    }
+    if (at.slots == 0)
+        return;
+    float gain[VEC], bias[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        gain[e] = rstd * param(a.weight, a.param_dtype, at.c0 + e, 1.0f);
+        bias[e] = param(a.bias, a.param_dtype, at.c0 + e, 0.0f);
+    }
+    T *y = static_cast<T *>(a.out) + at.n * a.out_sample + at.c0 + at.lane_row * a.out_row;
+    const int64_t out_step = at.rows_at_once * a.out_row;
+#pragma unroll 2
+    for (int i = 0; i < at.slots; ++i) {
+        const V v = held[i * kResident];
+        V o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            o.v[e] = down<T>(act_value<ACT>((up(v.v[e]) - mean) * gain[e] + bias[e]));
+        *reinterpret_cast<V *>(y + i * out_step) = o;
+    }
+}
+
+template <typename T, int VEC, int ACT>
+__global__ __launch_bounds__(kResident) void norm_resident_backward(NormArgs a)
+{
+    using V = Vec<T, VEC>;
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ float2 red[kResident * VEC];
+    const Resident at(a, VEC);
+    if (!at.active)
+        return;
+    const int t = (int)threadIdx.x, depth = (int)((a.positions + at.rows_at_once - 1) / at.rows_at_once);
+    V *hx = reinterpret_cast<V *>(lds) + t, *hd = hx + depth * kResident;
+    const T *x = static_cast<const T *>(a.x) + at.n * a.x_sample + at.c0 + at.lane_row * a.x_row;
+    const T *dy = static_cast<const T *>(a.dy) + at.n * a.dy_sample + at.c0 + at.lane_row * a.dy_row;
+    const int64_t x_step = at.rows_at_once * a.x_row, dy_step = at.rows_at_once * a.dy_row;
+    const int64_t group = (int64_t)at.n * a.groups + at.g;
+    const float mean = a.mean[group], rstd = a.rstd[group];
+    float gain[VEC], bias[VEC];
+    float2 s[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const bool mine = at.slots > 0;
+        gain[e] = mine ? rstd * param(a.weight, a.param_dtype, at.c0 + e, 1.0f) : 0.0f;
+        bias[e] = mine ? param(a.bias, a.param_dtype, at.c0 + e, 0.0f) : 0.0f;
+        s[e] = make_float2(0.0f, 0.0f);
+    }
+#pragma unroll 2
+    for (int i = 0; i < at.slots; ++i) {
+        const V v = *reinterpret_cast<const V *>(x + i * x_step);
+        const V d = *reinterpret_cast<const V *>(dy + i * dy_step);
+        hx[i * kResident] = v;
+        hd[i * kResident] = d;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float off = up(v.v[e]) - mean;
+            const float du = up(d.v[e]) * act_slope<ACT>(fmaf(off, gain[e], bias[e]));
+            s[e].x += du;
+            s[e].y = fmaf(du, off, s[e].y);
+        }
+    }
+    // a group's sums, then each channel's
+    float2 slope = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        s[e].y *= rstd; // xh = (x - mean) rstd
+        slope.x += gain[e] * s[e].x;
+        slope.y += gain[e] * s[e].y;
+        red[t * VEC + e] = s[e];
+    }
+    slope = block_sum<kResident>(slope);
+    const float m = (float)((double)a.positions * a.per_group);
+    slope.x /= m;
+    slope.y *= rstd / m; // the weights in slope hold one rstd already
+    for (int c = t; c < a.per_group; c += kResident) {
+        float2 sum = red[c];
+        for (int r = 1; r < at.rows_at_once; ++r) {
+            sum.x += red[r * a.per_group + c].x;
+            sum.y += red[r * a.per_group + c].y;
+        }
+        const int channel = at.g * a.per_group + c;
+        if (a.samples > 1) {
+            a.totals[(int64_t)at.n * a.channels + channel] = sum;
+        } else {
+            if (a.dbias)
+                put_param(a.dbias, a.param_dtype, channel, sum.x);
+            if (a.dweight)
+                put_param(a.dweight, a.param_dtype, channel, sum.y);
+        }
+    }
+    T *dx = static_cast<T *>(a.out) + at.n * a.out_sample + at.c0 + at.lane_row * a.out_row;
+    const int64_t out_step = at.rows_at_once * a.out_row;
+#pragma unroll 2
+    for (int i = 0; i < at.slots; ++i) {
+        const V v = hx[i * kResident], d = hd[i * kResident];
+        V o;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float off = up(v.v[e]) - mean;
+            const float du = up(d.v[e]) * act_slope<ACT>(fmaf(off, gain[e], bias[e]));
+            o.v[e] = down<T>(fmaf(gain[e], du, fmaf(-off, slope.y, -slope.x)));
+        }
+        *reinterpret_cast<V *>(dx + i * out_step) = o;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void norm_samples(NormArgs a) { sum_over_samples(a, (int)blockIdx.x); }
 
 // ---- host ----------------------------------------------------------------
 
@@ -524,20 +686,18 @@ void choose_tiles(NormArgs &a, int vec)
     }
 }
 
-// Chunks: eight blocks a CU if the rows allow it, each row loop at least once unrolled.
+// Chunks: about kBlocks blocks if the rows allow it, each thread a whole number of unrolled turns.
 void choose_chunks(NormArgs &a)
 {
-    const int64_t at_once = kThreads / a.tile_vecs;
-    const int64_t wanted = 2048 / ((int64_t)a.samples * a.tiles) + 1;
-    const int64_t most = (a.positions + at_once * kUnroll - 1) / (at_once * kUnroll);
-    const int64_t chunks = wanted < most ? wanted : most;
-    a.rows = (a.positions + chunks - 1) / chunks;
+    const int64_t at_once = kThreads / a.tile_vecs, turn = at_once * (a.dy ? kUnroll / 2 : kUnroll);
+    const int64_t wanted = kBlocks / ((int64_t)a.samples * a.tiles) + 1;
+    a.rows = (a.positions + wanted - 1) / wanted;
+    a.rows = (a.rows + turn - 1) / turn * turn;
     a.chunks = (int)((a.positions + a.rows - 1) / a.rows);
 }
 
-// What a workspace has to hold, whatever the vector width: chunks are most with
-// the widest tiles' rows, 2048 / samples + 1 of them a tile at most.
-int64_t most_chunks(int32_t samples) { return 2048 / (int64_t)samples + 1; }
+// The most chunks that any tiling of a row gives.
+int64_t most_chunks(int32_t samples) { return kBlocks / (int64_t)samples + 1; }
 
 uint64_t part_bytes(int32_t samples, int32_t channels)
 {
@@ -577,11 +737,97 @@ int with_act(int act, F &&f)
     }
 }
 
+// LDS that a resident block of VEC-wide vectors needs for one array, 0 if it cannot.
+template <typename T>
+int64_t resident_bytes(const NormArgs &a, int vec)
+{
+    if (a.per_group % vec || a.per_group / vec > kResident)
+        return 0;
+    const int64_t at_once = kResident / (a.per_group / vec);
+    const int64_t bytes = (a.positions + at_once - 1) / at_once * kResident * vec * (int64_t)sizeof(T);
+    return bytes;
+}
+
+// The widest vector that also divides a group.
+template <typename T>
+int resident_vec(const NormArgs &a, int vec)
+{
+    while (vec > 1 && a.per_group % vec)
+        vec = vec > 2 ? 2 : 1;
+    return vec;
+}
+
+template <typename T, typename F>
+int with_vec(int vec, F &&f)
+{
+    switch (vec) {
+    case 2: return f(std::integral_constant<int, 2>{});
+    case 1: return f(std::integral_constant<int, 1>{});
+    default: return f(std::integral_constant<int, 16 / sizeof(T)>{});
+    }
+}
+
+// Most LDS that a resident block takes for its values (of 160 KiB; the backward kernel's sums
+// take up to 32 more).
+constexpr int64_t kMostForward = 128 * 1024, kMostBackward = 96 * 1024;
+
+// One launch or three.  A resident block's time goes with its turns of 512 vectors (0.7 us each;
+// a CU takes one block after another), three launches take 10 us and 1.5 us a million values.
+// Measured (us, one / three launches, bfloat16): 1 x 192 x 510, 32 groups 5.4 / 12.1; 16 x 192 x 1024
+// 11.4 / 13.9; 32 x 1024 x 256 12.8 / 26; 16 x 192 x 4096 36 / 26; 29 x 32 x 4212 30 / 16.
+template <typename T>
+bool resident_pays(const NormArgs &a, int64_t lds, int vec)
+{
+    const int64_t arrays = a.dy ? 2 : 1, turns = lds / (arrays * kResident * vec * (int64_t)sizeof(T));
+    const double one = 3.5 + 0.7 * (double)(turns * ((a.blocks + 255) / 256));
+    const double three = 10.0 + 1.5e-6 * (double)a.samples * (double)a.positions * a.channels;
+    return one <= three && lds > 0 && lds <= (a.dy ? kMostBackward : kMostForward);
+}
+
+template <typename K>
+void allow_lds(K kernel, int64_t bytes)
+{
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)bytes);
+}
+
+template <typename T>
+int run_resident_forward(const NormArgs &a, int vec, int64_t lds, hipStream_t s)
+{
+    return with_vec<T>(vec, [&](auto v) {
+        return with_act(a.act, [&](auto act) {
+            constexpr auto kernel = norm_resident_forward<T, v.value, act.value>;
+            static const bool once = (allow_lds(kernel, kMostForward), true);
+            (void)once;
+            kernel<<<(a.blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
+            return launched();
+        });
+    });
+}
+
+template <typename T>
+int run_resident_backward(const NormArgs &a, int vec, int64_t lds, hipStream_t s)
+{
+    return with_vec<T>(vec, [&](auto v) {
+        return with_act(a.act, [&](auto act) {
+            constexpr auto kernel = norm_resident_backward<T, v.value, act.value>;
+            static const bool once = (allow_lds(kernel, kMostBackward), true);
+            (void)once;
+            kernel<<<(a.blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
+            if (a.samples > 1 && (a.dweight || a.dbias))
+                norm_samples<<<(a.channels + 31) / 32, kThreads, 0, s>>>(a);
+            return launched();
+        });
+    });
+}
+
 template <typename T, int VEC>
 int run_forward(NormArgs a, hipStream_t s)
 {
     choose_tiles(a, VEC);
     choose_chunks(a);
+    // 200 MB in and out: 117 us with outputs past the caches, 134 through them
+    a.past = 2 * (int64_t)sizeof(T) * a.samples * a.positions * a.channels > kCacheBytes;
     const dim3 grid((uint32_t)((int64_t)a.samples * a.chunks * a.tiles));
     norm_partial_forward<T, VEC><<<grid, kThreads, 0, s>>>(a);
     norm_join_forward<<<dim3(a.groups, a.samples), kThreads, 0, s>>>(a);
@@ -610,7 +856,7 @@ bool valid_sizes(int32_t samples, int64_t positions, int32_t channels, int32_t g
 {
     return samples >= 0 && samples <= LIC_MAX_SAMPLES && positions >= 0 &&
            positions <= (1ll << 40) && channels >= 1 && channels <= LIC_MAX_CHANNELS &&
-           groups >= 1 && channels % groups == 0;
+           groups >= 1 && channels % groups == 0 && (int64_t)samples * groups <= 0x7fffffff;
 }
 
 // A row must not overlap the next one; sample strides of inputs may be anything.
@@ -657,13 +903,14 @@ extern "C" int lic_group_norm_forward(const void *x, int64_t x_sample, int64_t x
     a.samples = samples, a.positions = positions, a.channels = channels, a.groups = groups;
     a.per_group = channels / groups;
     a.part = static_cast<float2 *>(workspace);
+    a.blocks = (uint32_t)samples * (uint32_t)groups;
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        switch (widest<T>(a)) {
-        case 2: return run_forward<T, 2>(a, hstream);
-        case 1: return run_forward<T, 1>(a, hstream);
-        default: return run_forward<T, 16 / sizeof(T)>(a, hstream);
-        }
+        const int vec = widest<T>(a), narrow = resident_vec<T>(a, vec);
+        const int64_t lds = resident_bytes<T>(a, narrow);
+        if (resident_pays<T>(a, lds, narrow))
+            return run_resident_forward<T>(a, narrow, lds, hstream);
+        return with_vec<T>(vec, [&](auto v) { return run_forward<T, v.value>(a, hstream); });
     });
 }
 
@@ -700,12 +947,13 @@ extern "C" int lic_group_norm_backward(const void *dy, int64_t dy_sample, int64_
     a.totals = reinterpret_cast<float2 *>(ws + part_bytes(samples, channels));
     a.slopes = reinterpret_cast<float2 *>(ws + part_bytes(samples, channels) +
                                           totals_bytes(samples, channels));
+    a.blocks = (uint32_t)samples * (uint32_t)groups;
     return with_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        switch (widest<T>(a)) {
-        case 2: return run_backward<T, 2>(a, hstream);
-        case 1: return run_backward<T, 1>(a, hstream);
-        default: return run_backward<T, 16 / sizeof(T)>(a, hstream);
-        }
+        const int vec = widest<T>(a), narrow = resident_vec<T>(a, vec);
+        const int64_t lds = 2 * resident_bytes<T>(a, narrow);
+        if (resident_pays<T>(a, lds, narrow))
+            return run_resident_backward<T>(a, narrow, lds, hstream);
+        return with_vec<T>(vec, [&](auto v) { return run_backward<T, v.value>(a, hstream); });
     });
 }

@@ -106,6 +106,17 @@ def _device_of(t: torch.Tensor, name: str):
     return t.device
 
 
+def _stream(device) -> int:
+    """The current stream's handle (without an object around it, which takes 2 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _dense_like(t: torch.Tensor) -> torch.Tensor:
+    if t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _like(t, dtype, device, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -160,6 +171,9 @@ def _rows(t: torch.Tensor, name: str):
 
 
 def _channels_last_empty(x: torch.Tensor) -> torch.Tensor:
+    if x.dim() == 4 and x.is_contiguous(memory_format=torch.channels_last) and \
+            (x.shape[1] == 1 or x.stride(1) == 1):
+        return torch.empty_like(x)
     n, c, *rest = x.shape
     return torch.empty((n, *rest, c), dtype=x.dtype, device=x.device).movedim(-1, 1)
 
@@ -209,7 +223,7 @@ def group_norm_forward(x: torch.Tensor, num_groups: int, weight=None, bias=None,
     if positions == 0 or n == 0:
         return out, mean.fill_(math.nan), rstd.fill_(math.nan)
     lib = load()
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _stream(device)
     ws = _workspace(device, stream, lib.lic_group_norm_workspace_bytes(n, positions, c, num_groups))
     rc = lib.lic_group_norm_forward(
         x.data_ptr(), xs, xr, n, positions, c, num_groups, DTYPES[x.dtype],
@@ -244,7 +258,7 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, num_groups: int, weig
     if positions == 0 or n == 0:
         return dx, dweight.zero_(), dbias.zero_()
     lib = load()
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _stream(device)
     ws = _workspace(device, stream, lib.lic_group_norm_workspace_bytes(n, positions, c, num_groups))
     rc = lib.lic_group_norm_backward(
         dy.data_ptr(), gs, gr, x.data_ptr(), xs, xr, n, positions, c, num_groups, DTYPES[x.dtype],
@@ -342,7 +356,7 @@ def rotary_table(coords: torch.Tensor, rotary_dim: int, *, base: float = 10000.0
     rows = coords.shape[0]
     cos = torch.empty((rows, rotary_dim // 2), dtype=torch.float32, device=coords.device)
     sin = torch.empty_like(cos)
-    stream = torch.cuda.current_stream(coords.device).cuda_stream
+    stream = _stream(coords.device)
     rc = load().lic_rotary_table(coords.data_ptr(), rows, axes, rotary_dim, base, factor, low, high,
                                  float(original), gain, cos.data_ptr(), sin.data_ptr(), stream)
     if rc:
@@ -391,8 +405,8 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
     if status is not None:
         _like(status, torch.int32, device, "status")
     if out is None:
-        qo = torch.empty((b, s, h, d), dtype=q.dtype, device=device)
-        ko = torch.empty((b, s, kh, d), dtype=q.dtype, device=device) if kh else None
+        qo = _dense_like(q)
+        ko = _dense_like(k) if kh else None
     else:
         qo, ko = out
         for o, t, name in ((qo, q, "q"), (ko, k, "k")):
@@ -411,7 +425,7 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
                         status.data_ptr() if status is not None else 0, batch_step, *qs, *ks, *qos,
                         *kos, b, s, h, kh, d, 2 * cos.shape[1], cos.shape[0], DTYPES[q.dtype],
                         1 if interleaved else 0, 1 if inverse else 0)
-    rc = load().lic_rotary(args, torch.cuda.current_stream(device).cuda_stream)
+    rc = load().lic_rotary(args, _stream(device))
     if rc:
         _check_rc(rc, "lic_rotary")
     return qo, ko
@@ -526,7 +540,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, caus
                                                               key_lengths, scale)
     b, n, h, d = q.shape
     if out is None:
-        out = torch.empty((b, n, h, d), dtype=q.dtype, device=device)
+        out = _dense_like(q)
     else:
         _like(out, q.dtype, device, "out")
         if out.shape != q.shape:
@@ -536,7 +550,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, caus
                            lse.data_ptr(), 0, 0, 0, 0, *ptrs, *qs, *ks, *vs, *_heads(out, "out"),
                            *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *ms, *sizes)
     lib = load()
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _stream(device)
     ws = _workspace(device, stream, lib.lic_attention_workspace_bytes(args, 0))
     rc = lib.lic_attention_forward(args, ws.data_ptr() if ws is not None else None,
                                    ws.numel() if ws is not None else 0, stream)
@@ -564,16 +578,14 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     b, n, h, d = q.shape
     if lse.shape != (b, h, n) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous [batch, heads, queries]")
-    dq = torch.empty((b, n, h, d), dtype=q.dtype, device=device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=device)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=device)
+    dq, dk, dv = _dense_like(q), _dense_like(k), _dense_like(v)
     s = dk.stride()[:3]
     args = _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                            lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                            dv.data_ptr(), *ptrs, *qs, *ks, *vs, *_heads(out, "out"),
                            *_heads(dout, "dout"), *dq.stride()[:3], *s, *s, *ms, *sizes)
     lib = load()
-    stream = torch.cuda.current_stream(device).cuda_stream
+    stream = _stream(device)
     ws = _workspace(device, stream, lib.lic_attention_workspace_bytes(args, 1))
     rc = lib.lic_attention_backward(args, ws.data_ptr() if ws is not None else None,
                                     ws.numel() if ws is not None else 0, stream)
