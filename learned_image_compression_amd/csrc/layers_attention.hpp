@@ -105,6 +105,13 @@ __device__ __forceinline__ void settle()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Two waves share a SIMD.  All but their exponentials goes first: then it is the other's
+// exponentials that fill the gaps, and neither the matrix unit nor the next tile's loads wait
+// for them (8160 x 8160 causal, 16 heads of 128: 300 -> 269 us; 8 heads of 32: 153 -> 125, and
+// 147 where the tile's end gave way too).
+__device__ __forceinline__ void products_first() { __builtin_amdgcn_s_setprio(1); }
+__device__ __forceinline__ void products_over() { __builtin_amdgcn_s_setprio(0); }
+
 // row of an accumulator that a lane's value i is
 __device__ __forceinline__ constexpr int acc_row(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
@@ -606,13 +613,13 @@ inline void allow_lds(K kernel, int bytes)
                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// Splits of the key axis that the rows kernel takes: enough blocks for two a CU, at least
-// 256 keys each, at most 64.
+// Splits of the key axis that the rows kernel takes: two blocks a CU, at least 256 keys
+// each, at most 64.
 inline int row_splits(const lic_attention_args &p)
 {
     const int64_t rows = p.queries * (p.heads / p.kv_heads);
     const int64_t blocks = (rows + 31) / 32 * p.batch * p.kv_heads;
-    int64_t n = (512 + blocks - 1) / blocks;
+    int64_t n = 512 / blocks;
     const int64_t most = (p.keys + 255) / 256;
     n = n < most ? n : most;
     n = n < 64 ? n : 64;
@@ -636,24 +643,33 @@ inline bool few_rows(const lic_attention_args &p)
     return row_tiles * (double)((p.keys + 31) / 32) / 1400.0 + fixed < rounds * (double)((p.keys + 63) / 64);
 }
 
-// Splits of the backward kernels' loops, where their blocks alone would not fill the CUs:
-// over the query tiles of all heads that share a kv head, and over key tiles.
-inline int backward_splits(int64_t blocks, int64_t steps)
+// Splits of the backward kernels' loops, where their blocks alone would not fill the CUs
+// (`at_once` of them run on one): over the query tiles of all heads that share a kv head, and over
+// key tiles.  Windows and causal order make blocks of very different length, which
+// twice as many even out (8160 x 8160 causal, 16 heads of 128 on 4: dk, dv 612 us with 512 blocks,
+// 892 with 256).  A split takes at least four tiles, or two where that gives only a few
+// splits: more would cost more in joining (1000 x 1000, 4 heads of 32, bfloat16: 25 us with 8 splits
+// of 4 tiles, 29 with 16 of 2; 300 x 300: 22 us with 2 of 4, 18 with 4 of 2).
+inline int backward_splits(const lic_attention_args &p, int at_once, int64_t blocks, int64_t steps)
 {
-    int64_t n = blocks > 0 ? 512 / blocks : 1;
-    const int64_t most = steps / 4; // a split takes at least four tiles
+    const bool uneven = p.window_left >= 0 || p.window_right >= 0;
+    int64_t n = blocks > 0 ? 256 * at_once * (uneven ? 2 : 1) / blocks : 1;
+    const int64_t few = steps / 2 < 4 ? steps / 2 : 4;
+    const int64_t most = steps / 4 > few ? steps / 4 : few;
     n = n < most ? n : most;
     n = n < 16 ? n : 16;
     return n < 1 ? 1 : (int)n;
 }
 inline int keys_splits(const lic_attention_args &p)
 {
-    return backward_splits((p.keys + 127) / 128 * p.batch * p.kv_heads,
+    return backward_splits(p, p.dim <= (p.dtype == LIC_F32 ? 32 : 96) ? 2 : 1,
+                           (p.keys + 127) / 128 * p.batch * p.kv_heads,
                            (p.queries + 31) / 32 * (p.heads / p.kv_heads));
 }
 inline int queries_splits(const lic_attention_args &p)
 {
-    return backward_splits((p.queries + 127) / 128 * p.batch * p.heads, (p.keys + 63) / 64);
+    return backward_splits(p, p.dtype != LIC_F32 || p.dim <= 32 ? 2 : 1,
+                           (p.queries + 127) / 128 * p.batch * p.heads, (p.keys + 63) / 64);
 }
 
 inline int tile_dim(int64_t dim, bool vec) { return vec ? (int)((dim + 31) / 32 * 32) : LIC_MAX_HEAD_DIM; }

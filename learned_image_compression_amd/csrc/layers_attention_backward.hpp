@@ -125,7 +125,7 @@ struct KeysBackward {
     static constexpr int kKeys = 4 * TileT::kBytes;          // after two buffers of q and dout: keys, values
     static constexpr int kStats = kKeys + (kWide ? 2 * KeysT::kBytes : 0); // two buffers of lse, D
     static constexpr int kLds = kStats + 2 * 2 * kQueries * 4;
-    static constexpr int kWaves = sizeof(T) == 2 ? 2 : 1;    // of a SIMD
+    static constexpr int kWaves = sizeof(T) == 2 || DT == 32 ? 2 : 1; // of a SIMD
 };
 
 template <typename T, int DT, bool VEC>
@@ -256,6 +256,7 @@ attention_keys_backward(AttnArgs a)
             const float *lse = reinterpret_cast<const float *>(lds + G::kStats) + buf * 2 * NQ + n32;
             const float *delta = lse + NQ;
             float16v s = zero16(), dp = zero16();
+            products_first();
             if constexpr (G::kWide) {
                 // q and keys in turn, then dout and values
                 const auto read = [&](int i) {
@@ -295,6 +296,7 @@ attention_keys_backward(AttnArgs a)
             };
             Pipe<T, 4 * ND, 4> pipe;
             pipe.start(read);
+            products_over();
             uint32_t seen = 0xffffu;
             // lanes beyond the keys are not stored
             const bool part = a.p.mask || !__all(key >= len || range.covers(qn, 32));
@@ -322,6 +324,7 @@ attention_keys_backward(AttnArgs a)
                     dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
                 }
             }
+            products_first();
             const FragV<T> p[2] = {operand<T>(s, 0), operand<T>(s, 1)};
             const FragV<T> ds[2] = {operand<T>(dp, 0), operand<T>(dp, 1)};
             pipe.run(read, [&](int i, const FragV<T> &f) {
@@ -425,7 +428,7 @@ struct QueriesBackward {
 };
 
 template <typename T, int DT, bool VEC>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries_backward(AttnArgs a)
+__global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void attention_queries_backward(AttnArgs a)
 {
     using G = QueriesBackward<T, DT>;
     using TileT = typename G::TileT;
@@ -529,6 +532,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
             if (__all(range.misses(kn, 32)))
                 continue;
             float16v s = zero16(), dp = zero16();
+            products_first();
             {
                 Pipe<T, 2 * KK, 4> pipe;
                 const auto read = [&](int i) {
@@ -548,6 +552,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
             };
             Pipe<T, 2 * ND, ND == 3 ? 3 : 4> pipe;
             pipe.start(read);
+            products_over();
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * fmaf(dp[r], kLower, -delta);
@@ -557,6 +562,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_queries
                 for (int r = 0; r < 16; ++r)
                     dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
             }
+            products_first();
             const FragV<T> ds[2] = {operand<T>(dp, 0), operand<T>(dp, 1)};
             pipe.run(read, [&](int i, const FragV<T> &f) { dq[i % ND] = mma(f, ds[i / ND], dq[i % ND]); });
         }

@@ -196,6 +196,7 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         if (!__all(range.misses(k0, G::kKeys))) {
             const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
             float16v s[2] = {zero16(), zero16()};
+            products_first();
             {
                 Pipe<T, 2 * KK, 4> pipe;
                 const auto read = [&](int i) {
@@ -213,7 +214,9 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
                 for (int n = 0; n < 2; ++n)
                     hide(s[n], a, range, mask, k0 + n * 32, h);
             }
+            products_over();
             soften(s, a.scale_log2, m, l, o);
+            products_first();
             const FragV<T> p[4] = {operand<T>(s[0], 0), operand<T>(s[0], 1), operand<T>(s[1], 0),
                                    operand<T>(s[1], 1)};
             pipe.run(read, [&](int i, const FragV<T> &f) { o[i % ND] = mma(f, p[i / ND], o[i % ND]); });

@@ -23,7 +23,7 @@ import threading
 
 import torch
 
-from .binding import _check_rc
+from .binding import NAME_TO_CODE, _check_rc
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(PKG, "liblic_layers.so")
@@ -120,33 +120,41 @@ def _dense_like(t: torch.Tensor) -> torch.Tensor:
 def _like(t, dtype, device, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is dtype and t.device == device:
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+_NO_WORKSPACE = (None, 0, None)  # address, bytes, owner
+_E_WORKSPACE = NAME_TO_CODE["RANS_E_WORKSPACE"]
 _workspaces: dict = {}
 
 
-def _workspace(device, stream: int, nbytes: int):
-    """(address, bytes) and owner of this stream's scratch memory, grown on demand.
+def _with_workspace(device, stream: int, call, size, where: str):
+    """``call(address, bytes)`` with this stream's scratch memory, grown when it is refused.
 
     Kept per device and stream: calls on one stream never overlap, and a buffer
     that is replaced goes back to the allocator of the stream that still uses
     it.  Under stream capture the memory is the graph's own.
     """
-    if nbytes == 0:
-        return None
     if torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, stream)
-    buf = _workspaces.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        with _lock:
-            _workspaces[key] = buf
-    return buf
+        held = _NO_WORKSPACE
+    else:
+        held = _workspaces.get((device.index, stream), _NO_WORKSPACE)
+    rc = call(held[0], held[1])
+    if rc == _E_WORKSPACE:
+        nbytes = max(size(), 1 << 20)
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        held = (buf.data_ptr(), nbytes, buf)
+        if not torch.cuda.is_current_stream_capturing():
+            with _lock:
+                _workspaces[(device.index, stream)] = held
+        rc = call(held[0], held[1])
+    if rc:
+        _check_rc(rc, where)
 
 
 # ---- group norm --------------------------------------------------------------
@@ -154,9 +162,11 @@ def _workspace(device, stream: int, nbytes: int):
 
 def _rows(t: torch.Tensor, name: str):
     """(sample stride, row stride, positions) of a channels-last [N, C, ...] tensor."""
-    if t.dim() < 2:
-        raise ValueError(f"{name} must be [N, C, ...]")
     shape, strides = t.shape, t.stride()
+    if len(shape) < 2:
+        raise ValueError(f"{name} must be [N, C, ...]")
+    if len(shape) == 4 and strides[1] == 1 and strides[2] == strides[3] * shape[3] and shape[3] > 1:
+        return strides[0], strides[3], shape[2] * shape[3]
     if shape[1] > 1 and strides[1] != 1:
         raise ValueError(f"{name} must be channels last (its channels next to each other)")
     positions, row = 1, None
@@ -224,15 +234,13 @@ def group_norm_forward(x: torch.Tensor, num_groups: int, weight=None, bias=None,
         return out, mean.fill_(math.nan), rstd.fill_(math.nan)
     lib = load()
     stream = _stream(device)
-    ws = _workspace(device, stream, lib.lic_group_norm_workspace_bytes(n, positions, c, num_groups))
-    rc = lib.lic_group_norm_forward(
-        x.data_ptr(), xs, xr, n, positions, c, num_groups, DTYPES[x.dtype],
-        weight.data_ptr() if weight is not None else None,
-        bias.data_ptr() if bias is not None else None, DTYPES[kind], eps, ACTIVATIONS[activation],
-        out.data_ptr(), ys, yr, mean.data_ptr(), rstd.data_ptr(),
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, stream)
-    if rc:
-        _check_rc(rc, "lic_group_norm_forward")
+    args = (x.data_ptr(), xs, xr, n, positions, c, num_groups, DTYPES[x.dtype],
+            weight.data_ptr() if weight is not None else None,
+            bias.data_ptr() if bias is not None else None, DTYPES[kind], eps,
+            ACTIVATIONS[activation], out.data_ptr(), ys, yr, mean.data_ptr(), rstd.data_ptr())
+    _with_workspace(device, stream, lambda p, size: lib.lic_group_norm_forward(*args, p, size, stream),
+                    lambda: lib.lic_group_norm_workspace_bytes(n, positions, c, num_groups),
+                    "lic_group_norm_forward")
     return out, mean, rstd
 
 
@@ -259,16 +267,14 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, num_groups: int, weig
         return dx, dweight.zero_(), dbias.zero_()
     lib = load()
     stream = _stream(device)
-    ws = _workspace(device, stream, lib.lic_group_norm_workspace_bytes(n, positions, c, num_groups))
-    rc = lib.lic_group_norm_backward(
-        dy.data_ptr(), gs, gr, x.data_ptr(), xs, xr, n, positions, c, num_groups, DTYPES[x.dtype],
-        weight.data_ptr() if weight is not None else None,
-        bias.data_ptr() if bias is not None else None, DTYPES[kind], ACTIVATIONS[activation],
-        mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), ds, dr, dweight.data_ptr(),
-        dbias.data_ptr(), ws.data_ptr() if ws is not None else None,
-        ws.numel() if ws is not None else 0, stream)
-    if rc:
-        _check_rc(rc, "lic_group_norm_backward")
+    args = (dy.data_ptr(), gs, gr, x.data_ptr(), xs, xr, n, positions, c, num_groups,
+            DTYPES[x.dtype], weight.data_ptr() if weight is not None else None,
+            bias.data_ptr() if bias is not None else None, DTYPES[kind], ACTIVATIONS[activation],
+            mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), ds, dr, dweight.data_ptr(),
+            dbias.data_ptr())
+    _with_workspace(device, stream, lambda p, size: lib.lic_group_norm_backward(*args, p, size, stream),
+                    lambda: lib.lic_group_norm_workspace_bytes(n, positions, c, num_groups),
+                    "lic_group_norm_backward")
     return dx, dweight, dbias
 
 
@@ -369,12 +375,12 @@ _ROTARY = struct.Struct("=8Qq12q7q3q")
 
 def _heads(t: torch.Tensor, name: str):
     """Strides (batch, row, head) of a [B, S, heads, dim] tensor."""
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [batch, rows, heads, dim]")
     s = t.stride()
-    if t.shape[3] > 1 and s[3] != 1:
+    if len(s) != 4:
+        raise ValueError(f"{name} must be [batch, rows, heads, dim]")
+    if s[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}: a head's values must be next to each other")
-    return s[0], s[1], s[2]
+    return s[:3]
 
 
 def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
@@ -388,11 +394,12 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
         kh = k.shape[2]
         if k.shape[0] != b or k.shape[1] != s or k.shape[3] != d:
             raise ValueError("q and k differ in batch, rows or dim")
-    for t, name in ((cos, "cos"), (sin, "sin")):
-        _like(t, torch.float32, device, name)
-        if t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
-            raise ValueError("cos and sin must be contiguous [rows, rotary_dim / 2]")
-    if cos.shape[1] < 1 or 2 * cos.shape[1] > d:
+    _like(cos, torch.float32, device, "cos")
+    _like(sin, torch.float32, device, "sin")
+    if cos.shape != sin.shape or cos.dim() != 2 or not (cos.is_contiguous() and sin.is_contiguous()):
+        raise ValueError("cos and sin must be contiguous [rows, rotary_dim / 2]")
+    rows, pairs = cos.shape
+    if pairs < 1 or 2 * pairs > d:
         raise ValueError("the tables have more pairs than a head")
     batch_step = 0
     if positions is not None:
@@ -400,7 +407,7 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
         if not positions.is_contiguous() or tuple(positions.shape) not in ((s,), (b, s)):
             raise ValueError("positions must be contiguous [rows] or [batch, rows]")
         batch_step = s if positions.dim() == 2 else 0
-    elif cos.shape[0] < s:
+    elif rows < s:
         raise ValueError("the tables have fewer rows than there are positions")
     if status is not None:
         _like(status, torch.int32, device, "status")
@@ -423,7 +430,7 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
                         ko.data_ptr() if kh else 0, cos.data_ptr(), sin.data_ptr(),
                         positions.data_ptr() if positions is not None else 0,
                         status.data_ptr() if status is not None else 0, batch_step, *qs, *ks, *qos,
-                        *kos, b, s, h, kh, d, 2 * cos.shape[1], cos.shape[0], DTYPES[q.dtype],
+                        *kos, b, s, h, kh, d, 2 * pairs, rows, DTYPES[q.dtype],
                         1 if interleaved else 0, 1 if inverse else 0)
     rc = load().lic_rotary(args, _stream(device))
     if rc:
@@ -551,11 +558,8 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, caus
                            *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *ms, *sizes)
     lib = load()
     stream = _stream(device)
-    ws = _workspace(device, stream, lib.lic_attention_workspace_bytes(args, 0))
-    rc = lib.lic_attention_forward(args, ws.data_ptr() if ws is not None else None,
-                                   ws.numel() if ws is not None else 0, stream)
-    if rc:
-        _check_rc(rc, "lic_attention_forward")
+    _with_workspace(device, stream, lambda p, size: lib.lic_attention_forward(args, p, size, stream),
+                    lambda: lib.lic_attention_workspace_bytes(args, 0), "lic_attention_forward")
     return out, lse
 
 
@@ -586,11 +590,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                            *_heads(dout, "dout"), *dq.stride()[:3], *s, *s, *ms, *sizes)
     lib = load()
     stream = _stream(device)
-    ws = _workspace(device, stream, lib.lic_attention_workspace_bytes(args, 1))
-    rc = lib.lic_attention_backward(args, ws.data_ptr() if ws is not None else None,
-                                    ws.numel() if ws is not None else 0, stream)
-    if rc:
-        _check_rc(rc, "lic_attention_backward")
+    _with_workspace(device, stream, lambda p, size: lib.lic_attention_backward(args, p, size, stream),
+                    lambda: lib.lic_attention_workspace_bytes(args, 1), "lic_attention_backward")
     return dq, dk, dv
 
 
