@@ -495,48 +495,43 @@ __device__ __forceinline__ const uint8_t *mask_row(const AttnArgs &a, int b, int
            (int64_t)query * a.p.mask_stride[2];
 }
 
-// Which of an accumulator's 16 pairs are visible, a bit each.  x0 + its row is what range
-// limits, of `extent` in all; mask: the entry of 0 there, `step` to the next.  All bytes are asked
-// for before the first is looked at; a pair outside the range reads one inside instead.  Where
-// they lie next to each other, four at a time (37 -> 15 us for 32 x 6 heads of 256 x 256).
-__device__ __forceinline__ uint32_t visible(const Range &range, const uint8_t *mask, int64_t step, int extent, int x0,
-                                            int h)
+// f(i, whether the mask shows it) for an accumulator's 16 pairs, at x0 + its row of `extent` in
+// all.  mask: the entry of 0, `step` bytes to the next.  All entries are asked for before the first
+// is looked at; four at a time where they lie next to each other.  One past the extent, which the
+// range hides, reads the last instead.  (32 x 6 heads of 256 x 256, forward: 37 us with single bytes.)
+template <typename F>
+__device__ __forceinline__ void each_shown(const uint8_t *mask, int64_t step, int extent, int x0, int h, F &&f)
 {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        bits |= (uint32_t)range.holds(x0 + acc_row(i, h)) << i;
-    if (!mask || !bits)
-        return bits;
-    uint32_t set = 0;
+    const int x = x0 + 4 * h;
     if (step == 1 && extent >= 4) {
         uint32_t word[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int x = x0 + acc_row(4 * i, h), at = min(x, extent - 4);
-            __builtin_memcpy(&word[i], mask + at, 4);
-        }
+        for (int i = 0; i < 4; ++i)
+            __builtin_memcpy(&word[i], mask + min(x + 8 * i, extent - 4), 4);
+        if (x0 + 32 > extent) { // a word at the end began before its pairs: what it has of them comes down
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int x = x0 + acc_row(4 * i, h);
-            // a word at the row's end began before x: what it has of x on comes down
-            const uint32_t w = word[i] >> (8 * min(x - min(x, extent - 4), 3));
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                set |= (uint32_t)((w & (0xffu << (8 * e))) != 0u) << (4 * i + e);
-        }
-    } else {
-        uint8_t byte[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int x = x0 + acc_row(i, h);
-            byte[i] = mask[(range.holds(x) ? x : range.first) * step];
+            for (int i = 0; i < 4; ++i)
+                word[i] >>= 8 * min(max(x + 8 * i - (extent - 4), 0), 3);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            set |= (uint32_t)(byte[i] != 0) << i;
+            f(i, (word[i >> 2] & (0xffu << (8 * (i & 3)))) != 0u);
+        return;
     }
-    return bits & set;
+    uint8_t byte[16];
+    if (x0 + 32 <= extent) {
+        const uint8_t *p = mask + x * step;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            byte[i] = p[acc_row(i, 0) * step];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            byte[i] = mask[min(x + acc_row(i, 0), extent - 1) * step];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        f(i, byte[i] != 0);
 }
 
 template <typename T>
@@ -604,6 +599,8 @@ struct Attention {
     static int forward(AttnArgs a, hipStream_t s);
     static int backward(AttnArgs a, hipStream_t s);
 };
+
+constexpr int kTwoBlocks = 64 * 1024; // of LDS: two blocks fit a CU's 160 KiB, three do not
 
 // A kernel of more than 64 KiB of LDS says so once.
 template <typename K>

@@ -297,14 +297,8 @@ attention_keys_backward(AttnArgs a)
             Pipe<T, 4 * ND, 4> pipe;
             pipe.start(read);
             products_over();
-            uint32_t seen = 0xffffu;
             // lanes beyond the keys are not stored
-            const bool part = a.p.mask || !__all(key >= len || range.covers(qn, 32));
-            if (part) {
-                const uint8_t *mask =
-                    a.p.mask ? mask_row(a, b, q_head, 0) + min(key, (int)a.p.keys - 1) * a.p.mask_stride[3] : nullptr;
-                seen = visible(range, mask, a.p.mask_stride[2], (int)a.p.queries, qn, h);
-            }
+            const bool inside = __all(key >= len || range.covers(qn, 32));
 #pragma unroll
             for (int i4 = 0; i4 < 16; i4 += 4) {
                 const float4 ls = *reinterpret_cast<const float4 *>(lse + acc_row(i4, h));
@@ -317,12 +311,17 @@ attention_keys_backward(AttnArgs a)
                     dp[r] = s[r] * fmaf(dp[r], kLower, -d4[e]);
                 }
             }
-            if (part) {
+            const auto show = [&](int r, bool shown) {
+                s[r] = shown ? s[r] : 0.0f;
+                dp[r] = shown ? dp[r] : 0.0f;
+            };
+            if (a.p.mask)
+                each_shown(mask_row(a, b, q_head, 0) + min(key, (int)a.p.keys - 1) * a.p.mask_stride[3],
+                           a.p.mask_stride[2], (int)a.p.queries, qn, h, show);
+            if (!inside) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    s[r] = (seen >> r) & 1 ? s[r] : 0.0f;
-                    dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
-                }
+                for (int r = 0; r < 16; ++r)
+                    show(r, range.holds(qn + acc_row(r, h)));
             }
             products_first();
             const FragV<T> p[2] = {operand<T>(s, 0), operand<T>(s, 1)};
@@ -556,11 +555,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * fmaf(dp[r], kLower, -delta);
-            if (mask || !__all(!there || range.covers(kn, 32))) {
-                const uint32_t seen = visible(range, mask, a.p.mask_stride[3], (int)a.p.keys, kn, h);
+            if (mask)
+                each_shown(mask, a.p.mask_stride[3], (int)a.p.keys, kn, h,
+                           [&](int r, bool shown) { dp[r] = shown ? dp[r] : 0.0f; });
+            if (!__all(!there || range.covers(kn, 32))) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    dp[r] = (seen >> r) & 1 ? dp[r] : 0.0f;
+                    dp[r] = range.holds(kn + acc_row(r, h)) ? dp[r] : 0.0f;
             }
             products_first();
             const FragV<T> ds[2] = {operand<T>(dp, 0), operand<T>(dp, 1)};
@@ -661,6 +662,8 @@ int run_backward(AttnArgs a, hipStream_t s)
 {
     const lic_attention_args &p = a.p;
     float *parts = a.part;
+    // two blocks a CU where blocks differ much in length, as in the forward call
+    const bool uneven = p.window_left >= 0 || p.window_right >= 0;
     JoinArgs j{};
     j.dim = (int)p.dim;
     const auto joined = [&](const float *part, void *out, const int64_t *stride, int64_t step, int64_t rows,
@@ -670,7 +673,8 @@ int run_backward(AttnArgs a, hipStream_t s)
     };
     if (p.queries > 0) {
         using G = QueriesBackward<T, DT>;
-        static const bool once = (allow_lds(attention_queries_backward<T, DT, VEC>, G::kLds), true);
+        constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
+        static const bool once = (allow_lds(attention_queries_backward<T, DT, VEC>, kMost), true);
         (void)once;
         a.splits = queries_splits(p);
         const int64_t lines = p.batch * p.heads * p.queries;
@@ -679,7 +683,7 @@ int run_backward(AttnArgs a, hipStream_t s)
             return RANS_E_ARG;
         a.blocks = (uint32_t)blocks;
         a.part = parts;
-        attention_queries_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
+        attention_queries_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, uneven ? kMost : G::kLds, s>>>(a);
         if (a.splits > 1) {
             joined(parts, p.dq, p.dq_stride, lines * DT, p.queries, p.heads, a.splits);
             parts += a.splits * lines * DT;
@@ -687,7 +691,8 @@ int run_backward(AttnArgs a, hipStream_t s)
     }
     if (p.keys > 0) {
         using G = KeysBackward<T, DT>;
-        static const bool once = (allow_lds(attention_keys_backward<T, DT, VEC>, G::kLds), true);
+        constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
+        static const bool once = (allow_lds(attention_keys_backward<T, DT, VEC>, kMost), true);
         (void)once;
         a.splits = keys_splits(p);
         const int64_t blocks = (p.keys + 127) / 128 * p.batch * p.kv_heads * a.splits;
@@ -695,7 +700,7 @@ int run_backward(AttnArgs a, hipStream_t s)
             return RANS_E_ARG;
         a.blocks = (uint32_t)blocks;
         a.part = parts;
-        attention_keys_backward<T, DT, VEC><<<xcd_grid(a.blocks), G::kThreads, G::kLds, s>>>(a);
+        attention_keys_backward<T, DT, VEC><<<xcd_grid(a.blocks), G::kThreads, uneven ? kMost : G::kLds, s>>>(a);
         if (a.splits > 1) {
             const int64_t all = p.batch * p.kv_heads * p.keys * DT;
             joined(parts, p.dk, p.dk_stride, 2 * all, p.keys, p.kv_heads, a.splits);

@@ -14,14 +14,19 @@ namespace {
 
 constexpr float kSlack = 8.0f; // in powers of two
 
-// Scores of one accumulator (keys along its rows) that a query does not see become -inf.
-__device__ __forceinline__ void hide(float16v &s, const AttnArgs &a, const Range &range, const uint8_t *mask,
-                                     int key0, int h)
+// Scores of one accumulator (keys along its rows) that a query does not see become -inf.  inside: all
+// of them are within the query's range.
+__device__ __forceinline__ void hide(float16v &s, const AttnArgs &a, const Range &range, bool inside,
+                                     const uint8_t *mask, int key0, int h)
 {
-    const uint32_t seen = visible(range, mask, a.p.mask_stride[3], (int)a.p.keys, key0, h);
+    if (mask)
+        each_shown(mask, a.p.mask_stride[3], (int)a.p.keys, key0, h,
+                   [&](int i, bool shown) { s[i] = shown ? s[i] : -INFINITY; });
+    if (!inside) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
+        for (int i = 0; i < 16; ++i)
+            s[i] = range.holds(key0 + acc_row(i, h)) ? s[i] : -INFINITY;
+    }
 }
 
 // The running softmax of a lane's query over N accumulators of scores, which become
@@ -209,10 +214,11 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
             const auto read = [&](int i) { return TileT::col_frag(vl, i / ND * 16, i % ND, lane); };
             Pipe<T, 4 * ND, 4> pipe;
             pipe.start(read);
-            if (mask || !__all(query >= a.p.queries || range.covers(k0, G::kKeys))) {
+            const bool inside = __all(query >= a.p.queries || range.covers(k0, G::kKeys));
+            if (mask || !inside) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
-                    hide(s[n], a, range, mask, k0 + n * 32, h);
+                    hide(s[n], a, range, inside, mask, k0 + n * 32, h);
             }
             products_over();
             soften(s, a.scale_log2, m, l, o);
@@ -377,8 +383,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
         settle<T>();
         // the tile may pass the split's end: those keys are the next split's
         const bool whole = k0 + 32 <= end;
-        if (mask || !whole || !__all(row >= rows || range.covers((int)k0, 32))) {
-            hide(s[0], a, range, mask, (int)k0, h);
+        const bool inside = __all(row >= rows || range.covers((int)k0, 32));
+        if (mask || !whole || !inside) {
+            hide(s[0], a, range, inside, mask, (int)k0, h);
             if (!whole) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -580,13 +587,18 @@ int run_forward(AttnArgs a, hipStream_t s)
         return launched();
     }
     using G = TilesForward<T, DT, VEC>;
-    static const bool once = (allow_lds(attention_tiles_forward<T, DT, VEC>, G::kLds), true);
+    static const bool once = (allow_lds(attention_tiles_forward<T, DT, VEC>, G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks), true);
     (void)once;
     const int64_t blocks = (a.p.queries + 127) / 128 * a.p.batch * a.p.heads;
     if (blocks > 0x7fffff00)
         return RANS_E_ARG;
     a.blocks = (uint32_t)blocks;
-    attention_tiles_forward<T, DT, VEC><<<xcd_grid(a.blocks), 256, G::kLds, s>>>(a);
+    // Where windows or causal order make blocks of very different length, more LDS than they need
+    // keeps a third block off a CU: more blocks are then left to fill the gaps that the short ones
+    // leave (8160 x 8160 causal, 16 heads of 32 on 4: 131 us with two at a time, 152 with three).
+    const bool uneven = a.p.window_left >= 0 || a.p.window_right >= 0;
+    const int lds = uneven && G::kLds < kTwoBlocks ? kTwoBlocks : G::kLds;
+    attention_tiles_forward<T, DT, VEC><<<xcd_grid(a.blocks), 256, lds, s>>>(a);
     return launched();
 }
 
