@@ -463,6 +463,45 @@ def test_attention_long_cache_offsets(L):
         attention_passes(L, (q, k, v, dout), {"causal": True}, BF16)
 
 
+@pytest.mark.parametrize("n", [1, 130])
+def test_attention_rows_far_apart(L, n):
+    """Rows so far apart that a tile's byte offsets pass 2^31 (32-bit heads, 64 rows of 2^26 bytes)."""
+    g = gen(13)
+    s, step = 65, (1 << 24) - 8
+    rows = torch.empty(s * step, device="cuda").view(1, s, 1, step)
+    k, v = rows[..., :32], rows[..., 32:64]
+    k.copy_(normal(g, 1, s, 1, 32))
+    v.copy_(normal(g, 1, s, 1, 32))
+    q, dout = normal(g, 1, n, 6, 32), normal(g, 1, n, 6, 32)
+    attention_passes(L, (q, k, v, dout), {}, F32)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("d", [96, 128])
+def test_attention_wide_heads_keep_masked_values_out(L, d, dtype):
+    """As above for the tiles of wide heads, with ragged keys whose unused rows hold NaN."""
+    t, options = attention_case(24, 140, 200, 4, 1, d, {"lengths": "ragged", "causal": True}, dtype)
+    q, k, v, dout = t
+    clean = [x.clone() for x in t]
+    for b in range(24):
+        n = int(options["key_lengths"][b])
+        k[b, n:], v[b, n:] = math.nan, math.inf
+        if n:  # the last key in use is seen by the last query alone
+            v[b, n - 1] = math.nan
+            clean[2][b, n - 1] = 0.0
+    r = R.attention(*clean, **options)
+    out, lse = L.attention_forward(q, k, v, **options)
+    u, e = R.UNIT[dtype], R.F32 + r["slack"]
+    passes(out[:, :-1], r["out"][:, :-1], (2 * u + e) * r["out_abs"][:, :-1], "out")
+    dq, dk, dv = L.attention_backward(dout, q, k, v, out, lse, **options)
+    least = R.STEP[dtype]
+    passes(dq[:, :-1], r["dq"][:, :-1], (3 * u + 2 * e) * r["dq_abs"][:, :-1] + least * (1 + r["dq_ones"][:, :-1]),
+           "dq")
+    # the last query sees every key in use and takes its NaN to all of them; the others get nothing
+    unused = torch.arange(200, device="cuda")[None] >= options["key_lengths"][:, None]
+    assert bool((dk[unused] == 0).all()) and bool((dv[unused] == 0).all())
+
+
 def test_attention_autograd_and_differences(L):
     g = gen(12)
     q, k, v = (normal(g, 2, 30, h, 16).requires_grad_() for h in (4, 2, 2))
