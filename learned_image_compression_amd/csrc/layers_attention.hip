@@ -42,9 +42,7 @@ uint64_t part_bytes(const lic_attention_args &p, bool backward)
     const uint64_t q_lines = (uint64_t)p.batch * p.heads * p.queries;
     const uint64_t k_lines = (uint64_t)p.batch * p.kv_heads * p.keys;
     if (!backward) {
-        if (!few_rows(p))
-            return 0;
-        const int n = row_splits(p);
+        const int n = forward_plan(p).splits;
         return n > 1 ? n * q_lines * (LIC_MAX_HEAD_DIM + 2) * 4 : 0;
     }
     const int nk = keys_splits(p), nq = queries_splits(p);

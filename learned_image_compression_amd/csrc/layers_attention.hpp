@@ -20,6 +20,7 @@
 // 32-bit tiles use eight 32x32x2 products where 16-bit ones use one 32x32x16.
 #pragma once
 
+#include <algorithm>
 #include <cmath>
 
 #include "layers_common.hpp"
@@ -623,21 +624,50 @@ inline int row_splits(const lic_attention_args &p)
     return n < 1 ? 1 : (int)n;
 }
 
-// Which forward kernel: the one of few queries (32 rows of all heads that share keys a block, the
-// key axis split over waves and blocks) or the one of many (128 queries of one head a block).
-// Both costs in units of what the second takes for 64 keys (about 1 us in 16 bits, 2.6 to 8.6
-// in 32): its blocks run 512 at once, two a CU; the first gets through 1400 tiles of 32 x 32
-// in that time and pays for joining, more where splits are joined by a second launch.
-// Measured (us, few / many), bfloat16, dim 64: 8160 x 8160, 1 head 51 / 123; 1000 x 1000, 8
-// heads 17 / 20; 510 x 510, 24 heads 22 / 13; 70 x 70, 128 heads 7.0 / 6.5; 40 x 500, 128 heads
-// 15.6 / 11.9; 8 x 1000, 256 heads on 32 11 / 19.
-inline bool few_rows(const lic_attention_args &p)
+// Which forward kernel: the one of few queries (32 rows of all heads that share keys a block) or the
+// one of many (128 queries of one head a block), and into how many splits of the key axis.  The
+// estimate, in us, fitted to measured calls of 1 to 1024 blocks: the first gets through 1000 tiles of
+// 32 x 32 in `row`; a CU of the second takes `unit` for a block's 64 keys, `pair` times that for two
+// blocks'; parts of a join are written and read from the caches at 8 TB/s.
+// Measured (us, few / many / many with splits), bfloat16, dim 64: 8160 x 8160, 1 head 41 / 127 / 38 of 8;
+// 1000 x 1000, 8 heads 15 / 20 / 16 of 4; 510 x 510, 24 heads 10 / 13 / 16 of 2; 8160 x 8160, 6 heads
+// - / 169 / 143 of 4; the same causal, 4 heads - / 122 / 65 of 4; 2048 x 2048, 64 heads - / 93 / 113 of 2.
+struct ForwardPlan {
+    bool few;
+    int splits;
+};
+
+inline ForwardPlan forward_plan(const lic_attention_args &p)
 {
-    const int64_t shared = p.batch * p.kv_heads;
-    const double row_tiles = (double)((p.queries * (p.heads / p.kv_heads) + 31) / 32 * shared);
-    const double rounds = (double)(((p.queries + 127) / 128 * p.batch * p.heads + 511) / 512);
-    const double fixed = (row_splits(p) > 1 ? 5.0 : 1.0) * (p.dtype == LIC_F32 ? 0.4 : 1.0);
-    return row_tiles * (double)((p.keys + 31) / 32) / 1400.0 + fixed < rounds * (double)((p.keys + 63) / 64);
+    const double nd = (double)((p.dim + 31) / 32), queries = (double)p.queries, keys = (double)p.keys;
+    const bool f32 = p.dtype == LIC_F32, left = p.window_left >= 0, right = p.window_right >= 0;
+    const double row = f32 ? 0.15 + 1.3 * nd : 0.3 + 0.044 * nd * nd;
+    const double unit = f32 ? 0.4 + 2.1 * nd : 0.65 + 0.15 * nd;
+    const double pair = f32 ? 1.95 : 1.1 + 0.17 * nd;
+    // keys that a row sees at most, and the part of them that a row sees on average
+    const double most = left && right ? std::min(keys, (double)(p.window_left + p.window_right) + 128.0) : keys;
+    const double part = left == right ? 1.0 : queries < keys ? 1.0 - 0.5 * queries / keys : 0.5 * keys / queries;
+
+    const int64_t row_tiles = (p.queries * (p.heads / p.kv_heads) + 31) / 32 * p.batch * p.kv_heads;
+    const int row_split = row_splits(p);
+    const double few = (double)row_tiles * most / 32000.0 * row * (part < 1.0 ? 0.85 : 1.0) + 5.3 +
+                       (f32 ? 2.0 : 0.55) * nd * nd * std::min(1.0, (double)(row_tiles * row_split) / 512.0) + (row_split > 1 ? 4.0 : 0.0);
+
+    const int64_t blocks = (p.queries + 127) / 128 * p.batch * p.heads, tiles = (int64_t)most / 64 + 1;
+    int best = 1;
+    double many = 0.0;
+    for (int n = 1; n <= 16 && (n == 1 || (blocks * n <= 2048 && tiles >= 4 * n)); n *= 2) {
+        const double share = (double)((tiles + n - 1) / n) * unit;
+        const double each = (double)(blocks * n) / 256.0; // blocks of a CU
+        const int64_t whole = (blocks * n + 255) / 256;
+        const double even = (double)(whole / 2) * pair + (double)(whole % 2);
+        const double uneven = std::max(each > 1.0 ? 0.5 + 0.5 * pair : 1.0, each * part * pair / 2.0);
+        const double join = n == 1 ? 0.0 : 6.0 + 1e-6 * n * (double)(p.batch * p.heads) * queries * 32.0 * nd;
+        const double cost = (4.0 + share * (part < 1.0 ? uneven : even) + join) * (n == 1 ? 0.93 : 1.0);
+        if (n == 1 || cost < many)
+            best = n, many = cost;
+    }
+    return few < many ? ForwardPlan{true, row_split} : ForwardPlan{false, best};
 }
 
 // Splits of the backward kernels' loops, where their blocks alone would not fill the CUs
@@ -668,7 +698,5 @@ inline int queries_splits(const lic_attention_args &p)
     return backward_splits(p, p.dtype != LIC_F32 || p.dim <= 32 ? 2 : 1,
                            (p.queries + 127) / 128 * p.batch * p.heads, (p.keys + 63) / 64);
 }
-
-inline int tile_dim(int64_t dim, bool vec) { return vec ? (int)((dim + 31) / 32 * 32) : LIC_MAX_HEAD_DIM; }
 
 }  // namespace lic

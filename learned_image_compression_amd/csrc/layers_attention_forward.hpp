@@ -116,11 +116,29 @@ __device__ __forceinline__ float log_sum(float m, float l)
     return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+// Where a split leaves its part of a row: sums [split][line][DT], then top and total [split][line].
+template <int DT>
+struct Part {
+    float *sums;
+    float2 *stat;
+
+    __device__ __forceinline__ Part(const AttnArgs &a, int split, int64_t line)
+    {
+        const int64_t lines = a.p.batch * a.p.heads * a.p.queries, at = split * lines + line;
+        sums = a.part + at * DT;
+        stat = reinterpret_cast<float2 *>(a.part + a.splits * lines * DT) + at;
+    }
+};
+
 // ---- many queries ----------------------------------------------------------
 //
 // A block of four waves holds 128 queries of one head, 32 a wave, in registers; keys
 // and values pass through LDS in tiles of 64, two buffers, so one barrier a tile.
-// A key tile serves four waves and costs each 1 LDS byte per 2 dim flops.
+// A key tile serves four waves and costs each 1 LDS byte per 2 dim flops.  Where that makes few or
+// unequal blocks the key axis is split and attention_rows_join adds the parts.  What bounds it: the
+// exponentials with heads of 32 (8160 x 8160, 8 heads, bfloat16: 125 us, 4.3e12 a second), with wider
+// ones the products and what the exponentials leave exposed of them (heads of 64: 168 us, 0.81 PFLOP/s;
+// of 128: 258 us, 1.06 PFLOP/s); in 32 bits the products (8 x 8 heads of 64, 2048 x 2048: 540 us, 127 TFLOP/s).
 template <typename T, int DT, bool VEC>
 struct TilesForward {
     static constexpr int kKeys = 64;
@@ -141,7 +159,7 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
     if (block >= a.blocks)
         return;
     const uint32_t q_blocks = (uint32_t)((a.p.queries + 127) / 128);
-    const uint32_t bh = block / q_blocks;
+    const uint32_t rest = block / q_blocks, bh = rest / (uint32_t)a.splits;
     const int head = (int)(bh % (uint32_t)a.p.heads), b = (int)(bh / (uint32_t)a.p.heads);
     const int kv = head / a.group;
     // the last queries see the most keys: they start first
@@ -169,6 +187,11 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
     int lo, hi;
     key_range(a, len, q0, min(q0 + 128, (int)a.p.queries), lo, hi);
     lo &= ~(G::kKeys - 1);
+    if (a.splits > 1) { // an even share of the tiles
+        const int share = ((hi - lo + G::kKeys - 1) / G::kKeys + a.splits - 1) / a.splits * G::kKeys;
+        lo += share * (int)(rest % (uint32_t)a.splits);
+        hi = min(hi, lo + share);
+    }
     const T *kbase = head_row<T>(a.p.k, a.p.k_stride, b, 0, kv);
     const T *vbase = head_row<T>(a.p.v, a.p.v_stride, b, 0, kv);
     const int64_t ks = a.p.k_stride[1], vs = a.p.v_stride[1];
@@ -242,18 +265,39 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
             bad |= not_finite(o[n][i]);
     uint64_t redo = rows_of(bad && query < a.p.queries);
     if (query < a.p.queries && !((redo >> (lane & 31)) & 1)) {
-        T *out = head_row<T>(a.p.out, a.p.out_stride, b, query, head);
+        const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
+        if (a.splits == 1) {
+            T *out = head_row<T>(a.p.out, a.p.out_stride, b, query, head);
 #pragma unroll
-        for (int n = 0; n < ND; ++n)
-            put_column<T, VEC>(out, o[n], inv, n, h, dim);
-        if (h == 0)
-            a.p.lse[((int64_t)b * a.p.heads + head) * a.p.queries + query] = log_sum(m, total);
+            for (int n = 0; n < ND; ++n)
+                put_column<T, VEC>(out, o[n], inv, n, h, dim);
+            if (h == 0)
+                a.p.lse[line] = log_sum(m, total);
+        } else {
+            const Part<DT> part(a, (int)(rest % (uint32_t)a.splits), line);
+#pragma unroll
+            for (int n = 0; n < ND; ++n)
+                put_column<float, true>(part.sums, o[n], 1.0f, n, h, DT);
+            if (h == 0)
+                *part.stat = make_float2(m, total);
+        }
     }
     for (; redo; redo &= redo - 1) {
         const AttnArgs &a = rare_args();
         const int qi = q0 + wave * 32 + __builtin_ctzll(redo);
         float cm, cl, co[2];
         careful_row<T>(a, b, head, qi, len, lo, hi, cm, cl, co);
+        const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + qi;
+        if (a.splits > 1) {
+            const Part<DT> part(a, (int)(rest % (uint32_t)a.splits), line);
+            if (lane < DT)
+                part.sums[lane] = co[0];
+            if (lane + 64 < DT)
+                part.sums[lane + 64] = co[1];
+            if (lane == 0)
+                *part.stat = make_float2(cm, cl);
+            continue;
+        }
         const float ci = cl == 0.0f ? 0.0f : 1.0f / cl;
         T *out = head_row<T>(a.p.out, a.p.out_stride, b, qi, head);
         if (lane < dim)
@@ -261,7 +305,7 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         if (lane + 64 < dim)
             out[lane + 64] = down<T>(co[1] * ci);
         if (lane == 0)
-            a.p.lse[((int64_t)b * a.p.heads + head) * a.p.queries + qi] = log_sum(cm, cl);
+            a.p.lse[line] = log_sum(cm, cl);
     }
 }
 
@@ -273,7 +317,8 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
 // which take tiles of 32 keys in turn, each in its own LDS and with no barrier: the next
 // tile is asked for before this one is waited for.  Memory bounds it: with a single row 31 of
 // 32 columns of the products are idle, and the matrix units still need less time than the
-// keys' way from HBM.  The waves' parts are joined in LDS, the blocks' by attention_rows_join.
+// keys' way from HBM (16 x 1 query of 16 heads of 64 on 4, up to 8160 keys, bfloat16: 24.5 us and 4 us for the join,
+// 4.6 TB/s of what is in use).  The waves' parts are joined in LDS, the blocks' by attention_rows_join.
 template <typename T, int DT, bool VEC>
 struct RowsForward {
     static constexpr int kKeys = 32;
@@ -467,7 +512,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
     }
     __syncthreads();
     const float *all = reinterpret_cast<const float *>(lds);
-    const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
     for (int e = t; e < 8 * DT; e += 256) { // 32 rows of DT / 4
         const int j = e / (DT / 4), d = e % (DT / 4) * 4, r = row_tile * 32 + j;
         if (r >= rows)
@@ -502,66 +546,87 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
             if (d == 0)
                 a.p.lse[line] = log_sum(top, total);
         } else {
-            // sums [split][line][DT], then top and total [split][line]
-            *reinterpret_cast<float4 *>(a.part + (split * lines + line) * DT + d) = sum;
+            const Part<DT> part(a, split, line);
+            *reinterpret_cast<float4 *>(part.sums + d) = sum;
             if (d == 0)
-                reinterpret_cast<float2 *>(a.part + a.splits * lines * DT)[split * lines + line] =
-                    make_float2(top, total);
+                *part.stat = make_float2(top, total);
         }
     }
 }
 
-// The splits' parts of each row joined, a wave a row: lane s weighs split s, then all splits'
-// sums are read at once.
-template <typename T, int DT>
-__global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a)
+// The splits' parts of each row joined: four columns of a row a thread, eight splits' parts asked for
+// at once; more than eight are shared out over `groups` neighbouring threads (a power of two), whose
+// sums are then joined the same way.
+template <int DT>
+constexpr int kJoinColumns = DT == 96 ? 32 : DT / 4; // threads of a row, of one group
+
+template <typename T, int DT, bool VEC>
+__global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a, int groups)
 {
-    const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
-    const int64_t line = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (line >= lines)
+    constexpr int COLS = kJoinColumns<DT>;
+    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / COLS, line = id / groups;
+    if (line >= a.p.batch * a.p.heads * a.p.queries) // all threads of a row, or none
         return;
-    const int lane = threadIdx.x & 63;
-    const float *part = a.part + line * DT;
-    const int64_t step = lines * DT;
-    float2 stat = make_float2(-INFINITY, 0.0f);
-    if (lane < a.splits)
-        stat = reinterpret_cast<const float2 *>(a.part + a.splits * step)[lane * lines + line];
-    float top = stat.x;
-    for (int x = 32; x > 0; x >>= 1)
-        top = fmaxf(top, __shfl_xor(top, x));
-    // a split that saw nothing has sums of 0 and no weight
-    const float weight = stat.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(stat.x - top);
-    float total = weight * stat.y;
-    for (int x = 32; x > 0; x >>= 1)
-        total += __shfl_xor(total, x);
-    float sum[2] = {0.0f, 0.0f};
-    const int d0 = min(lane, DT - 1), d1 = min(lane + 64, DT - 1);
-    for (int s0 = 0; s0 < a.splits; s0 += 8) {
-        float v[2][8];
+    const int d = (int)(threadIdx.x % COLS) * 4, at = DT == 96 ? min(d, DT - 4) : d;
+    float top = -INFINITY, total = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = (int)(id % groups) * 8; s0 < a.splits; s0 += 8 * groups) {
+        float2 stat[8];
+        float4 v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const float *p = part + min(s0 + u, a.splits - 1) * step;
-            v[0][u] = p[d0];
-            v[1][u] = DT > 64 ? p[d1] : 0.0f;
+            const Part<DT> part(a, min(s0 + u, a.splits - 1), line);
+            stat[u] = *part.stat;
+            v[u] = *reinterpret_cast<const float4 *>(part.sums + at);
         }
+        const float before = top;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            top = fmaxf(top, stat[u].x);
+        // a split that saw nothing has sums of 0 and no weight (a NaN has one)
+        const float keep = total == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(before - top);
+        total *= keep;
+        sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            // lanes past the splits have no weight
-            const float f = __shfl(weight, min(s0 + u, 63));
-            sum[0] = fmaf(f, s0 + u < a.splits ? v[0][u] : 0.0f, sum[0]);
-            sum[1] = fmaf(f, s0 + u < a.splits ? v[1][u] : 0.0f, sum[1]);
+            const bool is = s0 + u < a.splits && stat[u].y != 0.0f;
+            const float f = is ? __builtin_amdgcn_exp2f(stat[u].x - top) : 0.0f;
+            if (is) {
+                total += f * stat[u].y;
+                sum.x += f * v[u].x, sum.y += f * v[u].y, sum.z += f * v[u].z, sum.w += f * v[u].w;
+            }
         }
     }
+    for (int x = COLS; x < COLS * groups; x <<= 1) {
+        const float theirs = __shfl_xor(top, x), both = fmaxf(top, theirs);
+        const float their_total = __shfl_xor(total, x);
+        const float f = total == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(top - both);
+        const float g = their_total == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(theirs - both);
+        top = both;
+        total = f * total + g * their_total;
+        sum.x = f * sum.x + g * __shfl_xor(sum.x, x), sum.y = f * sum.y + g * __shfl_xor(sum.y, x);
+        sum.z = f * sum.z + g * __shfl_xor(sum.z, x), sum.w = f * sum.w + g * __shfl_xor(sum.w, x);
+    }
+    if (id % groups != 0 || d >= DT)
+        return;
     const int query = (int)(line % a.p.queries);
     const int64_t bh = line / a.p.queries;
-    const int head = (int)(bh % a.p.heads), b = (int)(bh / a.p.heads);
-    T *out = head_row<T>(a.p.out, a.p.out_stride, b, query, head);
+    const int head = (int)(bh % a.p.heads), b = (int)(bh / a.p.heads), dim = (int)a.p.dim;
+    T *out = head_row<T>(a.p.out, a.p.out_stride, b, query, head) + d;
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    if (lane < a.p.dim)
-        out[lane] = down<T>(sum[0] * inv);
-    if (lane + 64 < a.p.dim)
-        out[lane + 64] = down<T>(sum[1] * inv);
-    if (lane == 0)
+    Vec<T, 4> w;
+    w.v[0] = down<T>(sum.x * inv), w.v[1] = down<T>(sum.y * inv);
+    w.v[2] = down<T>(sum.z * inv), w.v[3] = down<T>(sum.w * inv);
+    if constexpr (VEC) {
+        if (d < dim)
+            *reinterpret_cast<Vec<T, 4> *>(out) = w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < dim)
+                out[e] = w.v[e];
+    }
+    if (d == 0)
         a.p.lse[line] = log_sum(top, total);
 }
 
@@ -570,26 +635,34 @@ __global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a)
 template <typename T, int DT, bool VEC>
 int run_forward(AttnArgs a, hipStream_t s)
 {
-    if (few_rows(a.p)) {
+    const ForwardPlan plan = forward_plan(a.p);
+    a.splits = plan.splits;
+    const auto join = [&] {
+        if (a.splits > 1) {
+            const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
+            int groups = 1;
+            while (8 * groups < a.splits && 2 * groups * kJoinColumns<DT> <= 64)
+                groups *= 2;
+            const int64_t threads = lines * groups * kJoinColumns<DT>;
+            attention_rows_join<T, DT, VEC><<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(a, groups);
+        }
+    };
+    if (plan.few) {
         using G = RowsForward<T, DT, VEC>;
         static const bool once = (allow_lds(attention_rows_forward<T, DT, VEC>, G::kLds), true);
         (void)once;
-        a.splits = row_splits(a.p);
         const int64_t rows = a.p.queries * a.group;
         const int64_t blocks = (rows + 31) / 32 * a.p.batch * a.p.kv_heads * a.splits;
         if (blocks > 0x7fffffff)
             return RANS_E_ARG;
         attention_rows_forward<T, DT, VEC><<<(uint32_t)blocks, 256, G::kLds, s>>>(a);
-        if (a.splits > 1) {
-            const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
-            attention_rows_join<T, DT><<<(uint32_t)((lines + 3) / 4), 256, 0, s>>>(a);
-        }
+        join();
         return launched();
     }
     using G = TilesForward<T, DT, VEC>;
     static const bool once = (allow_lds(attention_tiles_forward<T, DT, VEC>, G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks), true);
     (void)once;
-    const int64_t blocks = (a.p.queries + 127) / 128 * a.p.batch * a.p.heads;
+    const int64_t blocks = (a.p.queries + 127) / 128 * a.p.batch * a.p.heads * a.splits;
     if (blocks > 0x7fffff00)
         return RANS_E_ARG;
     a.blocks = (uint32_t)blocks;
@@ -599,6 +672,7 @@ int run_forward(AttnArgs a, hipStream_t s)
     const bool uneven = a.p.window_left >= 0 || a.p.window_right >= 0;
     const int lds = uneven && G::kLds < kTwoBlocks ? kTwoBlocks : G::kLds;
     attention_tiles_forward<T, DT, VEC><<<xcd_grid(a.blocks), 256, lds, s>>>(a);
+    join();
     return launched();
 }
 

@@ -502,6 +502,58 @@ def test_attention_wide_heads_keep_masked_values_out(L, d, dtype):
     assert bool((dk[unused] == 0).all()) and bool((dv[unused] == 0).all())
 
 
+# Many queries in few blocks: the tiles' kernel with its keys in splits
+SPLITS = [
+    (1, 2080, 2080, 1, 1, 128, {}),
+    (1, 1030, 1030, 4, 2, 128, {"causal": True}),
+    (1, 2080, 2080, 4, 2, 40, {"causal": True}),         # split in 32 bits
+    (1, 2080, 2080, 1, 1, 120, {"lengths": [900]}),      # splits without keys
+    (2, 1030, 1030, 2, 1, 128, {"lengths": [1030, 0]}),
+    (1, 1030, 2080, 2, 1, 104, {"window": (700, None)}),
+    (1, 1500, 1500, 2, 2, 128, {"window": (400, 500)}),
+    (1, 1030, 1500, 2, 2, 128, {"mask": "slices"}),
+    (1, 2080, 1030, 2, 2, 112, {"causal": True}),        # more queries than keys
+    (1, 2080, 2080, 1, 1, 125, {"mask": "keys"}),        # no 16-byte rows
+]
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("case", range(len(SPLITS)))
+def test_attention_split_tiles(L, case, dtype):
+    b, q, s, h, kv, d, options = SPLITS[case]
+    print(SPLITS[case], dtype, flush=True)
+    t, options = attention_case(b, q, s, h, kv, d, options, dtype)
+    attention_passes(L, t, options, dtype)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("n,h,kv,d", [(1030, 4, 2, 128), (2080, 1, 1, 128)])
+def test_attention_split_tiles_keep_masked_values_out(L, n, h, kv, d, dtype):
+    """NaN and infinities that one query sees, or none, in the first and the last split."""
+    t, options = attention_case(1, n, n, h, kv, d, {}, dtype)
+    q, k, v, dout = t
+    mask = torch.ones(n, n, dtype=torch.bool, device="cuda")
+    mask[:, [5, 6, 7, n - 9, n - 2]] = False
+    mask[n // 3, 7] = True       # one query sees this one
+    mask[n // 2] = False         # sees nothing
+    mask[n // 2 + 1] = False     # sees one key of a middle split
+    mask[n // 2 + 1, n // 2] = True
+    options["mask"] = mask
+    clean = [x.clone() for x in t]
+    k[:, 5], v[:, 6], v[:, 7] = math.nan, math.inf, math.nan
+    k[:, n - 9, :, 3], v[:, n - 2] = -math.inf, math.nan
+    for x, y in zip(clean[1:3], t[1:3]):
+        x[~torch.isfinite(y)] = 0.0
+    r = R.attention(*clean, **options)
+    out, lse = L.attention_forward(q, k, v, **options)
+    u, e = R.UNIT[dtype], R.F32 + r["slack"]
+    hit = torch.arange(n, device="cuda") == n // 3
+    assert bool(torch.isnan(out[:, hit]).all())
+    passes(out[:, ~hit], r["out"][:, ~hit], (2 * u + e) * r["out_abs"][:, ~hit], "out")
+    passes(lse, r["lse"], R.F32 * (1 + torch.nan_to_num(r["lse"], neginf=0.0).abs()) + r["slack"], "lse")
+    assert bool((out[:, n // 2] == 0).all()) and bool((lse[:, :, n // 2] == -math.inf).all())
+
+
 def test_attention_autograd_and_differences(L):
     g = gen(12)
     q, k, v = (normal(g, 2, 30, h, 16).requires_grad_() for h in (4, 2, 2))
