@@ -34,7 +34,10 @@ bool valid_call(const lic_attention_args &p, bool backward)
 
 uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-uint64_t row_bytes(const lic_attention_args &p) { return round256((uint64_t)p.batch * p.heads * p.queries * 2 * sizeof(float)); }
+uint64_t row_bytes(const lic_attention_args &p)
+{
+    return round256((uint64_t)p.batch * p.heads * p.queries * 2 * sizeof(float));
+}
 
 // Parts of split sums are as wide as the widest tile the call may take.
 uint64_t part_bytes(const lic_attention_args &p, bool backward)

@@ -302,8 +302,9 @@ __device__ __forceinline__ void loads_done_but()
 // LDS by itself: no register is held while they are under way, and store() only waits.  A
 // wave's 64 pieces land next to each other, so the permutation is in which piece a lane
 // asks for.  The load is written out: for the builtin the compiler waits at the next transposed
-// read, which cannot be of the same buffer.  store() waits instead, before the barrier.  Rows past the last repeat it (their scores are hidden); pieces past the head's
-// size are never written, and clear() made them 0.
+// read, which cannot be of the same buffer.  store() waits instead, before the barrier.  Rows past
+// the last repeat it (their scores are hidden); pieces past the head's size are never written, and
+// clear() made them 0.
 // Without VEC values pass through registers one by one, rows and columns past the end as 0.
 template <typename T, int ROWS, int DT, int THREADS, bool VEC>
 struct Stage {
@@ -628,7 +629,8 @@ inline int row_splits(const lic_attention_args &p)
 // one of many (128 queries of one head a block), and into how many splits of the key axis.  The
 // estimate, in us, fitted to measured calls of 1 to 1024 blocks: the first gets through 1000 tiles of
 // 32 x 32 in `row`; a CU of the second takes `unit` for a block's 64 keys, `pair` times that for two
-// blocks'; parts of a join are written and read from the caches at 8 TB/s.
+// blocks'; parts of a join are written and read from the caches at 8 TB/s.  It is within 12% of the
+// best choice for nearly all of 165 calls and sizes measured, and splits are taken where they gain 7%.
 // Measured (us, few / many / many with splits), bfloat16, dim 64: 8160 x 8160, 1 head 41 / 127 / 38 of 8;
 // 1000 x 1000, 8 heads 15 / 20 / 16 of 4; 510 x 510, 24 heads 10 / 13 / 16 of 2; 8160 x 8160, 6 heads
 // - / 169 / 143 of 4; the same causal, 4 heads - / 122 / 65 of 4; 2048 x 2048, 64 heads - / 93 / 113 of 2.
@@ -650,8 +652,9 @@ inline ForwardPlan forward_plan(const lic_attention_args &p)
 
     const int64_t row_tiles = (p.queries * (p.heads / p.kv_heads) + 31) / 32 * p.batch * p.kv_heads;
     const int row_split = row_splits(p);
+    const double turns = std::min(1.0, (double)(row_tiles * row_split) / 512.0); // wide heads: a block a CU
     const double few = (double)row_tiles * most / 32000.0 * row * (part < 1.0 ? 0.85 : 1.0) + 5.3 +
-                       (f32 ? 2.0 : 0.55) * nd * nd * std::min(1.0, (double)(row_tiles * row_split) / 512.0) + (row_split > 1 ? 4.0 : 0.0);
+                       (f32 ? 2.0 : 0.55) * nd * nd * turns + (row_split > 1 ? 4.0 : 0.0);
 
     const int64_t blocks = (p.queries + 127) / 128 * p.batch * p.heads, tiles = (int64_t)most / 64 + 1;
     int best = 1;

@@ -11,7 +11,9 @@
 // if one kernel's waves added into another's rows.
 //
 // Rounding: p and ds pass to their second product in the inputs' type, like any
-// operand; sums, D and the scores stay in 32 bits.  p is rounded as 2^10 p, which costs
+// operand; sums, D and the scores stay in 32 bits.  For bfloat16 that is 0.0017 of dq and dk in
+// the mean, as much as rounding the results themselves (0.0026 together; two operands a product
+// would buy it back at twice the products).  p is rounded as 2^10 p, which costs
 // nothing (the power goes into lse, its inverse into D and the last scaling): among
 // thousands of keys most p lie below float16's normal numbers.
 #pragma once
@@ -115,6 +117,10 @@ __device__ void careful_dkv(const AttnArgs &a, int b, int head, int key, int len
 // a SIMD, and one wave cannot overlap its exponentials with its products.  There keys and
 // values stay in LDS, half as many reads again, and eight waves work on a block: the upper
 // four take the second half of each query tile and their sums are added at the end.
+//
+// Products bound it with wide heads: 8160 x 8160 causal, 16 heads of 128 on 4, bfloat16 590 to 625 us,
+// 0.87 to 0.93 PFLOP/s of the four products (a large library product: 1.13).  32 x 6 heads of 32, 256 x 256,
+// float16 with a mask 18 us: four tiles a block, so loads, the mask and the start of each block.
 template <typename T, int DT>
 struct KeysBackward {
     static constexpr bool kWide = sizeof(T) == 2 && DT == 128;
@@ -419,6 +425,7 @@ attention_keys_backward(AttnArgs a)
 //
 // It runs first.  As the forward kernel of many queries: 128 queries of one head in a block, keys and
 // values through LDS in tiles of 64 taken as two halves, scores with keys along the rows.
+// The sizes of the keys' kernel: 415 to 435 us, 0.94 to 0.99 PFLOP/s of the three products; 17 us.
 template <typename T, int DT>
 struct QueriesBackward {
     static constexpr int kKeys = 64;

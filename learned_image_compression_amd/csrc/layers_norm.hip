@@ -227,6 +227,13 @@ __device__ float2 block_sum(float2 v)
 }
 
 // ---- three launches ------------------------------------------------------
+//
+// Measured, 192 channels of 544 x 960, bfloat16, silu: sums 56 us (3.6 TB/s read), join 6, outputs
+// 76 (5.3 TB/s read and written).  16 x 192 x 64 x 64, backward: sums 18 us (2.8 TB/s), join 4.5,
+// outputs 19 (4.0 TB/s); at 50 MB a launch's start and end are a third of it.  8 x 320 x 128 x 128,
+// float16, gelu: sums 27, outputs 40, backward 48 and 49 us; without the activation the backward call
+// takes 74 us instead of 95, so there arithmetic is a part of what bounds it.
+// Eight vectors in flight, or twice or four times the blocks, were no faster.
 
 // Forward: a channel's mean and squares about it over one chunk.
 template <typename T, int VEC>
@@ -305,6 +312,7 @@ __global__ __launch_bounds__(kThreads) void norm_join_forward(NormArgs a)
     }
 }
 
+// The outputs, last chunk first.
 template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_output_forward(NormArgs a)
 {
@@ -462,6 +470,7 @@ __device__ void sum_over_samples(const NormArgs &a, int block)
     }
 }
 
+// dx; the launch's last blocks sum dweight and dbias beside it.
 template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_output_backward(NormArgs a)
 {
@@ -500,7 +509,8 @@ __global__ __launch_bounds__(kThreads) void norm_output_backward(NormArgs a)
 //
 // A block keeps one group of one sample in LDS, each thread its own vectors (of channels of
 // the one group) of every rows_at_once-th row.  The blocks of a sample's groups run on one XCD: they
-// share its cache lines where a group's channels do not fill one.
+// share its cache lines where a group's channels do not fill one.  A block's latencies bound it (load,
+// two sums over the block, store): 1 x 192 x 17 x 30, 32 groups, float 5.3 us, where an empty launch takes 3.7.
 
 struct Resident {
     int n, g, lane_row, rows_at_once, c0, slots;
