@@ -497,29 +497,67 @@ __device__ __forceinline__ const uint8_t *mask_row(const AttnArgs &a, int b, int
            (int64_t)query * a.p.mask_stride[2];
 }
 
-// f(i, whether the mask shows it) for an accumulator's 16 pairs, at x0 + its row of `extent` in
-// all.  mask: the entry of 0, `step` bytes to the next.  All entries are asked for before the first
-// is looked at; four at a time where they lie next to each other.  One past the extent, which the
-// range hides, reads the last instead.  (32 x 6 heads of 256 x 256, forward: 37 us with single bytes.)
-template <typename F>
-__device__ __forceinline__ void each_shown(const uint8_t *mask, int64_t step, int extent, int x0, int h, F &&f)
-{
-    const int x = x0 + 4 * h;
-    if (step == 1 && extent >= 4) {
-        uint32_t word[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_memcpy(&word[i], mask + min(x + 8 * i, extent - 4), 4);
-        if (x0 + 32 > extent) { // a word at the end began before its pairs: what it has of them comes down
+// The mask's entries of an accumulator's 16 pairs, at x0 + its row of `extent` >= 4 in all, where they
+// lie next to each other.  Of each 32 a lane reads one half at once and gives its partner 32 lanes away the
+// words that are the partner's: reading its own four words costs four times as many accesses to
+// scattered lines.  The last entries are read word by word; one past the extent, which the range
+// hides, reads one before it instead.
+struct MaskWords {
+    uint32_t word[4];
+
+    __device__ __forceinline__ void ask(const uint8_t *mask, int extent, int x0, int h)
+    {
+        if (x0 + 32 <= extent) {
+            __builtin_memcpy(word, mask + x0 + 16 * h, 16);
+        } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                word[i] >>= 8 * min(max(x + 8 * i - (extent - 4), 0), 3);
+                __builtin_memcpy(&word[i], mask + min(x0 + 4 * h + 8 * i, extent - 4), 4);
+        }
+    }
+    // f(i, whether the mask shows it); the words are spent
+    template <typename F>
+    __device__ __forceinline__ void each_shown(int extent, int x0, int h, F &&f)
+    {
+        if (x0 + 32 <= extent) {
+            // words 0 .. 3 of the lower lane, 4 .. 7 of the upper: 0 2 4 6 and 1 3 5 7
+            const auto a = __builtin_amdgcn_permlane32_swap(word[0], word[1], false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(word[2], word[3], false, false);
+            word[0] = a[0], word[1] = b[0], word[2] = a[1], word[3] = b[1];
+        } else { // a word at the end began before its pairs: what it has of them comes down
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                word[i] >>= 8 * min(max(x0 + 4 * h + 8 * i - (extent - 4), 0), 3);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             f(i, (word[i >> 2] & (0xffu << (8 * (i & 3)))) != 0u);
+    }
+};
+__host__ __device__ __forceinline__ bool mask_in_words(int64_t step, int64_t extent)
+{
+    return step == 1 && extent >= 4;
+}
+
+// How the kernels that hold queries take a mask: there is none; in words, asked for a tile ahead; where
+// they need it.  Each has its own instance, since registers bound them.  (Forward, us, here / ahead,
+// float16: 4 x 8 heads of 32, 1000 x 1000 32 / 27; 8 x 8 of 64, 2048 x 2048 176 / 155; 2 x 8 of 96, 2040 x 2040 83 / 67;
+// 2 x 3 of 64, 4080 x 4080 68 / 80, since only two blocks fit a CU; without a mask 8 x 8 of 64 take 93.)
+enum class Masked { none, ahead, here };
+
+// f(i, whether the mask shows it) for an accumulator's 16 pairs, at x0 + its row of `extent` in
+// all.  mask: the entry of 0, `step` bytes to the next.  All entries are asked for before the first
+// is looked at.  (32 x 6 heads of 256 x 256, forward: 37 us with single bytes.)
+template <typename F>
+__device__ __forceinline__ void each_shown(const uint8_t *mask, int64_t step, int extent, int x0, int h, F &&f)
+{
+    if (mask_in_words(step, extent)) {
+        MaskWords words;
+        words.ask(mask, extent, x0, h);
+        words.each_shown(extent, x0, h, f);
         return;
     }
+    const int x = x0 + 4 * h;
     uint8_t byte[16];
     if (x0 + 32 <= extent) {
         const uint8_t *p = mask + x * step;
@@ -610,6 +648,24 @@ inline void allow_lds(K kernel, int bytes)
 {
     (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// ROOM: whether the 8 registers that words ahead take are there without spills.
+template <bool ROOM, typename F>
+void with_mask(const lic_attention_args &p, F &&f)
+{
+    using std::integral_constant;
+    if (!p.mask) {
+        f(integral_constant<Masked, Masked::none>{});
+        return;
+    }
+    if constexpr (ROOM) {
+        if (mask_in_words(p.mask_stride[3], p.keys)) {
+            f(integral_constant<Masked, Masked::ahead>{});
+            return;
+        }
+    }
+    f(integral_constant<Masked, Masked::here>{});
 }
 
 // Splits of the key axis that the rows kernel takes: two blocks a CU, at least 256 keys

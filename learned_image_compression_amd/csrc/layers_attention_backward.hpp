@@ -433,7 +433,7 @@ struct QueriesBackward {
     static constexpr int kLds = 4 * TileT::kBytes;
 };
 
-template <typename T, int DT, bool VEC>
+template <typename T, int DT, bool VEC, Masked MASK>
 __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void attention_queries_backward(AttnArgs a)
 {
     using G = QueriesBackward<T, DT>;
@@ -457,7 +457,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
     const bool there = query < a.p.queries;
     const int dim = (int)a.p.dim, len = key_length(a, b);
     const Range range = keys_of(a, len, query);
-    const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
+    const uint8_t *mask = nullptr;
+    if constexpr (MASK != Masked::none)
+        mask = mask_row(a, b, head, min(query, (int)a.p.queries - 1));
     const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
 
     FragV<T> qf[KK], gf[KK];
@@ -520,8 +522,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
         kst.store(lds + buf * TileT::kBytes, t);
         vst.store(lds + (2 + buf) * TileT::kBytes, t);
     };
+    MaskWords words[2];
+    const auto ask = [&](int n, int k) {
+        if constexpr (MASK == Masked::ahead)
+            words[n].ask(mask, (int)a.p.keys, k + n * 32, h);
+    };
     if (lo < hi) {
         fetch(0, len - lo);
+        ask(0, lo);
+        ask(1, lo);
         store(0);
     }
     loads_done();
@@ -535,8 +544,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const int kn = k0 + n * 32;
-            if (__all(range.misses(kn, 32)))
+            if (__all(range.misses(kn, 32))) {
+                ask(n, k0 + G::kKeys);
                 continue;
+            }
             float16v s = zero16(), dp = zero16();
             products_first();
             {
@@ -562,9 +573,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 dp[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse)) * fmaf(dp[r], kLower, -delta);
-            if (mask)
-                each_shown(mask, a.p.mask_stride[3], (int)a.p.keys, kn, h,
-                           [&](int r, bool shown) { dp[r] = shown ? dp[r] : 0.0f; });
+            const auto show = [&](int r, bool shown) { dp[r] = shown ? dp[r] : 0.0f; };
+            if constexpr (MASK == Masked::ahead) {
+                words[n].each_shown((int)a.p.keys, kn, h, show);
+                ask(n, k0 + G::kKeys);
+            } else if constexpr (MASK == Masked::here) {
+                each_shown(mask, a.p.mask_stride[3], (int)a.p.keys, kn, h, show);
+            }
             if (!__all(!there || range.covers(kn, 32))) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
@@ -576,6 +591,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
         }
         if (more)
             store(buf ^ 1);
+        if (MASK == Masked::ahead)
+            loads_done();
     }
 
     settle<T>();
@@ -680,9 +697,6 @@ int run_backward(AttnArgs a, hipStream_t s)
     };
     if (p.queries > 0) {
         using G = QueriesBackward<T, DT>;
-        constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
-        static const bool once = (allow_lds(attention_queries_backward<T, DT, VEC>, kMost), true);
-        (void)once;
         a.splits = queries_splits(p);
         const int64_t lines = p.batch * p.heads * p.queries;
         const int64_t blocks = (p.queries + 127) / 128 * p.batch * p.heads * a.splits;
@@ -690,7 +704,13 @@ int run_backward(AttnArgs a, hipStream_t s)
             return RANS_E_ARG;
         a.blocks = (uint32_t)blocks;
         a.part = parts;
-        attention_queries_backward<T, DT, VEC><<<xcd_grid(a.blocks), 256, uneven ? kMost : G::kLds, s>>>(a);
+        with_mask<VEC && (sizeof(T) == 4 || DT <= 96)>(p, [&](auto masked) {
+            constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
+            constexpr auto kernel = attention_queries_backward<T, DT, VEC, decltype(masked)::value>;
+            static const bool once = (allow_lds(kernel, kMost), true);
+            (void)once;
+            kernel<<<xcd_grid(a.blocks), 256, uneven ? kMost : G::kLds, s>>>(a);
+        });
         if (a.splits > 1) {
             joined(parts, p.dq, p.dq_stride, lines * DT, p.queries, p.heads, a.splits);
             parts += a.splits * lines * DT;

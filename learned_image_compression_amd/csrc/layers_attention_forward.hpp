@@ -15,13 +15,16 @@ namespace {
 constexpr float kSlack = 8.0f; // in powers of two
 
 // Scores of one accumulator (keys along its rows) that a query does not see become -inf.  inside: all
-// of them are within the query's range.
+// of them are within the query's range.  words: the mask's, where they were asked for before.
+template <Masked MASK>
 __device__ __forceinline__ void hide(float16v &s, const AttnArgs &a, const Range &range, bool inside,
-                                     const uint8_t *mask, int key0, int h)
+                                     const uint8_t *mask, MaskWords &words, int key0, int h)
 {
-    if (mask)
-        each_shown(mask, a.p.mask_stride[3], (int)a.p.keys, key0, h,
-                   [&](int i, bool shown) { s[i] = shown ? s[i] : -INFINITY; });
+    const auto show = [&](int i, bool shown) { s[i] = shown ? s[i] : -INFINITY; };
+    if constexpr (MASK == Masked::ahead)
+        words.each_shown((int)a.p.keys, key0, h, show);
+    else if constexpr (MASK == Masked::here)
+        each_shown(mask, a.p.mask_stride[3], (int)a.p.keys, key0, h, show);
     if (!inside) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -147,7 +150,7 @@ struct TilesForward {
     static constexpr int kLds = 4 * TileT::kBytes;
 };
 
-template <typename T, int DT, bool VEC>
+template <typename T, int DT, bool VEC, Masked MASK>
 __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void attention_tiles_forward(AttnArgs a)
 {
     using G = TilesForward<T, DT, VEC>;
@@ -169,7 +172,9 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
     const int query = q0 + wave * 32 + (lane & 31);
     const int dim = (int)a.p.dim, len = key_length(a, b);
     const Range range = keys_of(a, len, query);
-    const uint8_t *mask = a.p.mask ? mask_row(a, b, head, min(query, (int)a.p.queries - 1)) : nullptr;
+    const uint8_t *mask = nullptr;
+    if constexpr (MASK != Masked::none)
+        mask = mask_row(a, b, head, min(query, (int)a.p.queries - 1));
 
     FragV<T> qf[KK];
     {
@@ -210,8 +215,16 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         kst.store(lds + buf * TileT::kBytes, t);
         vst.store(lds + (2 + buf) * TileT::kBytes, t);
     };
+    MaskWords words[2];
+    const auto ask = [&](int k) {
+        if constexpr (MASK == Masked::ahead) {
+            words[0].ask(mask, (int)a.p.keys, k, h);
+            words[1].ask(mask, (int)a.p.keys, k + 32, h);
+        }
+    };
     if (lo < hi) {
         fetch(0, len - lo);
+        ask(lo);
         store(0);
     }
     loads_done();
@@ -221,7 +234,9 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         const bool more = k0 + G::kKeys < hi;
         if (more)
             fetch(buf ^ 1, len - k0 - G::kKeys);
-        if (!__all(range.misses(k0, G::kKeys))) {
+        if (__all(range.misses(k0, G::kKeys))) {
+            ask(k0 + G::kKeys);
+        } else {
             const uint8_t *kl = lds + buf * TileT::kBytes, *vl = lds + (2 + buf) * TileT::kBytes;
             float16v s[2] = {zero16(), zero16()};
             products_first();
@@ -238,11 +253,12 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
             Pipe<T, 4 * ND, 4> pipe;
             pipe.start(read);
             const bool inside = __all(query >= a.p.queries || range.covers(k0, G::kKeys));
-            if (mask || !inside) {
+            if (MASK != Masked::none || !inside) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
-                    hide(s[n], a, range, inside, mask, k0 + n * 32, h);
+                    hide<MASK>(s[n], a, range, inside, mask, words[n], k0 + n * 32, h);
             }
+            ask(k0 + G::kKeys);
             products_over();
             soften(s, a.scale_log2, m, l, o);
             products_first();
@@ -252,6 +268,8 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         }
         if (more)
             store(buf ^ 1);
+        if (MASK == Masked::ahead)
+            loads_done();
     }
 
     settle<T>();
@@ -430,7 +448,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
         const bool whole = k0 + 32 <= end;
         const bool inside = __all(row >= rows || range.covers((int)k0, 32));
         if (mask || !whole || !inside) {
-            hide(s[0], a, range, inside, mask, (int)k0, h);
+            MaskWords words;
+            if (mask)
+                hide<Masked::here>(s[0], a, range, inside, mask, words, (int)k0, h);
+            else
+                hide<Masked::none>(s[0], a, range, inside, mask, words, (int)k0, h);
             if (!whole) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -661,9 +683,6 @@ int run_forward(AttnArgs a, hipStream_t s)
         return launched();
     }
     using G = TilesForward<T, DT, VEC>;
-    constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
-    static const bool once = (allow_lds(attention_tiles_forward<T, DT, VEC>, kMost), true);
-    (void)once;
     const int64_t blocks = (a.p.queries + 127) / 128 * a.p.batch * a.p.heads * a.splits;
     if (blocks > 0x7fffff00)
         return RANS_E_ARG;
@@ -673,7 +692,12 @@ int run_forward(AttnArgs a, hipStream_t s)
     // leave (8160 x 8160 causal, 16 heads of 32 on 4: 131 us with two at a time, 152 with three).
     const bool uneven = a.p.window_left >= 0 || a.p.window_right >= 0;
     const int lds = uneven && G::kLds < kTwoBlocks ? kTwoBlocks : G::kLds;
-    attention_tiles_forward<T, DT, VEC><<<xcd_grid(a.blocks), 256, lds, s>>>(a);
+    with_mask<VEC && (sizeof(T) == 2 ? DT <= 96 : DT != 64)>(a.p, [&](auto masked) {
+        constexpr auto kernel = attention_tiles_forward<T, DT, VEC, decltype(masked)::value>;
+        static const bool once = (allow_lds(kernel, G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks), true);
+        (void)once;
+        kernel<<<xcd_grid(a.blocks), 256, lds, s>>>(a);
+    });
     join();
     return launched();
 }

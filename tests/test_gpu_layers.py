@@ -554,6 +554,28 @@ def test_attention_split_tiles_keep_masked_values_out(L, n, h, kv, d, dtype):
     assert bool((out[:, n // 2] == 0).all()) and bool((lse[:, :, n // 2] == -math.inf).all())
 
 
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("layout", ["dense", "odd rows", "keys first", "one row", "few keys"])
+def test_attention_mask_layouts(L, layout, d, dtype):
+    """Masks read in words ahead of their tiles, at the last keys, and entry by entry."""
+    s = 3 if layout == "few keys" else 197
+    t, options = attention_case(24, 140, s, 4, 4, d, {}, dtype)
+    g = gen(31)
+    if layout == "odd rows":
+        mask = torch.rand(24, 1, 140, s + 6, generator=g, device="cuda")[..., 5:5 + s] < 0.6
+        mask = torch.nn.functional.pad(mask, (5, 1))[..., 5:5 + s]
+    elif layout == "keys first":
+        mask = (torch.rand(4, s, 140, generator=g, device="cuda") < 0.6).transpose(1, 2)
+    elif layout == "one row":
+        mask = torch.rand(24, 1, 1, s, generator=g, device="cuda") < 0.6
+    else:
+        mask = torch.rand(140, s, generator=g, device="cuda") < 0.6
+        mask[77] = False
+    options["mask"] = mask
+    attention_passes(L, t, options, dtype)
+
+
 def test_attention_autograd_and_differences(L):
     g = gen(12)
     q, k, v = (normal(g, 2, 30, h, 16).requires_grad_() for h in (4, 2, 2))
