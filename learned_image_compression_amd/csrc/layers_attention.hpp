@@ -729,33 +729,58 @@ inline ForwardPlan forward_plan(const lic_attention_args &p)
     return few < many ? ForwardPlan{true, row_split} : ForwardPlan{false, best};
 }
 
-// Splits of the backward kernels' loops, where their blocks alone would not fill the CUs
-// (`at_once` of them run on one): over the query tiles of all heads that share a kv head, and over
-// key tiles.  Windows and causal order make blocks of very different length, which
-// twice as many even out (8160 x 8160 causal, 16 heads of 128 on 4: dk, dv 612 us with 512 blocks,
-// 892 with 256).  A split takes at least four tiles, or two where that gives only a few
-// splits: more would cost more in joining (1000 x 1000, 4 heads of 32, bfloat16: 25 us with 8 splits
-// of 4 tiles, 29 with 16 of 2; 300 x 300: 22 us with 2 of 4, 18 with 4 of 2).
-inline int backward_splits(const lic_attention_args &p, int at_once, int64_t blocks, int64_t steps)
+// Splits of the backward kernels' loops (over the query tiles of all heads that share a kv head, and over
+// key tiles), by the same kind of estimate: blocks, a block's steps, the time of a step, `at_once` blocks
+// on a CU, the floats of one split's parts.  Causal order makes blocks of very different length,
+// which more of them even out (8160 x 8160 causal, 16 heads of 128 on 4: dk, dv 612 us with 512 blocks,
+// 892 with 256); a split costs its part's way through memory.
+// Measured (both kernels and join, us, with 1 / 2 / 4 / 8 splits of keys' blocks): float, 4 x 6 heads of 32,
+// 510 x 510 74 / 58 / 60 / 63; bfloat16, 8 heads of 64, 1000 x 1000 50 / 43 / 42 / 44; 8 x 8 heads of 64, 510 x 510
+// causal 52 / 56 / 65 / 87; 4 heads of 64, 4080 x 4080 154 / 111 / 97 / 105.
+inline int backward_splits(const lic_attention_args &p, int at_once, int64_t blocks, double steps, double unit,
+                           double floats)
 {
-    const bool uneven = p.window_left >= 0 || p.window_right >= 0;
-    int64_t n = blocks > 0 ? 256 * at_once * (uneven ? 2 : 1) / blocks : 1;
-    const int64_t few = steps / 2 < 4 ? steps / 2 : 4;
-    const int64_t most = steps / 4 > few ? steps / 4 : few;
-    n = n < most ? n : most;
-    n = n < 16 ? n : 16;
-    return n < 1 ? 1 : (int)n;
+    const double nd = (double)((p.dim + 31) / 32);
+    const double pair = at_once == 1 ? 2.0 : p.dtype == LIC_F32 ? 1.95 : 1.1 + 0.17 * nd;
+    const bool one_sided = (p.window_left >= 0) != (p.window_right >= 0);
+    const double queries = (double)p.queries, keys = (double)p.keys;
+    const double part = !one_sided ? 1.0 : queries < keys ? 1.0 - 0.5 * queries / keys : 0.5 * keys / queries;
+    int best = 1;
+    double least = 0.0;
+    for (int n = 1; n <= 16 && (n == 1 || (double)(2 * n) <= steps); n += part < 1.0 ? n : 1) {
+        const double each = (double)(blocks * n) / 256.0;
+        const int64_t whole = (blocks * n + 255) / 256;
+        const double even = (double)(whole / 2) * pair + (double)(whole % 2);
+        const double uneven = std::max(each > 1.0 && at_once > 1 ? 0.5 + 0.5 * pair : 1.0, each * part * pair / 2.0);
+        const double load = part < 1.0 ? uneven : even;
+        const double join = n == 1 ? 0.0 : 4.0 + 1e-6 * n * floats;
+        const double cost = (load * (1.5 + std::ceil(steps / n) * unit) + join) * (n == 1 ? 0.93 : 1.0);
+        if (n == 1 || cost < least)
+            best = n, least = cost;
+    }
+    return best;
+}
+// rows of `all` that one of the other kind sees at most
+inline double rows_seen(const lic_attention_args &p, int64_t all)
+{
+    const bool both = p.window_left >= 0 && p.window_right >= 0;
+    return both ? std::min((double)all, (double)(p.window_left + p.window_right) + 128.0) : (double)all;
 }
 inline int keys_splits(const lic_attention_args &p)
 {
-    return backward_splits(p, p.dim <= (p.dtype == LIC_F32 ? 32 : 96) ? 2 : 1,
-                           (p.keys + 127) / 128 * p.batch * p.kv_heads,
-                           (p.queries + 31) / 32 * (p.heads / p.kv_heads));
+    const double nd = (double)((p.dim + 31) / 32), group = (double)(p.heads / p.kv_heads);
+    const bool f32 = p.dtype == LIC_F32;
+    return backward_splits(p, p.dim <= (f32 ? 32 : 96) ? 2 : 1, (p.keys + 127) / 128 * p.batch * p.kv_heads,
+                           std::ceil(rows_seen(p, p.queries) / 32.0) * group, f32 ? 2.3 * nd : 0.7 + 0.07 * nd,
+                           64.0 * nd * (double)(p.batch * p.kv_heads * p.keys));
 }
 inline int queries_splits(const lic_attention_args &p)
 {
-    return backward_splits(p, p.dtype != LIC_F32 || p.dim <= 32 ? 2 : 1,
-                           (p.queries + 127) / 128 * p.batch * p.heads, (p.keys + 63) / 64);
+    const double nd = (double)((p.dim + 31) / 32);
+    const bool f32 = p.dtype == LIC_F32;
+    return backward_splits(p, !f32 || p.dim <= 32 ? 2 : 1, (p.queries + 127) / 128 * p.batch * p.heads,
+                           std::ceil(rows_seen(p, p.keys) / 64.0), f32 ? 4.0 * nd : 1.2 + 0.2 * nd,
+                           32.0 * nd * (double)(p.batch * p.heads * p.queries));
 }
 
 }  // namespace lic
