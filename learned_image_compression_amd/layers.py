@@ -130,29 +130,45 @@ def _like(t, dtype, device, name):
 
 _NO_WORKSPACE = (None, 0, None)  # address, bytes, owner
 _E_WORKSPACE = NAME_TO_CODE["RANS_E_WORKSPACE"]
+
+
+class _Workspace:
+    """A stream's scratch memory, and the lock under which a call enqueues its launches."""
+
+    __slots__ = ("lock", "held")
+
+    def __init__(self):
+        # the allocator may run finalizers, which may call operators: the same thread enters again
+        self.lock = threading.RLock()
+        self.held = _NO_WORKSPACE
+
+
 _workspaces: dict = {}
 
 
 def _with_workspace(device, stream: int, call, size, where: str):
     """``call(address, bytes)`` with this stream's scratch memory, grown when it is refused.
 
-    Kept per device and stream: calls on one stream never overlap, and a buffer
-    that is replaced goes back to the allocator of the stream that still uses
-    it.  Under stream capture the memory is the graph's own.
+    Kept per device and stream.  A call is several launches that pass sums to each other
+    through that memory, so all of them are enqueued under the stream's lock: those of two
+    threads would otherwise mix (the interpreter's own lock is let go of within a call).  A
+    buffer that is replaced goes back to the allocator of the stream that still uses it.
+    Under stream capture the memory is the graph's own.
     """
-    if torch.cuda.is_current_stream_capturing():
-        held = _NO_WORKSPACE
-    else:
-        held = _workspaces.get((device.index, stream), _NO_WORKSPACE)
-    rc = call(held[0], held[1])
-    if rc == _E_WORKSPACE:
-        nbytes = max(size(), 1 << 20)
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        held = (buf.data_ptr(), nbytes, buf)
-        if not torch.cuda.is_current_stream_capturing():
-            with _lock:
-                _workspaces[(device.index, stream)] = held
+    workspace = _workspaces.get((device.index, stream))
+    if workspace is None:
+        workspace = _workspaces.setdefault((device.index, stream), _Workspace())
+    with workspace.lock:
+        capturing = torch.cuda.is_current_stream_capturing()
+        held = _NO_WORKSPACE if capturing else workspace.held
         rc = call(held[0], held[1])
+        if rc == _E_WORKSPACE:
+            nbytes = max(size(), 1 << 20)
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            held = (buf.data_ptr(), nbytes, buf)
+            if not capturing:
+                workspace.held = held
+            rc = call(held[0], held[1])
     if rc:
         _check_rc(rc, where)
 

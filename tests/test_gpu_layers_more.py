@@ -1,0 +1,76 @@
+"""The network operators on the GPU where their first tests did not look: gradients of small
+size, layouts of the same values, infinities, launches past 2^32 threads, threads that share a stream."""
+from __future__ import annotations
+
+import math
+import threading
+
+import pytest
+import torch
+
+import layers_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+ALL = (F32, F16, BF16)
+
+
+@pytest.fixture(scope="module")
+def L():
+    from learned_image_compression_amd import layers
+    layers.load()
+    return layers
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def normal(g, *shape, dtype=F32):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def passes(got, want, bound, what):
+    w = R.worst(got, want, bound)
+    print(f"{what}: {w:.3f} of the bound", flush=True)
+    assert w <= 1.0, (what, w)
+
+
+# ---- threads that share a stream ---------------------------------------------------
+
+
+def test_threads_that_share_a_stream(L):
+    """Each thread's results are the bits that it gets alone: calls of several launches do not mix."""
+    def job(i):
+        g = gen(i)
+        x = normal(g, 2, 3000 + 100 * i, 64).transpose(1, 2)                  # sums, join, outputs
+        q = normal(g, 2, 1, 8, 64, dtype=BF16)                                # split keys, join
+        k, v = (normal(g, 2, 2000 + 300 * i, 2, 64, dtype=BF16) for _ in range(2))
+        t = [normal(g, 1, 300 + 10 * i, 4, 32, dtype=F16) for _ in range(4)]  # row statistics, both gradients
+
+        def call():
+            y, mean, rstd = L.group_norm_forward(x, 8, activation="silu")
+            out, lse = L.attention_forward(*t[:3], causal=True)
+            return (y, *L.group_norm_backward(y, x, 8, None, None, mean, rstd, activation="silu"),
+                    *L.attention_forward(q, k, v), *L.attention_backward(t[3], *t[:3], out, lse, causal=True))
+        return call
+
+    calls = [job(i) for i in range(4)]
+    alone = [[t.clone() for t in c()] for c in calls]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(4)
+
+    def work(i):
+        start.wait(30)
+        for turn in range(50):
+            for n, (a, b) in enumerate(zip(calls[i](), alone[i])):
+                if not torch.equal(a, b):
+                    wrong.append((i, turn, n))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not any(t.is_alive() for t in threads) and wrong == []
