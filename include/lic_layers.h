@@ -142,7 +142,8 @@ int lic_rotary(const lic_rotary_args *args, hipStream_t hstream);
  * lse is float [batch][heads][queries].  Scores, sums and accumulators are held
  * in 32 bits, products of 32-bit inputs in 32 bits; probabilities (and, in the
  * backward call, their gradients) are rounded to q's type for the second
- * product, as its operands.
+ * product, as its operands; in half precision a power of two of each row lifts those
+ * gradients there, so their precision does not depend on the size of dout or v.
  *
  * dim is 1 .. 128 (16-bit types: vector loads for multiples of 8, with strides and
  * addresses to match; 32-bit: of 4), scale positive.  The backward call recomputes

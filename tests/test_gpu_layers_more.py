@@ -74,3 +74,32 @@ def test_threads_that_share_a_stream(L):
     for t in threads:
         t.join(60)
     assert not any(t.is_alive() for t in threads) and wrong == []
+
+
+# ---- half precision -------------------------------------------------------------
+
+
+@pytest.mark.parametrize("q,s,h,kv,d,options", [
+    (64, 8160, 2, 2, 64, {}),
+    (300, 1000, 4, 2, 128, {"causal": True}),
+    (130, 4000, 2, 1, 40, {"mask": True}),
+    (40, 700, 2, 2, 33, {"causal": True}),
+])
+@pytest.mark.parametrize("size,v_size", [(2.0 ** -7, 1.0), (2.0 ** -10, 1.0), (2.0 ** -13, 4.0), (1.0, 2.0 ** -10),
+                                         (2.0 ** 9, 2.0 ** 7)])
+def test_half_gradients_of_any_size(L, q, s, h, kv, d, options, size, v_size):
+    """The products' operands keep their relative precision whatever the size of dout or v: the
+    bound has no term for float16's least step but the results' own."""
+    g = gen(q + s)
+    options = dict(options)
+    if "mask" in options:
+        options["mask"] = torch.rand(q, s, generator=g, device="cuda") < 0.5
+    qt, k = normal(g, 1, q, h, d, dtype=F16), normal(g, 1, s, kv, d, dtype=F16)
+    v, dout = (v_size * normal(g, 1, s, kv, d)).half(), (size * normal(g, 1, q, h, d)).half()
+    out, lse = L.attention_forward(qt, k, v, **options)
+    r = R.attention(qt, k, v, dout, **options)
+    u, e = R.UNIT[F16], R.F32 + r["slack"]
+    # out, as the forward call rounded it, is an operand of D: off by u (and half a least step)
+    low = R.STEP[F16] * dout.double().abs().sum(3).amax().item() * max(qt.abs().max().item(), k.abs().max().item())
+    for x, name, n in zip(L.attention_backward(dout, qt, k, v, out, lse, **options), ("dq", "dk", "dv"), (3, 3, 2)):
+        passes(x, r[name], (n * u + 2 * e) * r[name + "_abs"] + R.STEP[F16] + low * d ** -0.5, name)
