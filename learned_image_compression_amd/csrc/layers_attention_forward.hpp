@@ -4,8 +4,11 @@
 // One pass over the keys with a running maximum m and sum l of each row.  The
 // maximum is only raised when a tile exceeds it by more than 2^8: below that the
 // probabilities stay under 256, which 32-bit sums and both 16-bit types hold, and the
-// accumulators need no scaling in most tiles.
+// accumulators need no scaling in most tiles.  float16 takes them 2^7 times as large: of 10^5 keys
+// below one of e^14, each p lies among its last numbers, and their sum was off by 0.05 of itself.
 #pragma once
+
+#include <type_traits>
 
 #include "layers_attention.hpp"
 
@@ -13,6 +16,8 @@ namespace lic {
 namespace {
 
 constexpr float kSlack = 8.0f; // in powers of two
+template <typename T>
+constexpr float kRaise = std::is_same<T, f16>::value ? 7.0f : 0.0f; // 2^(8 + 7) is below float16's end
 
 // Scores of one accumulator (keys along its rows) that a query does not see become -inf.  inside: all
 // of them are within the query's range.  words: the mask's, where they were asked for before.
@@ -33,8 +38,9 @@ __device__ __forceinline__ void hide(float16v &s, const AttnArgs &a, const Range
 }
 
 // The running softmax of a lane's query over N accumulators of scores, which become
-// probabilities relative to the running maximum.
-template <int N, int ACC>
+// probabilities relative to the running maximum (less kRaise, as all that follows from them: at the
+// end it comes off m, which is what the sums are relative to).
+template <typename T, int N, int ACC>
 __device__ __forceinline__ void soften(float16v (&s)[N], float scale, float &m, float &l, float16v (&o)[ACC])
 {
     float top = s[0][0];
@@ -55,7 +61,7 @@ __device__ __forceinline__ void soften(float16v (&s)[N], float scale, float &m, 
             for (int i = 0; i < 16; ++i)
                 o[n][i] *= shrink;
     }
-    const float base = m == -INFINITY ? 0.0f : m; // nothing seen yet: exp(-inf) below
+    const float base = (m == -INFINITY ? 0.0f : m) - kRaise<T>; // nothing seen yet: exp(-inf) below
     float sum = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -260,7 +266,7 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
             }
             ask(k0 + G::kKeys);
             products_over();
-            soften(s, a.scale_log2, m, l, o);
+            soften<T>(s, a.scale_log2, m, l, o);
             products_first();
             const FragV<T> p[4] = {operand<T>(s[0], 0), operand<T>(s[0], 1), operand<T>(s[1], 0),
                                    operand<T>(s[1], 1)};
@@ -273,6 +279,7 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
     }
 
     settle<T>();
+    m -= kRaise<T>;
     const float total = pair_sum(l);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     bool bad = false;
@@ -460,7 +467,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
                         s[0][i] = -INFINITY;
             }
         }
-        soften(s, a.scale_log2, m, l, o);
+        soften<T>(s, a.scale_log2, m, l, o);
         const FragV<T> p[2] = {operand<T>(s[0], 0), operand<T>(s[0], 1)};
         const auto read = [&](int i) { return TileT::col_frag(vl, i / ND * 16, i % ND, lane); };
         Pipe<T, 2 * ND, ND == 3 ? 3 : ND == 1 ? 2 : 4> pipe;
@@ -470,6 +477,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
 
     // a wave's part: sums [32][DT], then m and l
     settle<T>();
+    m -= kRaise<T>;
     l = pair_sum(l);
     bool bad = false;
     float *sums = reinterpret_cast<float *>(lds + wave * kRegion);

@@ -103,3 +103,19 @@ def test_half_gradients_of_any_size(L, q, s, h, kv, d, options, size, v_size):
     low = R.STEP[F16] * dout.double().abs().sum(3).amax().item() * max(qt.abs().max().item(), k.abs().max().item())
     for x, name, n in zip(L.attention_backward(dout, qt, k, v, out, lse, **options), ("dq", "dk", "dv"), (3, 3, 2)):
         passes(x, r[name], (n * u + 2 * e) * r[name + "_abs"] + R.STEP[F16] + low * d ** -0.5, name)
+
+
+@pytest.mark.parametrize("b,n,h", [(600, 1, 2), (20, 70, 8), (1, 16384, 2)])
+def test_half_probabilities_of_a_long_row(L, b, n, h):
+    """One key far above 40000 equal others, which together still count: their probabilities lie
+    among float16's last numbers, where rounding them would move the sum by per cents."""
+    s, d, high = 40000, 32, 14.4921875  # exp(-high) = 8.53 of float16's least steps
+    q, k, v = (torch.zeros(m, r, h, d, device="cuda", dtype=F16) for m, r in ((b, n), (1, s), (1, s)))
+    q[..., 0], k[:, 7, :, 0] = 1.0, high  # in the first tile, so all others are taken with its maximum
+    v.fill_(1.0)
+    v[:, 7] = 0.0
+    out, lse = L.attention_forward(q, k.expand(b, s, h, d), v.expand(b, s, h, d), scale=1.0)
+    share = (s - 1) * math.exp(-high) / (1 + (s - 1) * math.exp(-high))
+    passes(out, torch.full_like(out, share, dtype=torch.float64), (2 * R.UNIT[F16] + R.F32) * share, "out")
+    want = high + math.log1p((s - 1) * math.exp(-high))
+    passes(lse, torch.full_like(lse, want, dtype=torch.float64), R.F32 * (1 + want), "lse")
