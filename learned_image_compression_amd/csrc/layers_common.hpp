@@ -23,14 +23,24 @@ struct alignas(sizeof(T) * N) Vec {
     T v[N];
 };
 
-// A store that the caches need not keep.  For outputs that would push the inputs out of the 256
+// Global memory is read and written in vectors wherever an element may lie: the hardware takes
+// such accesses at any address, and the arithmetic, its order with it, does not depend on one.
+template <typename V>
+__device__ __forceinline__ V load_at(const void *p)
+{
+    V v;
+    __builtin_memcpy(&v, p, sizeof(V));
+    return v;
+}
+
+// past: a store that the caches need not keep.  For outputs that would push the inputs out of the 256
 // MB last-level cache between two readings of them (kCacheBytes), or out of it for the next reader.
 constexpr int64_t kCacheBytes = 256ll << 20;
 template <typename V>
-__device__ __forceinline__ void store_past(V *p, const V &v, bool past)
+__device__ __forceinline__ void store_at(void *p, const V &v, bool past = false)
 {
     if constexpr (sizeof(V) == 16) {
-        using W = uint32_t __attribute__((ext_vector_type(4)));
+        using W = uint32_t __attribute__((ext_vector_type(4), aligned(2)));
         if (past) {
             W w;
             __builtin_memcpy(&w, &v, 16);
@@ -38,7 +48,7 @@ __device__ __forceinline__ void store_past(V *p, const V &v, bool past)
             return;
         }
     }
-    *p = v;
+    __builtin_memcpy(p, &v, sizeof(V));
 }
 
 // rounding to 16 bits is to nearest, ties to even, in both types

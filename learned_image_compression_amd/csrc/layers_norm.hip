@@ -18,8 +18,7 @@
 //   (norm_output_*).  The outputs walk the chunks from the last to the first,
 //   since the last ones read are what the caches still hold.
 //
-// A thread owns VEC neighbouring channels (16 bytes where sizes and alignment
-// allow) and walks rows, so channel constants stay in registers and neighbouring
+// A thread owns VEC neighbouring channels (16 bytes where they divide the channels) and walks rows, so channel constants stay in registers and neighbouring
 // lanes read neighbouring memory; it does not matter where group borders fall.
 //
 // Sums of squares: about the chunk's first row, a value of the data itself.  If
@@ -168,8 +167,7 @@ __device__ __forceinline__ void walk(const Place &at, const V *const (&array)[AR
             if (p + u * step < at.row_end) {
 #pragma unroll
                 for (int k = 0; k < ARRAYS; ++k)
-                    v[u][k] = *reinterpret_cast<const V *>(reinterpret_cast<const uint8_t *>(array[k]) +
-                                                           (p + u * step) * row[k]);
+                    v[u][k] = load_at<V>(reinterpret_cast<const uint8_t *>(array[k]) + (p + u * step) * row[k]);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -249,7 +247,7 @@ __global__ __launch_bounds__(kThreads) void norm_partial_forward(NormArgs a)
         s[i] = make_float2(0.0f, 0.0f);
     if (at.active) {
         const T *x = base + at.c0;
-        const V first = *reinterpret_cast<const V *>(x + at.row * a.x_row);
+        const V first = load_at<V>(x + at.row * a.x_row);
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
             shift[i] = up(first.v[i]);
@@ -338,7 +336,7 @@ __global__ __launch_bounds__(kThreads) void norm_output_forward(NormArgs a)
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
             o.v[i] = down<T>(act_value<ACT>((up(v[0].v[i]) - mean[i]) * gain[i] + bias[i]));
-        store_past(reinterpret_cast<V *>(y + p * a.out_row), o, a.past);
+        store_at(y + p * a.out_row, o, a.past);
     });
 }
 
@@ -501,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void norm_output_backward(NormArgs a)
             const float du = up(v[1].v[i]) * act_slope<ACT>(fmaf(d, ch.gain[i], ch.bias[i]));
             o.v[i] = down<T>(fmaf(ch.gain[i], du, fmaf(-d, slope[i].y, -slope[i].x)));
         }
-        *reinterpret_cast<V *>(dx + p * a.out_row) = o;
+        store_at(dx + p * a.out_row, o);
     });
 }
 
@@ -548,7 +546,7 @@ __global__ __launch_bounds__(kResident) void norm_resident_forward(NormArgs a)
     float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll 4
     for (int i = 0; i < at.slots; ++i) {
-        const V v = *reinterpret_cast<const V *>(x + i * step);
+        const V v = load_at<V>(x + i * step);
         held[i * kResident] = v;
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
@@ -586,7 +584,7 @@ __global__ __launch_bounds__(kResident) void norm_resident_forward(NormArgs a)
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
             o.v[e] = down<T>(act_value<ACT>((up(v.v[e]) - mean) * gain[e] + bias[e]));
-        *reinterpret_cast<V *>(y + i * out_step) = o;
+        store_at(y + i * out_step, o);
     }
 }
 
@@ -617,8 +615,8 @@ __global__ __launch_bounds__(kResident) void norm_resident_backward(NormArgs a)
     }
 #pragma unroll 2
     for (int i = 0; i < at.slots; ++i) {
-        const V v = *reinterpret_cast<const V *>(x + i * x_step);
-        const V d = *reinterpret_cast<const V *>(dy + i * dy_step);
+        const V v = load_at<V>(x + i * x_step);
+        const V d = load_at<V>(dy + i * dy_step);
         hx[i * kResident] = v;
         hd[i * kResident] = d;
 #pragma unroll
@@ -670,7 +668,7 @@ __global__ __launch_bounds__(kResident) void norm_resident_backward(NormArgs a)
             const float du = up(d.v[e]) * act_slope<ACT>(fmaf(off, gain[e], bias[e]));
             o.v[e] = down<T>(fmaf(gain[e], du, fmaf(-off, slope.y, -slope.x)));
         }
-        *reinterpret_cast<V *>(dx + i * out_step) = o;
+        store_at(dx + i * out_step, o);
     }
 }
 
@@ -719,20 +717,14 @@ uint64_t totals_bytes(int32_t samples, int32_t channels)
     return ((uint64_t)samples * channels * sizeof(float2) + 255) / 256 * 256;
 }
 
-// The widest vector that channels, strides and addresses allow.
+// The widest vector that divides the channels.  Strides and addresses have no part in it: it decides
+// the order of sums, and the same values have to give the same bits wherever they lie.
 template <typename T>
 int widest(const NormArgs &a)
 {
-    for (int vec : {(int)(16 / sizeof(T)), 2}) {
-        const uint64_t bytes = vec * sizeof(T);
-        const auto fits = [&](const void *p, int64_t sample, int64_t row) {
-            return !p || (aligned_to(p, bytes) && (a.samples == 1 || sample % vec == 0) &&
-                          (a.positions == 1 || row % vec == 0));
-        };
-        if (a.channels % vec == 0 && fits(a.x, a.x_sample, a.x_row) &&
-            fits(a.dy, a.dy_sample, a.dy_row) && fits(a.out, a.out_sample, a.out_row))
+    for (int vec : {(int)(16 / sizeof(T)), 2})
+        if (a.channels % vec == 0)
             return vec;
-    }
     return 1;
 }
 

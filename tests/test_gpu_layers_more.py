@@ -119,3 +119,41 @@ def test_half_probabilities_of_a_long_row(L, b, n, h):
     passes(out, torch.full_like(out, share, dtype=torch.float64), (2 * R.UNIT[F16] + R.F32) * share, "out")
     want = high + math.log1p((s - 1) * math.exp(-high))
     passes(lse, torch.full_like(lse, want, dtype=torch.float64), R.F32 * (1 + want), "lse")
+
+
+# ---- the same bits from the same values --------------------------------------------
+
+
+def laid_out(x, how):
+    """The same values [N, S, C] in other places: at an odd address, with rows further apart, ..."""
+    n, s, c = x.shape
+    if how == "odd address":
+        y = torch.empty(n * s * c + 1, dtype=x.dtype, device="cuda")[1:].view(n, s, c)
+    elif how == "odd rows":
+        y = torch.empty(n, s, c + 3, dtype=x.dtype, device="cuda")[..., 1:c + 1]
+    elif how == "pairs":
+        y = torch.empty(n, s, c + 2, dtype=x.dtype, device="cuda")[..., 2:]
+    else:  # samples apart by an odd number
+        y = torch.empty(n, s * c + 1, dtype=x.dtype, device="cuda")[:, 1:].unflatten(1, (s, c))
+    y.copy_(x)
+    return y
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("how", ["odd address", "odd rows", "pairs", "odd samples"])
+@pytest.mark.parametrize("n,s,c,groups", [(1, 510, 192, 32), (2, 1600, 192, 32), (3, 4000, 64, 4), (2, 77, 30, 5),
+                                          (40, 700, 24, 3), (1, 9000, 320, 32)])
+def test_group_norm_bits_do_not_depend_on_layout(L, n, s, c, groups, how, dtype):
+    g = gen(s)
+    x, dy = (normal(g, n, s, c, dtype=dtype) for _ in range(2))
+    w, b = normal(g, c), normal(g, c)
+
+    def call(x, dy):
+        x, dy = x.transpose(1, 2), dy.transpose(1, 2)
+        out = L.group_norm_forward(x, groups, w, b, activation="silu")
+        return (*out, *L.group_norm_backward(dy, x, groups, w, b, *out[1:], activation="silu"))
+
+    first = call(x, dy)
+    for a, b_ in ((laid_out(x, how), dy), (x, laid_out(dy, how)), (laid_out(x, how), laid_out(dy, how))):
+        for got, want, name in zip(call(a, b_), first, ("y", "mean", "rstd", "dx", "dw", "db")):
+            assert torch.equal(got, want), name
