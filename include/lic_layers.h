@@ -11,9 +11,13 @@
  * 256-byte aligned; it needs no filling and keeps nothing from one call to the
  * next.  Calls that share a workspace or an output must not overlap in time.
  *
- * Results do not depend on timing: every sum is taken in an order that the
- * sizes alone decide, so an encoder and a decoder that make the same call get
- * the same bits.
+ * Results do not depend on timing nor on where the values lie (addresses, strides):
+ * every sum is taken in an order that a call's sizes, windows and key lengths
+ * alone decide, so an encoder and a decoder that make the same call get the same
+ * bits.  Calls of other sizes take other orders: a position by itself (a single
+ * token over a cache, another batch) differs in its last bits from the same
+ * position within a longer call, so a decoder that steps needs an encoder that
+ * steps.
  *
  * Errors: the return value is a rans_status.  Sizes, pointers and types are
  * checked on the host before any launch (RANS_E_ARG, RANS_E_WORKSPACE); a

@@ -123,7 +123,7 @@ __device__ __forceinline__ FragV<T> operand(const float16v &p, int half)
     FragV<T> r;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        r[i] = (T)p[half * 8 + i];
+        r[i] = down_apart<T>(p[half * 8 + i]);
     return r;
 }
 
@@ -620,7 +620,7 @@ __device__ __forceinline__ void put_column(T *out, const float16v &v, float f, i
         Vec<T, 4> w;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            w.v[e] = down<T>(v[i + e] * f);
+            w.v[e] = down_apart<T>(v[i + e] * f);
         if constexpr (VEC) {
             if (d < dim)
                 *reinterpret_cast<Vec<T, 4> *>(out + d) = w;

@@ -19,8 +19,6 @@
 // small as dout and v make it: in float16 a power of two of each row lifts it (Lift).
 #pragma once
 
-#include <type_traits>
-
 #include "layers_attention.hpp"
 
 namespace lic {
@@ -473,8 +471,8 @@ attention_keys_backward(AttnArgs a)
             const int d = lane + 64 * c;
             if (a.splits == 1) {
                 if (d < dim) {
-                    head_row<T>(a.p.dk, a.p.dk_stride, b, k, kv)[d] = down<T>(ck[c] * scale);
-                    head_row<T>(a.p.dv, a.p.dv_stride, b, k, kv)[d] = down<T>(cv[c] * kLower);
+                    head_row<T>(a.p.dk, a.p.dk_stride, b, k, kv)[d] = down_apart<T>(ck[c] * scale);
+                    head_row<T>(a.p.dv, a.p.dv_stride, b, k, kv)[d] = down_apart<T>(cv[c] * kLower);
                 }
             } else if (d < DT) {
                 part_row(k)[d] = ck[c] * scale;
@@ -692,7 +690,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
             const int d = lane + 64 * e;
             if (a.splits == 1) {
                 if (d < dim)
-                    head_row<T>(a.p.dq, a.p.dq_stride, b, qi, head)[d] = down<T>(c[e] * scale);
+                    head_row<T>(a.p.dq, a.p.dq_stride, b, qi, head)[d] = down_apart<T>(c[e] * scale);
             } else if (d < DT) {
                 const int64_t ln = ((int64_t)b * a.p.heads + head) * a.p.queries + qi;
                 a.part[(split * lines + ln) * DT + d] = c[e] * scale;
@@ -745,7 +743,7 @@ __global__ __launch_bounds__(256) void attention_join(JoinArgs j)
         const float v[4] = {s.x, s.y, s.z, s.w};
         for (int e = 0; e < 4; ++e)
             if (d + e < j.dim)
-                out[d + e] = down<T>(v[e]);
+                out[d + e] = down_apart<T>(v[e]);
         return;
     }
 }

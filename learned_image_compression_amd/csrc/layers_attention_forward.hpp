@@ -8,8 +8,6 @@
 // below one of e^14, each p lies among its last numbers, and their sum was off by 0.05 of itself.
 #pragma once
 
-#include <type_traits>
-
 #include "layers_attention.hpp"
 
 namespace lic {
@@ -271,6 +269,8 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
             const FragV<T> p[4] = {operand<T>(s[0], 0), operand<T>(s[0], 1), operand<T>(s[1], 0),
                                    operand<T>(s[1], 1)};
             pipe.run(read, [&](int i, const FragV<T> &f) { o[i % ND] = mma(f, p[i / ND], o[i % ND]); });
+            if constexpr (!VEC) // rows on their way take registers, so the sums may be moved next
+                settle<T>();
         }
         if (more)
             store(buf ^ 1);
@@ -326,9 +326,9 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
         const float ci = cl == 0.0f ? 0.0f : 1.0f / cl;
         T *out = head_row<T>(a.p.out, a.p.out_stride, b, qi, head);
         if (lane < dim)
-            out[lane] = down<T>(co[0] * ci);
+            out[lane] = down_apart<T>(co[0] * ci);
         if (lane + 64 < dim)
-            out[lane + 64] = down<T>(co[1] * ci);
+            out[lane + 64] = down_apart<T>(co[1] * ci);
         if (lane == 0)
             a.p.lse[line] = log_sum(cm, cl);
     }
@@ -564,14 +564,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
                 Vec<T, 4> w;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    w.v[i] = down<T>(v[i]);
+                    w.v[i] = down_apart<T>(v[i]);
                 if (d < dim)
                     *reinterpret_cast<Vec<T, 4> *>(out) = w;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (d + i < dim)
-                        out[i] = down<T>(v[i]);
+                        out[i] = down_apart<T>(v[i]);
             }
             if (d == 0)
                 a.p.lse[line] = log_sum(top, total);
@@ -646,8 +646,8 @@ __global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a, int group
     T *out = head_row<T>(a.p.out, a.p.out_stride, b, query, head) + d;
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     Vec<T, 4> w;
-    w.v[0] = down<T>(sum.x * inv), w.v[1] = down<T>(sum.y * inv);
-    w.v[2] = down<T>(sum.z * inv), w.v[3] = down<T>(sum.w * inv);
+    w.v[0] = down_apart<T>(sum.x * inv), w.v[1] = down_apart<T>(sum.y * inv);
+    w.v[2] = down_apart<T>(sum.z * inv), w.v[3] = down_apart<T>(sum.w * inv);
     if constexpr (VEC) {
         if (d < dim)
             *reinterpret_cast<Vec<T, 4> *>(out) = w;

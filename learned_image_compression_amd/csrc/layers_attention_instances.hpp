@@ -6,20 +6,21 @@
 
 namespace lic {
 
-// 16-byte loads: the head's size rounded up to 32 columns.  Without them (odd sizes, strides or
-// addresses) the loads bound the kernels whatever the tile, so one width serves.
+// The head's size rounded up to 32 columns, with 16-byte loads or without them (odd sizes, strides or
+// addresses).  Either way the sums of a size are taken in the same order, so the same values give the
+// same bits wherever they lie.
 template <typename F>
 int with_tile(int64_t dim, bool vec, F &&f)
 {
     using std::integral_constant;
-    if (!vec)
-        return f(integral_constant<int, 128>{}, integral_constant<bool, false>{});
-    const integral_constant<bool, true> yes{};
+    const auto width = [&](auto dt) {
+        return vec ? f(dt, integral_constant<bool, true>{}) : f(dt, integral_constant<bool, false>{});
+    };
     switch ((dim + 31) / 32) {
-    case 1: return f(integral_constant<int, 32>{}, yes);
-    case 2: return f(integral_constant<int, 64>{}, yes);
-    case 3: return f(integral_constant<int, 96>{}, yes);
-    default: return f(integral_constant<int, 128>{}, yes);
+    case 1: return width(integral_constant<int, 32>{});
+    case 2: return width(integral_constant<int, 64>{});
+    case 3: return width(integral_constant<int, 96>{});
+    default: return width(integral_constant<int, 128>{});
     }
 }
 

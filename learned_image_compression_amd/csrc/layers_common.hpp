@@ -4,6 +4,7 @@
 
 #include <cstdint>
 #include <hip/hip_runtime.h>
+#include <type_traits>
 
 #include "lic_layers.h"
 
@@ -61,6 +62,17 @@ __device__ __forceinline__ float up(T x)
 template <typename T>
 __device__ __forceinline__ T down(float x)
 {
+    return (T)x;
+}
+
+// The same of a product that rounds by itself first.  float16 has an instruction for product and
+// conversion that rounds once, and the compiler takes it in one kernel and not in the next: kernels that
+// differ in their loads alone would differ in their results.
+template <typename T>
+__device__ __forceinline__ T down_apart(float x)
+{
+    if constexpr (std::is_same<T, f16>::value)
+        asm("" : "+v"(x));
     return (T)x;
 }
 

@@ -4,8 +4,10 @@ positions and attention, forward and backward (``include/lic_layers.h``).
 A learned image codec's transforms and its entropy model run right before the
 coder; these are the parts of them that convolutions and matrix products leave
 over, as hand-written HIP kernels in ``liblic_layers.so``.  Sums are taken in an
-order that the sizes alone decide, so an encoder and a decoder that make the
-same call predict the same scales, bit for bit.
+order that a call's sizes, windows and key lengths alone decide, wherever its values
+lie, so an encoder and a decoder that make the same call predict the same scales, bit
+for bit.  A call of another size (a single token instead of a whole latent) may differ
+in the last bits: an encoder has to step where its decoder does.
 
 :func:`group_norm`, :func:`rotary` and :func:`attention` work with autograd.  The
 ``*_forward`` and ``*_backward`` functions are the calls beneath them, for

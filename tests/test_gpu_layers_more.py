@@ -157,3 +157,36 @@ def test_group_norm_bits_do_not_depend_on_layout(L, n, s, c, groups, how, dtype)
     for a, b_ in ((laid_out(x, how), dy), (x, laid_out(dy, how)), (laid_out(x, how), laid_out(dy, how))):
         for got, want, name in zip(call(a, b_), first, ("y", "mean", "rstd", "dx", "dw", "db")):
             assert torch.equal(got, want), name
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("how", ["odd address", "odd rows", "odd samples"])
+@pytest.mark.parametrize("b,q,s,h,kv,d,options", [
+    (1, 1, 20000, 2, 1, 32, {}),                      # many splits
+    (2, 1, 9000, 3, 1, 64, {}),
+    (1, 20, 7000, 2, 2, 96, {"causal": True}),
+    (32, 140, 200, 4, 2, 32, {"causal": True}),
+    (32, 140, 200, 4, 2, 64, {"window": (30, 40)}),
+    (3, 300, 300, 2, 2, 40, {"lengths": True}),
+    (1, 1030, 1030, 2, 1, 96, {"mask": True}),
+    (1, 1030, 1030, 4, 2, 128, {"causal": True}),
+])
+def test_attention_bits_do_not_depend_on_layout(L, b, q, s, h, kv, d, options, how, dtype):
+    g = gen(s)
+    options = dict(options)
+    if "lengths" in options:
+        options = {"key_lengths": torch.tensor([s, s // 2, 1], dtype=torch.int32, device="cuda")}
+    if "mask" in options:
+        options["mask"] = torch.rand(q, s, generator=g, device="cuda") < 0.7
+    t = [normal(g, b, q, h, d, dtype=dtype), normal(g, b, s, kv, d, dtype=dtype), normal(g, b, s, kv, d, dtype=dtype),
+         normal(g, b, q, h, d, dtype=dtype)]
+
+    def call(q, k, v, dout):
+        out, lse = L.attention_forward(q, k, v, **options)
+        return (out, lse, *L.attention_backward(dout, q, k, v, out, lse, **options))
+
+    first = call(*t)
+    moved = [laid_out(x.flatten(2), how).unflatten(2, x.shape[2:]) for x in t]
+    for args in (moved, [moved[0], *t[1:]], [*t[:2], moved[2], t[3]]):
+        for got, want, name in zip(call(*args), first, ("out", "lse", "dq", "dk", "dv")):
+            assert torch.equal(got, want), name
