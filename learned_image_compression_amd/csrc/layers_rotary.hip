@@ -3,8 +3,8 @@
 //
 // The rotation is bound by HBM: q and k are read and written once, the tables
 // are a small part (a row serves all heads of a token).  A thread turns V pairs
-// of one head (two 16-byte loads of 16-bit values, four of 32-bit ones with V = 8
-// and V = 4) or copies 2 V of the head's other values; neighbouring threads take
+// of one head (two 16-byte loads: V = 8 in 16 bits, V = 4 in 32; V = 4 or 1 where the head
+// does not divide) or copies 2 V of the head's other values; neighbouring threads take
 // the units of a head, then the heads of a token, so a token's table row is read
 // from L1 by all heads but the first.  q and k share one launch.
 // Measured, bfloat16: 8 x 32640 positions, 6 heads of 32 of q and k 77 us (5.3 TB/s read and written,
@@ -52,15 +52,13 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 if (d0 + h * V < p.dim)
-                    *reinterpret_cast<VT *>(out + d0 + h * V) =
-                        *reinterpret_cast<const VT *>(in + d0 + h * V);
+                    store_at(out + d0 + h * V, load_at<VT>(in + d0 + h * V));
         }
         return;
     }
     const int j = (int)unit * V;
     const int at0 = INTER ? 2 * j : j, at1 = INTER ? 2 * j + V : half + j;
-    const VT x0 = *reinterpret_cast<const VT *>(in + at0);
-    const VT x1 = *reinterpret_cast<const VT *>(in + at1);
+    const VT x0 = load_at<VT>(in + at0), x1 = load_at<VT>(in + at1);
     const int64_t pos = p.positions ? p.positions[b * p.pos_batch + s] : (int64_t)s;
     float c[V], n[V];
     if ((uint64_t)pos < (uint64_t)p.table_rows) {
@@ -68,8 +66,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
         const float *ct = p.cos + pos * half + j, *st = p.sin + pos * half + j;
 #pragma unroll
         for (int i = 0; i < V; i += W) {
-            const Vec<float, W> cv = *reinterpret_cast<const Vec<float, W> *>(ct + i);
-            const Vec<float, W> sv = *reinterpret_cast<const Vec<float, W> *>(st + i);
+            const auto cv = load_at<Vec<float, W>>(ct + i), sv = load_at<Vec<float, W>>(st + i);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 c[i + w] = cv.v[w];
@@ -100,8 +97,8 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
             y1.v[i] = t1;
         }
     }
-    *reinterpret_cast<VT *>(out + at0) = y0;
-    *reinterpret_cast<VT *>(out + at1) = y1;
+    store_at(out + at0, y0);
+    store_at(out + at1, y1);
 }
 
 struct TableArgs {
@@ -154,24 +151,9 @@ int run_rotary(RotaryArgs a, hipStream_t s)
     return launched();
 }
 
-// Whether heads, strides and addresses let V values be read at once.
-template <typename T>
-bool fits(const lic_rotary_args &p, int V)
-{
-    const uint64_t bytes = V * sizeof(T);
-    // the table is read by at most four values at once
-    const int w = V < 4 ? V : 4;
-    if ((p.rotary_dim / 2) % V || p.dim % V || !aligned_to(p.cos, 4 * w) ||
-        !aligned_to(p.sin, 4 * w))
-        return false;
-    const auto ok = [&](const void *x, const int64_t *st, int64_t heads) {
-        return aligned_to(x, bytes) && (p.batch == 1 || st[0] % V == 0) &&
-               (p.tokens == 1 || st[1] % V == 0) && (heads == 1 || st[2] % V == 0);
-    };
-    return ok(p.q, p.q_stride, p.heads) && ok(p.q_out, p.q_out_stride, p.heads) &&
-           (p.kv_heads == 0 || (ok(p.k, p.k_stride, p.kv_heads) &&
-                                ok(p.k_out, p.k_out_stride, p.kv_heads)));
-}
+// Whether heads divide into V values at once.  Strides and addresses have no part in it: kernels
+// of other widths round otherwise (products are combined with sums in one and not in the next).
+bool fits(const lic_rotary_args &p, int V) { return (p.rotary_dim / 2) % V == 0 && p.dim % V == 0; }
 
 bool extent(int64_t v, int64_t least, int64_t most) { return v >= least && v <= most; }
 
@@ -229,9 +211,9 @@ extern "C" int lic_rotary(const lic_rotary_args *args, hipStream_t hstream)
     return with_dtype(p.dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int V = 16 / sizeof(T);
-        if (fits<T>(p, V))
+        if (fits(p, V))
             return run_rotary<T, V>(a, hstream);
-        if (fits<T>(p, 4)) // 16-bit heads of 24, 40, 72: 8 bytes at once
+        if (fits(p, 4)) // 16-bit heads of 24, 40, 72: 8 bytes at once
             return run_rotary<T, 4>(a, hstream);
         return run_rotary<T, 1>(a, hstream);
     });

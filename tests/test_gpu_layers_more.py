@@ -190,3 +190,21 @@ def test_attention_bits_do_not_depend_on_layout(L, b, q, s, h, kv, d, options, h
     for args in (moved, [moved[0], *t[1:]], [*t[:2], moved[2], t[3]]):
         for got, want, name in zip(call(*args), first, ("out", "lse", "dq", "dk", "dv")):
             assert torch.equal(got, want), name
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,r", [(64, 64), (40, 20), (96, 48), (24, 24)])
+def test_rotary_bits_do_not_depend_on_layout(L, d, r, interleaved, dtype):
+    g = gen(d)
+    a = torch.rand(60, r // 2, generator=g, device="cuda", dtype=torch.float64) * 7
+    cos, sin = a.cos().float(), a.sin().float()
+    q = normal(g, 3, 60, 4, d, dtype=dtype)
+    want, _ = L.rotary(q, None, cos, sin, interleaved=interleaved)
+    for how in ("odd address", "odd rows", "pairs", "odd samples"):
+        moved = laid_out(q.flatten(2), how).unflatten(2, (4, d))
+        for out in (None, (torch.empty_like(q), None)):
+            assert torch.equal(L.rotary(moved, None, cos, sin, interleaved=interleaved, out=out)[0], want), how
+    odd = torch.empty(2, 60 * (r // 2) + 1, device="cuda")[:, 1:].unflatten(1, (60, r // 2))
+    odd[0], odd[1] = cos, sin
+    assert torch.equal(L.rotary(q, None, odd[0], odd[1], interleaved=interleaved)[0], want)
