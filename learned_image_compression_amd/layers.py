@@ -9,11 +9,11 @@ lie, so an encoder and a decoder that make the same call predict the same scales
 for bit.  A call of another size (a single token instead of a whole latent) may differ
 in the last bits: an encoder has to step where its decoder does.
 
-:func:`group_norm`, :func:`rotary` and :func:`attention` work with autograd.  The
-``*_forward`` and ``*_backward`` functions are the calls beneath them, for
-programs that keep their own gradients.  As in :mod:`.binding`, torch only
-supplies device memory and the current stream, nothing is synchronised, and
-there is no CPU path.
+:func:`group_norm`, :func:`rotary` and :func:`attention` work with autograd (what they cannot
+differentiate they refuse: forward mode, second derivatives but rotary's).  The
+``*_forward`` and ``*_backward`` functions are the calls beneath them, for programs that
+keep their own gradients.  As in :mod:`.binding`, torch only supplies device memory and
+the current stream, nothing is synchronised, and there is no CPU path.
 """
 from __future__ import annotations
 
@@ -24,6 +24,7 @@ import struct
 import threading
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import NAME_TO_CODE, _check_rc
 
@@ -175,6 +176,37 @@ def _with_workspace(device, stream: int, call, size, where: str):
         _check_rc(rc, where)
 
 
+# ---- derivatives -----------------------------------------------------------
+
+
+def _wants_gradient(*tensors) -> bool:
+    """Whether autograd has to know of a call.  Forward mode does not know the operators: their
+    results would have no tangents, so tensors that have one are refused."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("forward-mode derivatives are not supported")
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class _Once(torch.autograd.Function):
+    """Gradients as functions of what they were formed from, so that whoever differentiates them
+    again is refused instead of missing a term."""
+
+    @staticmethod
+    def forward(ctx, form, *inputs):
+        return form()
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("second derivatives are not supported")
+
+
+def _once(form, *inputs):
+    """``form()``, a tuple of gradients; with a graph (``create_graph``) that refuses."""
+    return _Once.apply(form, *inputs) if torch.is_grad_enabled() else form()
+
+
 # ---- group norm --------------------------------------------------------------
 
 
@@ -312,8 +344,9 @@ class _GroupNorm(torch.autograd.Function):
             _rows(dy, "dy")
         except ValueError:  # a gradient of another layout
             dy = _channels_last_empty(dy).copy_(dy)
-        dx, dw, db = group_norm_backward(dy, x, ctx.num_groups, weight, bias, mean, rstd,
-                                         activation=ctx.activation)
+        dx, dw, db = _once(lambda: group_norm_backward(dy, x, ctx.num_groups, weight, bias, mean, rstd,
+                                                       activation=ctx.activation),
+                           dy, x, weight, bias)
         need = ctx.needs_input_grad
         return (dx if need[0] else None, None, dw.view_as(weight) if need[2] else None,
                 db.view_as(bias) if need[3] else None, None, None)
@@ -322,9 +355,8 @@ class _GroupNorm(torch.autograd.Function):
 def group_norm(x: torch.Tensor, num_groups: int, weight=None, bias=None, eps: float = 1e-5,
                activation: str = "none") -> torch.Tensor:
     """Group norm of a channels-last [N, C, ...] tensor and an activation ("none",
-    "relu", "silu", "gelu"), differentiable in x, weight and bias."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (x, weight, bias)):
+    "relu", "silu", "gelu"), differentiable (once, in reverse) in x, weight and bias."""
+    if _wants_gradient(x, weight, bias):
         return _GroupNorm.apply(x, num_groups, weight, bias, eps, activation)
     return group_norm_forward(x, num_groups, weight, bias, eps=eps, activation=activation)[0]
 
@@ -471,7 +503,9 @@ class _Rotary(torch.autograd.Function):
         dq = dq if dq.stride(-1) == 1 else dq.contiguous()
         if dk is not None and dk.stride(-1) != 1:
             dk = dk.contiguous()
-        gq, gk = _rotary(dq, dk, cos, sin, positions, interleaved, not inverse, None, None)
+        # the turn is linear: its gradient is the inverse, which autograd knows in its turn
+        gq, gk = rotary(dq, dk, cos, sin, positions=positions, interleaved=interleaved,
+                        inverse=not inverse)
         return gq, gk, None, None, None, None, None, None
 
 
@@ -486,9 +520,12 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor, sin: torc
     a token of NaN and, where ``status`` (int32[1], zeroed by the caller) is given,
     RANS_E_INDEX in it.  ``inverse`` turns back, which is also the gradient with
     respect to the inputs.  ``out`` is a pair of outputs, possibly (q, k) themselves;
-    it is for calls outside autograd.
+    it is for calls outside autograd.  Gradients are those of q and k, of any order; the tables
+    have none.
     """
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+    if _wants_gradient(cos, sin):
+        raise NotImplementedError("cos and sin have no gradients")
+    if _wants_gradient(q, k):
         if out is not None:
             raise ValueError("out is for calls outside autograd")
         r = _Rotary.apply(q, k, cos, sin, positions, interleaved, inverse, status)
@@ -628,15 +665,17 @@ class _Attention(torch.autograd.Function):
         q, k, v, out, lse, mask, key_lengths = ctx.saved_tensors
         if dout.stride(-1) != 1:
             dout = dout.contiguous()
-        grads = attention_backward(dout, q, k, v, out, lse, mask=mask, key_lengths=key_lengths,
-                                   **ctx.options)
+        grads = _once(lambda: attention_backward(dout, q, k, v, out, lse, mask=mask,
+                                                 key_lengths=key_lengths, **ctx.options),
+                      dout, q, k, v)
         return (*grads, None, None, None, None, None)
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool = False,
               window=None, mask=None, key_lengths=None, scale: float | None = None) -> torch.Tensor:
-    """Attention as :func:`attention_forward`, differentiable in q, k and v; returns out."""
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+    """Attention as :func:`attention_forward`, differentiable (once, in reverse) in q, k and v;
+    returns out."""
+    if _wants_gradient(q, k, v):
         return _Attention.apply(q, k, v, mask, key_lengths, causal, window, scale)[0]
     return attention_forward(q, k, v, causal=causal, window=window, mask=mask,
                              key_lengths=key_lengths, scale=scale)[0]

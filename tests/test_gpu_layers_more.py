@@ -208,3 +208,68 @@ def test_rotary_bits_do_not_depend_on_layout(L, d, r, interleaved, dtype):
     odd = torch.empty(2, 60 * (r // 2) + 1, device="cuda")[:, 1:].unflatten(1, (60, r // 2))
     odd[0], odd[1] = cos, sin
     assert torch.equal(L.rotary(q, None, odd[0], odd[1], interleaved=interleaved)[0], want)
+
+
+# ---- derivatives ---------------------------------------------------------------------
+
+
+def operators(L, g):
+    """(name, function of one tensor, the tensor) of each operator that autograd knows."""
+    cos, sin = normal(g, 6, 4), normal(g, 6, 4)
+    k = normal(g, 1, 6, 2, 8)
+    return [("group_norm", lambda x: L.group_norm(x, 2, activation="silu"), normal(g, 1, 5, 8).transpose(1, 2)),
+            ("rotary", lambda x: L.rotary(x, k, cos, sin)[0], normal(g, 1, 6, 2, 8)),
+            ("attention", lambda x: L.attention(x, k, k), normal(g, 1, 6, 2, 8))]
+
+
+@pytest.mark.parametrize("which", [0, 2])
+def test_second_derivatives_are_refused(L, which):
+    """Also where the first gradient is but a part of what is differentiated, which is how it would
+    go missing; a graph that nobody walks costs nothing."""
+    _, f, x = operators(L, gen(1))[which]
+    x = x.detach().requires_grad_()
+    plain, = torch.autograd.grad(f(x).square().sum(), x)
+    for penalty in (lambda first: first.square().sum(), lambda first: first.square().sum() + x.square().sum()):
+        for again in (lambda y: torch.autograd.grad(y, x), lambda y: y.backward()):
+            first, = torch.autograd.grad(f(x).square().sum(), x, create_graph=True)
+            assert torch.equal(first, plain)
+            with pytest.raises(RuntimeError, match="second derivatives"):
+                again(penalty(first))
+
+
+def test_rotary_second_derivatives(L):
+    """The rotation is linear: its gradient's gradient is the rotation again."""
+    g = gen(2)
+    cos, sin = normal(g, 6, 4), normal(g, 6, 4)
+    x, k = normal(g, 1, 6, 2, 8).requires_grad_(), normal(g, 1, 6, 1, 8).requires_grad_()
+    a, b = L.rotary(x, k, cos, sin)
+    first = torch.autograd.grad((a.pow(3).sum() + b.pow(3).sum()) / 3, (x, k), create_graph=True)
+    w = normal(g, 1, 6, 2, 8), normal(g, 1, 6, 1, 8)
+    second = torch.autograd.grad(first, (x, k), w)
+    for t, v, got in ((x, w[0], second[0]), (k, w[1], second[1])):
+        turned, along = (R.turn(y.detach(), cos, sin, None, False) for y in (t, v))
+        want = R.turn(2 * turned * along, cos, sin, None, False, inverse=True)
+        passes(got, want, 1e-5 * (1 + want.abs().max()), "second")
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_forward_mode_is_refused(L, which):
+    from torch.autograd import forward_ad
+    _, f, x = operators(L, gen(3))[which]
+    for grad in (False, True):
+        with forward_ad.dual_level():
+            dual = forward_ad.make_dual(x.detach().requires_grad_(grad), torch.ones_like(x))
+            with pytest.raises(NotImplementedError, match="forward"):
+                f(dual)
+    f(x)
+
+
+def test_rotary_tables_that_want_gradients_are_refused(L):
+    g = gen(4)
+    cos, sin, q = normal(g, 6, 4), normal(g, 6, 4), normal(g, 1, 6, 2, 8)
+    for tables in ((cos.clone().requires_grad_(), sin), (cos, sin.clone().requires_grad_())):
+        for x in (q, q.clone().requires_grad_()):
+            with pytest.raises(NotImplementedError, match="cos and sin"):
+                L.rotary(x, None, *tables)
+        with torch.no_grad():
+            L.rotary(q, None, *tables)
