@@ -171,8 +171,10 @@ typedef struct lic_attention_args {
 } lic_attention_args;
 
 /* Bytes for lic_attention_forward (backward == 0) or lic_attention_backward of these
- * sizes; only batch, queries, keys, heads, kv_heads, dim and dtype are read.  0 is
- * possible: the workspace may then be null. */
+ * sizes and windows: batch, queries, keys, heads, kv_heads, dim, dtype, window_left and
+ * window_right are read and have to be the call's (other windows split the work otherwise).
+ * 0 is possible: the workspace may then be null; it is also the answer to sizes or windows
+ * that a call refuses. */
 uint64_t lic_attention_workspace_bytes(const lic_attention_args *args, int32_t backward);
 
 int lic_attention_forward(const lic_attention_args *args, void *workspace,

@@ -11,7 +11,8 @@ bool valid(const lic_attention_args *p)
     return p && valid_dtype(p->dtype) && in(p->batch, 0, 1 << 20) && in(p->queries, 0, 1 << 28) &&
            in(p->keys, 0, 1 << 28) && in(p->kv_heads, 1, 65536) && in(p->heads, p->kv_heads, 65536) &&
            p->heads % p->kv_heads == 0 && in(p->dim, 1, LIC_MAX_HEAD_DIM) &&
-           p->queries * (p->heads / p->kv_heads) <= (1ll << 30) &&
+           p->queries * (p->heads / p->kv_heads) <= (1ll << 30) && in(p->window_left, -1, 1ll << 40) &&
+           in(p->window_right, -1, 1ll << 40) &&
            p->batch * p->heads * p->queries <= (1ll << 33) && p->batch * p->kv_heads * p->keys <= (1ll << 33);
 }
 
@@ -19,8 +20,7 @@ bool valid_call(const lic_attention_args &p, bool backward)
 {
     const auto ok = [](const int64_t *s) { return s[0] >= 0 && s[1] >= 0 && s[2] >= 0; };
     if (!ok(p.q_stride) || !ok(p.k_stride) || !ok(p.v_stride) || !ok(p.out_stride) ||
-        (p.mask && (!ok(p.mask_stride) || p.mask_stride[3] < 0)) || !(p.scale > 0.0) || !(p.scale < 1e30) ||
-        p.window_left < -1 || p.window_right < -1 || p.window_left > (1ll << 40) || p.window_right > (1ll << 40))
+        (p.mask && (!ok(p.mask_stride) || p.mask_stride[3] < 0)) || !(p.scale > 0.0) || !(p.scale < 1e30))
         return false;
     if (p.queries > 0 && (!p.q || !p.out || !p.lse))
         return false;
