@@ -77,6 +77,9 @@ __device__ __forceinline__ void put_param(void *p, int dtype, int c, float v)
     }
 }
 
+// a sum of squares that rounding may have taken below 0; NaN stays NaN
+__device__ __forceinline__ float not_below_zero(float x) { return x < 0.0f ? 0.0f : x; }
+
 __device__ __forceinline__ float fast_exp(float x)
 {
     return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
@@ -271,7 +274,7 @@ __global__ __launch_bounds__(kThreads) void norm_partial_forward(NormArgs a)
             return;
         const float about = up(base[at.row * a.x_row + c]);
         const float off = t.x / count;
-        part[c] = make_float2(about + off, fmaxf(t.y - t.x * off, 0.0f));
+        part[c] = make_float2(about + off, not_below_zero(t.y - t.x * off));
     });
 }
 
@@ -304,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void norm_join_forward(NormArgs a)
     if (threadIdx.x == 0) {
         const float m = (float)((double)a.positions * a.per_group);
         const float off = s.x / m;
-        const float var = fmaxf(s.y - s.x * off, 0.0f) / m;
+        const float var = not_below_zero(s.y - s.x * off) / m;
         a.mean[(int64_t)n * a.groups + g] = about + off;
         a.rstd[(int64_t)n * a.groups + g] = 1.0f / sqrtf(var + a.eps);
     }

@@ -273,3 +273,23 @@ def test_rotary_tables_that_want_gradients_are_refused(L):
                 L.rotary(x, None, *tables)
         with torch.no_grad():
             L.rotary(q, None, *tables)
+
+
+# ---- infinities ----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("s", [100, 30000])  # one launch, three
+@pytest.mark.parametrize("at", [0, 57])
+def test_group_norm_statistics_of_infinities(L, s, value, at, dtype):
+    x = normal(gen(s), 2, s, 64, dtype=dtype)
+    x[1, at, 19] = value
+    y, mean, rstd = L.group_norm_forward(x.transpose(1, 2), 8)
+    assert bool(torch.isnan(rstd[1, 2])) and not bool(torch.isfinite(mean[1, 2]))
+    assert bool(torch.isnan(y[1, 16:24]).all())
+    clean = torch.ones(2, 64, dtype=torch.bool, device="cuda")
+    clean[1, 16:24] = False
+    assert bool(torch.isfinite(y[clean]).all())
+    clean = clean[:, ::8]
+    assert bool(torch.isfinite(mean[clean]).all()) and bool(torch.isfinite(rstd[clean]).all())
