@@ -77,7 +77,7 @@ __device__ __forceinline__ void put_param(void *p, int dtype, int c, float v)
     }
 }
 
-// a sum of squares that rounding may have taken below 0; NaN stays NaN
+// relu, and a sum of squares that rounding may have taken below 0; NaN stays NaN
 __device__ __forceinline__ float not_below_zero(float x) { return x < 0.0f ? 0.0f : x; }
 
 __device__ __forceinline__ float fast_exp(float x)
@@ -104,7 +104,7 @@ template <int ACT>
 __device__ __forceinline__ float act_value(float u)
 {
     if constexpr (ACT == LIC_ACT_RELU)
-        return u > 0.0f ? u : u * 0.0f; // NaN stays NaN
+        return not_below_zero(u);
     if constexpr (ACT == LIC_ACT_SILU)
         return u * __builtin_amdgcn_rcpf(1.0f + fast_exp(-u));
     if constexpr (ACT == LIC_ACT_GELU) {

@@ -293,3 +293,14 @@ def test_group_norm_statistics_of_infinities(L, s, value, at, dtype):
     assert bool(torch.isfinite(y[clean]).all())
     clean = clean[:, ::8]
     assert bool(torch.isfinite(mean[clean]).all()) and bool(torch.isfinite(rstd[clean]).all())
+
+
+@pytest.mark.parametrize("s", [100, 30000])
+def test_relu_of_minus_infinity_is_zero(L, s):
+    x = normal(gen(s), 1, s, 64).transpose(1, 2)
+    bias = torch.zeros(64, device="cuda")
+    bias[5], bias[6], bias[7] = -math.inf, math.inf, math.nan
+    y = L.group_norm_forward(x, 8, None, bias, activation="relu")[0]
+    assert bool((y[:, 5] == 0).all()) and bool((y[:, 6] == math.inf).all()) and bool(torch.isnan(y[:, 7]).all())
+    assert bool(torch.isfinite(y[:, :5]).all())
+    assert not bool(torch.signbit(y[:, :5]).any())  # and no zeros with a sign
