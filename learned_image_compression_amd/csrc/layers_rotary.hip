@@ -45,23 +45,30 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
     const T *in = static_cast<const T *>(is_q ? p.q : p.k) + b * si[0] + s * si[1] + head * si[2];
     T *out = static_cast<T *>(is_q ? p.q_out : p.k_out) + b * so[0] + s * so[1] + head * so[2];
 
+    const int64_t pos = p.positions ? p.positions[b * p.pos_batch + s] : (int64_t)s;
+    const bool there = (uint64_t)pos < (uint64_t)p.table_rows;
+
     const int half = (int)p.rotary_dim / 2;
     if (unit >= a.turn_units) { // values beyond the rotated part
         const int d0 = (int)p.rotary_dim + (int)(unit - a.turn_units) * 2 * V;
-        if (in != out) {
+        if (in != out || !there) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (d0 + h * V < p.dim)
-                    store_at(out + d0 + h * V, load_at<VT>(in + d0 + h * V));
+                if (d0 + h * V < p.dim) {
+                    VT x = load_at<VT>(in + d0 + h * V);
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        x.v[i] = there ? x.v[i] : (T)__builtin_nanf("");
+                    store_at(out + d0 + h * V, x);
+                }
         }
         return;
     }
     const int j = (int)unit * V;
     const int at0 = INTER ? 2 * j : j, at1 = INTER ? 2 * j + V : half + j;
     const VT x0 = load_at<VT>(in + at0), x1 = load_at<VT>(in + at1);
-    const int64_t pos = p.positions ? p.positions[b * p.pos_batch + s] : (int64_t)s;
     float c[V], n[V];
-    if ((uint64_t)pos < (uint64_t)p.table_rows) {
+    if (there) {
         constexpr int W = V < 4 ? V : 4;
         const float *ct = p.cos + pos * half + j, *st = p.sin + pos * half + j;
 #pragma unroll

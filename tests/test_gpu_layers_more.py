@@ -304,3 +304,21 @@ def test_relu_of_minus_infinity_is_zero(L, s):
     assert bool((y[:, 5] == 0).all()) and bool((y[:, 6] == math.inf).all()) and bool(torch.isnan(y[:, 7]).all())
     assert bool(torch.isfinite(y[:, :5]).all())
     assert not bool(torch.signbit(y[:, :5]).any())  # and no zeros with a sign
+
+
+# ---- rotary ----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("d,r", [(16, 8), (64, 32), (24, 10)])
+def test_rotary_positions_outside_the_tables_take_the_whole_token(L, d, r, in_place, dtype):
+    g = gen(d)
+    cos, sin = normal(g, 10, r // 2), normal(g, 10, r // 2)
+    q, k = normal(g, 1, 4, 3, d, dtype=dtype), normal(g, 1, 4, 1, d, dtype=dtype)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, -1, 9, 10], dtype=torch.int32, device="cuda")
+    got = L.rotary(q, k, cos, sin, positions=at, status=status, out=(q, k) if in_place else None)
+    assert int(status) == -3
+    for y in got:
+        assert bool(torch.isnan(y[:, [1, 3]]).all()) and bool(torch.isfinite(y[:, [0, 2]]).all())
