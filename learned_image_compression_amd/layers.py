@@ -437,6 +437,8 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
     device = _device_of(q, "q")
     qs = _heads(q, "q")
     b, s, h, d = q.shape
+    if h < 1:
+        raise ValueError("q has no heads")
     kh, ks, kos = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
         _like(k, q.dtype, device, "k")
@@ -474,7 +476,7 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
     qos = _heads(qo, "out of q")
     if kh:
         kos = _heads(ko, "out of k")
-    if q.numel() == 0 or h == 0:
+    if q.numel() == 0:
         return qo, ko if kh else (k if k is None else torch.empty_like(k))
     args = _ROTARY.pack(q.data_ptr(), k.data_ptr() if kh else 0, qo.data_ptr(),
                         ko.data_ptr() if kh else 0, cos.data_ptr(), sin.data_ptr(),

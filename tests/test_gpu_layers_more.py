@@ -322,3 +322,12 @@ def test_rotary_positions_outside_the_tables_take_the_whole_token(L, d, r, in_pl
     assert int(status) == -3
     for y in got:
         assert bool(torch.isnan(y[:, [1, 3]]).all()) and bool(torch.isfinite(y[:, [0, 2]]).all())
+
+
+def test_rotary_without_query_heads_is_refused(L):
+    """It used to return keys that no kernel had written."""
+    c, k = torch.zeros(4, 4, device="cuda"), torch.ones(1, 4, 2, 8, device="cuda")
+    with pytest.raises(ValueError, match="heads"):
+        L.rotary(torch.empty(1, 4, 0, 8, device="cuda"), k, c, c)
+    q, k = L.rotary(torch.empty(1, 0, 2, 8, device="cuda"), k[:, :0], c, c)
+    assert q.shape == (1, 0, 2, 8) and k.shape == (1, 0, 2, 8)
