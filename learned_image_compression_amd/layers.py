@@ -131,6 +131,15 @@ def _like(t, dtype, device, name):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _out_like(out, t, dtype, device, name):
+    """Checks of an output that the caller gives; two of its entries must not be one."""
+    _like(out, dtype, device, name)
+    if out.shape != t.shape:
+        raise ValueError(f"{name} differs in shape")
+    if any(stride == 0 and size > 1 for stride, size in zip(out.stride(), out.shape)):
+        raise ValueError(f"{name} overlaps itself")
+
+
 _NO_WORKSPACE = (None, 0, None)  # address, bytes, owner
 _E_WORKSPACE = NAME_TO_CODE["RANS_E_WORKSPACE"]
 
@@ -273,9 +282,7 @@ def group_norm_forward(x: torch.Tensor, num_groups: int, weight=None, bias=None,
     if out is None:
         out = _channels_last_empty(x)
     else:
-        _like(out, x.dtype, device, "out")
-        if out.shape != x.shape:
-            raise ValueError("out and x differ in shape")
+        _out_like(out, x, x.dtype, device, "out")
     ys, yr, _ = _rows(out, "out")
     n, c = x.shape[0], x.shape[1]
     stats = torch.empty((2, n, num_groups), dtype=torch.float32, device=device)
@@ -470,9 +477,7 @@ def _rotary(q, k, cos, sin, positions, interleaved, inverse, status, out):
         qo, ko = out
         for o, t, name in ((qo, q, "q"), (ko, k, "k")):
             if t is not None:
-                _like(o, q.dtype, device, f"out of {name}")
-                if o.shape != t.shape:
-                    raise ValueError(f"out of {name} differs in shape")
+                _out_like(o, t, q.dtype, device, f"out of {name}")
     qos = _heads(qo, "out of q")
     if kh:
         kos = _heads(ko, "out of k")
@@ -606,9 +611,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, caus
     if out is None:
         out = _dense_like(q)
     else:
-        _like(out, q.dtype, device, "out")
-        if out.shape != q.shape:
-            raise ValueError("out and q differ in shape")
+        _out_like(out, q, q.dtype, device, "out")
     lse = torch.empty((b, h, n), dtype=torch.float32, device=device)
     args = _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                            lse.data_ptr(), 0, 0, 0, 0, *ptrs, *qs, *ks, *vs, *_heads(out, "out"),

@@ -331,3 +331,16 @@ def test_rotary_without_query_heads_is_refused(L):
         L.rotary(torch.empty(1, 4, 0, 8, device="cuda"), k, c, c)
     q, k = L.rotary(torch.empty(1, 0, 2, 8, device="cuda"), k[:, :0], c, c)
     assert q.shape == (1, 0, 2, 8) and k.shape == (1, 0, 2, 8)
+
+
+def test_outputs_that_overlap_are_refused(L):
+    g = gen(5)
+    q = normal(g, 2, 4, 2, 8)
+    c = normal(g, 4, 4)
+    with pytest.raises(ValueError, match="overlap"):
+        L.attention_forward(q, q, q, out=torch.empty(1, 4, 2, 8, device="cuda").expand(2, 4, 2, 8))
+    with pytest.raises(ValueError, match="overlap"):
+        L.rotary(q, None, c, c, out=(torch.empty(2, 4, 1, 8, device="cuda").expand(2, 4, 2, 8), None))
+    x = normal(g, 2, 4, 8).transpose(1, 2)
+    with pytest.raises(ValueError, match="overlap"):
+        L.group_norm_forward(x, 2, out=torch.empty(2, 1, 8, device="cuda").expand(2, 4, 8).transpose(1, 2))
