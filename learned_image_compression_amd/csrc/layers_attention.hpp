@@ -642,30 +642,18 @@ struct Attention {
 
 constexpr int kTwoBlocks = 64 * 1024; // of LDS: two blocks fit a CU's 160 KiB, three do not
 
-// A kernel of more than 64 KiB of LDS says so once.
-template <typename K>
-inline void allow_lds(K kernel, int bytes)
-{
-    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 // ROOM: whether the 8 registers that words ahead take are there without spills.
 template <bool ROOM, typename F>
-void with_mask(const lic_attention_args &p, F &&f)
+int with_mask(const lic_attention_args &p, F &&f)
 {
     using std::integral_constant;
-    if (!p.mask) {
-        f(integral_constant<Masked, Masked::none>{});
-        return;
-    }
+    if (!p.mask)
+        return f(integral_constant<Masked, Masked::none>{});
     if constexpr (ROOM) {
-        if (mask_in_words(p.mask_stride[3], p.keys)) {
-            f(integral_constant<Masked, Masked::ahead>{});
-            return;
-        }
+        if (mask_in_words(p.mask_stride[3], p.keys))
+            return f(integral_constant<Masked, Masked::ahead>{});
     }
-    f(integral_constant<Masked, Masked::here>{});
+    return f(integral_constant<Masked, Masked::here>{});
 }
 
 // Splits of the key axis that the rows kernel takes: two blocks a CU, at least 256 keys

@@ -771,13 +771,16 @@ int run_backward(AttnArgs a, hipStream_t s)
             return RANS_E_ARG;
         a.blocks = (uint32_t)blocks;
         a.part = parts;
-        with_mask<VEC && (sizeof(T) == 4 || DT <= 96)>(p, [&](auto masked) {
+        const int rc = with_mask<VEC && (sizeof(T) == 4 || DT <= 96)>(p, [&](auto masked) {
             constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
             constexpr auto kernel = attention_queries_backward<T, DT, VEC, decltype(masked)::value>;
-            static const bool once = (allow_lds(kernel, kMost), true);
-            (void)once;
+            if (const int rc = allow_lds<kernel>(kMost))
+                return rc;
             kernel<<<xcd_grid(a.blocks), 256, uneven ? kMost : G::kLds, s>>>(a);
+            return (int)RANS_OK;
         });
+        if (rc)
+            return rc;
         if (a.splits > 1) {
             joined(parts, p.dq, p.dq_stride, lines * DT, p.queries, p.heads, a.splits);
             parts += a.splits * lines * DT;
@@ -786,8 +789,8 @@ int run_backward(AttnArgs a, hipStream_t s)
     if (p.keys > 0) {
         using G = KeysBackward<T, DT>;
         constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
-        static const bool once = (allow_lds(attention_keys_backward<T, DT, VEC>, kMost), true);
-        (void)once;
+        if (const int rc = allow_lds<attention_keys_backward<T, DT, VEC>>(kMost))
+            return rc;
         a.splits = keys_splits(p);
         const int64_t blocks = (p.keys + 127) / 128 * p.batch * p.kv_heads * a.splits;
         if (blocks > 0x7fffff00)

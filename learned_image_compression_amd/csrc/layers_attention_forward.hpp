@@ -680,8 +680,8 @@ int run_forward(AttnArgs a, hipStream_t s)
     };
     if (plan.few) {
         using G = RowsForward<T, DT, VEC>;
-        static const bool once = (allow_lds(attention_rows_forward<T, DT, VEC>, G::kLds), true);
-        (void)once;
+        if (const int rc = allow_lds<attention_rows_forward<T, DT, VEC>>(G::kLds))
+            return rc;
         const int64_t rows = a.p.queries * a.group;
         const int64_t blocks = (rows + 31) / 32 * a.p.batch * a.p.kv_heads * a.splits;
         if (blocks > 0x7fffffff)
@@ -700,12 +700,15 @@ int run_forward(AttnArgs a, hipStream_t s)
     // leave (8160 x 8160 causal, 16 heads of 32 on 4: 131 us with two at a time, 152 with three).
     const bool uneven = a.p.window_left >= 0 || a.p.window_right >= 0;
     const int lds = uneven && G::kLds < kTwoBlocks ? kTwoBlocks : G::kLds;
-    with_mask<VEC && (sizeof(T) == 2 ? DT <= 96 : DT != 64)>(a.p, [&](auto masked) {
+    const int rc = with_mask<VEC && (sizeof(T) == 2 ? DT <= 96 : DT != 64)>(a.p, [&](auto masked) {
         constexpr auto kernel = attention_tiles_forward<T, DT, VEC, decltype(masked)::value>;
-        static const bool once = (allow_lds(kernel, G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks), true);
-        (void)once;
+        if (const int rc = allow_lds<kernel>(G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks))
+            return rc;
         kernel<<<xcd_grid(a.blocks), 256, lds, s>>>(a);
+        return (int)RANS_OK;
     });
+    if (rc)
+        return rc;
     join();
     return launched();
 }

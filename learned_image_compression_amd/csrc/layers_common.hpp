@@ -2,6 +2,7 @@
 // operators' kernels (group norm, rotary positions, attention).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <hip/hip_runtime.h>
 #include <type_traits>
@@ -85,6 +86,27 @@ inline bool aligned_to(const void *p, uint64_t n)
 }
 
 inline int launched() { return hipGetLastError() == hipSuccess ? RANS_OK : RANS_E_HIP; }
+
+// Lets KERNEL take `bytes` of LDS, which is more than any may without it, on the current device; each
+// device is told once.
+template <auto KERNEL>
+int allow_lds(int bytes)
+{
+    static std::atomic<uint64_t> told{0}; // a bit for each of the first 64 devices
+    int device = 0;
+    if (hipGetDevice(&device) != hipSuccess)
+        return RANS_E_HIP;
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (told.load(std::memory_order_relaxed) & bit)
+        return RANS_OK;
+    if (hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            bytes) != hipSuccess) {
+        (void)hipGetLastError();
+        return RANS_E_HIP;
+    }
+    told.fetch_or(bit, std::memory_order_relaxed);
+    return RANS_OK;
+}
 
 // f(T{}) for the element type that `dtype` names
 template <typename F>

@@ -789,21 +789,14 @@ bool resident_pays(const NormArgs &a, int64_t lds, int vec)
     return one <= three && lds > 0 && lds <= (a.dy ? kMostBackward : kMostForward);
 }
 
-template <typename K>
-void allow_lds(K kernel, int64_t bytes)
-{
-    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)bytes);
-}
-
 template <typename T>
 int run_resident_forward(const NormArgs &a, int vec, int64_t lds, hipStream_t s)
 {
     return with_vec<T>(vec, [&](auto v) {
         return with_act(a.act, [&](auto act) {
             constexpr auto kernel = norm_resident_forward<T, v.value, act.value>;
-            static const bool once = (allow_lds(kernel, kMostForward), true);
-            (void)once;
+            if (const int rc = allow_lds<kernel>(kMostForward))
+                return rc;
             kernel<<<(a.blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
             return launched();
         });
@@ -816,8 +809,8 @@ int run_resident_backward(const NormArgs &a, int vec, int64_t lds, hipStream_t s
     return with_vec<T>(vec, [&](auto v) {
         return with_act(a.act, [&](auto act) {
             constexpr auto kernel = norm_resident_backward<T, v.value, act.value>;
-            static const bool once = (allow_lds(kernel, kMostBackward), true);
-            (void)once;
+            if (const int rc = allow_lds<kernel>(kMostBackward))
+                return rc;
             kernel<<<(a.blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
             if (a.samples > 1 && (a.dweight || a.dbias))
                 norm_samples<<<(a.channels + 31) / 32, kThreads, 0, s>>>(a);
