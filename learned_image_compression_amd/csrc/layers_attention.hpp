@@ -45,6 +45,7 @@ struct AttnArgs {
     int splits;
     int group;          // heads that share a kv head
     uint32_t blocks;    // of the launch's real work
+    uint32_t first;     // the launch's first block of the call's
 };
 
 // The kernel's arguments (its first and only parameter) read again where they are used: what
@@ -593,6 +594,8 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t block, uint32_t blocks)
     return (block & 7) * each + (block >> 3); // may be >= blocks: no work
 }
 inline uint32_t xcd_grid(uint32_t blocks) { return (blocks + 7) / 8 * 8; }
+// blocks of a call that its kernels count
+constexpr int64_t kMostBlocks = 0x7fffff00;
 
 // Orders a wave's own LDS writes before its other lanes' reads.
 __device__ __forceinline__ void wave_fence()

@@ -197,8 +197,8 @@ attention_keys_backward(AttnArgs a)
     constexpr int KK = DT / 16, ND = DT / 32, NQ = G::kQueries;
     extern __shared__ __align__(16) uint8_t lds[];
 
-    const uint32_t block = xcd_order(blockIdx.x, a.blocks);
-    if (block >= a.blocks)
+    const uint32_t place = xcd_order(blockIdx.x, a.blocks), block = a.first + place;
+    if (place >= a.blocks)
         return;
     const uint32_t k_blocks = (uint32_t)((a.p.keys + 127) / 128);
     const int key0 = (int)(block % k_blocks) * 128; // the first keys are seen by the most queries
@@ -502,8 +502,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
     constexpr int KK = DT / 16, ND = DT / 32;
     extern __shared__ __align__(16) uint8_t lds[];
 
-    const uint32_t block = xcd_order(blockIdx.x, a.blocks);
-    if (block >= a.blocks)
+    const uint32_t place = xcd_order(blockIdx.x, a.blocks), block = a.first + place;
+    if (place >= a.blocks)
         return;
     const uint32_t q_blocks = (uint32_t)((a.p.queries + 127) / 128);
     const int q0 = (int)(q_blocks - 1 - block % q_blocks) * 128;
@@ -711,12 +711,13 @@ struct JoinArgs {
         int splits;
     } one[3];
     int count, dim;
+    int64_t first; // the launch's first block of the call's
 };
 
 template <typename T, int DT>
 __global__ __launch_bounds__(256) void attention_join(JoinArgs j)
 {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t id = (j.first + blockIdx.x) * 256 + threadIdx.x;
     int64_t line = id / (DT / 4);
     const int d = (int)(id % (DT / 4)) * 4;
     for (int k = 0; k < j.count; ++k) {
@@ -755,6 +756,11 @@ int run_backward(AttnArgs a, hipStream_t s)
     float *parts = a.part;
     // two blocks a CU where blocks differ much in length, as in the forward call
     const bool uneven = p.window_left >= 0 || p.window_right >= 0;
+    const int q_splits = queries_splits(p), k_splits = keys_splits(p);
+    const int64_t q_blocks = (p.queries + 127) / 128 * p.batch * p.heads * q_splits;
+    const int64_t k_blocks = (p.keys + 127) / 128 * p.batch * p.kv_heads * k_splits;
+    if (q_blocks > kMostBlocks || k_blocks > kMostBlocks)
+        return RANS_E_ARG;
     JoinArgs j{};
     j.dim = (int)p.dim;
     const auto joined = [&](const float *part, void *out, const int64_t *stride, int64_t step, int64_t rows,
@@ -764,19 +770,18 @@ int run_backward(AttnArgs a, hipStream_t s)
     };
     if (p.queries > 0) {
         using G = QueriesBackward<T, DT>;
-        a.splits = queries_splits(p);
+        a.splits = q_splits;
         const int64_t lines = p.batch * p.heads * p.queries;
-        const int64_t blocks = (p.queries + 127) / 128 * p.batch * p.heads * a.splits;
-        if (blocks > 0x7fffff00)
-            return RANS_E_ARG;
-        a.blocks = (uint32_t)blocks;
         a.part = parts;
         const int rc = with_mask<VEC && (sizeof(T) == 4 || DT <= 96)>(p, [&](auto masked) {
             constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
             constexpr auto kernel = attention_queries_backward<T, DT, VEC, decltype(masked)::value>;
             if (const int rc = allow_lds<kernel>(kMost))
                 return rc;
-            kernel<<<xcd_grid(a.blocks), 256, uneven ? kMost : G::kLds, s>>>(a);
+            in_pieces(q_blocks, 256, [&](int64_t first, uint32_t piece) {
+                a.first = (uint32_t)first, a.blocks = piece;
+                kernel<<<xcd_grid(piece), 256, uneven ? kMost : G::kLds, s>>>(a);
+            });
             return (int)RANS_OK;
         });
         if (rc)
@@ -791,13 +796,12 @@ int run_backward(AttnArgs a, hipStream_t s)
         constexpr int kMost = G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks;
         if (const int rc = allow_lds<attention_keys_backward<T, DT, VEC>>(kMost))
             return rc;
-        a.splits = keys_splits(p);
-        const int64_t blocks = (p.keys + 127) / 128 * p.batch * p.kv_heads * a.splits;
-        if (blocks > 0x7fffff00)
-            return RANS_E_ARG;
-        a.blocks = (uint32_t)blocks;
+        a.splits = k_splits;
         a.part = parts;
-        attention_keys_backward<T, DT, VEC><<<xcd_grid(a.blocks), G::kThreads, uneven ? kMost : G::kLds, s>>>(a);
+        in_pieces(k_blocks, G::kThreads, [&](int64_t first, uint32_t piece) {
+            a.first = (uint32_t)first, a.blocks = piece;
+            attention_keys_backward<T, DT, VEC><<<xcd_grid(piece), G::kThreads, uneven ? kMost : G::kLds, s>>>(a);
+        });
         if (a.splits > 1) {
             const int64_t all = p.batch * p.kv_heads * p.keys * DT;
             joined(parts, p.dk, p.dk_stride, 2 * all, p.keys, p.kv_heads, a.splits);
@@ -808,10 +812,10 @@ int run_backward(AttnArgs a, hipStream_t s)
         int64_t lines = 0;
         for (int k = 0; k < j.count; ++k)
             lines += j.one[k].lines;
-        const int64_t blocks = (lines * (DT / 4) + 255) / 256;
-        if (blocks > 0x7fffffff)
-            return RANS_E_ARG;
-        attention_join<T, DT><<<(uint32_t)blocks, 256, 0, s>>>(j);
+        in_pieces((lines * (DT / 4) + 255) / 256, 256, [&](int64_t first, uint32_t piece) {
+            j.first = first;
+            attention_join<T, DT><<<piece, 256, 0, s>>>(j);
+        });
     }
     return launched();
 }

@@ -162,8 +162,8 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
     constexpr int KK = DT / 16, ND = DT / 32;
     extern __shared__ __align__(16) uint8_t lds[];
 
-    const uint32_t block = xcd_order(blockIdx.x, a.blocks);
-    if (block >= a.blocks)
+    const uint32_t place = xcd_order(blockIdx.x, a.blocks), block = a.first + place;
+    if (place >= a.blocks)
         return;
     const uint32_t q_blocks = (uint32_t)((a.p.queries + 127) / 128);
     const uint32_t rest = block / q_blocks, bh = rest / (uint32_t)a.splits;
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
     extern __shared__ __align__(16) uint8_t lds[];
 
     const int rows = (int)a.p.queries * a.group, row_tiles = (rows + 31) / 32;
-    const uint32_t block = blockIdx.x;
+    const uint32_t block = a.first + blockIdx.x;
     const int split = (int)(block % (uint32_t)a.splits);
     const uint32_t rest = block / (uint32_t)a.splits;
     const int row_tile = (int)(rest % (uint32_t)row_tiles);
@@ -595,7 +595,7 @@ template <typename T, int DT, bool VEC>
 __global__ __launch_bounds__(256) void attention_rows_join(AttnArgs a, int groups)
 {
     constexpr int COLS = kJoinColumns<DT>;
-    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / COLS, line = id / groups;
+    const int64_t id = (((int64_t)a.first + blockIdx.x) * 256 + threadIdx.x) / COLS, line = id / groups;
     if (line >= a.p.batch * a.p.heads * a.p.queries) // all threads of a row, or none
         return;
     const int d = (int)(threadIdx.x % COLS) * 4, at = DT == 96 ? min(d, DT - 4) : d;
@@ -675,7 +675,10 @@ int run_forward(AttnArgs a, hipStream_t s)
             while (8 * groups < a.splits && 2 * groups * kJoinColumns<DT> <= 64)
                 groups *= 2;
             const int64_t threads = lines * groups * kJoinColumns<DT>;
-            attention_rows_join<T, DT, VEC><<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(a, groups);
+            in_pieces((threads + 255) / 256, 256, [&](int64_t first, uint32_t blocks) {
+                a.first = (uint32_t)first;
+                attention_rows_join<T, DT, VEC><<<blocks, 256, 0, s>>>(a, groups);
+            });
         }
     };
     if (plan.few) {
@@ -684,17 +687,19 @@ int run_forward(AttnArgs a, hipStream_t s)
             return rc;
         const int64_t rows = a.p.queries * a.group;
         const int64_t blocks = (rows + 31) / 32 * a.p.batch * a.p.kv_heads * a.splits;
-        if (blocks > 0x7fffffff)
+        if (blocks > kMostBlocks)
             return RANS_E_ARG;
-        attention_rows_forward<T, DT, VEC><<<(uint32_t)blocks, 256, G::kLds, s>>>(a);
+        in_pieces(blocks, 256, [&](int64_t first, uint32_t piece) {
+            a.first = (uint32_t)first;
+            attention_rows_forward<T, DT, VEC><<<piece, 256, G::kLds, s>>>(a);
+        });
         join();
         return launched();
     }
     using G = TilesForward<T, DT, VEC>;
     const int64_t blocks = (a.p.queries + 127) / 128 * a.p.batch * a.p.heads * a.splits;
-    if (blocks > 0x7fffff00)
+    if (blocks > kMostBlocks)
         return RANS_E_ARG;
-    a.blocks = (uint32_t)blocks;
     // Where windows or causal order make blocks of very different length, more LDS than they need
     // keeps a third block off a CU: more blocks are then left to fill the gaps that the short ones
     // leave (8160 x 8160 causal, 16 heads of 32 on 4: 131 us with two at a time, 152 with three).
@@ -704,7 +709,10 @@ int run_forward(AttnArgs a, hipStream_t s)
         constexpr auto kernel = attention_tiles_forward<T, DT, VEC, decltype(masked)::value>;
         if (const int rc = allow_lds<kernel>(G::kLds > kTwoBlocks ? G::kLds : kTwoBlocks))
             return rc;
-        kernel<<<xcd_grid(a.blocks), 256, lds, s>>>(a);
+        in_pieces(blocks, 256, [&](int64_t first, uint32_t piece) {
+            a.first = (uint32_t)first, a.blocks = piece;
+            kernel<<<xcd_grid(piece), 256, lds, s>>>(a);
+        });
         return (int)RANS_OK;
     });
     if (rc)

@@ -87,6 +87,16 @@ inline bool aligned_to(const void *p, uint64_t n)
 
 inline int launched() { return hipGetLastError() == hipSuccess ? RANS_OK : RANS_E_HIP; }
 
+// launch(first block, blocks) for all `blocks` of a call.  A launch's threads are counted in 32 bits: more
+// than those go out in several launches (each of a multiple of eight blocks but the last).
+template <typename F>
+void in_pieces(int64_t blocks, int threads, F &&launch)
+{
+    const int64_t most = 0xffffffffll / threads / 8 * 8;
+    for (int64_t first = 0; first < blocks; first += most)
+        launch(first, (uint32_t)(blocks - first < most ? blocks - first : most));
+}
+
 // Lets KERNEL take `bytes` of LDS, which is more than any may without it, on the current device; each
 // device is told once.
 template <auto KERNEL>

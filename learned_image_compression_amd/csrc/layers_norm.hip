@@ -54,7 +54,8 @@ struct NormArgs {
     int samples, channels, groups, per_group, param_dtype, act;
     int vecs, tile_vecs, tiles, chunks; // 16-byte vectors of a row, of a tile; tiles of a row
     bool past;                          // forward outputs pass the caches
-    uint32_t blocks;                    // resident: samples * groups
+    uint32_t blocks;                    // resident: samples * groups of the launch
+    uint32_t first;                     // the launch's first block of the call's
 };
 
 __device__ __forceinline__ float param(const void *p, int dtype, int c, float none)
@@ -241,7 +242,8 @@ template <typename T, int VEC>
 __global__ __launch_bounds__(kThreads) void norm_partial_forward(NormArgs a)
 {
     using V = Vec<T, VEC>;
-    const Place at(a, blockIdx.x, VEC);
+    const int64_t block = (int64_t)a.first + blockIdx.x;
+    const Place at(a, block, VEC);
     const T *base = static_cast<const T *>(a.x) + at.n * a.x_sample;
     float2 s[VEC];
     float shift[VEC];
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void norm_partial_forward(NormArgs a)
         });
     }
     const float count = (float)(at.row_end - at.row);
-    const int c_tile = (int)(blockIdx.x % a.tiles) * a.tile_vecs * VEC;
+    const int c_tile = (int)(block % a.tiles) * a.tile_vecs * VEC;
     float2 *part = a.part + ((int64_t)at.n * a.chunks + at.chunk) * a.channels;
     sum_over_rows<VEC>(at, a.tile_vecs, s, [&](int c, float2 t) {
         c += c_tile;
@@ -318,7 +320,7 @@ template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_output_forward(NormArgs a)
 {
     using V = Vec<T, VEC>;
-    const Place at(a, (int64_t)gridDim.x - 1 - blockIdx.x, VEC);
+    const Place at(a, (int64_t)a.samples * a.chunks * a.tiles - 1 - a.first - blockIdx.x, VEC);
     if (!at.active)
         return;
     float mean[VEC], gain[VEC], bias[VEC];
@@ -365,7 +367,8 @@ template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_partial_backward(NormArgs a)
 {
     using V = Vec<T, VEC>;
-    const Place at(a, blockIdx.x, VEC);
+    const int64_t block = (int64_t)a.first + blockIdx.x;
+    const Place at(a, block, VEC);
     float2 s[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
@@ -386,7 +389,7 @@ __global__ __launch_bounds__(kThreads) void norm_partial_backward(NormArgs a)
             }
         });
     }
-    const int c_tile = (int)(blockIdx.x % a.tiles) * a.tile_vecs * VEC;
+    const int c_tile = (int)(block % a.tiles) * a.tile_vecs * VEC;
     float2 *part = a.part + ((int64_t)at.n * a.chunks + at.chunk) * a.channels;
     sum_over_rows<VEC>(at, a.tile_vecs, s, [&](int c, float2 t) {
         if (c + c_tile < a.channels)
@@ -476,12 +479,12 @@ template <typename T, int VEC, int ACT>
 __global__ __launch_bounds__(kThreads) void norm_output_backward(NormArgs a)
 {
     using V = Vec<T, VEC>;
-    const int64_t main_blocks = (int64_t)a.samples * a.chunks * a.tiles;
-    if (blockIdx.x >= main_blocks) { // the last blocks of the launch
-        sum_over_samples(a, (int)(blockIdx.x - main_blocks));
+    const int64_t main_blocks = (int64_t)a.samples * a.chunks * a.tiles, block = (int64_t)a.first + blockIdx.x;
+    if (block >= main_blocks) { // the last blocks of the call
+        sum_over_samples(a, (int)(block - main_blocks));
         return;
     }
-    const Place at(a, main_blocks - 1 - blockIdx.x, VEC);
+    const Place at(a, main_blocks - 1 - block, VEC);
     if (!at.active)
         return;
     const Channels<VEC> ch(a, at.n, at.c0);
@@ -519,8 +522,9 @@ struct Resident {
 
     __device__ Resident(const NormArgs &a, int vec)
     {
-        const uint32_t each = (a.blocks + 7) / 8, block = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
-        active = block < a.blocks;
+        const uint32_t each = (a.blocks + 7) / 8, place = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
+        const uint32_t block = a.first + place;
+        active = place < a.blocks;
         n = (int)(block / (uint32_t)a.groups);
         g = (int)(block - (uint32_t)n * a.groups);
         const int t = (int)threadIdx.x, width = a.per_group / vec;
@@ -790,28 +794,34 @@ bool resident_pays(const NormArgs &a, int64_t lds, int vec)
 }
 
 template <typename T>
-int run_resident_forward(const NormArgs &a, int vec, int64_t lds, hipStream_t s)
+int run_resident_forward(NormArgs a, int vec, int64_t lds, hipStream_t s)
 {
     return with_vec<T>(vec, [&](auto v) {
         return with_act(a.act, [&](auto act) {
             constexpr auto kernel = norm_resident_forward<T, v.value, act.value>;
             if (const int rc = allow_lds<kernel>(kMostForward))
                 return rc;
-            kernel<<<(a.blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
+            in_pieces((int64_t)a.samples * a.groups, kResident, [&](int64_t first, uint32_t blocks) {
+                a.first = (uint32_t)first, a.blocks = blocks;
+                kernel<<<(blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
+            });
             return launched();
         });
     });
 }
 
 template <typename T>
-int run_resident_backward(const NormArgs &a, int vec, int64_t lds, hipStream_t s)
+int run_resident_backward(NormArgs a, int vec, int64_t lds, hipStream_t s)
 {
     return with_vec<T>(vec, [&](auto v) {
         return with_act(a.act, [&](auto act) {
             constexpr auto kernel = norm_resident_backward<T, v.value, act.value>;
             if (const int rc = allow_lds<kernel>(kMostBackward))
                 return rc;
-            kernel<<<(a.blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
+            in_pieces((int64_t)a.samples * a.groups, kResident, [&](int64_t first, uint32_t blocks) {
+                a.first = (uint32_t)first, a.blocks = blocks;
+                kernel<<<(blocks + 7) / 8 * 8, kResident, (uint32_t)lds, s>>>(a);
+            });
             if (a.samples > 1 && (a.dweight || a.dbias))
                 norm_samples<<<(a.channels + 31) / 32, kThreads, 0, s>>>(a);
             return launched();
@@ -826,11 +836,17 @@ int run_forward(NormArgs a, hipStream_t s)
     choose_chunks(a);
     // 200 MB in and out: 117 us with outputs past the caches, 134 through them
     a.past = 2 * (int64_t)sizeof(T) * a.samples * a.positions * a.channels > kCacheBytes;
-    const dim3 grid((uint32_t)((int64_t)a.samples * a.chunks * a.tiles));
-    norm_partial_forward<T, VEC><<<grid, kThreads, 0, s>>>(a);
+    const int64_t blocks = (int64_t)a.samples * a.chunks * a.tiles;
+    in_pieces(blocks, kThreads, [&](int64_t first, uint32_t piece) {
+        a.first = (uint32_t)first;
+        norm_partial_forward<T, VEC><<<piece, kThreads, 0, s>>>(a);
+    });
     norm_join_forward<<<dim3(a.groups, a.samples), kThreads, 0, s>>>(a);
     return with_act(a.act, [&](auto act) {
-        norm_output_forward<T, VEC, act.value><<<grid, kThreads, 0, s>>>(a);
+        in_pieces(blocks, kThreads, [&](int64_t first, uint32_t piece) {
+            a.first = (uint32_t)first;
+            norm_output_forward<T, VEC, act.value><<<piece, kThreads, 0, s>>>(a);
+        });
         return launched();
     });
 }
@@ -840,12 +856,18 @@ int run_backward(NormArgs a, hipStream_t s)
 {
     choose_tiles(a, VEC);
     choose_chunks(a);
-    const uint32_t blocks = (uint32_t)((int64_t)a.samples * a.chunks * a.tiles);
-    const uint32_t more = a.dweight || a.dbias ? (uint32_t)((a.channels + 31) / 32) : 0u;
+    const int64_t blocks = (int64_t)a.samples * a.chunks * a.tiles;
+    const int more = a.dweight || a.dbias ? (a.channels + 31) / 32 : 0;
     return with_act(a.act, [&](auto act) {
-        norm_partial_backward<T, VEC, act.value><<<blocks, kThreads, 0, s>>>(a);
+        in_pieces(blocks, kThreads, [&](int64_t first, uint32_t piece) {
+            a.first = (uint32_t)first;
+            norm_partial_backward<T, VEC, act.value><<<piece, kThreads, 0, s>>>(a);
+        });
         norm_join_backward<<<dim3(a.groups, a.samples), kThreads, 0, s>>>(a);
-        norm_output_backward<T, VEC, act.value><<<blocks + more, kThreads, 0, s>>>(a);
+        in_pieces(blocks + more, kThreads, [&](int64_t first, uint32_t piece) {
+            a.first = (uint32_t)first;
+            norm_output_backward<T, VEC, act.value><<<piece, kThreads, 0, s>>>(a);
+        });
         return launched();
     });
 }

@@ -20,7 +20,7 @@ struct RotaryArgs {
     lic_rotary_args p;
     uint32_t turn_units, units; // units of a head: turning, then copying
     uint32_t all_heads;
-    uint64_t total;
+    uint64_t total, first; // threads of the call; the launch's first block
 };
 
 template <typename T, int V, bool INTER>
@@ -28,7 +28,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryArgs a)
 {
     using VT = Vec<T, V>;
     const lic_rotary_args &p = a.p;
-    const uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    const uint64_t id = (a.first + blockIdx.x) * kThreads + threadIdx.x;
     if (id >= a.total)
         return;
     const uint64_t row = id / a.units; // (batch, token, head)
@@ -112,14 +112,14 @@ struct TableArgs {
     const double *coords;
     float *cos, *sin;
     double base, factor, low, high, original, amplitude;
-    uint64_t total;
+    uint64_t total, first;
     int axes, pairs;
 };
 
 // One thread an angle.  Once for a model, so double precision costs nothing.
 __global__ __launch_bounds__(kThreads) void rotary_table_kernel(TableArgs a)
 {
-    const uint64_t id = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    const uint64_t id = (a.first + blockIdx.x) * kThreads + threadIdx.x;
     if (id >= a.total)
         return;
     const uint64_t row = id / (uint32_t)a.pairs;
@@ -147,14 +147,17 @@ int run_rotary(RotaryArgs a, hipStream_t s)
     a.turn_units = (uint32_t)(p.rotary_dim / 2 / V);
     a.units = a.turn_units + (uint32_t)((p.dim - p.rotary_dim + 2 * V - 1) / (2 * V));
     a.all_heads = (uint32_t)(p.heads + p.kv_heads);
-    a.total = (uint64_t)p.batch * p.tokens * a.all_heads * a.units;
-    const uint64_t blocks = (a.total + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffull)
+    const uint64_t rows = (uint64_t)p.batch * p.tokens * a.all_heads; // at most 2^57
+    if (rows > (1ull << 48) / a.units)
         return RANS_E_ARG;
-    if (p.interleaved)
-        rotary_kernel<T, V, true><<<(uint32_t)blocks, kThreads, 0, s>>>(a);
-    else
-        rotary_kernel<T, V, false><<<(uint32_t)blocks, kThreads, 0, s>>>(a);
+    a.total = rows * a.units;
+    in_pieces((int64_t)((a.total + kThreads - 1) / kThreads), kThreads, [&](int64_t first, uint32_t blocks) {
+        a.first = (uint64_t)first;
+        if (p.interleaved)
+            rotary_kernel<T, V, true><<<blocks, kThreads, 0, s>>>(a);
+        else
+            rotary_kernel<T, V, false><<<blocks, kThreads, 0, s>>>(a);
+    });
     return launched();
 }
 
@@ -185,11 +188,11 @@ extern "C" int lic_rotary_table(const double *coords, int64_t rows, int32_t axes
     if (!coords || !cos || !sin)
         return RANS_E_ARG;
     TableArgs a{coords, cos, sin, base, factor, low, high, original, amplitude,
-                (uint64_t)rows * (uint64_t)(rotary_dim / 2), axes, rotary_dim / 2};
-    const uint64_t blocks = (a.total + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffull)
-        return RANS_E_ARG;
-    rotary_table_kernel<<<(uint32_t)blocks, kThreads, 0, hstream>>>(a);
+                (uint64_t)rows * (uint64_t)(rotary_dim / 2), 0, axes, rotary_dim / 2};
+    in_pieces((int64_t)((a.total + kThreads - 1) / kThreads), kThreads, [&](int64_t first, uint32_t blocks) {
+        a.first = (uint64_t)first;
+        rotary_table_kernel<<<blocks, kThreads, 0, hstream>>>(a);
+    });
     return launched();
 }
 

@@ -344,3 +344,36 @@ def test_outputs_that_overlap_are_refused(L):
     x = normal(g, 2, 4, 8).transpose(1, 2)
     with pytest.raises(ValueError, match="overlap"):
         L.group_norm_forward(x, 2, out=torch.empty(2, 1, 8, device="cuda").expand(2, 4, 8).transpose(1, 2))
+
+
+# ---- launches past 2^32 threads ---------------------------------------------------------
+
+
+def test_rotary_of_more_threads_than_a_launch_has(L):
+    """2^32 threads and more of two values each (heads of 6): several launches."""
+    g = gen(1)
+    s, h = 1 << 20, 1366
+    cos, sin = normal(g, s, 3), normal(g, s, 3)
+    some = normal(g, 1, 1, h, 6, dtype=BF16)
+    q = torch.empty(1, s, h, 6, dtype=BF16, device="cuda")
+    q.copy_(some.expand(1, s, h, 6))
+    got, _ = L.rotary(q, None, cos, sin, out=(q, None))
+    at = torch.cat((torch.arange(3, device="cuda"), torch.randint(0, s, (200,), generator=g, device="cuda"),
+                    torch.arange(s - 3, s, device="cuda")))
+    want = R.turn(some.expand(1, len(at), h, 6), cos[at], sin[at], None, False)
+    passes(got[:, at], want, R.UNIT[BF16] * want.abs() + 4 * 2.0 ** -24 * some.double().abs().max() * 4, "turned")
+
+
+def test_attention_of_more_threads_than_a_launch_has(L):
+    """More than 2^24 blocks of 256 threads: one query on one key, whose value is the result."""
+    b, h, d = 1 << 20, 17, 8
+    g = gen(2)
+    q, k, v, dout = (normal(g, b, 1, h, d, dtype=BF16) for _ in range(4))
+    out, lse = L.attention_forward(q, k, v)
+    assert torch.equal(out, v)
+    want = (q.float() * k.float()).sum(3).transpose(1, 2) * d ** -0.5
+    assert float((lse - want).abs().max()) <= R.F32 * (1 + float(want.abs().max()))
+    dq, dk, dv = L.attention_backward(dout, q, k, v, out, lse)
+    # the probability is 1, off by what exp and lse leave of it
+    assert float(((dv.float() - dout.float()).abs() - (2.0 ** -8 + 1e-4) * dout.float().abs()).max()) <= 0
+    assert float(dq.abs().max()) < 0.01 and float(dk.abs().max()) < 0.01

@@ -9,7 +9,7 @@ import sys
 
 import pytest
 
-from test_layers_abi_cpu import NORM, attention_args, layers  # noqa: F401 - a fixture
+from test_layers_abi_cpu import NORM, ROTARY, attention_args, layers  # noqa: F401 - a fixture
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 NAMES = ("launches", "blocks", "too_many_threads", "too_much_lds", "attributes")
@@ -65,6 +65,14 @@ def norm(backward=0, device=0, **kw):
              a["eps"], a["act"], a["y"], a["ys"], a["yr"], a["mean"], a["rstd"], a["ws"], a["bytes"], 0]]
 
 
+def rotary(layers, **kw):  # noqa: F811
+    a = {**ROTARY, **kw}
+    args = layers._ROTARY.pack(*(a[k] for k in ("q", "k", "qo", "ko", "cos", "sin", "pos", "status", "step")),
+                               *a["strides"], *(a[k] for k in ("b", "s", "h", "kh", "d", "r", "rows", "dtype",
+                                                               "inter", "inv")))
+    return [0, 0, "lic_rotary", "bp", [args.hex(), 0]]
+
+
 def every_kernel(layers, device):  # noqa: F811
     """Calls of all types, widths, kinds of masks and loads, of few and of many queries; norms of one launch."""
     jobs = []
@@ -104,3 +112,30 @@ def test_a_device_without_the_lds_is_an_error(layers, stand_in):  # noqa: F811
     rows = stand_in(*jobs)
     assert [r["rc"] for r in rows] == [-8] * 3 + [0] * 3
     assert sum(r["too_much_lds"] for r in rows) == 0 and sum(r["launches"] for r in rows[:3]) == 0
+
+def test_no_launch_has_more_threads_than_it_can(layers, stand_in):  # noqa: F811
+    """Past 2^32 threads a call is several launches."""
+    few, many = dict(b=1 << 20, n=1, m=1, h=17, kv=17, d=8), dict(b=1 << 20, n=200, m=200, h=32, kv=32, d=8)
+    wide = (1 << 50, 1 << 20, 1 << 10) * 8
+    jobs, least = [], []
+    for sizes, blocks in ((few, 17 << 20), (many, 2 * (32 << 20))):
+        for backward in (0, 1):
+            jobs.append(attention(layers, backward, strides=wide, **sizes))
+            least.append(blocks * (2 if backward else 1))
+    jobs.append(rotary(layers, strides=wide[:12], s=1 << 20, h=1366, kh=0, d=6, r=6, rows=1 << 20))
+    least.append((1 << 20) * 1366 * 3 // 256)
+    jobs.append([0, 0, "lic_rotary_table", "pqiiddddddppp",
+                 [256, 1 << 31, 1, 64, 1e4, 1.0, 0.0, 0.0, 0.0, 1.0, 512, 1024, 0]])
+    least.append((1 << 31) * 32 // 256)
+    for backward in (0, 1):
+        jobs.append(norm(backward, n=65535, c=192, g=192, s=4096, dtype=2))  # one launch of 512 threads a group
+        least.append(65535 * 192)
+        jobs.append(norm(backward, n=65535, c=65533, g=1, s=9))              # single channels, three launches
+        least.append(2 * 65535 * (65533 // 256))
+    for row, blocks in zip(stand_in(*jobs), least):
+        assert row["rc"] == 0 and row["too_many_threads"] == 0 and row["launches"] >= 2 and row["blocks"] >= blocks
+
+
+def test_sizes_that_no_count_holds_are_refused(layers, stand_in):  # noqa: F811
+    row, = stand_in(rotary(layers, b=1 << 20, s=1 << 20, h=65536, kh=65536, d=65536, r=2, rows=1 << 20))
+    assert row["rc"] == -1 and row["launches"] == 0
