@@ -185,6 +185,17 @@ def _with_workspace(device, stream: int, call, size, where: str):
         _check_rc(rc, where)
 
 
+def release_workspaces() -> None:
+    """Give the scratch memory of all streams back to the allocator.
+
+    It is as large as a stream's largest call needed and otherwise kept for the next.  Work that
+    is still queued may go on using it, as any freed tensor of its stream.
+    """
+    for workspace in list(_workspaces.values()):
+        with workspace.lock:
+            workspace.held = _NO_WORKSPACE
+
+
 # ---- derivatives -----------------------------------------------------------
 
 

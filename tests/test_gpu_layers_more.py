@@ -377,3 +377,19 @@ def test_attention_of_more_threads_than_a_launch_has(L):
     # the probability is 1, off by what exp and lse leave of it
     assert float(((dv.float() - dout.float()).abs() - (2.0 ** -8 + 1e-4) * dout.float().abs()).max()) <= 0
     assert float(dq.abs().max()) < 0.01 and float(dk.abs().max()) < 0.01
+
+
+# ---- scratch memory ----------------------------------------------------------------------
+
+
+def test_scratch_memory_can_be_given_back_while_it_is_used(L):
+    g = gen(6)
+    q, k, v = normal(g, 8, 1, 8, 64, dtype=BF16), *(normal(g, 8, 6000, 2, 64, dtype=BF16) for _ in range(2))
+    want, _ = L.attention_forward(q, k, v)
+    before = torch.cuda.memory_allocated()
+    out = [L.attention_forward(q, k, v)[0]]
+    L.release_workspaces()
+    assert torch.cuda.memory_allocated() < before
+    torch.full((1 << 22,), math.nan, device="cuda")  # takes the memory, behind the call
+    out.append(L.attention_forward(q, k, v)[0])
+    assert all(torch.equal(o, want) for o in out)

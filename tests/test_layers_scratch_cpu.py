@@ -104,3 +104,19 @@ def test_a_refused_call_leaves_the_lock():
     with pytest.raises(RuntimeError):
         L._with_workspace(HOST, 0, lambda a, n: -1, lambda: 10, "stand-in")
     in_threads([lambda: L._with_workspace(HOST, 0, lambda a, n: 0, lambda: 10, "stand-in")])
+
+
+def test_scratch_memory_can_be_given_back():
+    import weakref
+
+    def call(address, nbytes):
+        return 0 if nbytes else REFUSED
+
+    for stream in (0, 1):
+        L._with_workspace(HOST, stream, call, lambda: 1 << 22, "stand-in")
+    kept = [weakref.ref(w.held[2]) for w in L._workspaces.values()]
+    assert len(kept) == 2 and all(k() is not None for k in kept)
+    L.release_workspaces()
+    assert all(k() is None for k in kept)
+    L._with_workspace(HOST, 0, call, lambda: 1 << 22, "stand-in")  # and taken again
+    assert L._workspaces[(None, 0)].held[1] == 1 << 22
