@@ -613,6 +613,56 @@ __device__ __forceinline__ uint64_t rows_of(bool flag)
     return (f | (f >> 32)) & 0xffffffffull;
 }
 
+// Whether a row holds a NaN, only NaN, or anything that is not finite.
+struct Kinds {
+    bool nan = false, all_nan = true, odd = false;
+
+    template <typename T>
+    __device__ __forceinline__ void add(const T *row, int dim)
+    {
+        for (int d = 0; d < dim; ++d) {
+            const float x = up(row[d]);
+            nan |= x != x, all_nan &= x != x, odd |= not_finite(x);
+        }
+    }
+};
+
+// Which of a wave's results that are not finite (rows: a lane's l % 32) have to be formed again.  Hidden
+// pairs have p = 0, but 0 times a NaN or an infinity of theirs is NaN.  So a row is right as it is if it
+// sees something that makes all of its values NaN whatever is hidden, or if it sees something that
+// is not finite and nothing hidden is.  The others, and those that see only finite numbers (sums too
+// large in 32 bits), are formed again, at hundreds of times the cost.
+struct Again {
+    static constexpr unsigned kStains = 1, kOdd = 2, kAllNan = 4; // where it is hidden; where it is seen
+    uint64_t rows, seen = 0, hidden = 0;
+
+    __device__ __forceinline__ explicit Again(uint64_t bad) : rows(bad) {}
+
+    // What the rows do or do not see at [x, x + n), n <= 64: kind(x) of what is there, sees(x) whether the
+    // lane's row does.  all: the lane's row sees all of it.
+    template <typename Kind, typename Sees>
+    __device__ __forceinline__ void look(int x, int n, bool all, Kind &&kind, Sees &&sees)
+    {
+        const int lane = threadIdx.x & 63;
+        const bool mine = (rows >> (lane & 31)) & 1;
+        if (!(rows & ~seen) && __all(all || !mine))
+            return;
+        const unsigned k = lane < n ? kind(x + lane) : 0u;
+        const uint64_t stains = __builtin_amdgcn_ballot_w64((k & kStains) != 0);
+        const uint64_t all_nan = __builtin_amdgcn_ballot_w64((k & kAllNan) != 0);
+        for (uint64_t at = __builtin_amdgcn_ballot_w64(k != 0); at && rows; at &= at - 1) {
+            const int j = __builtin_ctzll(at);
+            const uint64_t they = rows_of(sees(x + j));
+            seen |= they;
+            if ((stains >> j) & 1)
+                hidden |= ~they;
+            if ((all_nan >> j) & 1)
+                rows &= ~they;
+        }
+    }
+    __device__ __forceinline__ uint64_t which() const { return rows & (hidden | ~seen); }
+};
+
 // A lane's part of an accumulator's column, times f, to columns 32 block .. of a row.
 template <typename T, bool VEC>
 __device__ __forceinline__ void put_column(T *out, const float16v &v, float f, int block, int h, int dim)

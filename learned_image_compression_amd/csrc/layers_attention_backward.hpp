@@ -436,6 +436,40 @@ attention_keys_backward(AttnArgs a)
         for (int i = 0; i < 16; ++i)
             bad |= not_finite(dk[n][i]) || not_finite(dv[n][i]);
     uint64_t redo = rows_of(bad && key < len);
+    if (redo) {
+        const AttnArgs &a = rare_args();
+        Kinds own_key, own_value;
+        if (key < len) {
+            own_key.add(head_row<T>(a.p.k, a.p.k_stride, b, key, kv), dim);
+            own_value.add(head_row<T>(a.p.v, a.p.v_stride, b, key, kv), dim);
+        }
+        const uint64_t nan_keys = rows_of(own_key.nan); // all of it is NaN as soon as a query sees them
+        Again which(redo);
+        which.seen = rows_of(own_key.odd || own_value.odd);
+        for (int i = first; i < end; ++i) {
+            const int q0 = lo + (i % tiles) * NQ, hd = kv * a.group + i / tiles;
+            const int64_t line0 = ((int64_t)b * a.p.heads + hd) * a.p.queries;
+            const auto sees = [&](int query) {
+                return key < len && range.holds(query) &&
+                       (!a.p.mask || mask_row(a, b, hd, query)[key * a.p.mask_stride[3]] != 0);
+            };
+            which.look(
+                q0, NQ, !a.p.mask && range.covers(q0, NQ),
+                [&](int query) {
+                    query = min(query, (int)a.p.queries - 1); // as the last tile has it
+                    Kinds q, g;
+                    q.add(head_row<T>(a.p.q, a.p.q_stride, b, query, hd), dim);
+                    g.add(head_row<T>(a.p.dout, a.p.dout_stride, b, query, hd), dim);
+                    const float lse = a.row_lse[line0 + query], delta = a.row_delta[line0 + query];
+                    return (q.odd || g.odd ? 1u : 0u) | (q.odd || g.odd || lse != lse || not_finite(delta) ? 2u : 0u) |
+                           (q.nan || g.all_nan || lse != lse ? 4u : 0u);
+                },
+                sees);
+            for (int x = q0; x < q0 + NQ && (nan_keys & which.rows); ++x)
+                which.rows &= ~(nan_keys & rows_of(sees(x)));
+        }
+        redo = which.which();
+    }
     const bool again = (redo >> (lane & 31)) & 1;
     const float scale = (float)a.p.scale;
     const int64_t keys_all = a.p.batch * a.p.kv_heads * a.p.keys;
@@ -669,7 +703,26 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             bad |= not_finite(dq[n][i]);
-    uint64_t redo = rows_of(bad && there);
+    // D or lse of NaN: so is all of a row that sees a key
+    uint64_t redo = rows_of(bad && there && !(lse != lse || (delta != delta && lse < INFINITY)));
+    if (redo) {
+        const AttnArgs &a = rare_args();
+        Again again(redo);
+        again.seen = rows_of(not_finite(delta));
+        const int64_t step = a.p.mask_stride[3];
+        for (int k0 = lo; k0 < hi; k0 += G::kKeys)
+            again.look(
+                k0, G::kKeys, MASK == Masked::none && range.covers(k0, G::kKeys),
+                [&](int key) {
+                    key = min(key, len - 1); // as the last tile has it
+                    Kinds k, v;
+                    k.add(kbase + key * ks, dim);
+                    v.add(vbase + key * vs, dim);
+                    return (k.odd ? 1u : 0u) | (k.odd || v.odd ? 2u : 0u) | (k.nan || v.nan ? 4u : 0u);
+                },
+                [&](int key) { return range.holds(key) && (MASK == Masked::none || mask[key * step] != 0); });
+        redo = again.which();
+    }
     const float scale = (float)a.p.scale;
     const int64_t lines = a.p.batch * a.p.heads * a.p.queries;
     if (there && !((redo >> (lane & 31)) & 1)) {

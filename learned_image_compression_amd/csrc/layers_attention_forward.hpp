@@ -71,7 +71,7 @@ __device__ __forceinline__ void soften(float16v (&s)[N], float scale, float &m, 
     l += sum;
 }
 
-// A row that came out not finite, again and with the keys that it sees alone: a NaN or
+// A row that came out not finite (see Again), again and with the keys that it sees alone: a NaN or
 // an infinity of a key it does not see is multiplied by its probability 0 above.
 // Lane l takes key l of each 64, then column l (and l + 64) of the sum.
 template <typename T>
@@ -288,7 +288,23 @@ __global__ __launch_bounds__(256, (DT <= 64 || sizeof(T) == 2) ? 2 : 1) void att
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             bad |= not_finite(o[n][i]);
-    uint64_t redo = rows_of(bad && query < a.p.queries);
+    // a sum of NaN: the scores that the row sees, and all of it is NaN
+    uint64_t redo = rows_of(bad && query < a.p.queries && total == total);
+    if (redo) {
+        const AttnArgs &a = rare_args();
+        Again again(redo);
+        const int64_t step = a.p.mask_stride[3];
+        for (int k0 = lo; k0 < hi; k0 += G::kKeys) // the last tile repeats the last key
+            again.look(
+                k0, G::kKeys, MASK == Masked::none && range.covers(k0, G::kKeys),
+                [&](int key) {
+                    Kinds v;
+                    v.add(vbase + min(key, len - 1) * vs, dim);
+                    return v.all_nan ? 7u : v.odd ? 3u : 0u;
+                },
+                [&](int key) { return range.holds(key) && (MASK == Masked::none || mask[key * step] != 0); });
+        redo = again.which();
+    }
     if (query < a.p.queries && !((redo >> (lane & 31)) & 1)) {
         const int64_t line = ((int64_t)b * a.p.heads + head) * a.p.queries + query;
         if (a.splits == 1) {
@@ -494,7 +510,23 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void attention_rows_fo
     if (h == 0)
         stats[wave * 32 + lane] = make_float2(m, l);
     wave_fence();
-    for (uint64_t redo = rows_of(bad && row < rows); redo; redo &= redo - 1) {
+    uint64_t redo = rows_of(bad && row < rows && l == l); // as above, of this wave's tiles
+    if (redo) {
+        const AttnArgs &a = rare_args();
+        Again again(redo);
+        const int64_t step = a.p.mask_stride[3];
+        for (int64_t c0 = first + __builtin_amdgcn_readfirstlane(wave) * 32; c0 < end; c0 += 128)
+            again.look(
+                (int)c0, 32, !mask && c0 + 32 <= end && range.covers((int)c0, 32),
+                [&](int key) {
+                    Kinds v;
+                    v.add(vbase + min(key, end - 1) * vs, dim);
+                    return v.all_nan ? 7u : v.odd ? 3u : 0u;
+                },
+                [&](int key) { return key < end && range.holds(key) && (!mask || mask[key * step] != 0); });
+        redo = again.which();
+    }
+    for (; redo; redo &= redo - 1) {
         const AttnArgs &a = rare_args();
         const int j = __builtin_ctzll(redo);
         const int r = row_tile * 32 + j;

@@ -393,3 +393,42 @@ def test_scratch_memory_can_be_given_back_while_it_is_used(L):
     torch.full((1 << 22,), math.nan, device="cuda")  # takes the memory, behind the call
     out.append(L.attention_forward(q, k, v)[0])
     assert all(torch.equal(o, want) for o in out)
+
+
+# ---- what a NaN costs --------------------------------------------------------------------
+
+
+def microseconds(f):
+    f()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    start.record()
+    for _ in range(3):
+        f()
+    end.record()
+    torch.cuda.synchronize()
+    return start.elapsed_time(end) * 1000 / 3
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("options", [{}, {"causal": True}, {"window": (100, 50)}, {"mask": True}])
+@pytest.mark.parametrize("where,value", [("q", math.nan), ("q", math.inf), ("v", math.nan), ("dout", math.nan)])
+def test_overflow_costs_little(L, options, where, value, dtype):
+    """A training step that has overflowed takes about as long as any other (it took 14 to 216 times as
+    long): what is NaN because of what a row sees is not formed again."""
+    g = gen(3)
+    b, n, h, d = 2, 1500, 4, 64
+    options = dict(options)
+    if "mask" in options:
+        options["mask"] = torch.rand(n, n, generator=g, device="cuda") < 0.5
+    t = {name: normal(g, b, n, h, d, dtype=dtype) for name in ("q", "k", "v", "dout")}
+
+    def call():
+        out, lse = L.attention_forward(t["q"], t["k"], t["v"], **options)
+        L.attention_backward(t["dout"], t["q"], t["k"], t["v"], out, lse, **options)
+
+    usual = microseconds(call)
+    t[where].fill_(value)
+    strange = microseconds(call)
+    print(f"{usual:.0f} us, with {value} in {where} {strange:.0f} us", flush=True)
+    assert strange < 10 * usual
