@@ -50,9 +50,12 @@ struct Lift {
             top = fmaxf(top, fabsf(ds[i]));
         top = pair_max(top); // a row's two lanes
         if (__builtin_amdgcn_ballot_w64(top > kMost)) {
-            // an infinity stays one
-            const bool lower = top > kMost && top < INFINITY;
-            const float by = lower ? __builtin_amdgcn_ldexpf(1.0f, kAim - __builtin_amdgcn_frexp_expf(top)) : 1.0f;
+            top = 0.0f; // of the finite ones: the others stay as they are
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = fmaxf(top, not_finite(ds[i]) ? 0.0f : fabsf(ds[i]));
+            top = pair_max(top);
+            const float by = top > kMost ? __builtin_amdgcn_ldexpf(1.0f, kAim - __builtin_amdgcn_frexp_expf(top)) : 1.0f;
             f *= by;
             for (int i = 0; i < count; ++i)
                 more[i] *= by;

@@ -432,3 +432,77 @@ def test_overflow_costs_little(L, options, where, value, dtype):
     strange = microseconds(call)
     print(f"{usual:.0f} us, with {value} in {where} {strange:.0f} us", flush=True)
     assert strange < 10 * usual
+
+
+def seen_sum(weights, values, ok):
+    """[.., rows, dim] sums of weights x values over the last axis of `ok` [.., rows, others], over what it
+    shows alone: 0 times an infinity is not formed."""
+    return torch.where(ok[..., None], weights[..., None] * values[..., None, :, :], 0.0).sum(-2)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("b,q,s,h,kv,d,options", [
+    (1, 1, 300, 4, 2, 32, {}),
+    (2, 20, 200, 2, 1, 64, {"causal": True}),
+    (3, 150, 150, 2, 2, 32, {"causal": True}),
+    (12, 70, 130, 8, 4, 24, {"window": (20, 9)}),
+    (2, 140, 140, 2, 1, 128, {"mask": 0.5}),
+    (3, 130, 190, 2, 2, 40, {"lengths": [190, 77, 0]}),
+    (1, 140, 600, 1, 1, 96, {"mask": 0.9}),
+    (2, 129, 129, 2, 2, 33, {"causal": True}),
+])
+@pytest.mark.parametrize("where", ["k", "v", "q", "dout", "k v q dout"])
+def test_attention_of_scattered_infinities(L, b, q, s, h, kv, d, options, where, dtype):
+    """What is not finite is so in the very places, and of the very kind, that the formula gives when
+    it is summed over what is seen alone."""
+    g = gen(q + s)
+    options = dict(options)
+    if "mask" in options:
+        options["mask"] = torch.rand(b, 1, q, s, generator=g, device="cuda") < options["mask"]
+    if "lengths" in options:
+        options = {"key_lengths": torch.tensor(options["lengths"], dtype=torch.int32, device="cuda")}
+    t = {"q": normal(g, b, q, h, d), "k": normal(g, b, s, kv, d), "v": normal(g, b, s, kv, d),
+         "dout": normal(g, b, q, h, d)}
+    for name in where.split():
+        x = t[name]
+        rows = torch.rand(x.shape[:3], generator=g, device="cuda")[..., None]
+        part = torch.rand(x.shape, generator=g, device="cuda")
+        x[(rows < 0.03) & (part < 0.1)] = math.inf       # here and there in a row
+        x[(rows > 0.97) & (part < 0.1)] = -math.inf
+        x[(rows > 0.48) & (rows < 0.5) & (part < 0.2)] = math.nan
+        x[((rows > 0.5) & (rows < 0.51)).expand_as(x)] = math.nan  # all of a row
+    t = {k: x.to(dtype) for k, x in t.items()}
+    out, lse = L.attention_forward(t["q"], t["k"], t["v"], **options)
+    dq, dk, dv = L.attention_backward(t["dout"], t["q"], t["k"], t["v"], out, lse, **options)
+
+    ok = R.seen(b, h, q, s, "cuda", **options)
+    qd, dod = (t[n].double().permute(0, 2, 1, 3) for n in ("q", "dout"))
+    kd, vd = (t[n].double().permute(0, 2, 1, 3).repeat_interleave(h // kv, 1) for n in ("k", "v"))
+    scale = d ** -0.5
+    a = torch.where(ok, (qd @ kd.transpose(2, 3).contiguous()) * scale, -math.inf)
+    m = torch.nan_to_num(a, nan=-math.inf, posinf=math.inf).amax(3, keepdim=True)
+    e = torch.where(ok, torch.exp(a - torch.where(m == -math.inf, 0.0, m)), 0.0)
+    total = e.sum(3, keepdim=True)
+    p = e / torch.where(total == 0, 1.0, total)
+    o = seen_sum(p, vd, ok)
+    od = out.double().permute(0, 2, 1, 3)  # D is formed from what the forward call gave
+    ds = p * (dod @ vd.transpose(2, 3).contiguous() - (dod * od).sum(3, keepdim=True))
+    turned = ok.transpose(2, 3)
+
+    def back(x):
+        return x.permute(0, 2, 1, 3)
+
+    def gather(x):
+        return back(x.reshape(b, kv, h // kv, s, d).sum(2))
+
+    want = {"out": back(o), "dq": back(seen_sum(ds, kd, ok)) * scale,
+            "dk": gather(seen_sum(ds.transpose(2, 3), qd, turned)) * scale,
+            "dv": gather(seen_sum(p.transpose(2, 3), dod, turned))}
+    for name, got in (("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+        w = want[name]
+        kinds = [torch.nan_to_num(x.double(), nan=3.0, posinf=2.0, neginf=-2.0).where(~torch.isfinite(x), 0.0)
+                 for x in (got, w)]
+        assert torch.equal(*kinds), name
+        fine = torch.isfinite(w)
+        if bool(fine.any()):
+            assert float((got.double() - w)[fine].abs().max()) <= 0.05 * max(1.0, float(w[fine].abs().max())), name
