@@ -506,3 +506,42 @@ def test_attention_of_scattered_infinities(L, b, q, s, h, kv, d, options, where,
         fine = torch.isfinite(w)
         if bool(fine.any()):
             assert float((got.double() - w)[fine].abs().max()) <= 0.05 * max(1.0, float(w[fine].abs().max())), name
+
+
+# ---- group norm at other sizes -----------------------------------------------------------
+
+
+def norm_passes(L, n, s, c, groups, dtype, kind, backward=True):
+    g = gen(s + c)
+    x = (1.5 * normal(g, n, s, c) + normal(g, c)).to(dtype).transpose(1, 2)
+    w, b = 1 + 0.3 * normal(g, c), 0.3 * normal(g, c)
+    dy = normal(g, n, s, c, dtype=dtype).transpose(1, 2) if backward else None
+    y, mean, rstd = L.group_norm_forward(x, groups, w, b, activation=kind)
+    r = R.group_norm(x, groups, w, b, 1e-5, kind, dy)
+    u = R.UNIT[dtype]
+    passes(y, r["y"], u * r["y"].abs() + R.F32 * (1 + r["u"].abs()), "y")
+    passes(mean, r["mean"], R.F32 * (1 + r["mean"].abs()), "mean")
+    passes(rstd, r["rstd"], R.F32 * r["rstd"], "rstd")
+    if backward:
+        dx, dw, db = L.group_norm_backward(dy, x, groups, w, b, mean, rstd, activation=kind)
+        passes(dx, r["dx"], u * r["dx"].abs() + R.F32 * r["dx_abs"], "dx")
+        passes(dw, r["dw"], R.UNIT[F32] * r["dw"].abs() + R.F32 * (r["dw_abs"] + r["db_abs"]), "dw")
+        passes(db, r["db"], R.UNIT[F32] * r["db"].abs() + R.F32 * r["db_abs"], "db")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("n,s,c,groups", [(1, 8160, 192, 32), (2, 32640, 96, 8), (3, 5001, 30, 5), (1, 130560, 64, 1)])
+def test_group_norm_of_many_positions(L, n, s, c, groups, dtype):
+    norm_passes(L, n, s, c, groups, dtype, "silu")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("s", [1360, 1530, 1531, 1701])  # one launch up to about here, three from here on
+def test_group_norm_where_one_launch_becomes_three(L, s, dtype):
+    norm_passes(L, 16, s, 192, 32, dtype, "gelu")
+
+
+@pytest.mark.parametrize("dtype,c", [(BF16, 128), (F32, 64), (F16, 96)])
+def test_group_norm_past_the_caches(L, c, dtype):
+    """Inputs and outputs of more than 256 MB: the outputs' stores pass the caches."""
+    norm_passes(L, 1, 1100 * 1000, c, 8, dtype, "silu", backward=False)
