@@ -30,8 +30,9 @@ constexpr float kLift = 10.0f, kLower = 1.0f / 1024.0f; // 2^10 and its inverse
 // begins so high that no ds but 0 stays below 2^15, and comes down, the row's sums with it, wherever
 // one exceeds that: the largest so far then lies at 2^8 to 2^15, what is 2^-22 of it or more keeps its
 // precision, and nothing overflows.  (8160 keys, heads of 64, dout of size 1e-4: with ds as it is 45%
-// of them are 0 and dq is off by 0.1 of itself.)  It takes 2 to 5% of a float16 training pass (32 x 6
-// heads of 32, 256 x 256, with a mask 45.9 -> 46.8 us; 8160 x 8160 causal, 16 heads of 128 on 4 1.29 -> 1.32 ms).
+// of them are 0 and dq is off by 0.1 of itself.)  It takes 2 to 7% of a float16 training pass (32 x 6
+// heads of 32, 256 x 256, with a mask 45.8 -> 46.8 us; 8 x 8 of 64, 510 x 510 causal 48.9 -> 52.2; 8160 x 8160
+// causal, 16 heads of 128 on 4 1.28 -> 1.32 ms), most of it the product in the keys' kernel.
 // bfloat16 and 32 bits need none.
 template <typename T>
 struct Lift {
@@ -48,13 +49,12 @@ struct Lift {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             top = fmaxf(top, fabsf(ds[i]));
-        top = pair_max(top); // a row's two lanes
         if (__builtin_amdgcn_ballot_w64(top > kMost)) {
             top = 0.0f; // of the finite ones: the others stay as they are
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 top = fmaxf(top, not_finite(ds[i]) ? 0.0f : fabsf(ds[i]));
-            top = pair_max(top);
+            top = pair_max(top); // a row's two lanes
             const float by = top > kMost ? __builtin_amdgcn_ldexpf(1.0f, kAim - __builtin_amdgcn_frexp_expf(top)) : 1.0f;
             f *= by;
             for (int i = 0; i < count; ++i)
