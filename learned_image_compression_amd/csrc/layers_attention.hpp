@@ -776,8 +776,8 @@ inline ForwardPlan forward_plan(const lic_attention_args &p)
 // which more of them even out (8160 x 8160 causal, 16 heads of 128 on 4: dk, dv 612 us with 512 blocks,
 // 892 with 256); a split costs its part's way through memory.
 // Measured (both kernels and join, us, with 1 / 2 / 4 / 8 splits of keys' blocks): float, 4 x 6 heads of 32,
-// 510 x 510 74 / 58 / 60 / 63; bfloat16, 8 heads of 64, 1000 x 1000 50 / 43 / 42 / 44; 8 x 8 heads of 64, 510 x 510
-// causal 52 / 56 / 65 / 87; 4 heads of 64, 4080 x 4080 154 / 111 / 97 / 105.
+// 510 x 510 70 / 54 / 55 / 58; bfloat16, 8 heads of 64, 1000 x 1000 50 / 42 / 39 / 42; 8 x 8 heads of 64, 510 x 510
+// causal 36 / 46 / 55 / 76; 4 heads of 64, 4080 x 4080 149 / 107 / 93 / 105.
 inline int backward_splits(const lic_attention_args &p, int at_once, int64_t blocks, double steps, double unit,
                            double floats)
 {

@@ -684,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void norm_samples(NormArgs a) { sum_over_
 // ---- host ----------------------------------------------------------------
 
 // Channels of a tile: the split of a row into tiles that leaves the fewest of a
-// block's threads idle (a row of 160 vectors: 3 tiles of 54, 216 threads of 256).
+// block's threads idle (a row of 160 vectors: 5 tiles of 32 take all 256, one tile 160).
 void choose_tiles(NormArgs &a, int vec)
 {
     a.vecs = a.channels / vec;

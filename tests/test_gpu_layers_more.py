@@ -545,3 +545,25 @@ def test_group_norm_where_one_launch_becomes_three(L, s, dtype):
 def test_group_norm_past_the_caches(L, c, dtype):
     """Inputs and outputs of more than 256 MB: the outputs' stores pass the caches."""
     norm_passes(L, 1, 1100 * 1000, c, 8, dtype, "silu", backward=False)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("b,q,s,h,kv,d", [(24, 140, 197, 4, 4, 32), (24, 140, 197, 4, 2, 64), (8, 300, 300, 4, 4, 96),
+                                          (4, 130, 400, 2, 1, 128), (2, 9, 700, 4, 2, 64)])
+def test_attention_bits_do_not_depend_on_the_masks_layout(L, b, q, s, h, kv, d, dtype):
+    g = gen(s + d)
+    t = [normal(g, b, n, m, d, dtype=dtype) for n, m in ((q, h), (s, kv), (s, kv), (q, h))]
+    mask = torch.rand(b, 1, q, s, generator=g, device="cuda") < 0.6
+    spread = torch.zeros(b, 1, q, 2 * s + 1, dtype=torch.bool, device="cuda")[..., 1::2]
+    spread.copy_(mask)
+    layouts = [mask, mask.transpose(2, 3).contiguous().transpose(2, 3), mask.expand(b, h, q, s).contiguous(),
+               spread, torch.nn.functional.pad(mask, (3, 2))[..., 3:3 + s]]
+
+    def call(mask):
+        out, lse = L.attention_forward(*t[:3], mask=mask)
+        return (out, lse, *L.attention_backward(t[3], *t[:3], out, lse, mask=mask))
+
+    first = call(mask)
+    for other in layouts[1:]:
+        for got, want, name in zip(call(other), first, ("out", "lse", "dq", "dk", "dv")):
+            assert torch.equal(got, want), name
