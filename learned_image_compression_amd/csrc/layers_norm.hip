@@ -230,8 +230,8 @@ __device__ float2 block_sum(float2 v)
 
 // ---- three launches ------------------------------------------------------
 //
-// Measured, 192 channels of 544 x 960, bfloat16, silu: sums 56 us (3.6 TB/s read), join 6, outputs
-// 76 (5.3 TB/s read and written).  16 x 192 x 64 x 64, backward: sums 18 us (2.8 TB/s), join 4.5,
+// Measured, 192 channels of 544 x 960, bfloat16, silu: sums 37 us (5.4 TB/s read), join 5, outputs
+// 76 (5.3 TB/s read and written; through the caches sums take 56).  16 x 192 x 64 x 64, backward: sums 18 us (2.8 TB/s), join 4.5,
 // outputs 19 (4.0 TB/s); at 50 MB a launch's start and end are a third of it.  8 x 320 x 128 x 128,
 // float16, gelu: sums 27, outputs 40, backward 48 and 49 us; without the activation the backward call
 // takes 74 us instead of 95, so there arithmetic is a part of what bounds it.

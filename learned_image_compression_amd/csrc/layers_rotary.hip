@@ -7,7 +7,7 @@
 // does not divide) or copies 2 V of the head's other values; neighbouring threads take
 // the units of a head, then the heads of a token, so a token's table row is read
 // from L1 by all heads but the first.  q and k share one launch.
-// Measured, bfloat16: 8 x 32640 positions, 6 heads of 32 of q and k 77 us (5.3 TB/s read and written,
+// Measured, bfloat16: 8 x 32640 positions, 6 heads of 32 of q and k 74 us (5.4 TB/s read and written,
 // a large copy 5.0); 16 single tokens, 16 and 4 heads of 64 3.4 us, an empty launch's time.
 #include "layers_common.hpp"
 
