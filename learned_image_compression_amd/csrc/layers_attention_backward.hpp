@@ -27,9 +27,8 @@ namespace {
 constexpr float kLift = 10.0f, kLower = 1.0f / 1024.0f; // 2^10 and its inverse
 
 // The power of two, of a lane's row (a query, or a key), that ds takes on its way into float16.  It
-// begins so high that no ds but 0 stays below 2^15, and comes down, the row's sums with it, wherever
-// one exceeds that: the largest so far then lies at 2^8 to 2^15, what is 2^-22 of it or more keeps its
-// precision, and nothing overflows.  (8160 keys, heads of 64, dout of size 1e-4: with ds as it is 45%
+// begins at 2^60 and comes down, the row's sums with it, wherever a ds exceeds 2^15 with it: the largest
+// so far then lies at 2^8 to 2^15, what is 2^-22 of it or more keeps its precision, and nothing overflows.  (8160 keys, heads of 64, dout of size 1e-4: with ds as it is 45%
 // of them are 0 and dq is off by 0.1 of itself.)  It takes 2 to 7% of a float16 training pass (32 x 6
 // heads of 32, 256 x 256, with a mask 45.8 -> 46.8 us; 8 x 8 of 64, 510 x 510 causal 48.9 -> 52.2; 8160 x 8160
 // causal, 16 heads of 128 on 4 1.28 -> 1.32 ms), most of it the product in the keys' kernel.
@@ -591,7 +590,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 || DT == 32 ? 2 : 1) void atten
 #pragma unroll
     for (int n = 0; n < ND; ++n)
         dq[n] = zero16();
-    Lift<T> lift; // of the lane's query; in these two it is free
+    Lift<T> lift; // of the lane's query; dp and D bring it into ds
     float scaled[2] = {lift.f * kLower, lift.f * delta};
 
     int lo, hi;
