@@ -1,8 +1,9 @@
 /*
  * lic_layers.h -- C ABI of the gfx950 (MI355X) network operators that stand
  * around the coder of rans_hip.h in a learned image codec: group norm with an
- * activation (transforms), rotary positions and attention (entropy models
- * over the latent's positions), each forward and backward.
+ * activation (transforms), RMS norm with the residual's addition, rotary
+ * positions, attention and linear attention (entropy models over the latent's
+ * positions), each forward and backward, and clipping of gradients.
  *
  * Memory and ownership are the coder's: every array is a DEVICE pointer owned
  * by the caller, the library allocates nothing and keeps no state, all work
@@ -80,6 +81,48 @@ int lic_group_norm_backward(const void *dy, int64_t dy_sample, int64_t dy_row, c
                             const float *mean, const float *rstd, void *dx, int64_t dx_sample,
                             int64_t dx_row, void *dweight, void *dbias, void *workspace,
                             uint64_t workspace_bytes, hipStream_t hstream);
+
+/* ---- RMS norm with the residual's addition ------------------------------
+ *
+ * x holds `samples` x `positions` rows of `channels` values next to each other; every
+ * array of such rows has strides of its own (sample, row).
+ *   h = x + residual, rounded to their type (residual null: h = x)
+ *   rstd = 1 / sqrt(mean over the row of h^2 + eps),  y = weight[c] h rstd
+ * weight (param_dtype) may be null for 1.  sum receives h; it has to be null where
+ * residual is.  rstd (float [samples][positions]) may be null in the forward call; the
+ * backward call takes it, and h as x:
+ *   a = weight dy,  dx = rstd (a - xh mean(a xh)) + dsum,  dweight = sum over rows of dy xh
+ * with xh = h rstd; dx is the gradient of x and of residual alike, dsum the one
+ * that comes to h from elsewhere (null: 0).  dweight (param_dtype) may be null.
+ * An output may be an input of the same strides (sum: x or residual; dx: dy or dsum).
+ *
+ * format != LIC_FORMAT_NONE (forward only): y has one byte a value, an e4m3 number (up
+ * to 448) or a whole number (up to 127), and scales (float [samples][positions]) what
+ * one stands for:
+ *   top = max(max over the row of |weight h rstd|, 1e-30), scale = top / most,
+ *   y = round(weight h rstd * (most / top)), ties to even
+ * A row with a NaN has a scale of NaN.  Sums are held in 32 bits. */
+enum lic_format { LIC_FORMAT_NONE = 0, LIC_FORMAT_E4M3 = 1, LIC_FORMAT_INT8 = 2 };
+
+typedef struct lic_rms_norm_args {
+    const void *x, *residual, *weight;
+    void *y, *sum;
+    float *rstd, *scales;
+    const void *dy, *dsum;
+    void *dx, *dweight;
+    int64_t x_stride[2], residual_stride[2], y_stride[2], sum_stride[2]; /* sample, row */
+    int64_t dy_stride[2], dsum_stride[2], dx_stride[2];
+    int64_t samples, positions, channels, dtype, param_dtype, format;
+    double eps;
+} lic_rms_norm_args;
+
+/* Bytes for lic_rms_norm_backward with a dweight (without one none are needed). */
+uint64_t lic_rms_norm_workspace_bytes(int64_t samples, int64_t positions, int64_t channels);
+
+int lic_rms_norm_forward(const lic_rms_norm_args *args, hipStream_t hstream);
+
+int lic_rms_norm_backward(const lic_rms_norm_args *args, void *workspace, uint64_t workspace_bytes,
+                          hipStream_t hstream);
 
 /* ---- rotary positions ---------------------------------------------------
  *
@@ -182,6 +225,90 @@ int lic_attention_forward(const lic_attention_args *args, void *workspace,
 
 int lic_attention_backward(const lic_attention_args *args, void *workspace,
                            uint64_t workspace_bytes, hipStream_t hstream);
+
+/* ---- linear attention with a decay for each head ------------------------
+ *
+ * q, out, dout, dq are [batch][tokens][heads][..], k, v, dk, dv
+ * [batch][tokens][kv_heads][..] with any batch, row and head strides; q and k have
+ * `dim` values, v and out `value_dim`; heads is a multiple of kv_heads and head h
+ * reads kv head h / (heads / kv_heads).  With g = exp(log_decay[head]) and a state of
+ * dim x value_dim numbers for each batch and head,
+ *   S_t = g S_(t-1) + k_t v_t',   out_t = scale q_t S_t
+ * that is out_t = scale (sum over s <= t of g^(t-s) (q_t . k_s) v_s + g^(t+1) q_t S_(-1)),
+ * where S_(-1) is `state` (null: 0) and state_out (may be null) receives the last S.
+ * state_out may be `state` itself.  lengths (null: all) are the tokens in use of each
+ * batch, held to [0, tokens]: the state stops there, rows behind it are not read,
+ * and their out (dq, dk, dv) is 0.
+ *
+ * A token has no part in what comes before it, whatever its values are: a NaN or an
+ * infinity shows from its own row on (in gradients: up to it).
+ *
+ * States are float, [batch][head][dim][value_dim] with strides by batch, head and
+ * row of their own.  Sums and states are held in 32 bits, and what a state takes in and
+ * gives to the next position keeps that precision (16-bit types: an operand that carries a
+ * power of g is split in two); the products that form `out` take the scores and the
+ * state rounded to q's type, in half precision as a power of two times them, so their
+ * precision does not depend on the size of the inputs.  16-bit products of 32-bit sums
+ * and 32-bit products otherwise, as for attention.
+ *
+ * The backward call takes what the forward call took, dout, and dstate, the gradient
+ * that comes to state_out (null: 0).  dlog_decay (float [heads], summed over the batch)
+ * and dstate_in (the gradient of `state`) may be null.  dk and dv of heads that share a
+ * kv head are their sums.
+ *
+ * Long calls of few heads are split along the tokens; how is decided by the sizes
+ * alone.  tokens up to 2^28, dim and value_dim 1 .. 128, scale positive. */
+typedef struct lic_linear_attention_args {
+    const void *q, *k, *v;
+    const float *log_decay, *state;
+    const int32_t *lengths;
+    void *out;
+    float *state_out;
+    const void *dout;
+    const float *dstate;
+    void *dq, *dk, *dv;
+    float *dlog_decay, *dstate_in;
+    int64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3]; /* batch, row, head */
+    int64_t dout_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+    int64_t state_stride[3], state_out_stride[3], dstate_stride[3], dstate_in_stride[3]; /* batch, head, row */
+    int64_t batch, tokens, heads, kv_heads, dim, value_dim, dtype;
+    double scale;
+} lic_linear_attention_args;
+
+/* Bytes for lic_linear_attention_forward (backward == 0) or lic_linear_attention_backward:
+ * batch, tokens, heads, kv_heads, dim, value_dim and dtype are read. */
+uint64_t lic_linear_attention_workspace_bytes(const lic_linear_attention_args *args, int32_t backward);
+
+int lic_linear_attention_forward(const lic_linear_attention_args *args, void *workspace,
+                                 uint64_t workspace_bytes, hipStream_t hstream);
+
+int lic_linear_attention_backward(const lic_linear_attention_args *args, void *workspace,
+                                  uint64_t workspace_bytes, hipStream_t hstream);
+
+/* ---- clipping of gradients by their global norm --------------------------
+ *
+ *   norm = sqrt(sum over all values of all tensors of x^2)
+ *   out = x * min(1, max_norm / (norm + 1e-6))
+ * `tensors` is a HOST array of `count` entries, read before the call returns; x and out
+ * (which may be x) are device memory of n values next to each other, each of its own
+ * type.  Outputs must not overlap each other, nor an x but their own.  norm is one float on
+ * the device.  Squares are summed and the factor is formed in 64 bits, so no size of the values
+ * overflows (a norm past 32 bits' range is written as infinity).  An infinity
+ * among the values makes the factor 0 (and itself NaN), a NaN makes all outputs NaN.
+ * lic_gradient_norm leaves `out` alone (it may be null). */
+typedef struct lic_gradient {
+    const void *x;
+    void *out;
+    int64_t n, dtype;
+} lic_gradient;
+
+uint64_t lic_clip_gradients_workspace_bytes(const lic_gradient *tensors, int64_t count);
+
+int lic_gradient_norm(const lic_gradient *tensors, int64_t count, float *norm, void *workspace,
+                      uint64_t workspace_bytes, hipStream_t hstream);
+
+int lic_clip_gradients(const lic_gradient *tensors, int64_t count, double max_norm, float *norm,
+                       void *workspace, uint64_t workspace_bytes, hipStream_t hstream);
 
 /* Static text that names the library's build target. */
 const char *lic_layers_target(void);

@@ -20,9 +20,10 @@ LIBRARY = os.path.join(PKG, "librans_hip.so")
 SOURCES = ["rans_prep.hip", "rans_encode.hip", "rans_decode.hip", "rans_tables.hip", "rans_latent.hip",
            "rans_interleaved.hip", "rans_noalloc.hip", "rans_abi.hip"]
 LAYERS_LIBRARY = os.path.join(PKG, "liblic_layers.so")
-LAYERS_SOURCES = ["layers_norm.hip", "layers_rotary.hip", "layers_attention.hip",
+LAYERS_SOURCES = ["layers_norm.hip", "layers_rms.hip", "layers_rotary.hip", "layers_attention.hip",
                   "layers_attention_f32.hip", "layers_attention_f16.hip",
-                  "layers_attention_bf16.hip"]
+                  "layers_attention_bf16.hip", "layers_linear.hip", "layers_linear_f32.hip",
+                  "layers_linear_f16.hip", "layers_linear_bf16.hip", "layers_clip.hip"]
 ARCH = os.environ.get("RANS_HIP_ARCH", "gfx950")
 
 FLAGS = [

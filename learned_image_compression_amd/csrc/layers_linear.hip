@@ -1,0 +1,368 @@
+// layers_linear.hip -- linear attention's C entry points (checks, workspace, jobs), the step of single
+// tokens, and the sums over heads that share keys.
+#include "layers_linear.hpp"
+
+namespace lic {
+namespace {
+
+// ---- single tokens --------------------------------------------------------------
+//
+// S' = g S + k v',  out = scale q S'.  The state's way through memory bounds it: a block takes a head's
+// state, a thread four of its columns (one where value_dim does not divide) of every R-th row; out is added
+// up over the R threads of a column in LDS, in their order.
+constexpr int kStepThreads = 256;
+
+struct StepArgs {
+    lic_linear_attention_args p;
+    int32_t share, across, down; // heads of a kv head; threads of a state's row; rows at once
+    uint32_t first;
+};
+
+template <typename T, int V>
+__global__ __launch_bounds__(kStepThreads) void linear_step(StepArgs a)
+{
+    __shared__ float sums[kStepThreads * V];
+    const lic_linear_attention_args &p = a.p;
+    const uint32_t line = a.first + blockIdx.x;
+    const int b = (int)(line / (uint32_t)p.heads), head = (int)(line - (uint32_t)b * (uint32_t)p.heads), kv = head / a.share;
+    const int t = (int)threadIdx.x, row0 = t / a.across, e = (t - row0 * a.across) * V;
+    const bool live = !p.lengths || p.lengths[b] > 0;
+    const T *q = head_row<T>(p.q, p.q_stride, b, 0, head), *k = head_row<T>(p.k, p.k_stride, b, 0, kv);
+    const T *v = head_row<T>(p.v, p.v_stride, b, 0, kv);
+    const float *state = p.state ? p.state + b * p.state_stride[0] + head * p.state_stride[1] + e : nullptr;
+    float *last = p.state_out ? p.state_out + b * p.state_out_stride[0] + head * p.state_out_stride[1] + e : nullptr;
+    const float g = live ? expf(p.log_decay[head]) : 1.0f, scale = (float)p.scale;
+    using VT = Vec<float, V>;
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        o[i] = 0.0f;
+    if (row0 < a.down) {
+        float ve[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            ve[i] = live ? up(v[e + i]) : 0.0f;
+        constexpr int U = 4; // rows asked for at once
+        for (int d0 = row0; d0 < p.dim; d0 += U * a.down) {
+            VT s[U];
+            float qd[U], kd[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int d = d0 + u * a.down;
+                s[u] = VT{};
+                qd[u] = kd[u] = 0.0f;
+                if (d < p.dim) {
+                    if (state)
+                        s[u] = load_at<VT>(state + d * p.state_stride[2]);
+                    if (live) {
+                        qd[u] = up(q[d]);
+                        kd[u] = up(k[d]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int d = d0 + u * a.down;
+                if (d >= p.dim)
+                    break;
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        s[u].v[i] = fmaf(kd[u], ve[i], s[u].v[i] * g);
+                        o[i] = fmaf(qd[u], s[u].v[i], o[i]);
+                    }
+                }
+                if (last)
+                    store_at(last + d * p.state_out_stride[2], s[u]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            sums[row0 * (a.across * V) + e + i] = o[i];
+    }
+    __syncthreads();
+    if (t < p.value_dim) {
+        float s = 0.0f;
+        for (int r = 0; r < a.down; ++r)
+            s += sums[r * (a.across * V) + t];
+        head_row<T>(p.out, p.out_stride, b, 0, head)[t] = down_apart<T>(live ? s * scale : 0.0f);
+    }
+}
+
+template <typename T, int V>
+int run_step(StepArgs a, hipStream_t s)
+{
+    a.across = (int)((a.p.value_dim + V - 1) / V);
+    a.down = std::min<int>(kStepThreads / a.across, (int)a.p.dim);
+    in_pieces(a.p.batch * a.p.heads, kStepThreads, [&](int64_t first, uint32_t blocks) {
+        a.first = (uint32_t)first;
+        linear_step<T, V><<<blocks, kStepThreads, 0, s>>>(a);
+    });
+    return launched();
+}
+
+// ---- sums over heads that share ---------------------------------------------------
+
+struct JoinArgs {
+    const float *part; // [batch][kv head][share][token][dim]
+    void *out;
+    int64_t out_stride[3];
+    int64_t tokens, total, first;
+    int32_t heads, share, dim;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void linear_join(JoinArgs a)
+{
+    const int64_t id = (a.first + blockIdx.x) * 256 + threadIdx.x;
+    if (id >= a.total)
+        return;
+    const int64_t row = id / a.dim, line = row / a.tokens; // (batch, kv head)
+    const int d = (int)(id - row * a.dim);
+    const int64_t token = row - line * a.tokens, step = a.tokens * a.dim;
+    const float *part = a.part + line * a.share * step + token * a.dim + d;
+    float s = part[0];
+    for (int i = 1; i < a.share; ++i)
+        s += part[i * step];
+    const int64_t b = line / a.heads;
+    head_row<T>(a.out, a.out_stride, (int)b, token, (int)(line - b * a.heads))[d] = down<T>(s);
+}
+
+// dlog_decay[head]: one wave a head, over the batch.
+__global__ __launch_bounds__(64) void linear_decay_join(const float *sums, float *out, int32_t batch, int32_t heads, int32_t parts)
+{
+    const int head = blockIdx.x, lane = threadIdx.x;
+    float s = 0.0f;
+    for (int64_t i = lane; i < (int64_t)batch * parts; i += 64) {
+        const int64_t b = i / parts;
+        s += sums[(b * heads + head) * parts + (i - b * parts)];
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        s += __shfl_xor(s, d);
+    if (lane == 0)
+        out[head] = s;
+}
+
+// ---- entries -------------------------------------------------------------------------
+
+bool valid(const lic_linear_attention_args *p)
+{
+    const auto in = [](int64_t v, int64_t least, int64_t most) { return v >= least && v <= most; };
+    return p && valid_dtype(p->dtype) && in(p->batch, 0, 1 << 20) && in(p->tokens, 0, 1 << 28) &&
+           in(p->kv_heads, 1, 65536) && in(p->heads, p->kv_heads, 65536) && p->heads % p->kv_heads == 0 &&
+           in(p->dim, 1, LIC_MAX_HEAD_DIM) && in(p->value_dim, 1, LIC_MAX_HEAD_DIM) &&
+           p->batch * p->heads <= (1ll << 28) && p->batch * p->heads * p->tokens <= (1ll << 33);
+}
+
+bool ok(const int64_t *s) { return s[0] >= 0 && s[1] >= 0 && s[2] >= 0; }
+
+bool valid_call(const lic_linear_attention_args &p, bool backward)
+{
+    if (!ok(p.q_stride) || !ok(p.k_stride) || !ok(p.v_stride) || !(p.scale > 0.0) || !(p.scale < 1e30) || !p.log_decay ||
+        (p.state && !ok(p.state_stride)))
+        return false;
+    if (p.tokens > 0 && (!p.q || !p.k || !p.v))
+        return false;
+    if (!backward)
+        return ok(p.out_stride) && (p.tokens == 0 || p.out) && (!p.state_out || ok(p.state_out_stride));
+    return ok(p.dout_stride) && ok(p.dq_stride) && ok(p.dk_stride) && ok(p.dv_stride) &&
+           (p.tokens == 0 || (p.dout && p.dq && p.dk && p.dv)) && (!p.dstate || ok(p.dstate_stride)) &&
+           (!p.dstate_in || ok(p.dstate_in_stride));
+}
+
+uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
+
+// Scratch memory of a call: parts of dk and dv, sums of dlog_decay.
+struct Layout {
+    uint64_t dk, dv, sums, bytes;
+    Layout(const lic_linear_attention_args &p, bool backward)
+    {
+        const uint64_t lines = (uint64_t)p.batch * p.heads, shared = backward && p.heads > p.kv_heads;
+        dk = 0;
+        dv = dk + (shared ? round256(lines * p.tokens * p.dim * 4) : 0);
+        sums = dv + (shared ? round256(lines * p.tokens * p.value_dim * 4) : 0);
+        bytes = sums + (backward ? round256(lines * 4) : 0);
+    }
+};
+
+template <typename T>
+bool vector_rows(const lic_linear_attention_args &p, const void *x, const int64_t *stride, int64_t heads)
+{
+    constexpr int n = 16 / sizeof(T);
+    return !x || (aligned_to(x, 16) && (p.batch == 1 || stride[0] % n == 0) && (p.tokens == 1 || stride[1] % n == 0) &&
+                  stride[1] < (1 << 24) && (heads == 1 || stride[2] % n == 0));
+}
+
+void set3(int64_t *to, const int64_t *from) { std::copy(from, from + 3, to); }
+// a state's strides with its rows and columns in their order, or the other way round
+void set_state(int64_t *to, const int64_t *from, bool turned)
+{
+    to[0] = from[0], to[1] = from[1];
+    to[2] = turned ? 1 : from[2], to[3] = turned ? from[2] : 1;
+}
+
+LinearArgs common(const lic_linear_attention_args &p)
+{
+    LinearArgs a{};
+    a.log_decay = p.log_decay;
+    a.lengths = p.lengths;
+    a.tokens = p.tokens;
+    a.batch = (int32_t)p.batch;
+    a.heads = (int32_t)p.heads;
+    a.scale = (float)p.scale;
+    return a;
+}
+
+template <typename T>
+int forward(const lic_linear_attention_args &p, hipStream_t s)
+{
+    const int32_t share = (int32_t)(p.heads / p.kv_heads);
+    if (p.tokens == 1) {
+        StepArgs a{};
+        a.p = p;
+        a.share = share;
+        return p.value_dim % 4 == 0 ? run_step<T, 4>(a, s) : run_step<T, 1>(a, s);
+    }
+    constexpr int n = 16 / sizeof(T);
+    const bool vec = p.dim % n == 0 && p.value_dim % n == 0 && vector_rows<T>(p, p.q, p.q_stride, p.heads) &&
+                     vector_rows<T>(p, p.k, p.k_stride, p.kv_heads) && vector_rows<T>(p, p.v, p.v_stride, p.kv_heads) &&
+                     vector_rows<T>(p, p.out, p.out_stride, p.heads);
+    LinearArgs a = common(p);
+    LinearJob &j = a.job[0];
+    a.jobs = 1;
+    j.x = p.q, j.y = p.k, j.z = p.v, j.out = p.out, j.first = p.state, j.last = p.state_out;
+    set3(j.x_stride, p.q_stride), set3(j.y_stride, p.k_stride), set3(j.z_stride, p.v_stride);
+    set3(j.out_stride, p.out_stride);
+    set_state(j.first_stride, p.state_stride, false), set_state(j.last_stride, p.state_out_stride, false);
+    j.x_share = 1, j.y_share = j.z_share = share;
+    j.dim_x = (int32_t)p.dim, j.dim_z = (int32_t)p.value_dim;
+    j.read = a.scale, j.write = 1.0f;
+    return Linear<T>::sweep(a, vec, s);
+}
+
+template <typename T>
+int join(const lic_linear_attention_args &p, const float *part, void *out, const int64_t *stride, int64_t dim, hipStream_t s)
+{
+    JoinArgs a{};
+    a.part = part;
+    a.out = out;
+    set3(a.out_stride, stride);
+    a.tokens = p.tokens;
+    a.heads = (int32_t)p.kv_heads;
+    a.share = (int32_t)(p.heads / p.kv_heads);
+    a.dim = (int32_t)dim;
+    a.total = p.batch * p.kv_heads * p.tokens * dim;
+    in_pieces((a.total + 255) / 256, 256, [&](int64_t first, uint32_t blocks) {
+        a.first = first;
+        linear_join<T><<<blocks, 256, 0, s>>>(a);
+    });
+    return launched();
+}
+
+template <typename T>
+int backward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
+{
+    constexpr int n = 16 / sizeof(T);
+    const bool vec = p.dim % n == 0 && p.value_dim % n == 0 && vector_rows<T>(p, p.q, p.q_stride, p.heads) &&
+                     vector_rows<T>(p, p.k, p.k_stride, p.kv_heads) && vector_rows<T>(p, p.v, p.v_stride, p.kv_heads) &&
+                     vector_rows<T>(p, p.dout, p.dout_stride, p.heads) && vector_rows<T>(p, p.dq, p.dq_stride, p.heads) &&
+                     vector_rows<T>(p, p.dk, p.dk_stride, p.kv_heads) && vector_rows<T>(p, p.dv, p.dv_stride, p.kv_heads);
+    const Layout at(p, true);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    const int32_t share = (int32_t)(p.heads / p.kv_heads);
+    LinearArgs a = common(p);
+    a.jobs = 3;
+    const auto job = [&](int i, const void *x, const int64_t *xs, int32_t x_share, const void *y, const int64_t *ys,
+                         int32_t y_share, const void *z, const int64_t *zs, int32_t z_share, void *out,
+                         const int64_t *os, int64_t dim_x, int64_t dim_z) -> LinearJob & {
+        LinearJob &j = a.job[i];
+        j.x = x, j.y = y, j.z = z, j.out = out;
+        set3(j.x_stride, xs), set3(j.y_stride, ys), set3(j.z_stride, zs), set3(j.out_stride, os);
+        j.x_share = x_share, j.y_share = y_share, j.z_share = z_share;
+        j.dim_x = (int32_t)dim_x, j.dim_z = (int32_t)dim_z;
+        j.reverse = i > 0;
+        j.read = i > 0 ? 1.0f : a.scale, j.write = i > 0 ? a.scale : 1.0f;
+        j.first = i > 0 ? p.dstate : p.state;
+        return j;
+    };
+    LinearJob &dq = job(0, p.dout, p.dout_stride, 1, p.v, p.v_stride, share, p.k, p.k_stride, share, p.dq, p.dq_stride,
+                        p.value_dim, p.dim);
+    set_state(dq.first_stride, p.state_stride, true);
+    LinearJob &dv = job(1, p.k, p.k_stride, share, p.q, p.q_stride, 1, p.dout, p.dout_stride, 1, p.dv, p.dv_stride, p.dim,
+                        p.value_dim);
+    set_state(dv.first_stride, p.dstate_stride, false);
+    dv.last = p.dstate_in;
+    set_state(dv.last_stride, p.dstate_in_stride, false);
+    LinearJob &dk = job(2, p.v, p.v_stride, share, p.dout, p.dout_stride, 1, p.q, p.q_stride, 1, p.dk, p.dk_stride,
+                        p.value_dim, p.dim);
+    set_state(dk.first_stride, p.dstate_stride, true);
+    if (share > 1) {
+        dk.part = reinterpret_cast<float *>(base + at.dk);
+        dv.part = reinterpret_cast<float *>(base + at.dv);
+    }
+    if (const int rc = Linear<T>::sweep(a, vec, s))
+        return rc;
+    if (share > 1 && p.tokens > 0) {
+        if (const int rc = join<T>(p, dk.part, p.dk, p.dk_stride, p.dim, s))
+            return rc;
+        if (const int rc = join<T>(p, dv.part, p.dv, p.dv_stride, p.value_dim, s))
+            return rc;
+    }
+    if (!p.dlog_decay)
+        return RANS_OK;
+    DecayArgs d{};
+    d.q = p.q, d.k = p.k, d.v = p.v, d.dout = p.dout, d.state = p.state, d.dstate = p.dstate;
+    d.sums = reinterpret_cast<float *>(base + at.sums);
+    set3(d.q_stride, p.q_stride), set3(d.k_stride, p.k_stride), set3(d.v_stride, p.v_stride);
+    set3(d.dout_stride, p.dout_stride), set3(d.state_stride, p.state_stride), set3(d.dstate_stride, p.dstate_stride);
+    d.log_decay = p.log_decay, d.lengths = p.lengths, d.tokens = p.tokens;
+    d.batch = (int32_t)p.batch, d.heads = (int32_t)p.heads, d.share = share;
+    d.dim = (int32_t)p.dim, d.value_dim = (int32_t)p.value_dim, d.scale = a.scale;
+    if (const int rc = Linear<T>::decay(d, vec, s))
+        return rc;
+    linear_decay_join<<<(uint32_t)p.heads, 64, 0, s>>>(d.sums, p.dlog_decay, d.batch, d.heads, 1);
+    return launched();
+}
+
+int call(const lic_linear_attention_args *args, void *ws, uint64_t ws_bytes, hipStream_t s, bool back)
+{
+    if (!valid(args))
+        return RANS_E_ARG;
+    const lic_linear_attention_args &p = *args;
+    if (p.batch == 0 && !(back && p.dlog_decay))
+        return RANS_OK;
+    if (p.batch == 0) { // a sum over nothing
+        linear_decay_join<<<(uint32_t)p.heads, 64, 0, s>>>(nullptr, p.dlog_decay, 0, (int32_t)p.heads, 1);
+        return launched();
+    }
+    if (!valid_call(p, back))
+        return RANS_E_ARG;
+    const uint64_t need = Layout(p, back).bytes;
+    if (need > 0 && (!ws || !aligned_to(ws, 256) || ws_bytes < need))
+        return RANS_E_WORKSPACE;
+    return with_dtype(p.dtype, [&](auto t) {
+        using T = decltype(t);
+        return back ? backward<T>(p, ws, s) : forward<T>(p, s);
+    });
+}
+
+}  // namespace
+}  // namespace lic
+
+extern "C" uint64_t lic_linear_attention_workspace_bytes(const lic_linear_attention_args *args, int32_t backward)
+{
+    return lic::valid(args) ? lic::Layout(*args, backward != 0).bytes : 0;
+}
+
+extern "C" int lic_linear_attention_forward(const lic_linear_attention_args *args, void *workspace,
+                                            uint64_t workspace_bytes, hipStream_t hstream)
+{
+    return lic::call(args, workspace, workspace_bytes, hstream, false);
+}
+
+extern "C" int lic_linear_attention_backward(const lic_linear_attention_args *args, void *workspace,
+                                             uint64_t workspace_bytes, hipStream_t hstream)
+{
+    return lic::call(args, workspace, workspace_bytes, hstream, true);
+}

@@ -1,5 +1,6 @@
-"""Network operators around the coder: group norm with an activation, rotary
-positions and attention, forward and backward (``include/lic_layers.h``).
+"""Network operators around the coder: group norm with an activation, RMS norm with the
+residual's addition, rotary positions, attention and linear attention, forward and backward,
+and clipping of gradients (``include/lic_layers.h``).
 
 A learned image codec's transforms and its entropy model run right before the
 coder; these are the parts of them that convolutions and matrix products leave
@@ -9,8 +10,9 @@ lie, so an encoder and a decoder that make the same call predict the same scales
 for bit.  A call of another size (a single token instead of a whole latent) may differ
 in the last bits: an encoder has to step where its decoder does.
 
-:func:`group_norm`, :func:`rotary` and :func:`attention` work with autograd (what they cannot
-differentiate they refuse: forward mode, second derivatives but rotary's).  The
+:func:`group_norm`, :func:`rms_norm`, :func:`rotary`, :func:`attention` and
+:func:`linear_attention` work with autograd (what they cannot differentiate they refuse: forward
+mode, second derivatives but rotary's).  The
 ``*_forward`` and ``*_backward`` functions are the calls beneath them, for programs that
 keep their own gradients.  As in :mod:`.binding`, torch only supplies device memory and
 the current stream, nothing is synchronised, and there is no CPU path.
@@ -36,15 +38,25 @@ EXPORTS = (
     "lic_group_norm_workspace_bytes",
     "lic_group_norm_forward",
     "lic_group_norm_backward",
+    "lic_rms_norm_workspace_bytes",
+    "lic_rms_norm_forward",
+    "lic_rms_norm_backward",
     "lic_rotary_table",
     "lic_rotary",
     "lic_attention_workspace_bytes",
     "lic_attention_forward",
     "lic_attention_backward",
+    "lic_linear_attention_workspace_bytes",
+    "lic_linear_attention_forward",
+    "lic_linear_attention_backward",
+    "lic_clip_gradients_workspace_bytes",
+    "lic_gradient_norm",
+    "lic_clip_gradients",
     "lic_layers_target",
 )
 
 DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+FORMATS = {"e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 MAX_HEAD_DIM = 128
 
@@ -87,6 +99,23 @@ def load(path: str | None = None):
         for name in ("lic_attention_forward", "lic_attention_backward"):
             getattr(lib, name).argtypes = [st, vp, u64, vp]
             getattr(lib, name).restype = ctypes.c_int
+        lib.lic_rms_norm_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.lic_rms_norm_workspace_bytes.restype = u64
+        lib.lic_rms_norm_forward.argtypes = [st, vp]
+        lib.lic_rms_norm_forward.restype = ctypes.c_int
+        lib.lic_rms_norm_backward.argtypes = [st, vp, u64, vp]
+        lib.lic_rms_norm_backward.restype = ctypes.c_int
+        lib.lic_linear_attention_workspace_bytes.argtypes = [st, i32]
+        lib.lic_linear_attention_workspace_bytes.restype = u64
+        for name in ("lic_linear_attention_forward", "lic_linear_attention_backward"):
+            getattr(lib, name).argtypes = [st, vp, u64, vp]
+            getattr(lib, name).restype = ctypes.c_int
+        lib.lic_clip_gradients_workspace_bytes.argtypes = [st, i64]
+        lib.lic_clip_gradients_workspace_bytes.restype = u64
+        lib.lic_gradient_norm.argtypes = [st, i64, vp, vp, u64, vp]
+        lib.lic_gradient_norm.restype = ctypes.c_int
+        lib.lic_clip_gradients.argtypes = [st, i64, f64, vp, vp, u64, vp]
+        lib.lic_clip_gradients.restype = ctypes.c_int
         lib.lic_layers_target.argtypes = []
         lib.lic_layers_target.restype = ctypes.c_char_p
         if path is None:
@@ -377,6 +406,223 @@ def group_norm(x: torch.Tensor, num_groups: int, weight=None, bias=None, eps: fl
     if _wants_gradient(x, weight, bias):
         return _GroupNorm.apply(x, num_groups, weight, bias, eps, activation)
     return group_norm_forward(x, num_groups, weight, bias, eps=eps, activation=activation)[0]
+
+
+# ---- RMS norm ------------------------------------------------------------------
+
+
+_RMS_NORM = struct.Struct("=11Q14q6qd")
+_NO_ROWS = (0, 0)
+
+
+def _token_rows(t: torch.Tensor, name: str):
+    """(sample stride, row stride) of a [N, ..., C] tensor whose rows are evenly spaced within a sample."""
+    shape, strides = t.shape, t.stride()
+    if shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"{name}: a row's values must be next to each other")
+    if len(shape) == 1:
+        return 0, shape[0]
+    if len(shape) == 2:
+        return 0, strides[0]
+    positions, row = 1, None
+    for size, stride in zip(reversed(shape[1:-1]), reversed(strides[1:-1])):
+        if size != 1 and positions > 0:
+            if row is None:
+                row = stride
+            elif stride != row * positions and size > 0:
+                raise ValueError(f"{name}: rows must be evenly spaced in memory")
+        positions *= size
+    return strides[0], shape[-1] if row is None else row
+
+
+def _sample_rows(shape):
+    """(samples, positions): all but the first axis count as positions, a matrix is one sample."""
+    if len(shape) < 3:
+        return 1, shape[0] if len(shape) == 2 else 1
+    return shape[0], math.prod(shape[1:-1])
+
+
+def _rms_params(x, name, weight, eps):
+    device = _device_of(x, name)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name} must be [..., C]")
+    if not 0 <= eps < 1e30:
+        raise ValueError("eps must be at least 0")
+    if weight is None:
+        return device, torch.float32
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in DTYPES:
+        raise TypeError("weight must be a float32, float16 or bfloat16 tensor")
+    if weight.device != device:
+        raise ValueError(f"weight must be on {device}, got {weight.device}")
+    if weight.numel() != x.shape[-1] or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous, one value a channel")
+    return device, weight.dtype
+
+
+def _same(t, x, device, name):
+    _like(t, x.dtype, device, name)
+    if t.shape != x.shape:
+        raise ValueError(f"{name} and x differ in shape")
+
+
+def _rms_forward(x, weight, residual, eps, code, y, stat, rstd, sum_out, device, kind):
+    """The call beneath the forward functions; returns h.  ``stat`` holds the scales of 8 bits."""
+    xs = _token_rows(x, "x")
+    h, rs, hs = x, _NO_ROWS, _NO_ROWS
+    if residual is not None:
+        _same(residual, x, device, "residual")
+        rs = _token_rows(residual, "residual")
+        if sum_out is None:
+            h = _dense_like(x)
+        else:
+            _out_like(sum_out, x, x.dtype, device, "sum_out")
+            h = sum_out
+        hs = _token_rows(h, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out is for calls with a residual")
+    samples, positions = _sample_rows(x.shape)
+    if samples and positions:
+        args = _RMS_NORM.pack(x.data_ptr(), residual.data_ptr() if residual is not None else 0,
+                              weight.data_ptr() if weight is not None else 0, y.data_ptr(),
+                              h.data_ptr() if residual is not None else 0,
+                              rstd.data_ptr() if rstd is not None else 0,
+                              stat.data_ptr() if stat is not None else 0, 0, 0, 0, 0, *xs, *rs,
+                              *_token_rows(y, "out"), *hs, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS, samples,
+                              positions, x.shape[-1], DTYPES[x.dtype], DTYPES[kind], code, eps)
+        rc = load().lic_rms_norm_forward(args, _stream(device))
+        if rc:
+            _check_rc(rc, "lic_rms_norm_forward")
+    return h
+
+
+def rms_norm_forward(x: torch.Tensor, weight=None, *, residual=None, eps: float = 1e-6, out=None,
+                     sum_out=None):
+    """Enqueue the norm of ``h = x + residual`` over the last axis; returns (y, h, rstd).
+
+    ``x`` is [..., C] with a row's values next to each other and the rows of a sample (all axes but
+    the first) evenly spaced, for example tokens [N, S, C] cut out of a wider tensor; ``residual`` is
+    like it.  ``h`` is rounded to x's type before the norm (without a residual it is ``x``
+    itself), ``y = weight * h * rstd`` and ``rstd = 1 / sqrt(mean(h^2) + eps)``, float32 [...].
+    ``out`` and ``sum_out`` are places for y and h; ``sum_out`` may be x or residual.
+    """
+    device, kind = _rms_params(x, "x", weight, eps)
+    if out is None:
+        out = _dense_like(x)
+    else:
+        _out_like(out, x, x.dtype, device, "out")
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+    h = _rms_forward(x, weight, residual, eps, 0, out, None, rstd, sum_out, device, kind)
+    return out, h, rstd
+
+
+def rms_norm_8bit(x: torch.Tensor, weight=None, *, residual=None, eps: float = 1e-6,
+                  format: str = "e4m3", out=None, sum_out=None):
+    """The norm of ``h = x + residual`` in 8 bits, for a product that takes them; returns
+    (y, scales, h).
+
+    ``y`` is float8_e4m3fn ("e4m3") or int8 ("int8") and stands for ``y * scales[..., None]``: a
+    row's scale (float32) is its largest size over 448 or 127, so nothing is cut off.  A row
+    with a NaN has a scale of NaN.  The rest is as in :func:`rms_norm_forward`.  There is no gradient.
+    """
+    if _wants_gradient(x, weight, residual):
+        raise NotImplementedError("the norm in 8 bits has no gradients")
+    device, kind = _rms_params(x, "x", weight, eps)
+    if format not in FORMATS:
+        raise ValueError(f"format must be one of {', '.join(FORMATS)}")
+    code, dtype = FORMATS[format]
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=device)
+    else:
+        _out_like(out, x, dtype, device, "out")
+    scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
+    h = _rms_forward(x, weight, residual, eps, code, out, scales, None, sum_out, device, kind)
+    return out, scales, h
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Tensor, *, dsum=None,
+                      out=None):
+    """Enqueue the gradients; returns (dx, dweight).
+
+    Takes the forward call's h and rstd.  ``dx`` is the gradient of x and of the residual alike;
+    ``dsum`` is what comes to h from elsewhere (the residual stream behind it), and is in it.
+    ``dweight`` is of the weight's type (float32 without one).  ``out`` is a place for dx, and may
+    be dy or dsum.
+    """
+    device, kind = _rms_params(h, "h", weight, 0.0)
+    _same(dy, h, device, "dy")
+    if dsum is not None:
+        _same(dsum, h, device, "dsum")
+    _like(rstd, torch.float32, device, "rstd")
+    if rstd.shape != h.shape[:-1] or not rstd.is_contiguous():
+        raise ValueError("rstd must be contiguous, one value a row")
+    if out is None:
+        out = _dense_like(h)
+    else:
+        _out_like(out, h, h.dtype, device, "out")
+    c = h.shape[-1]
+    dweight = torch.empty(c, dtype=kind, device=device)
+    samples, positions = _sample_rows(h.shape)
+    args = _RMS_NORM.pack(h.data_ptr(), 0, weight.data_ptr() if weight is not None else 0, 0, 0,
+                          rstd.data_ptr(), 0, dy.data_ptr(),
+                          dsum.data_ptr() if dsum is not None else 0, out.data_ptr(),
+                          dweight.data_ptr(), *_token_rows(h, "h"), *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
+                          *_token_rows(dy, "dy"),
+                          *(_token_rows(dsum, "dsum") if dsum is not None else _NO_ROWS),
+                          *_token_rows(out, "out"), samples, positions, c, DTYPES[h.dtype],
+                          DTYPES[kind], 0, 0.0)
+    if samples == 0 or positions == 0:
+        return out, dweight.zero_()
+    lib = load()
+    stream = _stream(device)
+    _with_workspace(device, stream, lambda p, size: lib.lic_rms_norm_backward(args, p, size, stream),
+                    lambda: lib.lic_rms_norm_workspace_bytes(samples, positions, c),
+                    "lic_rms_norm_backward")
+    return out, dweight
+
+
+def _rows_or_dense(t, name):
+    """A gradient as it is if its layout is taken, else a copy."""
+    if t is None:
+        return None
+    try:
+        _token_rows(t, name)
+    except ValueError:
+        return t.contiguous()
+    return t
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, h, rstd = rms_norm_forward(x, weight, residual=residual, eps=eps)
+        ctx.save_for_backward(h, weight, rstd)
+        ctx.set_materialize_grads(False)
+        return y, (h if residual is not None else None)
+
+    @staticmethod
+    def backward(ctx, dy, dsum):
+        h, weight, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None:  # the norm itself was not used
+            return dsum, None, dsum if need[2] else None, None
+        dy, dsum = _rows_or_dense(dy, "dy"), _rows_or_dense(dsum, "dsum")
+        inputs = [t for t in (dy, dsum, h, weight) if t is not None]
+        dx, dw = _once(lambda: rms_norm_backward(dy, h, weight, rstd, dsum=dsum), *inputs)
+        return (dx if need[0] else None, dw.view_as(weight) if need[1] else None,
+                dx if need[2] else None, None)
+
+
+def rms_norm(x: torch.Tensor, weight=None, residual=None, eps: float = 1e-6):
+    """RMS norm over the last axis, differentiable (once, in reverse) in x, weight and residual.
+
+    Returns y; with a ``residual`` it returns (y, x + residual), so the sum is formed where it is
+    read.
+    """
+    if _wants_gradient(x, weight, residual):
+        y, h = _RMSNorm.apply(x, weight, residual, eps)
+    else:
+        y, h, _ = rms_norm_forward(x, weight, residual=residual, eps=eps)
+    return (y, h) if residual is not None else y
 
 
 # ---- rotary positions ----------------------------------------------------------
@@ -695,3 +941,245 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, causal: bool
         return _Attention.apply(q, k, v, mask, key_lengths, causal, window, scale)[0]
     return attention_forward(q, k, v, causal=causal, window=window, mask=mask,
                              key_lengths=key_lengths, scale=scale)[0]
+
+
+# ---- linear attention ---------------------------------------------------------------
+
+
+_LINEAR = struct.Struct("=15Q36q7qd")
+
+
+def _state(t, shape, device, name):
+    """Address and strides (batch, head, row) of a state, or of none."""
+    if t is None:
+        return 0, _NO_STRIDES
+    _like(t, torch.float32, device, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [batch, heads, dim, value dim]")
+    s = t.stride()
+    if s[3] != 1 and shape[3] > 1:
+        raise ValueError(f"{name}: a row's values must be next to each other")
+    return t.data_ptr(), s[:3]
+
+
+def _linear_common(q, k, v, log_decay, state, lengths, scale):
+    device = _device_of(q, "q")
+    _like(k, q.dtype, device, "k")
+    _like(v, q.dtype, device, "v")
+    strides = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
+    b, s, h, d = q.shape
+    kv, e = v.shape[2], v.shape[3]
+    if k.shape != (b, s, kv, d) or v.shape[:2] != (b, s):
+        raise ValueError("q, k and v differ in batch, rows or dim, or k and v in heads")
+    if kv < 1 or h % kv or h < 1:
+        raise ValueError("heads must be a multiple of kv heads")
+    if not (1 <= d <= MAX_HEAD_DIM and 1 <= e <= MAX_HEAD_DIM):
+        raise ValueError(f"dim and value dim must be 1 .. {MAX_HEAD_DIM}")
+    _like(log_decay, torch.float32, device, "log_decay")
+    if log_decay.shape != (h,) or not log_decay.is_contiguous():
+        raise ValueError("log_decay must be contiguous [heads]")
+    length_ptr = 0
+    if lengths is not None:
+        _like(lengths, torch.int32, device, "lengths")
+        if lengths.shape != (b,) or not lengths.is_contiguous():
+            raise ValueError("lengths must be contiguous [batch]")
+        length_ptr = lengths.data_ptr()
+    if scale is None:
+        scale = d ** -0.5
+    elif not (scale > 0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive and finite")
+    shape = torch.Size((b, h, d, e))
+    return device, strides, _state(state, shape, device, "state"), length_ptr, shape, \
+        (b, s, h, kv, d, e, DTYPES[q.dtype], scale)
+
+
+def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             log_decay: torch.Tensor, *, state=None, lengths=None,
+                             scale: float | None = None, out=None, state_out=None):
+    """Enqueue linear attention with a decay for each head; returns (out, state_out).
+
+    A head's state S, float32 [dim, value dim], goes from token to token:
+    ``S = exp(log_decay[head]) * S + outer(k, v)``, ``out = scale * q @ S``.  ``q`` is [B, S, heads,
+    dim], ``k`` [B, S, kv_heads, dim], ``v`` [B, S, kv_heads, value_dim] (any strides but the last;
+    kv_heads divides heads), ``log_decay`` float32 [heads], ``out`` [B, S, heads, value_dim].
+    ``state`` and ``state_out``, [B, heads, dim, value_dim], are S before the first token (None:
+    zeros) and behind the last; a decoder that steps passes one tensor as both.  ``lengths``
+    (int32 [B]) are the tokens in use: rows behind them are not read, their out is 0, and the
+    state is that behind the last one in use.
+    """
+    device, strides, (state_ptr, ss), length_ptr, shape, sizes = \
+        _linear_common(q, k, v, log_decay, state, lengths, scale)
+    if out is None:
+        out = torch.empty((*q.shape[:3], shape[3]), dtype=q.dtype, device=device)
+    else:
+        _out_like(out, torch.empty((*q.shape[:3], shape[3]), device="meta"), q.dtype, device, "out")
+    if state_out is None:
+        state_out = torch.empty(shape, dtype=torch.float32, device=device)
+    else:
+        _out_like(state_out, torch.empty(shape, device="meta"), torch.float32, device, "state_out")
+    last_ptr, ls = _state(state_out, shape, device, "state_out")
+    args = _LINEAR.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state_ptr, length_ptr,
+                        out.data_ptr(), last_ptr, 0, 0, 0, 0, 0, 0, 0, *strides[0], *strides[1], *strides[2],
+                        *_heads(out, "out"), *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *_NO_STRIDES, *ss, *ls,
+                        *_NO_STRIDES, *_NO_STRIDES, *sizes)
+    lib = load()
+    stream = _stream(device)
+    _with_workspace(device, stream, lambda p, size: lib.lic_linear_attention_forward(args, p, size, stream),
+                    lambda: lib.lic_linear_attention_workspace_bytes(args, 0),
+                    "lic_linear_attention_forward")
+    return out, state_out
+
+
+def linear_attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              log_decay: torch.Tensor, *, dstate=None, state=None, lengths=None,
+                              scale: float | None = None, decay: bool = True):
+    """Enqueue the gradients of :func:`linear_attention_forward`; returns (dq, dk, dv, dlog_decay,
+    dstate_in).
+
+    Takes the forward call's inputs, ``dout``, and ``dstate``, the gradient that comes to
+    ``state_out`` (None: 0).  ``dlog_decay`` is float32 [heads], or None with ``decay=False``;
+    ``dstate_in`` is the gradient of ``state``, or None without one.  dk and dv of heads that share a
+    kv head are their sums; rows behind ``lengths`` are 0.
+    """
+    device, strides, (state_ptr, ss), length_ptr, shape, sizes = \
+        _linear_common(q, k, v, log_decay, state, lengths, scale)
+    _like(dout, q.dtype, device, "dout")
+    if dout.shape != (*q.shape[:3], shape[3]):
+        raise ValueError("dout must be [batch, rows, heads, value dim]")
+    dstate_ptr, ds = _state(dstate, shape, device, "dstate")
+    dq, dk, dv = _dense_like(q), _dense_like(k), _dense_like(v)
+    dlog = torch.empty(shape[1], dtype=torch.float32, device=device) if decay else None
+    first = torch.empty(shape, dtype=torch.float32, device=device) if state is not None else None
+    first_ptr, fs = _state(first, shape, device, "dstate_in")
+    args = _LINEAR.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state_ptr, length_ptr, 0, 0,
+                        dout.data_ptr(), dstate_ptr, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                        dlog.data_ptr() if decay else 0, first_ptr, *strides[0], *strides[1], *strides[2],
+                        *_NO_STRIDES, *_heads(dout, "dout"), *dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3],
+                        *ss, *_NO_STRIDES, *ds, *fs, *sizes)
+    lib = load()
+    stream = _stream(device)
+    _with_workspace(device, stream, lambda p, size: lib.lic_linear_attention_backward(args, p, size, stream),
+                    lambda: lib.lic_linear_attention_workspace_bytes(args, 1),
+                    "lic_linear_attention_backward")
+    return dq, dk, dv, dlog, first
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, state, lengths, scale):
+        out, last = linear_attention_forward(q, k, v, log_decay, state=state, lengths=lengths, scale=scale)
+        ctx.save_for_backward(q, k, v, log_decay, state, lengths)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return out, last
+
+    @staticmethod
+    def backward(ctx, dout, dstate):
+        q, k, v, log_decay, state, lengths = ctx.saved_tensors
+        if dout is None:
+            dout = q.new_zeros((*q.shape[:3], v.shape[3]))
+        elif dout.stride(-1) != 1 and dout.shape[-1] > 1:
+            dout = dout.contiguous()
+        if dstate is not None and dstate.stride(-1) != 1 and dstate.shape[-1] > 1:
+            dstate = dstate.contiguous()
+        need = ctx.needs_input_grad
+        inputs = [t for t in (dout, dstate, q, k, v, log_decay, state) if t is not None]
+
+        def form():
+            grads = linear_attention_backward(dout, q, k, v, log_decay, dstate=dstate, state=state,
+                                              lengths=lengths, scale=ctx.scale, decay=need[3])
+            return tuple(g for g in grads if g is not None)
+
+        grads = list(_once(form, *inputs))
+        if not need[3]:
+            grads.insert(3, None)
+        return (*grads, *[None] * (7 - len(grads)))
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, *,
+                     state=None, lengths=None, scale: float | None = None):
+    """Linear attention as :func:`linear_attention_forward`, differentiable (once, in reverse) in q, k,
+    v, log_decay and state; returns (out, state_out)."""
+    if _wants_gradient(q, k, v, log_decay, state):
+        return _LinearAttention.apply(q, k, v, log_decay, state, lengths, scale)
+    return linear_attention_forward(q, k, v, log_decay, state=state, lengths=lengths, scale=scale)
+
+
+# ---- clipping of gradients -----------------------------------------------------------
+
+
+def _dense(t) -> bool:
+    """Whether a tensor's values fill a piece of memory, in whatever order of its axes."""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _gradients(tensors, out):
+    """The packed list, its length and the tensors' device (None without tensors)."""
+    if isinstance(tensors, torch.Tensor):
+        tensors = [tensors]
+    tensors = [t for t in tensors if t is not None]
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else [o for o in out if o is not None]
+        if len(out) != len(tensors):
+            raise ValueError("out has to have a place for each tensor")
+    flat, device = [], None
+    if _wants_gradient(*tensors):
+        raise NotImplementedError("clipping has no gradients")
+    for i, t in enumerate(tensors):
+        device = _device_of(t, f"tensor {i}")
+        if not _dense(t):
+            raise ValueError(f"tensor {i} has gaps between its values")
+        to = t
+        if out is not None:
+            to = out[i]
+            _out_like(to, t, t.dtype, device, f"out {i}")
+            if to.stride() != t.stride():
+                raise ValueError(f"out {i} differs in layout")
+        flat += (t.data_ptr(), to.data_ptr(), t.numel(), DTYPES[t.dtype])
+    return struct.pack("=" + "QQqq" * len(tensors), *flat), len(tensors), device
+
+
+def _clip(tensors, max_norm, out, where):
+    packed, n, device = _gradients(tensors, out)
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    lib = load()
+    stream = _stream(device)
+    if max_norm is None:
+        def call(p, size):
+            return lib.lic_gradient_norm(packed, n, norm.data_ptr(), p, size, stream)
+    else:
+        def call(p, size):
+            return lib.lic_clip_gradients(packed, n, max_norm, norm.data_ptr(), p, size, stream)
+    _with_workspace(device, stream, call, lambda: lib.lic_clip_gradients_workspace_bytes(packed, n), where)
+    return norm
+
+
+def gradient_norm(tensors) -> torch.Tensor:
+    """Enqueue the norm of all values of all tensors together; returns it, float32 [].
+
+    ``tensors`` is a list of tensors without gaps, of any types and shapes (None is passed over), or
+    one tensor.  Squares are summed in 64 bits.
+    """
+    return _clip(tensors, None, None, "lic_gradient_norm")
+
+
+def clip_gradients(tensors, max_norm: float, *, out=None) -> torch.Tensor:
+    """Enqueue the scaling of all tensors by min(1, max_norm / (norm + 1e-6)); returns the norm, float32 [].
+
+    As in :func:`gradient_norm`; in place, or into ``out``, a list of tensors laid out the same.
+    No tensor may overlap another that is written.  A NaN anywhere makes everything NaN; with an
+    infinity the factor is 0.
+    """
+    max_norm = float(max_norm)
+    if not (max_norm >= 0 and math.isfinite(max_norm)):
+        raise ValueError("max_norm must be finite and at least 0")
+    return _clip(tensors, max_norm, out, "lic_clip_gradients")
