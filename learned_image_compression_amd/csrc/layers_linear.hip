@@ -128,11 +128,11 @@ __global__ __launch_bounds__(256) void linear_join(JoinArgs a)
     head_row<T>(a.out, a.out_stride, (int)b, token, (int)(line - b * a.heads))[d] = down<T>(s);
 }
 
-// dlog_decay[head]: one wave a head, over the batch.
-__global__ __launch_bounds__(64) void linear_decay_join(const float *sums, float *out, int32_t batch, int32_t heads, int32_t parts)
+// dlog_decay[head]: one wave a head, over the batch's parts (its segments).
+__global__ __launch_bounds__(64) void linear_decay_join(const double *sums, float *out, int32_t batch, int32_t heads, int32_t parts)
 {
     const int head = blockIdx.x, lane = threadIdx.x;
-    float s = 0.0f;
+    double s = 0.0;
     for (int64_t i = lane; i < (int64_t)batch * parts; i += 64) {
         const int64_t b = i / parts;
         s += sums[(b * heads + head) * parts + (i - b * parts)];
@@ -141,7 +141,121 @@ __global__ __launch_bounds__(64) void linear_decay_join(const float *sums, float
     for (int d = 32; d > 0; d >>= 1)
         s += __shfl_xor(s, d);
     if (lane == 0)
-        out[head] = s;
+        out[head] = (float)s;
+}
+
+// ---- the states before the segments ------------------------------------------------
+//
+// start_(k+1) = g^(tokens of k) start_k + what k adds, in place of what the segments add.  A block takes 64
+// numbers of a state, four a thread, and all segments: 16 groups of up to 16 neighbours.  Each group adds up
+// its own, then what comes from the groups before it, so a thread waits for memory once.
+constexpr int kMostSegments = 256, kScanGroups = 16;
+
+struct ScanArgs {
+    LinearJob job[2];
+    const float *log_decay;
+    const int32_t *lengths;
+    int64_t tokens, first;
+    int32_t heads, jobs, segments, each, start_floats, tiles; // of 64 numbers
+    int32_t group;                                            // segments of a group
+};
+
+template <int EACH>
+__global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
+{
+    using VT = Vec<float, 4>;
+    __shared__ VT ends[kScanGroups][16];
+    __shared__ float powers[kScanGroups];
+    const int64_t id = a.first + blockIdx.x, line = id / a.tiles / a.jobs;
+    const int tile = (int)(id % a.tiles), which = (int)(id / a.tiles % a.jobs);
+    const LinearJob &p = a.job[which];
+    const int b = (int)(line / a.heads), head = (int)(line - (int64_t)b * a.heads);
+    const int t = (int)threadIdx.x, x = t & 15, group = t >> 4;
+    const int at = (tile * 16 + x) * 4; // its numbers of a state
+    const bool there = at < a.start_floats;
+    float *starts = p.starts + line * a.segments * a.start_floats + at;
+    // in the order of time: segment 0 first, or the last one
+    const auto index = [&](int k) { return p.reverse ? a.segments - 1 - k : k; };
+    const int k0 = group * a.group;
+    VT add[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        add[i] = VT{};
+        // what the last one adds goes nowhere
+        if (there && i < a.group && k0 + i < a.segments - 1)
+            add[i] = load_at<VT>(starts + (int64_t)index(k0 + i) * a.start_floats);
+    }
+    VT run{};
+    if (group == 0 && there && p.first) {
+        const float *first = p.first + b * p.first_stride[0] + head * p.first_stride[1];
+        const int columns = p.dim_z;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (at + i < p.dim_x * columns)
+                run.v[i] = first[(at + i) / columns * p.first_stride[2] + (at + i) % columns * p.first_stride[3]];
+    }
+    const double log_decay = a.log_decay[head];
+    const int all = a.lengths ? min(max(a.lengths[b], 0), (int)a.tokens) : (int)a.tokens;
+    const auto tokens_of = [&](int k) { return min(max(all - index(k) * a.each, 0), a.each); };
+    const float whole = (float)exp(log_decay * a.each), part = (float)exp(log_decay * (all % a.each));
+    const auto power = [&](int k) {
+        const int n = tokens_of(k);
+        return n == a.each ? whole : n == 0 ? 1.0f : part;
+    };
+    VT sum = run;
+    float all_power = 1.0f;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        if (i < a.group && k0 + i < a.segments) {
+            const float g = power(k0 + i);
+            all_power *= g;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum.v[e] = fmaf(sum.v[e], g, add[i].v[e]);
+        }
+    ends[group][x] = sum;
+    if (x == 0)
+        powers[group] = all_power;
+    __syncthreads();
+    if (group > 0) {
+        run = ends[0][x];
+        for (int k = 1; k < group; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                run.v[e] = fmaf(run.v[e], powers[k], ends[k][x].v[e]);
+    }
+    if (!there)
+        return;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        if (i < a.group && k0 + i < a.segments) {
+            store_at(starts + (int64_t)index(k0 + i) * a.start_floats, run);
+            const float g = power(k0 + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                run.v[e] = fmaf(run.v[e], g, add[i].v[e]);
+        }
+}
+
+int run_scan(const LinearArgs &l, hipStream_t s)
+{
+    ScanArgs a{};
+    for (int i = 0; i < l.jobs; ++i)
+        a.job[i] = l.job[i];
+    a.log_decay = l.log_decay, a.lengths = l.lengths, a.tokens = l.tokens;
+    a.heads = l.heads, a.jobs = l.jobs, a.segments = l.segments, a.each = l.each, a.start_floats = l.start_floats;
+    a.tiles = (l.start_floats + 63) / 64;
+    a.group = (l.segments + kScanGroups - 1) / kScanGroups;
+    in_pieces((int64_t)l.batch * l.heads * l.jobs * a.tiles, 256, [&](int64_t first, uint32_t blocks) {
+        a.first = first;
+        if (a.group == 1)
+            linear_scan<1><<<blocks, 256, 0, s>>>(a);
+        else if (a.group <= 4)
+            linear_scan<4><<<blocks, 256, 0, s>>>(a);
+        else
+            linear_scan<16><<<blocks, 256, 0, s>>>(a);
+    });
+    return launched();
 }
 
 // ---- entries -------------------------------------------------------------------------
@@ -173,16 +287,37 @@ bool valid_call(const lic_linear_attention_args &p, bool backward)
 
 uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-// Scratch memory of a call: parts of dk and dv, sums of dlog_decay.
+// How the tokens are split: into as many segments as make four blocks a CU (heads wider than 64: one, since their
+// states' way through memory is as long as their tokens'), each of at least 32 tokens.
+struct Split {
+    int32_t segments, each;
+    explicit Split(const lic_linear_attention_args &p)
+    {
+        const int64_t want = std::max(p.dim, p.value_dim) <= 64 ? 1024 : 256;
+        int64_t n = std::min<int64_t>(want / std::max<int64_t>(p.batch * p.heads, 1), p.tokens / kRun);
+        n = std::max<int64_t>(1, std::min<int64_t>(n, kMostSegments));
+        each = (int32_t)std::max<int64_t>(kRun, ((p.tokens + n - 1) / n + kRun - 1) / kRun * kRun);
+        segments = (int32_t)std::max<int64_t>(1, (p.tokens + each - 1) / each);
+    }
+};
+
+int32_t start_floats(const lic_linear_attention_args &p) { return (int32_t)(p.dim * p.value_dim + 3) / 4 * 4; }
+
+// Scratch memory of a call: the states before segments (and their gradients behind them), parts of dk and
+// dv, sums of dlog_decay.
 struct Layout {
-    uint64_t dk, dv, sums, bytes;
+    uint64_t starts, ends, dk, dv, sums, bytes;
     Layout(const lic_linear_attention_args &p, bool backward)
     {
+        const Split split(p);
         const uint64_t lines = (uint64_t)p.batch * p.heads, shared = backward && p.heads > p.kv_heads;
-        dk = 0;
+        const uint64_t states = split.segments > 1 ? round256(lines * split.segments * start_floats(p) * 4) : 0;
+        starts = 0;
+        ends = starts + states;
+        dk = ends + (backward ? states : 0);
         dv = dk + (shared ? round256(lines * p.tokens * p.dim * 4) : 0);
         sums = dv + (shared ? round256(lines * p.tokens * p.value_dim * 4) : 0);
-        bytes = sums + (backward ? round256(lines * 4) : 0);
+        bytes = sums + (backward ? round256(lines * split.segments * 8) : 0);
     }
 };
 
@@ -204,7 +339,11 @@ void set_state(int64_t *to, const int64_t *from, bool turned)
 
 LinearArgs common(const lic_linear_attention_args &p)
 {
+    const Split split(p);
     LinearArgs a{};
+    a.segments = split.segments;
+    a.each = split.each;
+    a.start_floats = start_floats(p);
     a.log_decay = p.log_decay;
     a.lengths = p.lengths;
     a.tokens = p.tokens;
@@ -214,8 +353,18 @@ LinearArgs common(const lic_linear_attention_args &p)
     return a;
 }
 
+// The states before the segments of the first `jobs` jobs.
 template <typename T>
-int forward(const lic_linear_attention_args &p, hipStream_t s)
+int make_states(LinearArgs a, int jobs, bool vec, hipStream_t s)
+{
+    a.jobs = jobs;
+    if (const int rc = Linear<T>::states(a, vec, s))
+        return rc;
+    return run_scan(a, s);
+}
+
+template <typename T>
+int forward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
 {
     const int32_t share = (int32_t)(p.heads / p.kv_heads);
     if (p.tokens == 1) {
@@ -238,6 +387,12 @@ int forward(const lic_linear_attention_args &p, hipStream_t s)
     j.x_share = 1, j.y_share = j.z_share = share;
     j.dim_x = (int32_t)p.dim, j.dim_z = (int32_t)p.value_dim;
     j.read = a.scale, j.write = 1.0f;
+    j.starts = static_cast<float *>(ws);
+    j.start_stride[0] = j.dim_z, j.start_stride[1] = 1;
+    if (a.segments > 1) {
+        if (const int rc = make_states<T>(a, 1, vec, s))
+            return rc;
+    }
     return Linear<T>::sweep(a, vec, s);
 }
 
@@ -284,19 +439,34 @@ int backward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
         j.reverse = i > 0;
         j.read = i > 0 ? 1.0f : a.scale, j.write = i > 0 ? a.scale : 1.0f;
         j.first = i > 0 ? p.dstate : p.state;
+        j.starts = reinterpret_cast<float *>(base + (i > 0 ? at.ends : at.starts));
         return j;
     };
     LinearJob &dq = job(0, p.dout, p.dout_stride, 1, p.v, p.v_stride, share, p.k, p.k_stride, share, p.dq, p.dq_stride,
                         p.value_dim, p.dim);
     set_state(dq.first_stride, p.state_stride, true);
+    dq.start_stride[0] = 1, dq.start_stride[1] = (int32_t)p.value_dim;
     LinearJob &dv = job(1, p.k, p.k_stride, share, p.q, p.q_stride, 1, p.dout, p.dout_stride, 1, p.dv, p.dv_stride, p.dim,
                         p.value_dim);
     set_state(dv.first_stride, p.dstate_stride, false);
+    dv.start_stride[0] = (int32_t)p.value_dim, dv.start_stride[1] = 1;
     dv.last = p.dstate_in;
     set_state(dv.last_stride, p.dstate_in_stride, false);
     LinearJob &dk = job(2, p.v, p.v_stride, share, p.dout, p.dout_stride, 1, p.q, p.q_stride, 1, p.dk, p.dk_stride,
                         p.value_dim, p.dim);
     set_state(dk.first_stride, p.dstate_stride, true);
+    dk.start_stride[0] = 1, dk.start_stride[1] = (int32_t)p.value_dim;
+    if (a.segments > 1) {
+        LinearArgs st = a; // the states themselves, as the forward call's, and their gradients, as dv's
+        LinearJob &j = st.job[0];
+        j.y = p.k, j.z = p.v;
+        set3(j.y_stride, p.k_stride), set3(j.z_stride, p.v_stride);
+        set_state(j.first_stride, p.state_stride, false);
+        j.dim_x = (int32_t)p.dim, j.dim_z = (int32_t)p.value_dim;
+        j.start_stride[0] = j.dim_z, j.start_stride[1] = 1;
+        if (const int rc = make_states<T>(st, 2, vec, s))
+            return rc;
+    }
     if (share > 1) {
         dk.part = reinterpret_cast<float *>(base + at.dk);
         dv.part = reinterpret_cast<float *>(base + at.dv);
@@ -313,7 +483,10 @@ int backward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
         return RANS_OK;
     DecayArgs d{};
     d.q = p.q, d.k = p.k, d.v = p.v, d.dout = p.dout, d.state = p.state, d.dstate = p.dstate;
-    d.sums = reinterpret_cast<float *>(base + at.sums);
+    d.sums = reinterpret_cast<double *>(base + at.sums);
+    d.starts = reinterpret_cast<float *>(base + at.starts);
+    d.ends = reinterpret_cast<float *>(base + at.ends);
+    d.segments = a.segments, d.each = a.each, d.start_floats = a.start_floats;
     set3(d.q_stride, p.q_stride), set3(d.k_stride, p.k_stride), set3(d.v_stride, p.v_stride);
     set3(d.dout_stride, p.dout_stride), set3(d.state_stride, p.state_stride), set3(d.dstate_stride, p.dstate_stride);
     d.log_decay = p.log_decay, d.lengths = p.lengths, d.tokens = p.tokens;
@@ -321,7 +494,7 @@ int backward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
     d.dim = (int32_t)p.dim, d.value_dim = (int32_t)p.value_dim, d.scale = a.scale;
     if (const int rc = Linear<T>::decay(d, vec, s))
         return rc;
-    linear_decay_join<<<(uint32_t)p.heads, 64, 0, s>>>(d.sums, p.dlog_decay, d.batch, d.heads, 1);
+    linear_decay_join<<<(uint32_t)p.heads, 64, 0, s>>>(d.sums, p.dlog_decay, d.batch, d.heads, d.segments);
     return launched();
 }
 
@@ -343,7 +516,7 @@ int call(const lic_linear_attention_args *args, void *ws, uint64_t ws_bytes, hip
         return RANS_E_WORKSPACE;
     return with_dtype(p.dtype, [&](auto t) {
         using T = decltype(t);
-        return back ? backward<T>(p, ws, s) : forward<T>(p, s);
+        return back ? backward<T>(p, ws, s) : forward<T>(p, ws, s);
     });
 }
 

@@ -2,7 +2,7 @@
 //
 //   M_t = g M_(t-1) + y_t z_t',   out_t = s x_t M_t
 //
-// Runs of C tokens: with M the state before a run and i, j its tokens (0 .. C - 1),
+// Runs of C = 32 tokens: with M the state before a run and i, j its tokens (0 .. C - 1),
 //   out_i = s (sum over j <= i of g^(i-j) (x_i . y_j) z_j + g^(i+1) x_i M),
 //   M    <- g^C M + sum over j of g^(C-1-j) y_j z_j'
 // so all work is in matrix products and only the states go from run to run.
@@ -13,11 +13,12 @@
 // (backward in time M holds s sum of g^(i+1) q_i dout_i' of the tokens after a run: the gradient of the
 // state between, so the powers of g are one less where it is read and one more where it is written).
 //
-// A block takes one head of one batch, a wave 32 columns of z: of the state (32 DT of it in its
-// accumulators) and of the outputs.  Outputs are formed transposed, so what a token is multiplied by
-// (powers of g) is one number a lane, and scores and states are operands of the next product as they
-// stand in their accumulators.  Each wave forms the scores for itself: with C = 64 that is a third of the
-// products, none of which bounds the kernel, and saves their way through LDS.
+// A block takes a segment of the tokens of one head of one batch, a wave 32 columns of z: of the state (its
+// DT rows in the accumulators) and of the outputs.  Outputs are formed transposed, so what a token is
+// multiplied by (a power of g) is one number a lane, and scores and states are operands of the next
+// product as they stand in their accumulators.  Each wave forms the scores for itself, which saves their
+// way through LDS.  Where heads are few, tokens are split into segments: linear_states forms what each adds
+// to the state, linear_scan goes over the segments, and the sweep begins each with its state.
 #pragma once
 
 #include "layers_attention.hpp"
@@ -25,13 +26,15 @@
 namespace lic {
 
 struct LinearJob {
-    const void *x, *y, *z;
+    const void *x, *y, *z; // (the states' kernel reads y and z)
     void *out;
     float *part;        // out, or (where heads share it) each head's part: [batch][head][token][dim_z]
     const float *first; // the state before the tokens (null: 0), element [x's value][z's value]
     float *last;        // and behind them (may be null)
+    float *starts;      // where the tokens are split: the state before each segment, [batch][head][segment]
     int64_t x_stride[3], y_stride[3], z_stride[3], out_stride[3]; // batch, row, head
     int64_t first_stride[4], last_stride[4];                      // batch, head, x's value, z's value
+    int32_t start_stride[2];                                      // x's value, z's value
     int32_t x_share, y_share, z_share; // heads that share one of x's (y's, z's)
     int32_t dim_x, dim_z;
     int32_t reverse;   // 0, 1: backward in time
@@ -46,20 +49,40 @@ struct LinearArgs {
     const int32_t *lengths;
     int64_t tokens;
     int32_t batch, heads, jobs;
+    int32_t segments, each;  // of the tokens, and tokens of one
+    int32_t start_floats;    // of one segment's state
     float scale;
     uint32_t blocks, first;
 };
 
+// A segment of a batch's tokens: [from, to), of which `len` are in use.
+struct Segment {
+    int from, to, len;
+    bool last; // the one behind whose tokens the state is the call's
+    __device__ __forceinline__ Segment(const int32_t *lengths, int b, int tokens, int each, int index)
+    {
+        const int all = lengths ? min(max(lengths[b], 0), tokens) : tokens;
+        from = index * each;
+        to = min(tokens, from + each);
+        len = min(max(all - from, 0), each);
+        last = index == max(all - 1, 0) / each;
+    }
+};
+
 // Splits a 32-bit fragment into two operands of T whose sum is it to 2^-17 (bfloat16) or 2^-22.  (float
-// is its own operand.)  What is not finite stays in the first alone.
+// is its own operand.)  odd: some are not finite; those stay in the first alone.
 template <typename T>
-__device__ __forceinline__ void split(const float (&v)[8], FragV<T> &hi, FragV<T> &lo)
+__device__ __forceinline__ void split(const float (&v)[8], FragV<T> &hi, FragV<T> &lo, bool odd)
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         hi[i] = down_apart<T>(v[i]);
-        const float rest = v[i] - (float)hi[i];
-        lo[i] = (T)(not_finite(rest) ? 0.0f : rest);
+        lo[i] = (T)(v[i] - (float)hi[i]);
+    }
+    if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            lo[i] = not_finite((float)hi[i]) ? (T)0.0f : lo[i];
     }
 }
 
@@ -82,30 +105,63 @@ __device__ __forceinline__ float finite_size(float x) { return not_finite(x) ? 0
 template <typename T>
 constexpr bool kLifts = std::is_same<T, f16>::value;
 
-// Rows of a head on their way to a tile, as Stage, but the first tile row may be the last in memory, and
-// rows that are not there become 0: sums go over all of a tile's rows.
+// Rows of a head on their way to a tile, as Stage, run after run; backward in time the last in memory
+// becomes the tile's first.  The last run may have fewer rows: it ends where the tile ends, with rows of 0
+// before it, since sums go over all of a tile's rows and what a token is multiplied by is then the same in
+// every run.
 template <typename T, int ROWS, int DT, int THREADS, bool VEC>
 struct Run {
     using StageT = Stage<T, ROWS, DT, THREADS, VEC>;
     using TileT = Tile<T, ROWS, DT>;
     StageT stage;
+    const T *base, *next; // the segment's first row, and the next run's lowest
+    int64_t stride;
+    int dim;
+    bool reverse;
+    uint32_t from[VEC ? StageT::kEach : 1]; // bytes to a thread's pieces from the run's lowest row
 
-    // rows `rows` >= 1 from `base`, the lowest in memory
-    __device__ __forceinline__ void fetch(uint8_t *lds, const T *base, int64_t stride, int rows, int dim, bool reverse, int t)
+    __device__ __forceinline__ Run(const T *base, int64_t stride, int dim, bool reverse, int len, int t)
+        : base(base), next(base + (reverse ? max(len - ROWS, 0) : 0) * stride), stride(stride), dim(dim), reverse(reverse)
+    {
+        aim(ROWS, t);
+    }
+    // rows before a short run repeat its first
+    __device__ __forceinline__ void aim(int rows, int t)
     {
         if constexpr (VEC) {
-            const uint32_t first = __builtin_amdgcn_readfirstlane(
-                (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + (t & ~63) * 16);
 #pragma unroll
             for (int i = 0; i < StageT::kEach; ++i) {
                 int row, block, piece;
                 StageT::place(i, t, row, block, piece);
-                row = min(row, rows - 1);
-                const int d = block * 32 + piece * TileT::kPiece;
-                const uint32_t at = (uint32_t)(reverse ? rows - 1 - row : row) * (uint32_t)(stride * sizeof(T)) +
-                                    d * sizeof(T);
-                if (d < dim)
-                    load_lds<16>(first + i * THREADS * 16, base, at);
+                row = max(row - (ROWS - rows), 0);
+                from[i] = (uint32_t)(reverse ? rows - 1 - row : row) * (uint32_t)(stride * sizeof(T)) +
+                          (block * 32 + piece * TileT::kPiece) * sizeof(T);
+            }
+        }
+    }
+
+    // the next run, of `rows` >= 1 rows
+    __device__ __forceinline__ void fetch(uint8_t *lds, int rows, int t)
+    {
+        if (rows < ROWS) {
+            next = reverse ? base : next;
+            aim(rows, t);
+        }
+        if constexpr (VEC) {
+            const uint32_t first = __builtin_amdgcn_readfirstlane(
+                (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + (t & ~63) * 16);
+            if (dim == DT) {
+#pragma unroll
+                for (int i = 0; i < StageT::kEach; ++i)
+                    load_lds<16>(first + i * THREADS * 16, next, from[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < StageT::kEach; ++i) {
+                    int row, block, piece;
+                    StageT::place(i, t, row, block, piece);
+                    if (block * 32 + piece * TileT::kPiece < dim)
+                        load_lds<16>(first + i * THREADS * 16, next, from[i]);
+                }
             }
         } else {
 #pragma unroll
@@ -113,14 +169,16 @@ struct Run {
                 int row, block, piece;
                 StageT::place(i, t, row, block, piece);
                 const int d = block * 32 + piece * TileT::kPiece;
-                const T *p = base + (int64_t)(reverse ? rows - 1 - row : row) * stride + d;
+                row -= ROWS - rows;
+                const T *p = next + (int64_t)(reverse ? rows - 1 - row : row) * stride + d;
                 Vec<T, TileT::kPiece> v;
 #pragma unroll
                 for (int e = 0; e < TileT::kPiece; ++e)
-                    v.v[e] = row < rows && d + e < dim ? p[e] : (T)0.0f;
+                    v.v[e] = row >= 0 && d + e < dim ? p[e] : (T)0.0f;
                 stage.r[i] = *reinterpret_cast<const uint4 *>(&v);
             }
         }
+        next += reverse ? -ROWS * stride : ROWS * stride;
     }
     // what fetch() asked for is in LDS (after this and a barrier)
     __device__ __forceinline__ void store(uint8_t *lds, int rows, int t) const
@@ -132,7 +190,7 @@ struct Run {
                 for (int i = 0; i < StageT::kEach; ++i) {
                     int row, block, piece;
                     StageT::place(i, t, row, block, piece);
-                    if (row >= rows)
+                    if (row < ROWS - rows)
                         *reinterpret_cast<uint4 *>(lds + TileT::at(row, block, piece)) = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
@@ -140,30 +198,43 @@ struct Run {
     }
 };
 
-// A row fragment whose eight values are a column operand's: values 16 kk + 4 h .. and 16 kk + 8 + 4 h .. of `row`.
-template <typename T, int ROWS, int DT>
-__device__ __forceinline__ FragV<T> row_as_column(const uint8_t *lds, int row, int kk, int h)
+// The state's rows stand in its accumulators so that eight of them are neighbours as an operand, like a row
+// fragment's values: row `acc` of an accumulator is row state_row(acc) of its 32.  The products that form
+// the state take y's columns in that order (column c of them is state_row(c)).
+__host__ __device__ __forceinline__ constexpr int state_row(int acc)
 {
-    using TileT = Tile<T, ROWS, DT>;
+    return (acc & 0x13) | (acc & 4) << 1 | (acc & 8) >> 1;
+}
+
+// y's columns 32 block + state_row(l % 32), as Tile::col_frag
+template <typename T, typename TileT>
+__device__ __forceinline__ FragV<T> state_columns(const uint8_t *lds, int row0, int block, int lane)
+{
     FragV<T> f;
-    const int block = kk >> 1;
+    const int h = lane >> 5;
     if constexpr (sizeof(T) == 2) {
-        const int piece = (kk & 1) * 2;
+        // the middle two of the four fours of columns that 16 lanes ask for, the other way round
+        const int j = lane & 15;
+        const int row = row0 + 4 * h + (j >> 2);
+        const int piece = ((lane >> 4) & 1) * 2 + (j & 1);
+        using Lds = __attribute__((address_space(3))) short4v;
+        const auto read = [&](int r) {
+            const uint8_t *p = lds + TileT::at(r, block, piece) + ((j & 2) >> 1) * 8;
+            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds *)(__attribute__((address_space(3))) void *)p);
+        };
         union {
-            uint2 u[2];
+            short4v s[2];
             FragV<T> f;
         } u;
-        u.u[0] = *reinterpret_cast<const uint2 *>(lds + TileT::at(row, block, piece) + 8 * h);
-        u.u[1] = *reinterpret_cast<const uint2 *>(lds + TileT::at(row, block, piece + 1) + 8 * h);
+        u.s[0] = read(row);
+        u.s[1] = read(row + 8);
         f = u.f;
     } else {
-        using Q = float __attribute__((ext_vector_type(4)));
-        const Q a = *reinterpret_cast<const Q *>(lds + TileT::at(row, block, (kk & 1) * 4 + h));
-        const Q b = *reinterpret_cast<const Q *>(lds + TileT::at(row, block, (kk & 1) * 4 + 2 + h));
+        const int c = state_row(lane & 31);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = a[i];
-            f[4 + i] = b[i];
+        for (int i = 0; i < 8; ++i) {
+            const int row = row0 + acc_row(i, h);
+            f[i] = *reinterpret_cast<const float *>(lds + TileT::at(row, block, c >> 2) + (c & 3) * 4);
         }
     }
     return f;
@@ -178,22 +249,30 @@ __device__ __forceinline__ float tile_value(const uint8_t *lds, int row, int d)
                                            (d % TileT::kPiece) * sizeof(T)));
 }
 
-// Powers of a head's g, g^0 .. g^N, in LDS as a number and the rest to it: formed in 64 bits, since a state
-// takes them again with each run.
+// Powers of a head's g, g^0 .. g^N, in LDS.
 struct Powers {
-    float2 *at;
-    __device__ __forceinline__ float operator[](int n) const { return at[n].x; }
+    float *at;
+    __device__ __forceinline__ float operator[](int n) const { return at[n]; }
     __device__ __forceinline__ void fill(float log_decay, int n, int t, int threads)
     {
-        for (int e = t; e <= n; e += threads) {
-            const double p = e == 0 ? 1.0 : exp((double)log_decay * e);
-            const float hi = (float)p;
-            const float lo = (float)(p - (double)hi);
-            at[e] = make_float2(hi, not_finite(lo) ? 0.0f : lo);
-        }
+        for (int e = t; e <= n; e += threads)
+            at[e] = e == 0 ? 1.0f : expf(log_decay * (float)e);
     }
-    // x g^n
-    __device__ __forceinline__ float times(float x, float2 p) const { return fmaf(x, p.x, x * p.y); }
+};
+
+// What a state is multiplied by from run to run, g^32.  Its rounding to 32 bits would grow with the
+// number of runs, so every sixteenth run takes it with the sixteen errors' sum: what a sixteenth
+// of that is off by stays, 2^-29 a run, and what came in since is off by 2^-21 at most, once.
+struct Step {
+    float whole, mended;
+    __device__ __forceinline__ Step(float log_decay, int n)
+    {
+        const double p = exp((double)log_decay * n);
+        whole = (float)p;
+        const float rest = (float)(p - (double)whole);
+        mended = not_finite(rest) ? whole : fmaf(16.0f, rest, whole);
+    }
+    __device__ __forceinline__ float at(int run) const { return (run & 15) == 15 ? mended : whole; }
 };
 
 __device__ __forceinline__ float *part_row(const LinearArgs &a, const LinearJob &p, int b, int head, int64_t row)
@@ -201,14 +280,17 @@ __device__ __forceinline__ float *part_row(const LinearArgs &a, const LinearJob 
     return p.part + (((int64_t)b * a.heads + head) * a.tokens + row) * p.dim_z;
 }
 
-template <typename T, int DT, bool VEC>
-struct Sweep {
-    static constexpr int kTiles = sizeof(T) == 2 ? 2 : 1;
-    static constexpr int kRun = 32 * kTiles;             // tokens of a run
-    static constexpr int kBlocks = DT / 32;              // of 32 columns
+constexpr int kRun = 32; // tokens of a run
+
+// What the kernels hold of their tiles: TILES of kRun rows for each of two runs, and g's powers.
+template <typename T, int DT, bool VEC, int TILES>
+struct Runs {
+    static constexpr int kBlocks = DT / 32; // of 32 columns, and waves
     static constexpr int kThreads = 64 * kBlocks;
     static constexpr int kTileBytes = kRun * DT * sizeof(T);
-    static constexpr int kLds = 6 * kTileBytes + (kRun + 2) * 8;
+    static constexpr int kPowers = 2 * TILES * kTileBytes;
+    static constexpr int kFactors = kPowers + (kRun + 4) * 4; // of a token where the state takes it in
+    static constexpr int kLds = kFactors + 4 * kRun * 4;
     using RunT = Run<T, kRun, DT, kThreads, VEC>;
     using TileT = Tile<T, kRun, DT>;
 };
@@ -239,141 +321,237 @@ __device__ __forceinline__ bool odd_values(const FragV<T> &f)
     }
 }
 
-// m += sum over a run's tokens of y (z f)', z's columns as fragments, f(token) a token's factor.  The sums are
-// exact but for the split of z f.  The accumulators are settled.
-template <typename T, typename TileT, int ND, int N, typename F>
-__device__ __forceinline__ void add_outer(float16v (&m)[ND], const uint8_t *yt, const FragV<T> (&zf)[N], int lane, F &&f)
+// Tokens' factors where the state takes them in, as a column operand holds the tokens.
+struct Factors {
+    float f[2][8];
+
+    __device__ __forceinline__ Factors(const float *of, int h)
+    {
+        using V4 = float __attribute__((ext_vector_type(4)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const V4 v = *reinterpret_cast<const V4 *>(of + 8 * j + 4 * h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[j >> 1][4 * (j & 1) + e] = v[e];
+        }
+    }
+};
+
+// z's columns of a run
+template <typename T, typename TileT>
+__device__ __forceinline__ void columns(FragV<T> (&zf)[2], const uint8_t *zt, int block, int lane)
 {
-    const int h = lane >> 5;
-    float zw[N][8], top = 0.0f;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < 2; ++j)
+        zf[j] = TileT::col_frag(zt, 16 * j, block, lane);
+}
+
+// z f of a run's tokens as two operands each, in half precision times a power of two for each column.
+template <typename T>
+struct Taken {
+    FragV<T> hi[2], lo[2];
+    float back;
+
+    // odd: some of z f are not finite
+    __device__ __forceinline__ Taken(const FragV<T> (&zf)[2], const Factors &f, bool odd) : back(1.0f)
+    {
+        float zw[2][8], top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            zw[j][e] = (float)zf[j][e] * f(16 * j + (e & 3) + 4 * h + 8 * (e >> 2));
-            if constexpr (kLifts<T>)
-                top = fmaxf(top, finite_size(zw[j][e]));
-        }
-    const auto products = [&](float16v(&to)[ND]) {
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            FragV<T> hi, lo;
-            split<T>(zw[j], hi, lo);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const FragV<T> yf = TileT::col_frag(yt, 16 * j, d, lane);
-                to[d] = mma(yf, hi, to[d]);
-                if constexpr (sizeof(T) == 2)
-                    to[d] = mma(yf, lo, to[d]);
+            for (int e = 0; e < 8; ++e) {
+                zw[j][e] = (float)zf[j][e] * f.f[j][e];
+                if constexpr (kLifts<T>)
+                    top = fmaxf(top, finite_size(zw[j][e]));
             }
+        if constexpr (kLifts<T>) {
+            const float lift = lift_of<kStateLift>(pair_max(top));
+            back = inverse_lift(lift);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    zw[j][e] *= lift;
         }
-        settle<T>();
-    };
-    if constexpr (kLifts<T>) { // a column's power of two, multiplied back before the sum with m
-        const float lift = lift_of<kStateLift>(pair_max(top)), back = inverse_lift(lift);
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int j = 0; j < 2; ++j)
+            split<T>(zw[j], hi[j], lo[j], odd);
+    }
+    // m + sum over the tokens of y (z f)' / back, y's columns as fragments
+    __device__ __forceinline__ float16v times(const FragV<T> (&yf)[2], float16v m) const
+    {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                zw[j][e] *= lift;
-        float16v sum[ND];
+        for (int j = 0; j < 2; ++j) {
+            m = mma(yf[j], hi[j], m);
+            if constexpr (sizeof(T) == 2)
+                m = mma(yf[j], lo[j], m);
+        }
+        return m;
+    }
+};
+
+// m += sum over a run's tokens of y (z f)'.  The sums are exact but for the split of z f; the accumulators are
+// settled.
+template <typename T, typename TileT, int ND>
+__device__ __forceinline__ void add_outer(float16v (&m)[ND], const uint8_t *yt, const Taken<T> &z, int lane)
+{
+    float16v sum[ND];
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-            sum[d] = zero16();
-        products(sum);
+    for (int d = 0; d < ND; ++d) {
+        const FragV<T> yf[2] = {state_columns<T, TileT>(yt, 0, d, lane), state_columns<T, TileT>(yt, 16, d, lane)};
+        if constexpr (kLifts<T>)
+            sum[d] = z.times(yf, zero16());
+        else
+            m[d] = z.times(yf, m[d]);
+    }
+    settle<T>();
+    if constexpr (kLifts<T>) {
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                m[d][i] = fmaf(sum[d][i], back, m[d][i]);
-    } else {
-        products(m);
+                m[d][i] = fmaf(sum[d][i], z.back, m[d][i]);
     }
 }
 
-// z's columns of a run
-template <typename T, typename TileT, int N>
-__device__ __forceinline__ void columns(FragV<T> (&zf)[N], const uint8_t *zt, int block, int lane)
+template <int ND>
+__device__ __forceinline__ void decay(float16v (&m)[ND], float power)
 {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        zf[j] = TileT::col_frag(zt, 16 * j, block, lane);
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            m[d][i] *= power;
 }
 
-template <typename T, int DT, bool VEC>
-__global__ __launch_bounds__(2 * DT) void linear_sweep(LinearArgs a)
+// A wave's columns of a state to or from memory: at(row) is where row `row` of its lane's column is.
+template <int ND, typename F>
+__device__ __forceinline__ void each_row_of_state(int rows, int h, F &&f)
 {
-    using G = Sweep<T, DT, VEC>;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int row = 32 * d + state_row(acc_row(i, h));
+            if (row < rows)
+                f(d, i, row);
+        }
+}
+
+// Which job, batch, head and segment a block has; neighbours share a head's tokens.
+struct Work {
+    int job, b, head, segment;
+    int64_t line;
+    __device__ __forceinline__ Work(uint32_t which, int jobs, int segments, int heads)
+    {
+        const uint32_t rest = which / (uint32_t)jobs;
+        job = (int)(which - rest * (uint32_t)jobs);
+        line = rest / (uint32_t)segments;
+        segment = (int)(rest - (uint32_t)line * (uint32_t)segments);
+        b = (int)((uint32_t)line / (uint32_t)heads);
+        head = (int)((uint32_t)line - (uint32_t)b * (uint32_t)heads);
+    }
+};
+
+__device__ __forceinline__ float *start_of(const LinearArgs &a, const LinearJob &p, int64_t line, int segment)
+{
+    return p.starts + (line * a.segments + segment) * a.start_floats;
+}
+
+// ---- outputs -------------------------------------------------------------------
+
+template <typename T, int DT, bool VEC>
+__global__ __launch_bounds__(2 * DT, 2) void linear_sweep(LinearArgs a)
+{
+    using G = Runs<T, DT, VEC, 3>;
     using RunT = typename G::RunT;
     using TileT = typename G::TileT;
-    constexpr int ND = G::kBlocks, TILES = G::kTiles, C = G::kRun;
+    constexpr int ND = G::kBlocks, C = kRun;
     extern __shared__ __align__(16) uint8_t lds[];
 
     const uint32_t at = xcd_order(blockIdx.x, a.blocks);
     if (at >= a.blocks)
         return;
-    const uint32_t which = a.first + at;
-    const LinearJob &p = a.job[which % (uint32_t)a.jobs];
-    const uint32_t line = which / (uint32_t)a.jobs;
-    const int b = (int)(line / (uint32_t)a.heads), head = (int)(line - (uint32_t)b * a.heads);
+    const Work work(a.first + at, a.jobs, a.segments, a.heads);
+    const LinearJob &p = a.job[work.job];
+    const int b = work.b, head = work.head;
     const int t = (int)threadIdx.x, lane = t & 63, c = lane & 31, h = lane >> 5;
-    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-    const bool reverse = p.reverse != 0, works = 32 * w < p.dim_z;
-
-    const int tokens = (int)a.tokens;
-    const int len = a.lengths ? min(max(a.lengths[b], 0), tokens) : tokens;
-    const T *x = head_row<T>(p.x, p.x_stride, b, 0, head / p.x_share);
-    const T *y = head_row<T>(p.y, p.y_stride, b, 0, head / p.y_share);
-    const T *z = head_row<T>(p.z, p.z_stride, b, 0, head / p.z_share);
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6), col = 32 * w + c;
+    const int dim_z = p.dim_z;
+    const bool reverse = p.reverse != 0, works = 32 * w < dim_z;
+    const Segment seg(a.lengths, b, (int)a.tokens, a.each, work.segment);
+    const int len = seg.len, runs = (len + C - 1) / C;
 
     const auto tile = [&](int buffer, int which) { return lds + (3 * buffer + which) * G::kTileBytes; };
-    Powers g{reinterpret_cast<float2 *>(lds + 6 * G::kTileBytes)};
-    g.fill(a.log_decay[head], C, t, G::kThreads);
-    for (int i = 0; i < 6; ++i)
-        RunT::StageT::clear(lds + i * G::kTileBytes, i % 3 == 2 ? p.dim_z : p.dim_x, t);
-
-    // the state, columns 32 w + c
-    float16v m[ND];
-    const int col = 32 * w + c;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-        m[d] = zero16();
-        if (p.first && col < p.dim_z) {
-            const float *first = p.first + b * p.first_stride[0] + head * p.first_stride[1] + col * p.first_stride[3];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 32 * d + acc_row(i, h);
-                if (row < p.dim_x)
-                    m[d][i] = first[row * p.first_stride[2]];
-            }
-        }
-    }
-
-    RunT rx, ry, rz;
+    RunT rx(head_row<T>(p.x, p.x_stride, b, seg.from, head / p.x_share), p.x_stride[1], p.dim_x, reverse, len, t);
+    RunT ry(head_row<T>(p.y, p.y_stride, b, seg.from, head / p.y_share), p.y_stride[1], p.dim_x, reverse, len, t);
+    RunT rz(head_row<T>(p.z, p.z_stride, b, seg.from, head / p.z_share), p.z_stride[1], dim_z, reverse, len, t);
     const auto rows_of_run = [&](int k) { return min(C, len - k * C); };
-    // the lowest row of run k
-    const auto low = [&](int k) { return reverse ? len - k * C - rows_of_run(k) : k * C; };
     const auto fetch = [&](int k, int buffer) {
         const int n = rows_of_run(k);
-        const int64_t row = low(k);
-        rx.fetch(tile(buffer, 0), x + row * p.x_stride[1], p.x_stride[1], n, p.dim_x, reverse, t);
-        ry.fetch(tile(buffer, 1), y + row * p.y_stride[1], p.y_stride[1], n, p.dim_x, reverse, t);
-        rz.fetch(tile(buffer, 2), z + row * p.z_stride[1], p.z_stride[1], n, p.dim_z, reverse, t);
+        rx.fetch(tile(buffer, 0), n, t);
+        ry.fetch(tile(buffer, 1), n, t);
+        rz.fetch(tile(buffer, 2), n, t);
     };
-    const int runs = (len + C - 1) / C;
-    __syncthreads(); // the powers, and the tiles' unused columns
     if (runs > 0)
         fetch(0, 0);
+    for (int i = 0; i < 6; ++i) // what no load writes
+        RunT::StageT::clear(lds + i * G::kTileBytes, i % 3 == 2 ? p.dim_z : p.dim_x, t);
 
-    // g^(i - j) of a tile on the diagonal and of the one before it
-    float16v weight[TILES];
+    // the state before the segment
+    float16v m[ND];
 #pragma unroll
-    for (int n = 0; n < TILES; ++n)
+    for (int d = 0; d < ND; ++d)
+        m[d] = zero16();
+    if (col < p.dim_z && a.segments > 1) {
+        const float *start = start_of(a, p, work.line, work.segment) + col * p.start_stride[1];
+        each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { m[d][i] = start[row * p.start_stride[0]]; });
+    } else if (col < p.dim_z && p.first) {
+        const float *first = p.first + b * p.first_stride[0] + head * p.first_stride[1] + col * p.first_stride[3];
+        each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { m[d][i] = first[row * p.first_stride[2]]; });
+    }
+
+    Powers g{reinterpret_cast<float *>(lds + G::kPowers)};
+    float *factors = reinterpret_cast<float *>(lds + G::kFactors);
+    const float log_decay = a.log_decay[head];
+    g.fill(log_decay, C, t, G::kThreads);
+    const Step step(log_decay, C);
+    __syncthreads();
+    if (t < C)
+        factors[t] = g[C - 1 - t + (reverse ? 1 : 0)] * p.write;
+    // s g^(i - j), tokens j along the rows
+    float16v weight;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int e = 32 * n + c - acc_row(i, h);
-            weight[n][i] = e >= 0 ? g[max(e, 0)] * a.scale : 0.0f;
+    for (int i = 0; i < 16; ++i)
+        weight[i] = g[max(c - acc_row(i, h), 0)] * a.scale;
+    const float come = g[c + (reverse ? 0 : 1)] * p.read;
+
+    // A run's outputs go out during the next: the wait for its tiles would wait for them too.  A lane's row of
+    // a whole run, and the step to the next run's.
+    float *const part = p.part;
+    const int64_t out_stride = part ? (int64_t)dim_z * 4 : p.out_stride[1] * (int64_t)sizeof(T);
+    uint8_t *out = part ? reinterpret_cast<uint8_t *>(part_row(a, p, b, head, seg.from))
+                        : reinterpret_cast<uint8_t *>(head_row<T>(p.out, p.out_stride, b, seg.from, head));
+    out += (reverse ? (int64_t)max(len - C, 0) + C - 1 - c : (int64_t)c) * out_stride;
+    const int64_t out_step = reverse ? -C * out_stride : C * out_stride;
+    float16v o;
+    float lift = 1.0f;
+    const auto put = [&](int k) {
+        const int short_by = C - rows_of_run(k);
+        uint8_t *row = out;
+        if (short_by > 0) { // the last run: it ends with the tile, backward in time at row 0
+            row += reverse ? (k > 0 ? short_by * out_stride : 0) : -short_by * out_stride;
+            if (c < short_by)
+                return;
         }
+        const float back = kLifts<T> ? inverse_lift(lift) : 1.0f;
+        if (part)
+            put_column<float, VEC>(reinterpret_cast<float *>(row), o, back, w, h, dim_z);
+        else
+            put_column<T, VEC>(reinterpret_cast<T *>(row), o, back, w, h, dim_z);
+        out += out_step;
+    };
 
     for (int k = 0; k < runs; ++k) {
         const int n = rows_of_run(k), buffer = k & 1;
@@ -386,18 +564,12 @@ __global__ __launch_bounds__(2 * DT) void linear_sweep(LinearArgs a)
             fetch(k + 1, buffer ^ 1);
         if (!works)
             continue;
+        if (k > 0)
+            put(k - 1);
 
-        // z's columns, as they are and as the state takes them
-        FragV<T> zf[2 * TILES];
-        columns<T, TileT>(zf, zt, w, lane);
-        bool odd = false;
-#pragma unroll
-        for (int j = 0; j < 2 * TILES; ++j)
-            odd |= odd_values<T>(zf[j]);
-        odd = __any(odd);
-
-        // x M, the state rounded to an operand
-        FragV<T> mf[2 * ND];
+        // scores, and x M with the state rounded to an operand
+        float16v s = zero16();
+        o = zero16();
         float m_lift = 1.0f;
         if constexpr (kLifts<T>) {
             float top = 0.0f;
@@ -407,8 +579,8 @@ __global__ __launch_bounds__(2 * DT) void linear_sweep(LinearArgs a)
                 for (int i = 0; i < 16; ++i)
                     top = fmaxf(top, finite_size(m[d][i]));
 #pragma unroll
-            for (int s = 32; s > 0; s >>= 1)
-                top = fmaxf(top, __shfl_xor(top, s));
+            for (int x = 32; x > 0; x >>= 1)
+                top = fmaxf(top, __shfl_xor(top, x));
             m_lift = lift_of<kStateLift>(top);
         }
 #pragma unroll
@@ -419,140 +591,164 @@ __global__ __launch_bounds__(2 * DT) void linear_sweep(LinearArgs a)
                 for (int i = 0; i < 16; ++i)
                     lifted[i] *= m_lift;
             }
-            mf[2 * d] = operand<T>(lifted, 0);
-            mf[2 * d + 1] = operand<T>(lifted, 1);
-        }
-        float16v o[TILES];
-        float o_lift[TILES];
 #pragma unroll
-        for (int it = 0; it < TILES; ++it) {
-            FragV<T> xf[2 * ND];
-#pragma unroll
-            for (int kk = 0; kk < 2 * ND; ++kk)
-                xf[kk] = row_as_column<T, C, DT>(xt, 32 * it + c, kk, h);
-            o[it] = zero16();
-#pragma unroll
-            for (int kk = 0; kk < 2 * ND; ++kk)
-                o[it] = mma(mf[kk], xf[kk], o[it]);
-            // scores, tokens before along the rows
-            float16v s[TILES];
-#pragma unroll
-            for (int jt = 0; jt <= it; ++jt) {
-                s[jt] = zero16();
-#pragma unroll
-                for (int kk = 0; kk < 2 * ND; ++kk)
-                    s[jt] = mma(row_as_column<T, C, DT>(yt, 32 * jt + c, kk, h), xf[kk], s[jt]);
+            for (int half = 0; half < 2; ++half) {
+                const FragV<T> xf = TileT::row_frag(xt, c, 2 * d + half, h);
+                s = mma(TileT::row_frag(yt, c, 2 * d + half, h), xf, s);
+                o = mma(operand<T>(lifted, half), xf, o);
             }
-            float top = 0.0f;
+        }
+        FragV<T> zf[2];
+        columns<T, TileT>(zf, zt, w, lane);
+        const bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1]));
+
+        settle<T>();
+        if (n < C) { // rows before a short run are no tokens: 0 times an infinity is not theirs
 #pragma unroll
-            for (int jt = 0; jt <= it; ++jt)
+            for (int i = 0; i < 16; ++i)
+                s[i] = acc_row(i, h) < C - n ? 0.0f : s[i];
+        }
+        float top = 0.0f, f = n < C ? g[max(c - (C - n), 0) + (reverse ? 0 : 1)] * p.read : come;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            // a later token's score counts for nothing, whatever it is
+            s[i] = acc_row(i, h) <= c ? s[i] * weight[i] : 0.0f;
+            if constexpr (kLifts<T>)
+                top = fmaxf(top, finite_size(s[i]));
+        }
+        if constexpr (kLifts<T>) {
+            lift = lift_of<kScoreLift>(pair_max(top));
+            f *= lift * inverse_lift(m_lift);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[i] *= lift;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[i] *= f;
+        if (!odd) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                o = mma(zf[half], operand<T>(s, half), o); // settled with the state
+        } else {
+            // a later token's NaN times its score of 0 would be NaN here: what is not finite is left out of the
+            // product and added where it is seen
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                FragV<T> fine = zf[half];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    fine[e] = not_finite((float)fine[e]) ? (T)0.0f : fine[e];
+                o = mma(fine, operand<T>(s, half), o);
+            }
+            settle<T>();
+            for (int j = C - n; j < C; ++j) {
+                // the score of token j and this lane's, from the lane and register that hold it
+                const int from = (j >> 2) & 1, i0 = 4 * (j >> 3) + (j & 3);
+                float score = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    score = i == i0 ? s[i] : score;
+                score = __shfl(score, c + 32 * from);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    // a later token's score counts for nothing, whatever it is
-                    const bool seen = jt < it || acc_row(i, h) <= c;
-                    s[jt][i] = seen ? s[jt][i] * weight[it - jt][i] : 0.0f;
-                    if constexpr (kLifts<T>)
-                        top = fmaxf(top, finite_size(s[jt][i]));
-                }
-            o_lift[it] = 1.0f;
-            if constexpr (kLifts<T>) {
-                o_lift[it] = lift_of<kScoreLift>(pair_max(top));
-#pragma unroll
-                for (int jt = 0; jt <= it; ++jt)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[jt][i] *= o_lift[it];
-            }
-            const int i = 32 * it + c;
-            float f = g[i + (reverse ? 0 : 1)] * p.read;
-            if constexpr (kLifts<T>)
-                f *= o_lift[it] * inverse_lift(m_lift);
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                o[it][r] *= f;
-#pragma unroll
-            for (int jt = 0; jt < it; ++jt)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    o[it] = mma(zf[2 * jt + half], operand<T>(s[jt], half), o[it]);
-            if (!odd) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    o[it] = mma(zf[2 * it + half], operand<T>(s[it], half), o[it]);
-                settle<T>();
-            } else {
-                // a later token's NaN times its score of 0 would be NaN here: what is not finite is left
-                // out of the product and added where it is seen
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    FragV<T> fine = zf[2 * it + half];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        fine[e] = not_finite((float)fine[e]) ? (T)0.0f : fine[e];
-                    o[it] = mma(fine, operand<T>(s[it], half), o[it]);
-                }
-                settle<T>();
-                for (int j = 0; j < 32; ++j) {
-                    // the score of token j and this lane's, from the lane and register that hold it
-                    const int from = (j >> 2) & 1, i0 = 4 * (j >> 3) + (j & 3);
-                    float score = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        score = r == i0 ? s[it][r] : score;
-                    score = __shfl(score, c + 32 * from);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float v = tile_value<T, C, DT>(zt, 32 * it + j, 32 * w + acc_row(r, h));
-                        if (j <= c && not_finite(v))
-                            o[it][r] += score * v;
-                    }
+                    const float v = tile_value<T, C, DT>(zt, j, 32 * w + acc_row(i, h));
+                    if (j <= c && not_finite(v))
+                        o[i] += score * v;
                 }
             }
         }
 
         // the state behind the run
-        const float2 whole = g.at[n];
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                m[d][i] = g.times(m[d][i], whole);
-        add_outer<T, TileT>(m, yt, zf, lane, [&](int j) { return g[max(n - 1 - j, 0) + (reverse ? 1 : 0)] * p.write; });
-        const int64_t row0 = low(k);
-#pragma unroll
-        for (int it = 0; it < TILES; ++it) {
-            const int i = 32 * it + c;
-            const int64_t row = row0 + (reverse ? n - 1 - i : i);
-            const float f = kLifts<T> ? inverse_lift(o_lift[it]) : 1.0f;
-            if (i >= n)
-                continue;
-            if (p.part)
-                put_column<float, VEC>(part_row(a, p, b, head, row), o[it], f, w, h, p.dim_z);
-            else
-                put_column<T, VEC>(head_row<T>(p.out, p.out_stride, b, row, head), o[it], f, w, h, p.dim_z);
-        }
+        decay(m, n < C ? g[n] : step.at(k));
+        add_outer<T, TileT>(m, yt, Taken<T>(zf, Factors(factors, h), odd || log_decay > 0.0f), lane);
     }
 
-    if (!works)
+    if (works && runs > 0)
+        put(runs - 1);
+    if (col >= dim_z)
         return;
     // rows behind the last token
-    for (int row = len + h; row < tokens; row += 2)
-        if (col < p.dim_z) {
-            if (p.part)
-                part_row(a, p, b, head, row)[col] = 0.0f;
-            else
-                head_row<T>(p.out, p.out_stride, b, row, head)[col] = (T)0.0f;
-        }
-    if (p.last && col < p.dim_z) {
+    for (int row = seg.from + len + h; row < seg.to; row += 2) {
+        if (p.part)
+            part_row(a, p, b, head, row)[col] = 0.0f;
+        else
+            head_row<T>(p.out, p.out_stride, b, row, head)[col] = (T)0.0f;
+    }
+    if (p.last && (reverse ? work.segment == 0 : seg.last)) {
         float *last = p.last + b * p.last_stride[0] + head * p.last_stride[1] + col * p.last_stride[3];
+        each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { last[row * p.last_stride[2]] = m[d][i]; });
+    }
+}
+
+// ---- what segments add to the state ---------------------------------------------
+
+template <typename T, int DT, bool VEC>
+__global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(LinearArgs a)
+{
+    using G = Runs<T, DT, VEC, 2>;
+    using RunT = typename G::RunT;
+    using TileT = typename G::TileT;
+    constexpr int ND = G::kBlocks, C = kRun;
+    extern __shared__ __align__(16) uint8_t lds[];
+
+    const uint32_t at = xcd_order(blockIdx.x, a.blocks);
+    if (at >= a.blocks)
+        return;
+    const Work work(a.first + at, a.jobs, a.segments, a.heads);
+    const LinearJob &p = a.job[work.job];
+    const int b = work.b, head = work.head;
+    const int t = (int)threadIdx.x, lane = t & 63, c = lane & 31, h = lane >> 5;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6), col = 32 * w + c;
+    const bool reverse = p.reverse != 0, works = 32 * w < p.dim_z;
+    const Segment seg(a.lengths, b, (int)a.tokens, a.each, work.segment);
+    if (reverse ? work.segment == 0 : work.segment == a.segments - 1)
+        return; // no segment begins behind it
+    const int len = seg.len, runs = (len + C - 1) / C;
+
+    const auto tile = [&](int buffer, int which) { return lds + (2 * buffer + which) * G::kTileBytes; };
+    RunT ry(head_row<T>(p.y, p.y_stride, b, seg.from, head / p.y_share), p.y_stride[1], p.dim_x, reverse, len, t);
+    RunT rz(head_row<T>(p.z, p.z_stride, b, seg.from, head / p.z_share), p.z_stride[1], p.dim_z, reverse, len, t);
+    const auto rows_of_run = [&](int k) { return min(C, len - k * C); };
+    const auto fetch = [&](int k, int buffer) {
+        ry.fetch(tile(buffer, 0), rows_of_run(k), t);
+        rz.fetch(tile(buffer, 1), rows_of_run(k), t);
+    };
+    if (runs > 0)
+        fetch(0, 0);
+    for (int i = 0; i < 4; ++i) // what no load writes
+        RunT::StageT::clear(lds + i * G::kTileBytes, i % 2 == 1 ? p.dim_z : p.dim_x, t);
+    float16v m[ND];
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 32 * d + acc_row(i, h);
-                if (row < p.dim_x)
-                    last[row * p.last_stride[2]] = m[d][i];
-            }
+    for (int d = 0; d < ND; ++d)
+        m[d] = zero16();
+    Powers g{reinterpret_cast<float *>(lds + G::kPowers)};
+    float *factors = reinterpret_cast<float *>(lds + G::kFactors);
+    const float log_decay = a.log_decay[head];
+    g.fill(log_decay, C, t, G::kThreads);
+    const Step step(log_decay, C);
+    __syncthreads();
+    if (t < C)
+        factors[t] = g[C - 1 - t + (reverse ? 1 : 0)] * p.write;
+    for (int k = 0; k < runs; ++k) {
+        const int n = rows_of_run(k), buffer = k & 1;
+        uint8_t *yt = tile(buffer, 0), *zt = tile(buffer, 1);
+        ry.store(yt, n, t);
+        rz.store(zt, n, t);
+        __syncthreads();
+        if (k + 1 < runs)
+            fetch(k + 1, buffer ^ 1);
+        if (!works)
+            continue;
+        FragV<T> zf[2];
+        columns<T, TileT>(zf, zt, w, lane);
+        const bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1]));
+        decay(m, n < C ? g[n] : step.at(k));
+        add_outer<T, TileT>(m, yt, Taken<T>(zf, Factors(factors, h), odd || log_decay > 0.0f), lane);
+    }
+    if (col < p.dim_z) {
+        float *start = start_of(a, p, work.line, work.segment) + col * p.start_stride[1];
+        each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { start[row * p.start_stride[0]] = m[d][i]; });
     }
 }
 
@@ -566,96 +762,101 @@ __global__ __launch_bounds__(2 * DT) void linear_sweep(LinearArgs a)
 //   the others: <T, U> + <S, V>,  U = scale sum_i g^(i+1) q_i dout_i',  V the same with i + 1 in front
 //   T <- g^C (T + C S) + sum_j (C-1-j) g^(C-1-j) k_j v_j'
 // All of these are sums over tokens of an exact operand and one that is split in two, so nothing is rounded
-// to 16 bits on its way.  At the end <T, dstate> counts the steps of what is left over.
+// to 16 bits on its way.  A segment begins with T = 0 and counts the steps within it; <T, dS> at its end, dS
+// the gradient of the state there, counts them for the tokens behind it.
 struct DecayArgs {
     const void *q, *k, *v, *dout;
-    const float *state, *dstate;
-    float *sums; // [batch][heads]
+    const float *state, *dstate;   // one segment: the call's
+    const float *starts, *ends;    // else of each segment, [batch][head][segment]
+    double *sums;                  // [batch][heads][segments]
     int64_t q_stride[3], k_stride[3], v_stride[3], dout_stride[3], state_stride[3], dstate_stride[3];
     const float *log_decay;
     const int32_t *lengths;
     int64_t tokens;
     int32_t batch, heads, share, dim, value_dim;
+    int32_t segments, each, start_floats;
     float scale;
     uint32_t blocks, first;
 };
 
 template <typename T, int DT, bool VEC>
-struct Decay {
-    using S = Sweep<T, DT, VEC>;
-    static constexpr int kRun = 32;
-    static constexpr int kBlocks = DT / 32, kThreads = 64 * kBlocks;
-    static constexpr int kTileBytes = kRun * DT * sizeof(T);
-    static constexpr int kLds = 8 * kTileBytes + (kRun + 2) * 8 + kBlocks * 8;
-    using RunT = Run<T, kRun, DT, kThreads, VEC>;
-    using TileT = Tile<T, kRun, DT>;
-};
-
-template <typename T, int DT, bool VEC>
 __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
 {
-    using G = Decay<T, DT, VEC>;
+    using G = Runs<T, DT, VEC, 4>;
     using RunT = typename G::RunT;
     using TileT = typename G::TileT;
-    constexpr int ND = G::kBlocks, C = G::kRun;
+    constexpr int ND = G::kBlocks, C = kRun;
     extern __shared__ __align__(16) uint8_t lds[];
 
     const uint32_t at = xcd_order(blockIdx.x, a.blocks);
     if (at >= a.blocks)
         return;
-    const uint32_t line = a.first + at;
-    const int b = (int)(line / (uint32_t)a.heads), head = (int)(line - (uint32_t)b * a.heads), kv = head / a.share;
+    const Work work(a.first + at, 1, a.segments, a.heads);
+    const int b = work.b, head = work.head, kv = head / a.share;
     const int t = (int)threadIdx.x, lane = t & 63, c = lane & 31, h = lane >> 5;
-    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int tokens = (int)a.tokens;
-    const int len = a.lengths ? min(max(a.lengths[b], 0), tokens) : tokens;
-    const T *src[4] = {head_row<T>(a.q, a.q_stride, b, 0, head), head_row<T>(a.k, a.k_stride, b, 0, kv),
-                       head_row<T>(a.v, a.v_stride, b, 0, kv), head_row<T>(a.dout, a.dout_stride, b, 0, head)};
-    const int64_t step[4] = {a.q_stride[1], a.k_stride[1], a.v_stride[1], a.dout_stride[1]};
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6), col = 32 * w + c;
+    const Segment seg(a.lengths, b, (int)a.tokens, a.each, work.segment);
+    const int len = seg.len, runs = (len + C - 1) / C;
     const int dims[4] = {a.dim, a.dim, a.value_dim, a.value_dim};
 
     const auto tile = [&](int buffer, int which) { return lds + (4 * buffer + which) * G::kTileBytes; };
-    Powers g{reinterpret_cast<float2 *>(lds + 8 * G::kTileBytes)};
-    float *waves = reinterpret_cast<float *>(lds + 8 * G::kTileBytes + (C + 2) * 8);
-    g.fill(a.log_decay[head], C, t, G::kThreads);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        RunT::StageT::clear(lds + i * G::kTileBytes, dims[i % 4], t);
-
-    float16v s[ND], u[ND];
-    const int col = 32 * w + c;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-        s[d] = u[d] = zero16();
-        if (a.state && col < a.value_dim) {
-            const float *state = a.state + b * a.state_stride[0] + head * a.state_stride[1] + col;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 32 * d + acc_row(i, h);
-                if (row < a.dim)
-                    s[d][i] = state[row * a.state_stride[2]];
-            }
-        }
-    }
-
-    RunT run[4];
+    RunT run[4] = {
+        RunT(head_row<T>(a.q, a.q_stride, b, seg.from, head), a.q_stride[1], a.dim, false, len, t),
+        RunT(head_row<T>(a.k, a.k_stride, b, seg.from, kv), a.k_stride[1], a.dim, false, len, t),
+        RunT(head_row<T>(a.v, a.v_stride, b, seg.from, kv), a.v_stride[1], a.value_dim, false, len, t),
+        RunT(head_row<T>(a.dout, a.dout_stride, b, seg.from, head), a.dout_stride[1], a.value_dim, false, len, t)};
     const auto rows_of_run = [&](int k) { return min(C, len - k * C); };
     const auto fetch = [&](int k, int buffer) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            run[i].fetch(tile(buffer, i), src[i] + (int64_t)k * C * step[i], step[i], rows_of_run(k), dims[i], false, t);
+            run[i].fetch(tile(buffer, i), rows_of_run(k), t);
     };
-    const int runs = (len + C - 1) / C;
-    __syncthreads();
     if (runs > 0)
         fetch(0, 0);
-    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) // what no load writes
+        RunT::StageT::clear(lds + i * G::kTileBytes, dims[i % 4], t);
+    float16v s[ND], u[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+        s[d] = u[d] = zero16();
+    const int64_t place = (work.line * a.segments + work.segment) * a.start_floats;
+    if (col < a.value_dim && a.segments > 1) {
+        const float *start = a.starts + place + col;
+        each_row_of_state<ND>(a.dim, h, [&](int d, int i, int row) { s[d][i] = start[row * a.value_dim]; });
+    } else if (col < a.value_dim && a.state) {
+        const float *state = a.state + b * a.state_stride[0] + head * a.state_stride[1] + col;
+        each_row_of_state<ND>(a.dim, h, [&](int d, int i, int row) { s[d][i] = state[row * a.state_stride[2]]; });
+    }
+    // factors of a token: where a state takes it in for T and S, and for U and V, whose first token of a run
+    // of n is token C - n of the tile
+    Powers g{reinterpret_cast<float *>(lds + G::kPowers)};
+    float *factors = reinterpret_cast<float *>(lds + G::kFactors);
+    const float log_decay = a.log_decay[head];
+    g.fill(log_decay, C, t, G::kThreads);
+    const Step decays(log_decay, C);
+    const auto fill = [&](int n) {
+        if (t < C) {
+            const int i = max(t - (C - n), 0) + 1;
+            factors[t] = a.scale * g[i];
+            factors[C + t] = a.scale * (float)i * g[i];
+            factors[2 * C + t] = (float)(C - 1 - t) * g[C - 1 - t];
+            factors[3 * C + t] = g[C - 1 - t];
+        }
+    };
+    __syncthreads();
+    fill(C);
+    double sum = 0.0; // of the runs' sums in 32 bits
     for (int k = 0; k < runs; ++k) {
         const int n = rows_of_run(k), buffer = k & 1;
         const uint8_t *qt = tile(buffer, 0), *kt = tile(buffer, 1), *vt = tile(buffer, 2), *dt = tile(buffer, 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             run[i].store(tile(buffer, i), n, t);
+        if (n < C) {
+            __syncthreads(); // the last run's factors
+            fill(n);
+        }
         __syncthreads();
         if (k + 1 < runs)
             fetch(k + 1, buffer ^ 1);
@@ -667,65 +868,81 @@ __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
                 y = mma(TileT::row_frag(vt, c, kk, h), TileT::row_frag(dt, c, kk, h), y);
             }
             settle<T>();
+            float part = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int e = c - acc_row(i, h);
                 if (e > 0)
-                    sum = fmaf(x[i] * y[i], a.scale * (float)e * g[max(e, 0)], sum);
+                    part = fmaf(x[i] * y[i], a.scale * (float)e * g[max(e, 0)], part);
             }
+            sum += part;
         }
         if (32 * w >= a.value_dim)
             continue;
-        float16v m[ND];
+        const bool grows = log_decay > 0.0f;
+        FragV<T> zf[2];
+        columns<T, TileT>(zf, dt, w, lane);
+        bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
+        const Taken<T> for_u(zf, Factors(factors, h), odd);
+        const Taken<T> for_v(zf, Factors(factors + C, h), odd);
+        columns<T, TileT>(zf, vt, w, lane);
+        odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
+        const Taken<T> to_t(zf, Factors(factors + 2 * C, h), odd);
+        const Taken<T> to_s(zf, Factors(factors + 3 * C, h), odd);
+        const float whole = n < C ? g[n] : decays.at(k);
+        float part = 0.0f;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-            m[d] = zero16();
-        FragV<T> df[2];
-        columns<T, TileT>(df, dt, w, lane);
-        add_outer<T, TileT>(m, qt, df, lane, [&](int i) { return a.scale * g[i + 1]; });
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                sum = fmaf(m[d][i], u[d][i], sum);
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-            m[d] = zero16();
-        add_outer<T, TileT>(m, qt, df, lane, [&](int i) { return a.scale * (float)(i + 1) * g[i + 1]; });
-        const float2 whole = g.at[n];
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
+        for (int d = 0; d < ND; ++d) {
+            FragV<T> yf[2] = {state_columns<T, TileT>(qt, 0, d, lane), state_columns<T, TileT>(qt, 16, d, lane)};
+            float16v x = for_u.times(yf, zero16()), y = for_v.times(yf, zero16());
+            settle<T>();
+            float by_t = 0.0f, by_s = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                sum = fmaf(m[d][i], s[d][i], sum);
-                u[d][i] = g.times(fmaf((float)n, s[d][i], u[d][i]), whole);
-                s[d][i] = g.times(s[d][i], whole);
+                by_t = fmaf(x[i], u[d][i], by_t);
+                by_s = fmaf(y[i], s[d][i], by_s);
+                u[d][i] = fmaf((float)n, s[d][i], u[d][i]) * whole;
+                s[d][i] *= whole;
             }
-        columns<T, TileT>(df, vt, w, lane);
-        add_outer<T, TileT>(u, kt, df, lane, [&](int j) { return (float)max(n - 1 - j, 0) * g[max(n - 1 - j, 0)]; });
-        add_outer<T, TileT>(s, kt, df, lane, [&](int j) { return g[max(n - 1 - j, 0)]; });
+            part = fmaf(by_t, for_u.back, fmaf(by_s, for_v.back, part));
+            yf[0] = state_columns<T, TileT>(kt, 0, d, lane), yf[1] = state_columns<T, TileT>(kt, 16, d, lane);
+            if constexpr (kLifts<T>) {
+                x = to_t.times(yf, zero16());
+                y = to_s.times(yf, zero16());
+                settle<T>();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    u[d][i] = fmaf(x[i], to_t.back, u[d][i]);
+                    s[d][i] = fmaf(y[i], to_s.back, s[d][i]);
+                }
+            } else {
+                u[d] = to_t.times(yf, u[d]);
+                s[d] = to_s.times(yf, s[d]);
+            }
+        }
+        settle<T>();
+        sum += part;
     }
-    if (a.dstate && col < a.value_dim) {
-        const float *dstate = a.dstate + b * a.dstate_stride[0] + head * a.dstate_stride[1] + col;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int row = 32 * d + acc_row(i, h);
-                if (row < a.dim)
-                    sum = fmaf(u[d][i], dstate[row * a.dstate_stride[2]], sum);
-            }
+    if (col < a.value_dim && (a.segments > 1 || a.dstate)) {
+        const float *end = a.segments > 1 ? a.ends + place + col
+                                          : a.dstate + b * a.dstate_stride[0] + head * a.dstate_stride[1] + col;
+        const int64_t step = a.segments > 1 ? a.value_dim : a.dstate_stride[2];
+        float part = 0.0f;
+        each_row_of_state<ND>(a.dim, h, [&](int d, int i, int row) { part = fmaf(u[d][i], end[row * step], part); });
+        sum += part;
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
         sum += __shfl_xor(sum, d);
+    double *waves = reinterpret_cast<double *>(lds); // the tiles are done with
+    __syncthreads();
     if (lane == 0)
         waves[w] = sum;
     __syncthreads();
     if (t == 0) {
         for (int i = 1; i < ND; ++i)
             sum += waves[i];
-        a.sums[line] = sum;
+        a.sums[work.line * a.segments + work.segment] = sum;
     }
 }
 
@@ -733,6 +950,7 @@ __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
 template <typename T>
 struct Linear {
     static int sweep(LinearArgs a, bool vec, hipStream_t s);
+    static int states(LinearArgs a, bool vec, hipStream_t s);
     static int decay(DecayArgs a, bool vec, hipStream_t s);
 };
 

@@ -20,22 +20,38 @@ int with_linear_tile(int64_t dim, bool vec, F &&f)
     }
 }
 
+// A launch of KERNEL over `blocks` blocks of `threads`, in pieces.
+template <auto KERNEL, typename ARGS>
+int run_linear(ARGS a, int64_t blocks, int threads, int bytes, hipStream_t s)
+{
+    if (const int rc = allow_lds<KERNEL>(bytes))
+        return rc;
+    in_pieces(blocks, threads, [&](int64_t first, uint32_t n) {
+        a.first = (uint32_t)first;
+        a.blocks = n;
+        KERNEL<<<xcd_grid(n), threads, bytes, s>>>(a);
+    });
+    return launched();
+}
+
+inline int64_t blocks_of(const LinearArgs &a) { return (int64_t)a.batch * a.heads * a.segments * a.jobs; }
+inline int widest(const LinearArgs &a) { return std::max(a.job[0].dim_x, a.job[0].dim_z); }
+
 template <typename T>
 int Linear<T>::sweep(LinearArgs a, bool vec, hipStream_t s)
 {
-    const int dim = std::max(a.job[0].dim_x, a.job[0].dim_z);
-    return with_linear_tile(dim, vec, [&](auto dt, auto v) {
-        using G = Sweep<T, dt.value, v.value>;
-        constexpr auto kernel = linear_sweep<T, dt.value, v.value>;
-        if (const int rc = allow_lds<kernel>(G::kLds))
-            return rc;
-        const int64_t blocks = (int64_t)a.batch * a.heads * a.jobs;
-        in_pieces(blocks, G::kThreads, [&](int64_t first, uint32_t n) {
-            a.first = (uint32_t)first;
-            a.blocks = n;
-            kernel<<<xcd_grid(n), G::kThreads, G::kLds, s>>>(a);
-        });
-        return launched();
+    return with_linear_tile(widest(a), vec, [&](auto dt, auto v) {
+        using G = Runs<T, dt.value, v.value, 3>;
+        return run_linear<linear_sweep<T, dt.value, v.value>>(a, blocks_of(a), G::kThreads, G::kLds, s);
+    });
+}
+
+template <typename T>
+int Linear<T>::states(LinearArgs a, bool vec, hipStream_t s)
+{
+    return with_linear_tile(widest(a), vec, [&](auto dt, auto v) {
+        using G = Runs<T, dt.value, v.value, 2>;
+        return run_linear<linear_states<T, dt.value, v.value>>(a, blocks_of(a), G::kThreads, G::kLds, s);
     });
 }
 
@@ -43,16 +59,9 @@ template <typename T>
 int Linear<T>::decay(DecayArgs a, bool vec, hipStream_t s)
 {
     return with_linear_tile(std::max(a.dim, a.value_dim), vec, [&](auto dt, auto v) {
-        using G = Decay<T, dt.value, v.value>;
-        constexpr auto kernel = linear_decay<T, dt.value, v.value>;
-        if (const int rc = allow_lds<kernel>(G::kLds))
-            return rc;
-        in_pieces((int64_t)a.batch * a.heads, G::kThreads, [&](int64_t first, uint32_t n) {
-            a.first = (uint32_t)first;
-            a.blocks = n;
-            kernel<<<xcd_grid(n), G::kThreads, G::kLds, s>>>(a);
-        });
-        return launched();
+        using G = Runs<T, dt.value, v.value, 4>;
+        return run_linear<linear_decay<T, dt.value, v.value>>(a, (int64_t)a.batch * a.heads * a.segments, G::kThreads,
+                                                              G::kLds, s);
     });
 }
 
