@@ -7,7 +7,7 @@
 //
 // HBM bounds it: a row is read once and stays in registers, so everything that depends on the
 // whole row is in one launch.  A team of lanes takes a row: 2^k lanes of a wave (rows of up to 256
-// vectors of 16 bytes, up to four a lane, so a wave works on 64 / 2^k rows at once), a block of 256 (up
+// vectors of 16 bytes, up to four a lane; a wave works on 64 / 2^k rows at once), a block of 256 (up
 // to 1024 vectors), and past that a block that reads the row again from the caches (rms_far_*).
 // Teams walk rows with the weights (backward: the sums of dw) in registers.  The backward call's sums
 // leave each block once and a second launch adds the blocks up, in the blocks' order.
@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kRmsThreads = 256;
 constexpr int kFarThreads = 1024;
+constexpr int kBlocks = 1024; // of a launch: four a CU, more only begin more often
 
 struct RmsArgs {
     lic_rms_norm_args p;
@@ -31,6 +32,7 @@ struct RmsArgs {
     int units, whole;     // vectors of a row; those that begin at a multiple of their size
     int team;             // lanes of a row
     uint32_t blocks;
+    bool past;            // y (dx) passes the caches, which the arrays exceed; h does not: the next block reads it
 };
 
 __device__ __forceinline__ float weight_at(const lic_rms_norm_args &p, int c)
@@ -109,16 +111,29 @@ struct At {
     }
 };
 
-// f(row, whether it is one) for each of a team's rows; all lanes of a wave go through every turn, since
-// they exchange values.
-template <int THREADS, bool WIDE, typename F>
-__device__ __forceinline__ void each_row(const RmsArgs &a, F &&f)
+// f(values, place, row, whether it is one) for each of a team's rows, with values = ask(place) that were asked for
+// a row ahead; all lanes of a wave go through every turn, since they exchange values.
+template <int THREADS, bool WIDE, typename A, typename F>
+__device__ __forceinline__ void each_row(const RmsArgs &a, A &&ask, F &&f)
 {
     const int t = (int)threadIdx.x, at_once = WIDE ? 1 : THREADS / a.team;
     const int64_t base = (int64_t)blockIdx.x * at_once, step = (int64_t)a.blocks * at_once;
     const int mine = WIDE ? 0 : t / a.team, wave = WIDE ? 0 : (t & ~63) / a.team;
-    for (int64_t r = base; r + wave < a.rows; r += step)
-        f(least(r + mine, a.rows - 1), r + mine < a.rows);
+    const auto row = [&](int64_t r) { return least(r + mine, a.rows - 1); };
+    if (base + wave >= a.rows)
+        return;
+    At place(a, row(base));
+    auto values = ask(place);
+    for (int64_t r = base; r + wave < a.rows; r += step) {
+        const At next(a, row(r + step));
+        const bool more = r + step + wave < a.rows;
+        auto ahead = values;
+        if (more)
+            ahead = ask(next);
+        f(values, place, row(r), r + mine < a.rows);
+        values = ahead;
+        place = next;
+    }
 }
 
 // four numbers as e4m3 or whole numbers of a byte
@@ -172,24 +187,31 @@ __global__ __launch_bounds__(THREADS) void rms_forward(RmsArgs a)
 #pragma unroll
         for (int i = 0; i < V; ++i)
             w[n][i] = weight_at(p, vec.at[n] + i);
-    each_row<THREADS, WIDE>(a, [&](int64_t row, bool there) {
-        const At place(a, row);
+    struct Values {
+        VT h[N], o[N];
+    };
+    const auto ask = [&](const At &place) {
+        Values v{};
         const T *x = place(static_cast<const T *>(p.x), p.x_stride);
-        VT h[N];
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            h[n] = load_at<VT>(x + vec.at[n]);
+            v.h[n] = load_at<VT>(x + vec.at[n]);
         if (p.residual) {
             const T *residual = place(static_cast<const T *>(p.residual), p.residual_stride);
-            VT o[N];
 #pragma unroll
             for (int n = 0; n < N; ++n)
-                o[n] = load_at<VT>(residual + vec.at[n]);
+                v.o[n] = load_at<VT>(residual + vec.at[n]);
+        }
+        return v;
+    };
+    each_row<THREADS, WIDE>(a, ask, [&](Values &v, const At &place, int64_t row, bool there) {
+        VT(&h)[N] = v.h;
+        if (p.residual) {
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    h[n].v[i] = down<T>(up(h[n].v[i]) + up(o[n].v[i]));
+                    h[n].v[i] = down<T>(up(h[n].v[i]) + up(v.o[n].v[i]));
         }
         float s = 0.0f;
 #pragma unroll
@@ -251,7 +273,7 @@ __global__ __launch_bounds__(THREADS) void rms_forward(RmsArgs a)
                 for (int i = 0; i < V; ++i)
                     o.v[i] = down_apart<T>(up(h[n].v[i]) * rstd * w[n][i]);
                 if (there && vec.there(n))
-                    store_at(out + vec.at[n], o);
+                    store_at(out + vec.at[n], o, a.past);
             }
         }
     });
@@ -275,22 +297,28 @@ __global__ __launch_bounds__(THREADS) void rms_backward(RmsArgs a)
             w[n][i] = weight_at(p, vec.at[n] + i);
             dw[n][i] = 0.0f;
         }
-    each_row<THREADS, WIDE>(a, [&](int64_t row, bool there) {
-        const At place(a, row);
+    struct Values {
+        VT h[N], g[N], s[N];
+    };
+    const auto ask = [&](const At &place) {
+        Values v{};
         const T *h = place(static_cast<const T *>(p.x), p.x_stride);
         const T *dy = place(static_cast<const T *>(p.dy), p.dy_stride);
-        VT hv[N], gv[N], sv[N];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            hv[n] = load_at<VT>(h + vec.at[n]);
-            gv[n] = load_at<VT>(dy + vec.at[n]);
+            v.h[n] = load_at<VT>(h + vec.at[n]);
+            v.g[n] = load_at<VT>(dy + vec.at[n]);
         }
         if (p.dsum) {
             const T *dsum = place(static_cast<const T *>(p.dsum), p.dsum_stride);
 #pragma unroll
             for (int n = 0; n < N; ++n)
-                sv[n] = load_at<VT>(dsum + vec.at[n]);
+                v.s[n] = load_at<VT>(dsum + vec.at[n]);
         }
+        return v;
+    };
+    each_row<THREADS, WIDE>(a, ask, [&](const Values &v, const At &place, int64_t row, bool there) {
+        const VT(&hv)[N] = v.h, (&gv)[N] = v.g, (&sv)[N] = v.s;
         const float rstd = p.rstd[row];
         float s = 0.0f;
 #pragma unroll
@@ -315,7 +343,7 @@ __global__ __launch_bounds__(THREADS) void rms_backward(RmsArgs a)
                 o.v[i] = down_apart<T>(p.dsum ? d + up(sv[n].v[i]) : d);
             }
             if (there && vec.there(n))
-                store_at(dx + vec.at[n], o);
+                store_at(dx + vec.at[n], o, a.past);
         }
     });
     if (!a.part)
@@ -549,7 +577,7 @@ __global__ __launch_bounds__(1024) void rms_join(RmsArgs a)
 int64_t sum_blocks(int64_t channels)
 {
     const int64_t most = (16ll << 20) / (4 * channels);
-    return most < 64 ? 64 : most > 1024 ? 1024 : most;
+    return most < 64 ? 64 : most > kBlocks ? kBlocks : most;
 }
 
 bool valid(const lic_rms_norm_args *p, bool backward)
@@ -579,6 +607,8 @@ RmsArgs arguments(const lic_rms_norm_args &p, bool backward)
     a.p = p;
     a.rows = p.samples * p.positions;
     a.inverse = 1.0f / (float)p.channels;
+    const int arrays = 2 + (backward ? 1 + (p.dsum != nullptr) : 2 * (p.residual != nullptr));
+    a.past = (double)a.rows * (double)p.channels * dtype_bytes(p.dtype) * arrays > (double)kCacheBytes;
     const auto even = [&](const int64_t *s) { return s[0] == s[1] * p.positions; };
     const bool one = even(p.x_stride) &&
                      (backward ? even(p.dy_stride) && even(p.dx_stride) && (!p.dsum || even(p.dsum_stride))
@@ -591,8 +621,9 @@ RmsArgs arguments(const lic_rms_norm_args &p, bool backward)
 }
 
 // f(values of a vector, vectors a lane, whether a block takes a row, whether a vector overlaps): the narrowest
-// team that holds a row with up to four vectors a lane, so a wave has several rows under way where they are
-// short.  far() where no block holds it.
+// team up to a wave that holds a row with a vector a lane, then up to four vectors a lane (fewer lanes with more
+// vectors each wait longer: 16320 rows of 1024 values to e4m3 39 us with four a lane, 29 with two).  far() where no
+// block holds it.
 template <typename T, typename F, typename G>
 int with_team(RmsArgs &a, F &&f, G &&far)
 {
@@ -619,7 +650,7 @@ int with_team(RmsArgs &a, F &&f, G &&far)
         return a.units <= 512 ? go(integral_constant<int, 2>{}, yes) : go(integral_constant<int, 4>{}, yes);
     }
     a.team = 1;
-    while (4 * a.team < a.units)
+    while (a.team < a.units && a.team < 64)
         a.team *= 2;
     switch ((a.units + a.team - 1) / a.team) {
     case 1: return go(integral_constant<int, 1>{}, no);
@@ -662,7 +693,7 @@ extern "C" int lic_rms_norm_forward(const lic_rms_norm_args *args, hipStream_t h
             [&](auto vec, auto n, auto wide, auto tail) {
                 constexpr int V = decltype(vec)::value, N = decltype(n)::value;
                 constexpr bool WIDE = decltype(wide)::value, TAIL = decltype(tail)::value;
-                a.blocks = blocks_of(a, WIDE ? 1 : kRmsThreads / a.team, 2048);
+                a.blocks = blocks_of(a, WIDE ? 1 : kRmsThreads / a.team, kBlocks);
                 if (a.p.format == LIC_FORMAT_NONE)
                     rms_forward<T, V, N, kRmsThreads, WIDE, TAIL, false><<<a.blocks, kRmsThreads, 0, hstream>>>(a);
                 else
@@ -691,7 +722,7 @@ extern "C" int lic_rms_norm_backward(const lic_rms_norm_args *args, void *worksp
             return RANS_E_WORKSPACE;
         a.part = static_cast<float *>(workspace);
     }
-    const int64_t most = a.part ? sum_blocks(a.p.channels) : 2048;
+    const int64_t most = a.part ? sum_blocks(a.p.channels) : kBlocks;
     const int rc = with_dtype(a.p.dtype, [&](auto t) {
         using T = decltype(t);
         return with_team<T>(

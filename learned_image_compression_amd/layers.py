@@ -19,6 +19,7 @@ the current stream, nothing is synchronised, and there is no CPU path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -133,9 +134,10 @@ def _device_of(t: torch.Tensor, name: str):
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t.device
+    device = t.device
+    if device.index != torch._C._cuda_getDevice():  # a tensor there has initialised the GPU
+        raise ValueError(f"{name} is on {device}, which is not the current device")
+    return device
 
 
 def _stream(device) -> int:
@@ -162,9 +164,15 @@ def _like(t, dtype, device, name):
 
 def _out_like(out, t, dtype, device, name):
     """Checks of an output that the caller gives; two of its entries must not be one."""
+    _out_of(out, t.shape, dtype, device, name)
+
+
+def _out_of(out, shape, dtype, device, name):
     _like(out, dtype, device, name)
-    if out.shape != t.shape:
+    if out.shape != shape:
         raise ValueError(f"{name} differs in shape")
+    if out.is_contiguous():
+        return
     if any(stride == 0 and size > 1 for stride, size in zip(out.stride(), out.shape)):
         raise ValueError(f"{name} overlaps itself")
 
@@ -467,28 +475,34 @@ def _same(t, x, device, name):
 
 def _rms_forward(x, weight, residual, eps, code, y, stat, rstd, sum_out, device, kind):
     """The call beneath the forward functions; returns h.  ``stat`` holds the scales of 8 bits."""
-    xs = _token_rows(x, "x")
     h, rs, hs = x, _NO_ROWS, _NO_ROWS
     if residual is not None:
         _same(residual, x, device, "residual")
-        rs = _token_rows(residual, "residual")
         if sum_out is None:
             h = _dense_like(x)
         else:
             _out_like(sum_out, x, x.dtype, device, "sum_out")
             h = sum_out
-        hs = _token_rows(h, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out is for calls with a residual")
-    samples, positions = _sample_rows(x.shape)
+    c = x.shape[-1]
+    if x.is_contiguous() and y.is_contiguous() and \
+            (residual is None or (residual.is_contiguous() and h.is_contiguous())):
+        samples, positions = 1, x.numel() // c  # the usual layout: all rows one after another
+        xs = rs = ys = hs = (0, c)
+    else:
+        samples, positions = _sample_rows(x.shape)
+        xs, ys = _token_rows(x, "x"), _token_rows(y, "out")
+        if residual is not None:
+            rs, hs = _token_rows(residual, "residual"), _token_rows(h, "sum_out")
     if samples and positions:
         args = _RMS_NORM.pack(x.data_ptr(), residual.data_ptr() if residual is not None else 0,
                               weight.data_ptr() if weight is not None else 0, y.data_ptr(),
                               h.data_ptr() if residual is not None else 0,
                               rstd.data_ptr() if rstd is not None else 0,
-                              stat.data_ptr() if stat is not None else 0, 0, 0, 0, 0, *xs, *rs,
-                              *_token_rows(y, "out"), *hs, *_NO_ROWS, *_NO_ROWS, *_NO_ROWS, samples,
-                              positions, x.shape[-1], DTYPES[x.dtype], DTYPES[kind], code, eps)
+                              stat.data_ptr() if stat is not None else 0, 0, 0, 0, 0, *xs, *rs, *ys,
+                              *hs, 0, 0, 0, 0, 0, 0, samples, positions, c, DTYPES[x.dtype],
+                              DTYPES[kind], code, eps)
         rc = load().lic_rms_norm_forward(args, _stream(device))
         if rc:
             _check_rc(rc, "lic_rms_norm_forward")
@@ -968,8 +982,8 @@ def _linear_common(q, k, v, log_decay, state, lengths, scale):
     _like(v, q.dtype, device, "v")
     strides = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
     b, s, h, d = q.shape
-    kv, e = v.shape[2], v.shape[3]
-    if k.shape != (b, s, kv, d) or v.shape[:2] != (b, s):
+    vb, vs, kv, e = v.shape
+    if k.shape != (b, s, kv, d) or vb != b or vs != s:
         raise ValueError("q, k and v differ in batch, rows or dim, or k and v in heads")
     if kv < 1 or h % kv or h < 1:
         raise ValueError("heads must be a multiple of kv heads")
@@ -988,7 +1002,7 @@ def _linear_common(q, k, v, log_decay, state, lengths, scale):
         scale = d ** -0.5
     elif not (scale > 0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
-    shape = torch.Size((b, h, d, e))
+    shape = (b, h, d, e)
     return device, strides, _state(state, shape, device, "state"), length_ptr, shape, \
         (b, s, h, kv, d, e, DTYPES[q.dtype], scale)
 
@@ -1009,14 +1023,15 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """
     device, strides, (state_ptr, ss), length_ptr, shape, sizes = \
         _linear_common(q, k, v, log_decay, state, lengths, scale)
+    out_shape = (*q.shape[:3], shape[3])
     if out is None:
-        out = torch.empty((*q.shape[:3], shape[3]), dtype=q.dtype, device=device)
+        out = torch.empty(out_shape, dtype=q.dtype, device=device)
     else:
-        _out_like(out, torch.empty((*q.shape[:3], shape[3]), device="meta"), q.dtype, device, "out")
+        _out_of(out, out_shape, q.dtype, device, "out")
     if state_out is None:
         state_out = torch.empty(shape, dtype=torch.float32, device=device)
     else:
-        _out_like(state_out, torch.empty(shape, device="meta"), torch.float32, device, "state_out")
+        _out_of(state_out, shape, torch.float32, device, "state_out")
     last_ptr, ls = _state(state_out, shape, device, "state_out")
     args = _LINEAR.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state_ptr, length_ptr,
                         out.data_ptr(), last_ptr, 0, 0, 0, 0, 0, 0, 0, *strides[0], *strides[1], *strides[2],
@@ -1024,6 +1039,11 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                         *_NO_STRIDES, *_NO_STRIDES, *sizes)
     lib = load()
     stream = _stream(device)
+    if q.shape[1] == 1:  # a single token takes no scratch memory
+        rc = lib.lic_linear_attention_forward(args, None, 0, stream)
+        if rc:
+            _check_rc(rc, "lic_linear_attention_forward")
+        return out, state_out
     _with_workspace(device, stream, lambda p, size: lib.lic_linear_attention_forward(args, p, size, stream),
                     lambda: lib.lic_linear_attention_workspace_bytes(args, 0),
                     "lic_linear_attention_forward")
@@ -1129,21 +1149,25 @@ def _gradients(tensors, out):
         out = [out] if isinstance(out, torch.Tensor) else [o for o in out if o is not None]
         if len(out) != len(tensors):
             raise ValueError("out has to have a place for each tensor")
-    flat, device = [], None
     if _wants_gradient(*tensors):
         raise NotImplementedError("clipping has no gradients")
-    for i, t in enumerate(tensors):
-        device = _device_of(t, f"tensor {i}")
-        if not _dense(t):
+    flat, device = [], None
+    places = tensors if out is None else out
+    for i, (t, to) in enumerate(zip(tensors, places)):
+        if device is None or not isinstance(t, torch.Tensor) or t.dtype not in DTYPES or \
+                t.get_device() != device.index:
+            device = _device_of(t, f"tensor {i}")
+        whole = t.is_contiguous()
+        if not (whole or _dense(t)):
             raise ValueError(f"tensor {i} has gaps between its values")
-        to = t
-        if out is not None:
-            to = out[i]
+        if to is not t and not (whole and isinstance(to, torch.Tensor) and to.dtype is t.dtype and
+                                to.shape == t.shape and to.get_device() == device.index and
+                                to.is_contiguous()):
             _out_like(to, t, t.dtype, device, f"out {i}")
             if to.stride() != t.stride():
                 raise ValueError(f"out {i} differs in layout")
         flat += (t.data_ptr(), to.data_ptr(), t.numel(), DTYPES[t.dtype])
-    return struct.pack("=" + "QQqq" * len(tensors), *flat), len(tensors), device
+    return array.array("q", flat).tobytes(), len(tensors), device
 
 
 def _clip(tensors, max_norm, out, where):
