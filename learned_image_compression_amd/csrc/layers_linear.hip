@@ -103,29 +103,45 @@ int run_step(StepArgs a, hipStream_t s)
 
 // ---- sums over heads that share ---------------------------------------------------
 
+// dk and dv in one launch: their parts [batch][kv head][share][token][dim], four values a thread where they divide.
 struct JoinArgs {
-    const float *part; // [batch][kv head][share][token][dim]
-    void *out;
-    int64_t out_stride[3];
-    int64_t tokens, total, first;
-    int32_t heads, share, dim;
+    const float *part[2];
+    void *out[2];
+    int64_t out_stride[2][3];
+    int64_t total[2]; // threads of each
+    int32_t dim[2];
+    int64_t tokens, first;
+    int32_t heads, share;
 };
 
-template <typename T>
+template <typename T, int V>
 __global__ __launch_bounds__(256) void linear_join(JoinArgs a)
 {
-    const int64_t id = (a.first + blockIdx.x) * 256 + threadIdx.x;
-    if (id >= a.total)
+    using VT = Vec<float, V>;
+    int64_t id = (a.first + blockIdx.x) * 256 + threadIdx.x;
+    const int which = id >= a.total[0];
+    if (which)
+        id -= a.total[0];
+    if (id >= a.total[which])
         return;
-    const int64_t row = id / a.dim, line = row / a.tokens; // (batch, kv head)
-    const int d = (int)(id - row * a.dim);
-    const int64_t token = row - line * a.tokens, step = a.tokens * a.dim;
-    const float *part = a.part + line * a.share * step + token * a.dim + d;
-    float s = part[0];
-    for (int i = 1; i < a.share; ++i)
-        s += part[i * step];
+    const int dim = a.dim[which], units = dim / V;
+    const int64_t row = id / units, line = row / a.tokens; // (batch, kv head)
+    const int d = (int)(id - row * units) * V;
+    const int64_t token = row - line * a.tokens, step = a.tokens * dim;
+    const float *part = a.part[which] + line * a.share * step + token * dim + d;
+    VT s = load_at<VT>(part);
+    for (int i = 1; i < a.share; ++i) {
+        const VT o = load_at<VT>(part + i * step);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            s.v[e] += o.v[e];
+    }
     const int64_t b = line / a.heads;
-    head_row<T>(a.out, a.out_stride, (int)b, token, (int)(line - b * a.heads))[d] = down<T>(s);
+    Vec<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        o.v[e] = down<T>(s.v[e]);
+    store_at(head_row<T>(a.out[which], a.out_stride[which], (int)b, token, (int)(line - b * a.heads)) + d, o);
 }
 
 // dlog_decay[head]: one wave a head, over the batch's parts (its segments).
@@ -157,6 +173,7 @@ struct ScanArgs {
     const int32_t *lengths;
     int64_t tokens, first;
     int32_t heads, jobs, segments, each, start_floats, tiles; // of 64 numbers
+    int32_t blocks;                                           // of 32 columns
     int32_t group;                                            // segments of a group
 };
 
@@ -171,28 +188,28 @@ __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
     const LinearJob &p = a.job[which];
     const int b = (int)(line / a.heads), head = (int)(line - (int64_t)b * a.heads);
     const int t = (int)threadIdx.x, x = t & 15, group = t >> 4;
-    const int at = (tile * 16 + x) * 4; // its numbers of a state
-    const bool there = at < a.start_floats;
+    const int at = (tile * 16 + x) * 4; // its numbers of a state: four rows of a column of StateImage
+    const int place = at / 4 / 64, lane = at / 4 & 63, fours = place / a.blocks;
+    const int row0 = 32 * (fours >> 2) + state_row(8 * (fours & 3) + 4 * (lane >> 5));
+    const int column = 32 * (place % a.blocks) + (lane & 31);
     float *starts = p.starts + line * a.segments * a.start_floats + at;
     // in the order of time: segment 0 first, or the last one
     const auto index = [&](int k) { return p.reverse ? a.segments - 1 - k : k; };
-    const int k0 = group * a.group;
+    const int k0 = group * a.group, adding = a.segments - (p.last ? 0 : 1);
     VT add[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         add[i] = VT{};
-        // what the last one adds goes nowhere
-        if (there && i < a.group && k0 + i < a.segments - 1)
+        if (i < a.group && k0 + i < adding)
             add[i] = load_at<VT>(starts + (int64_t)index(k0 + i) * a.start_floats);
     }
     VT run{};
-    if (group == 0 && there && p.first) {
-        const float *first = p.first + b * p.first_stride[0] + head * p.first_stride[1];
-        const int columns = p.dim_z;
+    if (group == 0 && p.first && column < p.dim_z) {
+        const float *first = p.first + b * p.first_stride[0] + head * p.first_stride[1] + column * p.first_stride[3];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (at + i < p.dim_x * columns)
-                run.v[i] = first[(at + i) / columns * p.first_stride[2] + (at + i) % columns * p.first_stride[3]];
+            if (row0 + i < p.dim_x)
+                run.v[i] = first[(row0 + i) * p.first_stride[2]];
     }
     const double log_decay = a.log_decay[head];
     const int all = a.lengths ? min(max(a.lengths[b], 0), (int)a.tokens) : (int)a.tokens;
@@ -224,8 +241,6 @@ __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
             for (int e = 0; e < 4; ++e)
                 run.v[e] = fmaf(run.v[e], powers[k], ends[k][x].v[e]);
     }
-    if (!there)
-        return;
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
         if (i < a.group && k0 + i < a.segments) {
@@ -235,6 +250,13 @@ __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
             for (int e = 0; e < 4; ++e)
                 run.v[e] = fmaf(run.v[e], g, add[i].v[e]);
         }
+    if (p.last && k0 < a.segments && k0 + a.group >= a.segments && column < p.dim_z) { // behind the last one
+        float *last = p.last + b * p.last_stride[0] + head * p.last_stride[1] + column * p.last_stride[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row0 + i < p.dim_x)
+                last[(row0 + i) * p.last_stride[2]] = run.v[i];
+    }
 }
 
 int run_scan(const LinearArgs &l, hipStream_t s)
@@ -244,7 +266,8 @@ int run_scan(const LinearArgs &l, hipStream_t s)
         a.job[i] = l.job[i];
     a.log_decay = l.log_decay, a.lengths = l.lengths, a.tokens = l.tokens;
     a.heads = l.heads, a.jobs = l.jobs, a.segments = l.segments, a.each = l.each, a.start_floats = l.start_floats;
-    a.tiles = (l.start_floats + 63) / 64;
+    a.tiles = l.start_floats / 64;
+    a.blocks = (std::max(l.job[0].dim_x, l.job[0].dim_z) + 31) / 32;
     a.group = (l.segments + kScanGroups - 1) / kScanGroups;
     in_pieces((int64_t)l.batch * l.heads * l.jobs * a.tiles, 256, [&](int64_t first, uint32_t blocks) {
         a.first = first;
@@ -287,21 +310,29 @@ bool valid_call(const lic_linear_attention_args &p, bool backward)
 
 uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-// How the tokens are split: into as many segments as make four blocks a CU (heads wider than 64: one, since their
-// states' way through memory is as long as their tokens'), each of at least 32 tokens.
+// How the tokens are split: into as many segments as make four blocks a CU, each of at least 64 tokens.  A state's way
+// through scratch memory (written, scanned, read) is as long as that of 4 * dim tokens' rows, so heads wider than
+// 64 take one block a CU.  Measured (us, all kernels, with 256 / 512 / 1024 / 1536 blocks): forward, bfloat16, 2 x
+// 16 heads of 64, 8160 tokens 97 / 68 / 53 / 65; 6 heads of 32, 32640 tokens 64 / 44 / 39 / 41; trained, 16 heads of
+// 128, 8160 tokens 343 / 357 / 480 / 620; float, 4 x 6 heads of 32, 510 tokens in segments of 510 / 128 / 64 / 32: 200 /
+// 120 / 64 / 68.
 struct Split {
     int32_t segments, each;
     explicit Split(const lic_linear_attention_args &p)
     {
         const int64_t want = std::max(p.dim, p.value_dim) <= 64 ? 1024 : 256;
-        int64_t n = std::min<int64_t>(want / std::max<int64_t>(p.batch * p.heads, 1), p.tokens / kRun);
+        int64_t n = want / std::max<int64_t>(p.batch * p.heads, 1);
         n = std::max<int64_t>(1, std::min<int64_t>(n, kMostSegments));
-        each = (int32_t)std::max<int64_t>(kRun, ((p.tokens + n - 1) / n + kRun - 1) / kRun * kRun);
+        each = (int32_t)std::max<int64_t>(2 * kRun, ((p.tokens + n - 1) / n + kRun - 1) / kRun * kRun);
         segments = (int32_t)std::max<int64_t>(1, (p.tokens + each - 1) / each);
     }
 };
 
-int32_t start_floats(const lic_linear_attention_args &p) { return (int32_t)(p.dim * p.value_dim + 3) / 4 * 4; }
+int32_t start_floats(const lic_linear_attention_args &p)
+{
+    const int32_t wide = (int32_t)(std::max(p.dim, p.value_dim) + 31) / 32 * 32;
+    return wide * wide;
+}
 
 // Scratch memory of a call: the states before segments (and their gradients behind them), parts of dk and
 // dv, sums of dlog_decay.
@@ -388,29 +419,34 @@ int forward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
     j.dim_x = (int32_t)p.dim, j.dim_z = (int32_t)p.value_dim;
     j.read = a.scale, j.write = 1.0f;
     j.starts = static_cast<float *>(ws);
-    j.start_stride[0] = j.dim_z, j.start_stride[1] = 1;
     if (a.segments > 1) {
         if (const int rc = make_states<T>(a, 1, vec, s))
             return rc;
+        j.last = nullptr;
     }
     return Linear<T>::sweep(a, vec, s);
 }
 
 template <typename T>
-int join(const lic_linear_attention_args &p, const float *part, void *out, const int64_t *stride, int64_t dim, hipStream_t s)
+int join(const lic_linear_attention_args &p, const float *dk, const float *dv, hipStream_t s)
 {
     JoinArgs a{};
-    a.part = part;
-    a.out = out;
-    set3(a.out_stride, stride);
+    a.part[0] = dk, a.part[1] = dv;
+    a.out[0] = p.dk, a.out[1] = p.dv;
+    set3(a.out_stride[0], p.dk_stride), set3(a.out_stride[1], p.dv_stride);
+    a.dim[0] = (int32_t)p.dim, a.dim[1] = (int32_t)p.value_dim;
     a.tokens = p.tokens;
     a.heads = (int32_t)p.kv_heads;
     a.share = (int32_t)(p.heads / p.kv_heads);
-    a.dim = (int32_t)dim;
-    a.total = p.batch * p.kv_heads * p.tokens * dim;
-    in_pieces((a.total + 255) / 256, 256, [&](int64_t first, uint32_t blocks) {
+    const int vec = p.dim % 4 == 0 && p.value_dim % 4 == 0 ? 4 : 1;
+    for (int i = 0; i < 2; ++i)
+        a.total[i] = p.batch * p.kv_heads * p.tokens * (a.dim[i] / vec);
+    in_pieces((a.total[0] + a.total[1] + 255) / 256, 256, [&](int64_t first, uint32_t blocks) {
         a.first = first;
-        linear_join<T><<<blocks, 256, 0, s>>>(a);
+        if (vec == 4)
+            linear_join<T, 4><<<blocks, 256, 0, s>>>(a);
+        else
+            linear_join<T, 1><<<blocks, 256, 0, s>>>(a);
     });
     return launched();
 }
@@ -445,17 +481,16 @@ int backward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
     LinearJob &dq = job(0, p.dout, p.dout_stride, 1, p.v, p.v_stride, share, p.k, p.k_stride, share, p.dq, p.dq_stride,
                         p.value_dim, p.dim);
     set_state(dq.first_stride, p.state_stride, true);
-    dq.start_stride[0] = 1, dq.start_stride[1] = (int32_t)p.value_dim;
+    dq.turned = 1;
     LinearJob &dv = job(1, p.k, p.k_stride, share, p.q, p.q_stride, 1, p.dout, p.dout_stride, 1, p.dv, p.dv_stride, p.dim,
                         p.value_dim);
     set_state(dv.first_stride, p.dstate_stride, false);
-    dv.start_stride[0] = (int32_t)p.value_dim, dv.start_stride[1] = 1;
     dv.last = p.dstate_in;
     set_state(dv.last_stride, p.dstate_in_stride, false);
     LinearJob &dk = job(2, p.v, p.v_stride, share, p.dout, p.dout_stride, 1, p.q, p.q_stride, 1, p.dk, p.dk_stride,
                         p.value_dim, p.dim);
     set_state(dk.first_stride, p.dstate_stride, true);
-    dk.start_stride[0] = 1, dk.start_stride[1] = (int32_t)p.value_dim;
+    dk.turned = 1;
     if (a.segments > 1) {
         LinearArgs st = a; // the states themselves, as the forward call's, and their gradients, as dv's
         LinearJob &j = st.job[0];
@@ -463,9 +498,9 @@ int backward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
         set3(j.y_stride, p.k_stride), set3(j.z_stride, p.v_stride);
         set_state(j.first_stride, p.state_stride, false);
         j.dim_x = (int32_t)p.dim, j.dim_z = (int32_t)p.value_dim;
-        j.start_stride[0] = j.dim_z, j.start_stride[1] = 1;
         if (const int rc = make_states<T>(st, 2, vec, s))
             return rc;
+        dv.last = nullptr;
     }
     if (share > 1) {
         dk.part = reinterpret_cast<float *>(base + at.dk);
@@ -474,9 +509,7 @@ int backward(const lic_linear_attention_args &p, void *ws, hipStream_t s)
     if (const int rc = Linear<T>::sweep(a, vec, s))
         return rc;
     if (share > 1 && p.tokens > 0) {
-        if (const int rc = join<T>(p, dk.part, p.dk, p.dk_stride, p.dim, s))
-            return rc;
-        if (const int rc = join<T>(p, dv.part, p.dv, p.dv_stride, p.value_dim, s))
+        if (const int rc = join<T>(p, dk.part, dv.part, s))
             return rc;
     }
     if (!p.dlog_decay)

@@ -31,13 +31,14 @@ struct LinearJob {
     float *part;        // out, or (where heads share it) each head's part: [batch][head][token][dim_z]
     const float *first; // the state before the tokens (null: 0), element [x's value][z's value]
     float *last;        // and behind them (may be null)
-    float *starts;      // where the tokens are split: the state before each segment, [batch][head][segment]
+    float *starts;      // where the tokens are split: the state before each segment, [batch][head][segment],
+                        // as a wave's accumulators hold it (StateImage)
     int64_t x_stride[3], y_stride[3], z_stride[3], out_stride[3]; // batch, row, head
     int64_t first_stride[4], last_stride[4];                      // batch, head, x's value, z's value
-    int32_t start_stride[2];                                      // x's value, z's value
     int32_t x_share, y_share, z_share; // heads that share one of x's (y's, z's)
     int32_t dim_x, dim_z;
     int32_t reverse;   // 0, 1: backward in time
+    int32_t turned;    // 0, 1: `starts` holds the state transposed
     float read, write; // what of s goes to where the state is read, and to where it is written
 };
 
@@ -58,31 +59,42 @@ struct LinearArgs {
 // A segment of a batch's tokens: [from, to), of which `len` are in use.
 struct Segment {
     int from, to, len;
-    bool last; // the one behind whose tokens the state is the call's
     __device__ __forceinline__ Segment(const int32_t *lengths, int b, int tokens, int each, int index)
     {
         const int all = lengths ? min(max(lengths[b], 0), tokens) : tokens;
         from = index * each;
         to = min(tokens, from + each);
         len = min(max(all - from, 0), each);
-        last = index == max(all - 1, 0) / each;
     }
 };
 
-// Splits a 32-bit fragment into two operands of T whose sum is it to 2^-17 (bfloat16) or 2^-22.  (float
-// is its own operand.)  odd: some are not finite; those stay in the first alone.
+// Operands of T whose sum is a 32-bit fragment: three of bfloat16 (off by 2^-27 of it; two are by 2^-18, five
+// times what 32-bit sums lose), two of float16 (2^-22).  float is its own operand.
 template <typename T>
-__device__ __forceinline__ void split(const float (&v)[8], FragV<T> &hi, FragV<T> &lo, bool odd)
+constexpr int kParts = std::is_same<T, float>::value ? 1 : std::is_same<T, f16>::value ? 2 : 3;
+// For a state that only outputs of T see.
+template <typename T>
+constexpr int kFewParts = std::is_same<T, float>::value ? 1 : 2;
+
+// odd: some are not finite; those stay in the first part alone.
+template <typename T, int PARTS>
+__device__ __forceinline__ void split(const float (&v)[8], FragV<T> (&part)[PARTS], bool odd)
 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        hi[i] = down_apart<T>(v[i]);
-        lo[i] = (T)(v[i] - (float)hi[i]);
+        float rest = v[i];
+#pragma unroll
+        for (int n = 0; n < PARTS; ++n) {
+            part[n][i] = n + 1 < PARTS || PARTS == 1 ? down_apart<T>(rest) : (T)rest;
+            rest -= (float)part[n][i];
+        }
     }
     if (odd) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            lo[i] = not_finite((float)hi[i]) ? (T)0.0f : lo[i];
+        for (int n = 1; n < PARTS; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                part[n][i] = not_finite((float)part[0][i]) ? (T)0.0f : part[n][i];
     }
 }
 
@@ -282,11 +294,12 @@ __device__ __forceinline__ float *part_row(const LinearArgs &a, const LinearJob 
 
 constexpr int kRun = 32; // tokens of a run
 
-// What the kernels hold of their tiles: TILES of kRun rows for each of two runs, and g's powers.
-template <typename T, int DT, bool VEC, int TILES>
+// What the kernels hold of their tiles: TILES of kRun rows for each of two runs, and g's powers.  WAVES for each
+// 32 columns.
+template <typename T, int DT, bool VEC, int TILES, int WAVES = 1>
 struct Runs {
-    static constexpr int kBlocks = DT / 32; // of 32 columns, and waves
-    static constexpr int kThreads = 64 * kBlocks;
+    static constexpr int kBlocks = DT / 32; // of 32 columns
+    static constexpr int kThreads = 64 * kBlocks * WAVES;
     static constexpr int kTileBytes = kRun * DT * sizeof(T);
     static constexpr int kPowers = 2 * TILES * kTileBytes;
     static constexpr int kFactors = kPowers + (kRun + 4) * 4; // of a token where the state takes it in
@@ -347,10 +360,10 @@ __device__ __forceinline__ void columns(FragV<T> (&zf)[2], const uint8_t *zt, in
         zf[j] = TileT::col_frag(zt, 16 * j, block, lane);
 }
 
-// z f of a run's tokens as two operands each, in half precision times a power of two for each column.
-template <typename T>
+// z f of a run's tokens as operands that are their parts, in half precision times a power of two for each column.
+template <typename T, int PARTS>
 struct Taken {
-    FragV<T> hi[2], lo[2];
+    FragV<T> part[2][PARTS];
     float back;
 
     // odd: some of z f are not finite
@@ -376,25 +389,24 @@ struct Taken {
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            split<T>(zw[j], hi[j], lo[j], odd);
+            split<T, PARTS>(zw[j], part[j], odd);
     }
     // m + sum over the tokens of y (z f)' / back, y's columns as fragments
     __device__ __forceinline__ float16v times(const FragV<T> (&yf)[2], float16v m) const
     {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            m = mma(yf[j], hi[j], m);
-            if constexpr (sizeof(T) == 2)
-                m = mma(yf[j], lo[j], m);
-        }
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int n = 0; n < PARTS; ++n)
+                m = mma(yf[j], part[j][n], m);
         return m;
     }
 };
 
 // m += sum over a run's tokens of y (z f)'.  The sums are exact but for the split of z f; the accumulators are
 // settled.
-template <typename T, typename TileT, int ND>
-__device__ __forceinline__ void add_outer(float16v (&m)[ND], const uint8_t *yt, const Taken<T> &z, int lane)
+template <typename T, typename TileT, int ND, int PARTS>
+__device__ __forceinline__ void add_outer(float16v (&m)[ND], const uint8_t *yt, const Taken<T, PARTS> &z, int lane)
 {
     float16v sum[ND];
 #pragma unroll
@@ -439,6 +451,57 @@ __device__ __forceinline__ void each_row_of_state(int rows, int h, F &&f)
         }
 }
 
+// Where a segment's state lies in scratch memory: as the accumulators of the waves hold it, so a lane reads and
+// writes 16 bytes at a time, a wave 1 KiB.  For a DT x DT state, four rows a vector:
+//   vector ((d * 4 + i / 4) * ND + w) * 64 + lane
+template <int ND>
+struct StateImage {
+    static constexpr int kFloats = 1024 * ND * ND;
+    using V4 = Vec<float, 4>;
+
+    static __device__ __forceinline__ int at(int d, int fours, int w, int lane) { return ((d * 4 + fours) * ND + w) * 64 + lane; }
+    template <typename F>
+    static __device__ __forceinline__ void each(int w, int lane, F &&f)
+    {
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f(d, i, at(d, i, w, lane));
+    }
+    static __device__ __forceinline__ void load(float16v (&m)[ND], const float *image, int w, int lane)
+    {
+        each(w, lane, [&](int d, int i, int at) {
+            const V4 v = load_at<V4>(image + 4 * at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m[d][4 * i + e] = v.v[e];
+        });
+    }
+    static __device__ __forceinline__ void store(const float16v (&m)[ND], float *image, int w, int lane)
+    {
+        each(w, lane, [&](int d, int i, int at) {
+            V4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v.v[e] = m[d][4 * i + e];
+            store_at(image + 4 * at, v);
+        });
+    }
+    // The transposed state: its column 32 w + c is row c of the image's rows' block w, and its rows are
+    // columns there.
+    static __device__ __forceinline__ void load_turned(float16v (&m)[ND], const float *image, int w, int lane)
+    {
+        const int c = lane & 31, h = lane >> 5, acc = state_row(c); // its own inverse
+        const float *mine = image + 4 * (acc & 4 ? 32 : 0) + (acc & 3);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                m[d][i] = mine[4 * at(w, acc >> 3, d, state_row(acc_row(i, h)))];
+    }
+};
+
 // Which job, batch, head and segment a block has; neighbours share a head's tokens.
 struct Work {
     int job, b, head, segment;
@@ -461,7 +524,8 @@ __device__ __forceinline__ float *start_of(const LinearArgs &a, const LinearJob 
 
 // ---- outputs -------------------------------------------------------------------
 
-template <typename T, int DT, bool VEC>
+// PARTS of what a state takes in: all of them where the state leaves the call, with the precision of 32-bit sums.
+template <typename T, int DT, bool VEC, int PARTS>
 __global__ __launch_bounds__(2 * DT, 2) void linear_sweep(LinearArgs a)
 {
     using G = Runs<T, DT, VEC, 3>;
@@ -504,9 +568,12 @@ __global__ __launch_bounds__(2 * DT, 2) void linear_sweep(LinearArgs a)
 #pragma unroll
     for (int d = 0; d < ND; ++d)
         m[d] = zero16();
-    if (col < p.dim_z && a.segments > 1) {
-        const float *start = start_of(a, p, work.line, work.segment) + col * p.start_stride[1];
-        each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { m[d][i] = start[row * p.start_stride[0]]; });
+    if (a.segments > 1) {
+        const float *start = start_of(a, p, work.line, work.segment);
+        if (p.turned)
+            StateImage<ND>::load_turned(m, start, w, lane);
+        else
+            StateImage<ND>::load(m, start, w, lane);
     } else if (col < p.dim_z && p.first) {
         const float *first = p.first + b * p.first_stride[0] + head * p.first_stride[1] + col * p.first_stride[3];
         each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { m[d][i] = first[row * p.first_stride[2]]; });
@@ -661,7 +728,7 @@ __global__ __launch_bounds__(2 * DT, 2) void linear_sweep(LinearArgs a)
 
         // the state behind the run
         decay(m, n < C ? g[n] : step.at(k));
-        add_outer<T, TileT>(m, yt, Taken<T>(zf, Factors(factors, h), odd || log_decay > 0.0f), lane);
+        add_outer<T, TileT>(m, yt, Taken<T, PARTS>(zf, Factors(factors, h), odd || log_decay > 0.0f), lane);
     }
 
     if (works && runs > 0)
@@ -675,7 +742,7 @@ __global__ __launch_bounds__(2 * DT, 2) void linear_sweep(LinearArgs a)
         else
             head_row<T>(p.out, p.out_stride, b, row, head)[col] = (T)0.0f;
     }
-    if (p.last && (reverse ? work.segment == 0 : seg.last)) {
+    if (p.last) { // the tokens are one segment
         float *last = p.last + b * p.last_stride[0] + head * p.last_stride[1] + col * p.last_stride[3];
         each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { last[row * p.last_stride[2]] = m[d][i]; });
     }
@@ -698,12 +765,12 @@ __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(Linear
     const Work work(a.first + at, a.jobs, a.segments, a.heads);
     const LinearJob &p = a.job[work.job];
     const int b = work.b, head = work.head;
-    const int t = (int)threadIdx.x, lane = t & 63, c = lane & 31, h = lane >> 5;
-    const int w = __builtin_amdgcn_readfirstlane(t >> 6), col = 32 * w + c;
+    const int t = (int)threadIdx.x, lane = t & 63, h = lane >> 5;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
     const bool reverse = p.reverse != 0, works = 32 * w < p.dim_z;
     const Segment seg(a.lengths, b, (int)a.tokens, a.each, work.segment);
-    if (reverse ? work.segment == 0 : work.segment == a.segments - 1)
-        return; // no segment begins behind it
+    if (!p.last && (reverse ? work.segment == 0 : work.segment == a.segments - 1))
+        return; // no one asks what is behind it
     const int len = seg.len, runs = (len + C - 1) / C;
 
     const auto tile = [&](int buffer, int which) { return lds + (2 * buffer + which) * G::kTileBytes; };
@@ -744,12 +811,9 @@ __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(Linear
         columns<T, TileT>(zf, zt, w, lane);
         const bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1]));
         decay(m, n < C ? g[n] : step.at(k));
-        add_outer<T, TileT>(m, yt, Taken<T>(zf, Factors(factors, h), odd || log_decay > 0.0f), lane);
+        add_outer<T, TileT>(m, yt, Taken<T, kParts<T>>(zf, Factors(factors, h), odd || log_decay > 0.0f), lane);
     }
-    if (col < p.dim_z) {
-        float *start = start_of(a, p, work.line, work.segment) + col * p.start_stride[1];
-        each_row_of_state<ND>(p.dim_x, h, [&](int d, int i, int row) { start[row * p.start_stride[0]] = m[d][i]; });
-    }
+    StateImage<ND>::store(m, start_of(a, p, work.line, work.segment), w, lane);
 }
 
 // ---- the decay's gradient ----------------------------------------------------
@@ -761,8 +825,9 @@ __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(Linear
 //   pairs within it: elementwise, from the two score matrices in 32 bits
 //   the others: <T, U> + <S, V>,  U = scale sum_i g^(i+1) q_i dout_i',  V the same with i + 1 in front
 //   T <- g^C (T + C S) + sum_j (C-1-j) g^(C-1-j) k_j v_j'
-// All of these are sums over tokens of an exact operand and one that is split in two, so nothing is rounded
-// to 16 bits on its way.  A segment begins with T = 0 and counts the steps within it; <T, dS> at its end, dS
+// All of these are sums over tokens of an exact operand and one that is split in two parts, so nothing is rounded
+// to 16 bits on its way (a third part of bfloat16 would take registers that are not there: 16 heads of 128, 8160
+// tokens 145 us instead of 75).  A segment begins with T = 0 and counts the steps within it; <T, dS> at its end, dS
 // the gradient of the state there, counts them for the tokens behind it.
 struct DecayArgs {
     const void *q, *k, *v, *dout;
@@ -779,13 +844,17 @@ struct DecayArgs {
     uint32_t blocks, first;
 };
 
+// Waves that share 32 columns, each with its part of the states' rows: two waves a SIMD hide more than one.
+template <int DT>
+constexpr int kDecayWaves = DT == 64 || DT == 128 ? 2 : 1;
+
 template <typename T, int DT, bool VEC>
-__global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
+__global__ __launch_bounds__(2 * DT * kDecayWaves<DT>, DT == 128 ? 2 : 1) void linear_decay(DecayArgs a)
 {
-    using G = Runs<T, DT, VEC, 4>;
+    using G = Runs<T, DT, VEC, 4, kDecayWaves<DT>>;
     using RunT = typename G::RunT;
     using TileT = typename G::TileT;
-    constexpr int ND = G::kBlocks, C = kRun;
+    constexpr int ND = G::kBlocks, C = kRun, WAVES = kDecayWaves<DT>, MINE = ND / WAVES;
     extern __shared__ __align__(16) uint8_t lds[];
 
     const uint32_t at = xcd_order(blockIdx.x, a.blocks);
@@ -794,7 +863,7 @@ __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
     const Work work(a.first + at, 1, a.segments, a.heads);
     const int b = work.b, head = work.head, kv = head / a.share;
     const int t = (int)threadIdx.x, lane = t & 63, c = lane & 31, h = lane >> 5;
-    const int w = __builtin_amdgcn_readfirstlane(t >> 6), col = 32 * w + c;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6), w = wave % ND, d0 = wave / ND * MINE, col = 32 * w + c;
     const Segment seg(a.lengths, b, (int)a.tokens, a.each, work.segment);
     const int len = seg.len, runs = (len + C - 1) / C;
     const int dims[4] = {a.dim, a.dim, a.value_dim, a.value_dim};
@@ -816,23 +885,38 @@ __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
 #pragma unroll
     for (int i = 0; i < 8; ++i) // what no load writes
         RunT::StageT::clear(lds + i * G::kTileBytes, dims[i % 4], t);
-    float16v s[ND], u[ND];
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-        s[d] = u[d] = zero16();
+    // this wave's rows of a state: of the call's, or of a segment's
     const int64_t place = (work.line * a.segments + work.segment) * a.start_floats;
-    if (col < a.value_dim && a.segments > 1) {
-        const float *start = a.starts + place + col;
-        each_row_of_state<ND>(a.dim, h, [&](int d, int i, int row) { s[d][i] = start[row * a.value_dim]; });
-    } else if (col < a.value_dim && a.state) {
-        const float *state = a.state + b * a.state_stride[0] + head * a.state_stride[1] + col;
-        each_row_of_state<ND>(a.dim, h, [&](int d, int i, int row) { s[d][i] = state[row * a.state_stride[2]]; });
-    }
+    const auto each_mine = [&](const float *state, const int64_t *stride, const float *image, auto &&f) {
+        if (a.segments > 1) {
+#pragma unroll
+            for (int d = 0; d < MINE; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    f(d, i, image[place + 4 * StateImage<ND>::at(d0 + d, i >> 2, w, lane) + (i & 3)]);
+        } else if (state && col < a.value_dim) {
+            const float *mine = state + b * stride[0] + head * stride[1] + col;
+#pragma unroll
+            for (int d = 0; d < MINE; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int row = 32 * (d0 + d) + state_row(acc_row(i, h));
+                    if (row < a.dim)
+                        f(d, i, mine[row * stride[2]]);
+                }
+        }
+    };
+    float16v s[MINE], u[MINE];
+#pragma unroll
+    for (int d = 0; d < MINE; ++d)
+        s[d] = u[d] = zero16();
+    each_mine(a.state, a.state_stride, a.starts, [&](int d, int i, float v) { s[d][i] = v; });
     // factors of a token: where a state takes it in for T and S, and for U and V, whose first token of a run
     // of n is token C - n of the tile
     Powers g{reinterpret_cast<float *>(lds + G::kPowers)};
     float *factors = reinterpret_cast<float *>(lds + G::kFactors);
     const float log_decay = a.log_decay[head];
+    const bool grows = log_decay > 0.0f;
     g.fill(log_decay, C, t, G::kThreads);
     const Step decays(log_decay, C);
     const auto fill = [&](int n) {
@@ -860,7 +944,7 @@ __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
         __syncthreads();
         if (k + 1 < runs)
             fetch(k + 1, buffer ^ 1);
-        if (k % ND == w) { // pairs within the run: the waves take turns
+        if (k % (ND * WAVES) == wave) { // pairs within the run: the waves take turns
             float16v x = zero16(), y = zero16();
 #pragma unroll
             for (int kk = 0; kk < 2 * ND; ++kk) {
@@ -879,36 +963,40 @@ __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
         }
         if (32 * w >= a.value_dim)
             continue;
-        const bool grows = log_decay > 0.0f;
-        FragV<T> zf[2];
-        columns<T, TileT>(zf, dt, w, lane);
-        bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
-        const Taken<T> for_u(zf, Factors(factors, h), odd);
-        const Taken<T> for_v(zf, Factors(factors + C, h), odd);
-        columns<T, TileT>(zf, vt, w, lane);
-        odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
-        const Taken<T> to_t(zf, Factors(factors + 2 * C, h), odd);
-        const Taken<T> to_s(zf, Factors(factors + 3 * C, h), odd);
         const float whole = n < C ? g[n] : decays.at(k);
         float part = 0.0f;
+        {
+            FragV<T> zf[2];
+            columns<T, TileT>(zf, dt, w, lane);
+            const bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
+            const Taken<T, kFewParts<T>> for_u(zf, Factors(factors, h), odd), for_v(zf, Factors(factors + C, h), odd);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            FragV<T> yf[2] = {state_columns<T, TileT>(qt, 0, d, lane), state_columns<T, TileT>(qt, 16, d, lane)};
-            float16v x = for_u.times(yf, zero16()), y = for_v.times(yf, zero16());
-            settle<T>();
-            float by_t = 0.0f, by_s = 0.0f;
+            for (int d = 0; d < MINE; ++d) {
+                const FragV<T> yf[2] = {state_columns<T, TileT>(qt, 0, d0 + d, lane),
+                                        state_columns<T, TileT>(qt, 16, d0 + d, lane)};
+                const float16v x = for_u.times(yf, zero16()), y = for_v.times(yf, zero16());
+                settle<T>();
+                float by_t = 0.0f, by_s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                by_t = fmaf(x[i], u[d][i], by_t);
-                by_s = fmaf(y[i], s[d][i], by_s);
-                u[d][i] = fmaf((float)n, s[d][i], u[d][i]) * whole;
-                s[d][i] *= whole;
+                for (int i = 0; i < 16; ++i) {
+                    by_t = fmaf(x[i], u[d][i], by_t);
+                    by_s = fmaf(y[i], s[d][i], by_s);
+                    u[d][i] = fmaf((float)n, s[d][i], u[d][i]) * whole;
+                    s[d][i] *= whole;
+                }
+                part = fmaf(by_t, for_u.back, fmaf(by_s, for_v.back, part));
             }
-            part = fmaf(by_t, for_u.back, fmaf(by_s, for_v.back, part));
-            yf[0] = state_columns<T, TileT>(kt, 0, d, lane), yf[1] = state_columns<T, TileT>(kt, 16, d, lane);
+        }
+        FragV<T> zf[2];
+        columns<T, TileT>(zf, vt, w, lane);
+        const bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
+        const Taken<T, kFewParts<T>> to_t(zf, Factors(factors + 2 * C, h), odd), to_s(zf, Factors(factors + 3 * C, h), odd);
+#pragma unroll
+        for (int d = 0; d < MINE; ++d) {
+            const FragV<T> yf[2] = {state_columns<T, TileT>(kt, 0, d0 + d, lane),
+                                    state_columns<T, TileT>(kt, 16, d0 + d, lane)};
             if constexpr (kLifts<T>) {
-                x = to_t.times(yf, zero16());
-                y = to_s.times(yf, zero16());
+                const float16v x = to_t.times(yf, zero16()), y = to_s.times(yf, zero16());
                 settle<T>();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -923,24 +1011,19 @@ __global__ __launch_bounds__(2 * DT) void linear_decay(DecayArgs a)
         settle<T>();
         sum += part;
     }
-    if (col < a.value_dim && (a.segments > 1 || a.dstate)) {
-        const float *end = a.segments > 1 ? a.ends + place + col
-                                          : a.dstate + b * a.dstate_stride[0] + head * a.dstate_stride[1] + col;
-        const int64_t step = a.segments > 1 ? a.value_dim : a.dstate_stride[2];
-        float part = 0.0f;
-        each_row_of_state<ND>(a.dim, h, [&](int d, int i, int row) { part = fmaf(u[d][i], end[row * step], part); });
-        sum += part;
-    }
+    float part = 0.0f;
+    each_mine(a.dstate, a.dstate_stride, a.ends, [&](int d, int i, float v) { part = fmaf(u[d][i], v, part); });
+    sum += part;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
         sum += __shfl_xor(sum, d);
     double *waves = reinterpret_cast<double *>(lds); // the tiles are done with
     __syncthreads();
     if (lane == 0)
-        waves[w] = sum;
+        waves[wave] = sum;
     __syncthreads();
     if (t == 0) {
-        for (int i = 1; i < ND; ++i)
+        for (int i = 1; i < ND * WAVES; ++i)
             sum += waves[i];
         a.sums[work.line * a.segments + work.segment] = sum;
     }

@@ -42,7 +42,12 @@ int Linear<T>::sweep(LinearArgs a, bool vec, hipStream_t s)
 {
     return with_linear_tile(widest(a), vec, [&](auto dt, auto v) {
         using G = Runs<T, dt.value, v.value, 3>;
-        return run_linear<linear_sweep<T, dt.value, v.value>>(a, blocks_of(a), G::kThreads, G::kLds, s);
+        bool leaves = false;
+        for (int i = 0; i < a.jobs; ++i)
+            leaves |= a.job[i].last != nullptr;
+        if (leaves)
+            return run_linear<linear_sweep<T, dt.value, v.value, kParts<T>>>(a, blocks_of(a), G::kThreads, G::kLds, s);
+        return run_linear<linear_sweep<T, dt.value, v.value, kFewParts<T>>>(a, blocks_of(a), G::kThreads, G::kLds, s);
     });
 }
 
@@ -59,7 +64,7 @@ template <typename T>
 int Linear<T>::decay(DecayArgs a, bool vec, hipStream_t s)
 {
     return with_linear_tile(std::max(a.dim, a.value_dim), vec, [&](auto dt, auto v) {
-        using G = Runs<T, dt.value, v.value, 4>;
+        using G = Runs<T, dt.value, v.value, 4, kDecayWaves<dt.value>>;
         return run_linear<linear_decay<T, dt.value, v.value>>(a, (int64_t)a.batch * a.heads * a.segments, G::kThreads,
                                                               G::kLds, s);
     });
