@@ -1,6 +1,7 @@
 """A transformer that predicts a latent's means and scales, trained and then used to code it.
 
     python examples/latent_transformer.py [--rows 68 --columns 120 --channels 192 --steps 40]
+                                          [--model recurrent --clip 1.0]
 
 From a hyper latent z (a quarter of y's sides) the model predicts mean and scale of every value
 of y.  Its blocks are group norm (channels last), attention with rotary positions (rows turn one
@@ -9,6 +10,9 @@ half of a head's pairs, columns the other) and group norm with SiLU, all from
 trained on the number of bits that the coder will need, then y is coded with its predictions: the
 encoder's front end and coder run fused, the decoder predicts again from z, which gives the same
 bits, looks up the same tables and gets the same symbols.  z and y are synthetic.
+
+``--model recurrent`` mixes positions by linear attention, each head with a decay that it learns, between
+RMS norms that add the residual where they read it; ``--clip`` bounds the gradients' global norm.
 """
 from __future__ import annotations
 
@@ -75,6 +79,52 @@ class LatentTransformer(nn.Module):
         return means, torch.exp(logs.clamp(-2.0, 5.0)) + 0.11
 
 
+class RecurrentBlock(nn.Module):
+    """What comes to the residual stream x goes along as `delta` and is added by the next norm."""
+
+    def __init__(self, channels, heads):
+        super().__init__()
+        self.heads = heads
+        self.before, self.between = nn.Parameter(torch.ones(channels)), nn.Parameter(torch.ones(channels))
+        self.qkv, self.out = nn.Linear(channels, 3 * channels), nn.Linear(channels, channels)
+        self.widen, self.narrow = nn.Linear(channels, 2 * channels), nn.Linear(2 * channels, channels)
+        # decays of exp(-softplus(rate)): memories from two positions to some hundred
+        self.rate = nn.Parameter(torch.linspace(0.0, -5.0, heads))
+
+    def forward(self, x, delta, table):
+        n, s, c = x.shape
+        y, x = L.rms_norm(delta, self.before, residual=x)
+        q, k, v = self.qkv(y).view(n, s, 3, self.heads, c // self.heads).unbind(2)
+        q, k = L.rotary(q, k, *table)
+        mixed, _ = L.linear_attention(q, k, v, -nn.functional.softplus(self.rate.float()))
+        y, x = L.rms_norm(self.out(mixed.reshape(n, s, c)), self.between, residual=x)
+        return x, self.narrow(nn.functional.silu(self.widen(y)))
+
+
+class LatentRecurrent(nn.Module):
+    """As LatentTransformer, with positions in raster order mixed by a state."""
+
+    def __init__(self, channels, heads, blocks=2):
+        super().__init__()
+        self.up = nn.Linear(channels, 16 * channels)
+        self.blocks = nn.ModuleList(RecurrentBlock(channels, heads) for _ in range(blocks))
+        self.last = nn.Parameter(torch.ones(channels))
+        self.head = nn.Linear(channels, 2 * channels)
+
+    def forward(self, z, table):
+        n, h, w, c = z.shape
+        x = self.up(z).view(n, h, w, 4, 4, c).permute(0, 1, 3, 2, 4, 5).reshape(n, 16 * h * w, c)
+        delta = torch.zeros_like(x)
+        for block in self.blocks:
+            x, delta = block(x, delta, table)
+        y, _ = L.rms_norm(delta, self.last, residual=x)
+        means, logs = self.head(y).float().view(n, 4 * h, 4 * w, 2 * c).chunk(2, dim=-1)
+        return means, torch.exp(logs.clamp(-2.0, 5.0)) + 0.11
+
+
+MODELS = {"transformer": LatentTransformer, "recurrent": LatentRecurrent}
+
+
 def positions(rows, columns, dim):
     """Tables of an image's positions, its rows and columns as two axes."""
     at = torch.cartesian_prod(torch.arange(rows, dtype=torch.float64), torch.arange(columns, dtype=torch.float64))
@@ -96,10 +146,10 @@ def synthetic(rows, columns, channels, seed):
     return z, 3.0 * wide + spread * torch.randn(wide.shape, generator=g, device="cuda")
 
 
-def run(rows=32, columns=48, channels=64, heads=2, steps=40, seed=0, say=print):
+def run(rows=32, columns=48, channels=64, heads=2, steps=40, seed=0, say=print, model="transformer", clip=None):
     torch.manual_seed(seed)
     z, y = synthetic(rows, columns, channels, seed)
-    model = LatentTransformer(channels, heads).cuda().to(torch.bfloat16)
+    model = MODELS[model](channels, heads).cuda().to(torch.bfloat16)
     table = positions(rows, columns, channels // heads)
     z16 = z.to(torch.bfloat16)
     optimizer = torch.optim.Adam(model.parameters(), lr=2e-3)
@@ -108,6 +158,8 @@ def run(rows=32, columns=48, channels=64, heads=2, steps=40, seed=0, say=print):
         loss = bits(y, *model(z16, table))
         optimizer.zero_grad()
         loss.backward()
+        if clip is not None:
+            L.clip_gradients([p.grad for p in model.parameters()], clip)
         optimizer.step()
         history.append(float(loss.detach()))
         if step % 10 == 0 or step == steps - 1:
@@ -143,5 +195,7 @@ if __name__ == "__main__":
     parser.add_argument("--channels", type=int, default=192)
     parser.add_argument("--heads", type=int, default=6)
     parser.add_argument("--steps", type=int, default=40)
+    parser.add_argument("--model", choices=sorted(MODELS), default="transformer")
+    parser.add_argument("--clip", type=float, default=None)
     a = parser.parse_args()
-    sys.exit(0 if run(a.rows, a.columns, a.channels, a.heads, a.steps)["same"] else 1)
+    sys.exit(0 if run(a.rows, a.columns, a.channels, a.heads, a.steps, model=a.model, clip=a.clip)["same"] else 1)

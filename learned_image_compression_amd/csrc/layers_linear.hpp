@@ -825,10 +825,11 @@ __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(Linear
 //   pairs within it: elementwise, from the two score matrices in 32 bits
 //   the others: <T, U> + <S, V>,  U = scale sum_i g^(i+1) q_i dout_i',  V the same with i + 1 in front
 //   T <- g^C (T + C S) + sum_j (C-1-j) g^(C-1-j) k_j v_j'
-// All of these are sums over tokens of an exact operand and one that is split in two parts, so nothing is rounded
-// to 16 bits on its way (a third part of bfloat16 would take registers that are not there: 16 heads of 128, 8160
-// tokens 145 us instead of 75).  A segment begins with T = 0 and counts the steps within it; <T, dS> at its end, dS
-// the gradient of the state there, counts them for the tokens behind it.
+// All of these are sums over tokens of an exact operand and one that is split in parts, so nothing is rounded to
+// 16 bits on its way.  (bfloat16: three parts where the registers are there, 4% slower than two; heads wider than
+// 64 take two, with three 16 heads of 128, 8160 tokens take 145 us instead of 75.)  A segment begins with T = 0 and
+// counts the steps within it; <T, dS> at its end, dS the gradient of the state there, counts them for the tokens
+// behind it.
 struct DecayArgs {
     const void *q, *k, *v, *dout;
     const float *state, *dstate;   // one segment: the call's
@@ -855,6 +856,7 @@ __global__ __launch_bounds__(2 * DT * kDecayWaves<DT>, DT == 128 ? 2 : 1) void l
     using RunT = typename G::RunT;
     using TileT = typename G::TileT;
     constexpr int ND = G::kBlocks, C = kRun, WAVES = kDecayWaves<DT>, MINE = ND / WAVES;
+    constexpr int PARTS = DT <= 64 ? kParts<T> : kFewParts<T>;
     extern __shared__ __align__(16) uint8_t lds[];
 
     const uint32_t at = xcd_order(blockIdx.x, a.blocks);
@@ -969,7 +971,7 @@ __global__ __launch_bounds__(2 * DT * kDecayWaves<DT>, DT == 128 ? 2 : 1) void l
             FragV<T> zf[2];
             columns<T, TileT>(zf, dt, w, lane);
             const bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
-            const Taken<T, kFewParts<T>> for_u(zf, Factors(factors, h), odd), for_v(zf, Factors(factors + C, h), odd);
+            const Taken<T, PARTS> for_u(zf, Factors(factors, h), odd), for_v(zf, Factors(factors + C, h), odd);
 #pragma unroll
             for (int d = 0; d < MINE; ++d) {
                 const FragV<T> yf[2] = {state_columns<T, TileT>(qt, 0, d0 + d, lane),
@@ -990,7 +992,7 @@ __global__ __launch_bounds__(2 * DT * kDecayWaves<DT>, DT == 128 ? 2 : 1) void l
         FragV<T> zf[2];
         columns<T, TileT>(zf, vt, w, lane);
         const bool odd = __any(odd_values<T>(zf[0]) || odd_values<T>(zf[1])) || grows;
-        const Taken<T, kFewParts<T>> to_t(zf, Factors(factors + 2 * C, h), odd), to_s(zf, Factors(factors + 3 * C, h), odd);
+        const Taken<T, PARTS> to_t(zf, Factors(factors + 2 * C, h), odd), to_s(zf, Factors(factors + 3 * C, h), odd);
 #pragma unroll
         for (int d = 0; d < MINE; ++d) {
             const FragV<T> yf[2] = {state_columns<T, TileT>(kt, 0, d0 + d, lane),

@@ -575,15 +575,19 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
         _out_like(out, h, h.dtype, device, "out")
     c = h.shape[-1]
     dweight = torch.empty(c, dtype=kind, device=device)
-    samples, positions = _sample_rows(h.shape)
+    if h.is_contiguous() and dy.is_contiguous() and out.is_contiguous() and \
+            (dsum is None or dsum.is_contiguous()):
+        samples, positions = 1, h.numel() // c
+        hs = gs = ss = outs = (0, c)
+    else:
+        samples, positions = _sample_rows(h.shape)
+        hs, gs, outs = _token_rows(h, "h"), _token_rows(dy, "dy"), _token_rows(out, "out")
+        ss = _token_rows(dsum, "dsum") if dsum is not None else _NO_ROWS
     args = _RMS_NORM.pack(h.data_ptr(), 0, weight.data_ptr() if weight is not None else 0, 0, 0,
                           rstd.data_ptr(), 0, dy.data_ptr(),
                           dsum.data_ptr() if dsum is not None else 0, out.data_ptr(),
-                          dweight.data_ptr(), *_token_rows(h, "h"), *_NO_ROWS, *_NO_ROWS, *_NO_ROWS,
-                          *_token_rows(dy, "dy"),
-                          *(_token_rows(dsum, "dsum") if dsum is not None else _NO_ROWS),
-                          *_token_rows(out, "out"), samples, positions, c, DTYPES[h.dtype],
-                          DTYPES[kind], 0, 0.0)
+                          dweight.data_ptr(), *hs, 0, 0, 0, 0, 0, 0, *gs, *ss, *outs, samples, positions,
+                          c, DTYPES[h.dtype], DTYPES[kind], 0, 0.0)
     if samples == 0 or positions == 0:
         return out, dweight.zero_()
     lib = load()
