@@ -94,14 +94,15 @@ int lic_group_norm_backward(const void *dy, int64_t dy_sample, int64_t dy_row, c
  *   a = weight dy,  dx = rstd (a - xh mean(a xh)) + dsum,  dweight = sum over rows of dy xh
  * with xh = h rstd; dx is the gradient of x and of residual alike, dsum the one
  * that comes to h from elsewhere (null: 0).  dweight (param_dtype) may be null.
- * An output may be an input of the same strides (sum: x or residual; dx: dy or dsum).
+ * An output may be an input of the same strides (y and sum: x or residual; dx: dy or dsum).
  *
  * format != LIC_FORMAT_NONE (forward only): y has one byte a value, an e4m3 number (up
  * to 448) or a whole number (up to 127), and scales (float [samples][positions]) what
  * one stands for:
  *   top = max(max over the row of |weight h rstd|, 1e-30), scale = top / most,
  *   y = round(weight h rstd * (most / top)), ties to even
- * A row with a NaN has a scale of NaN.  Sums are held in 32 bits. */
+ * Where a row of weight h rstd is not all finite, neither is its scale, and all that the row
+ * stands for is NaN.  Sums are held in 32 bits; a row whose squares overflow them has an rstd of 0. */
 enum lic_format { LIC_FORMAT_NONE = 0, LIC_FORMAT_E4M3 = 1, LIC_FORMAT_INT8 = 2 };
 
 typedef struct lic_rms_norm_args {
@@ -236,7 +237,7 @@ int lic_attention_backward(const lic_attention_args *args, void *workspace,
  *   S_t = g S_(t-1) + k_t v_t',   out_t = scale q_t S_t
  * that is out_t = scale (sum over s <= t of g^(t-s) (q_t . k_s) v_s + g^(t+1) q_t S_(-1)),
  * where S_(-1) is `state` (null: 0) and state_out (may be null) receives the last S.
- * state_out may be `state` itself.  lengths (null: all) are the tokens in use of each
+ * state_out may be `state` itself; no other output may be an input.  lengths (null: all) are the tokens in use of each
  * batch, held to [0, tokens]: the state stops there, rows behind it are not read,
  * and their out (dq, dk, dv) is 0.
  *
@@ -244,12 +245,11 @@ int lic_attention_backward(const lic_attention_args *args, void *workspace,
  * infinity shows from its own row on (in gradients: up to it).
  *
  * States are float, [batch][head][dim][value_dim] with strides by batch, head and
- * row of their own.  Sums and states are held in 32 bits, and what a state takes in and
- * gives to the next position keeps that precision (16-bit types: an operand that carries a
- * power of g is split in two); the products that form `out` take the scores and the
- * state rounded to q's type, in half precision as a power of two times them, so their
- * precision does not depend on the size of the inputs.  16-bit products of 32-bit sums
- * and 32-bit products otherwise, as for attention.
+ * row of their own.  Sums and states are held in 32 bits, and a state that leaves the call has
+ * that precision (16-bit types: an operand that carries a power of g is split into parts);
+ * the products that form `out` take the scores and the state rounded to q's type, in half
+ * precision as a power of two times them, so their precision does not depend on the size
+ * of the inputs.  Products of 32-bit inputs are in 32 bits.
  *
  * The backward call takes what the forward call took, dout, and dstate, the gradient
  * that comes to state_out (null: 0).  dlog_decay (float [heads], summed over the batch)

@@ -693,7 +693,13 @@ __global__ __launch_bounds__(2 * DT, 2) void linear_sweep(LinearArgs a)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             o[i] *= f;
-        if (!odd) {
+        bool careful = false;
+        if (odd) { // what is NaN as it is needs no care: a step that overflowed is NaN nearly everywhere
+            for (int i = 0; i < 16; ++i)
+                careful |= o[i] == o[i] && 32 * w + acc_row(i, h) < dim_z;
+            careful = __any(careful && c >= C - n);
+        }
+        if (!careful) {
 #pragma unroll
             for (int half = 0; half < 2; ++half)
                 o = mma(zf[half], operand<T>(s, half), o); // settled with the state

@@ -177,6 +177,12 @@ def _out_of(out, shape, dtype, device, name):
         raise ValueError(f"{name} overlaps itself")
 
 
+def _written(tensors):
+    """Tells autograd of tensors of the caller's that a call writes, so that a graph that still needs
+    their old values says so."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
+
+
 _NO_WORKSPACE = (None, 0, None)  # address, bytes, owner
 _E_WORKSPACE = NAME_TO_CODE["RANS_E_WORKSPACE"]
 
@@ -517,15 +523,18 @@ def rms_norm_forward(x: torch.Tensor, weight=None, *, residual=None, eps: float 
     the first) evenly spaced, for example tokens [N, S, C] cut out of a wider tensor; ``residual`` is
     like it.  ``h`` is rounded to x's type before the norm (without a residual it is ``x``
     itself), ``y = weight * h * rstd`` and ``rstd = 1 / sqrt(mean(h^2) + eps)``, float32 [...].
-    ``out`` and ``sum_out`` are places for y and h; ``sum_out`` may be x or residual.
+    ``out`` and ``sum_out`` are places for y and h, and may be x or residual.
     """
     device, kind = _rms_params(x, "x", weight, eps)
+    given = (out, sum_out)
     if out is None:
         out = _dense_like(x)
     else:
         _out_like(out, x, x.dtype, device, "out")
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
     h = _rms_forward(x, weight, residual, eps, 0, out, None, rstd, sum_out, device, kind)
+    if given[0] is not None or given[1] is not None:
+        _written(given)
     return out, h, rstd
 
 
@@ -535,8 +544,8 @@ def rms_norm_8bit(x: torch.Tensor, weight=None, *, residual=None, eps: float = 1
     (y, scales, h).
 
     ``y`` is float8_e4m3fn ("e4m3") or int8 ("int8") and stands for ``y * scales[..., None]``: a
-    row's scale (float32) is its largest size over 448 or 127, so nothing is cut off.  A row
-    with a NaN has a scale of NaN.  The rest is as in :func:`rms_norm_forward`.  There is no gradient.
+    row's scale (float32) is its largest size over 448 or 127, so nothing is cut off.  A row that is
+    not all finite stands for NaN.  The rest is as in :func:`rms_norm_forward`.  There is no gradient.
     """
     if _wants_gradient(x, weight, residual):
         raise NotImplementedError("the norm in 8 bits has no gradients")
@@ -544,12 +553,15 @@ def rms_norm_8bit(x: torch.Tensor, weight=None, *, residual=None, eps: float = 1
     if format not in FORMATS:
         raise ValueError(f"format must be one of {', '.join(FORMATS)}")
     code, dtype = FORMATS[format]
+    given = (out, sum_out)
     if out is None:
         out = torch.empty(x.shape, dtype=dtype, device=device)
     else:
         _out_like(out, x, dtype, device, "out")
     scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
     h = _rms_forward(x, weight, residual, eps, code, out, scales, None, sum_out, device, kind)
+    if given[0] is not None or given[1] is not None:
+        _written(given)
     return out, scales, h
 
 
@@ -573,6 +585,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
         out = _dense_like(h)
     else:
         _out_like(out, h, h.dtype, device, "out")
+        _written((out,))
     c = h.shape[-1]
     dweight = torch.empty(c, dtype=kind, device=device)
     if h.is_contiguous() and dy.is_contiguous() and out.is_contiguous() and \
@@ -1032,10 +1045,12 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         out = torch.empty(out_shape, dtype=q.dtype, device=device)
     else:
         _out_of(out, out_shape, q.dtype, device, "out")
+        _written((out,))
     if state_out is None:
         state_out = torch.empty(shape, dtype=torch.float32, device=device)
     else:
         _out_of(state_out, shape, torch.float32, device, "state_out")
+        _written((state_out,))
     last_ptr, ls = _state(state_out, shape, device, "state_out")
     args = _LINEAR.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state_ptr, length_ptr,
                         out.data_ptr(), last_ptr, 0, 0, 0, 0, 0, 0, 0, *strides[0], *strides[1], *strides[2],
@@ -1171,11 +1186,12 @@ def _gradients(tensors, out):
             if to.stride() != t.stride():
                 raise ValueError(f"out {i} differs in layout")
         flat += (t.data_ptr(), to.data_ptr(), t.numel(), DTYPES[t.dtype])
-    return array.array("q", flat).tobytes(), len(tensors), device
+    return array.array("q", flat).tobytes(), places, device
 
 
 def _clip(tensors, max_norm, out, where):
-    packed, n, device = _gradients(tensors, out)
+    packed, places, device = _gradients(tensors, out)
+    n = len(places)
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())
     norm = torch.empty((), dtype=torch.float32, device=device)
@@ -1185,6 +1201,8 @@ def _clip(tensors, max_norm, out, where):
         def call(p, size):
             return lib.lic_gradient_norm(packed, n, norm.data_ptr(), p, size, stream)
     else:
+        _written(places)
+
         def call(p, size):
             return lib.lic_clip_gradients(packed, n, max_norm, norm.data_ptr(), p, size, stream)
     _with_workspace(device, stream, call, lambda: lib.lic_clip_gradients_workspace_bytes(packed, n), where)

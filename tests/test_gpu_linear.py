@@ -438,3 +438,49 @@ def test_rows_far_apart(L):
     dout = normal(g, 3, 64, 1, d, dtype=F16)
     for a, b in zip(L.linear_attention_backward(dout, q, rows, v, log)[:4], L.linear_attention_backward(dout, q, rows.contiguous(), v, log)[:4]):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("s", [600, 4000])
+def test_overflow_costs_little(L, s, dtype):
+    """A training pass whose values are NaN everywhere takes little longer than one of numbers."""
+    x, more, grads = inputs(2, s, 8, 8, 64, 64, dtype, False, False)
+    bad = {**x, "v": torch.full_like(x["v"], math.nan)}
+
+    def took(y):
+        best = math.inf
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(5):
+                L.linear_attention_forward(**y, **more)
+                L.linear_attention_backward(grads["dout"], *y.values(), **more)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    plain, odd = took(x), took(bad)
+    print(f"{odd / plain:.2f} times as long", flush=True)
+    assert odd < 6 * plain
+    out, last = L.linear_attention_forward(**bad, **more)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(last).all())
+
+
+def test_what_is_written_is_known_to_autograd(L):
+    """A state that a graph keeps, and that a step then overwrites, is an error and no wrong gradient."""
+    x, more, _ = inputs(1, 40, 2, 2, 16, 16, F32, True, False)
+    q = x["q"].clone().requires_grad_()
+    out, _ = L.linear_attention(q, x["k"], x["v"], x["log_decay"], state=more["state"])
+    L.linear_attention_forward(*(x[n][:, :1] for n in "qkv"), x["log_decay"], state=more["state"], state_out=more["state"])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    w = torch.randn(3, 8, device="cuda", requires_grad=True)
+    loss = (w * w).sum()
+    L.clip_gradients(w.detach(), 1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        state = torch.zeros(1, 2, 16, 16, device="cuda")
+        L.linear_attention_forward(*(x[n][:, :1] for n in "qkv"), x["log_decay"], state=state, state_out=state)
+        assert bool((state != 0).any())
