@@ -162,33 +162,35 @@ __global__ __launch_bounds__(64) void linear_decay_join(const double *sums, floa
 
 // ---- the states before the segments ------------------------------------------------
 //
-// start_(k+1) = g^(tokens of k) start_k + what k adds, in place of what the segments add.  A block takes 64
-// numbers of a state, four a thread, and all segments: 16 groups of up to 16 neighbours.  Each group adds up
-// its own, then what comes from the groups before it, so a thread waits for memory once.
-constexpr int kMostSegments = 256, kScanGroups = 16;
+// start_(k+1) = g^(tokens of k) start_k + what k adds, in place of what the segments add.  A block takes all
+// segments of 1024 / GROUPS numbers of a state, four a thread, in GROUPS groups of up to EACH neighbours.  Each
+// group adds up its own, then what comes from the groups before it, so a thread waits for memory once.  (The
+// powers are formed in 64 bits, by one wave of the block: by all of them they were most of its time.)
+constexpr int kMostSegments = 256;
 
 struct ScanArgs {
     LinearJob job[2];
     const float *log_decay;
     const int32_t *lengths;
     int64_t tokens, first;
-    int32_t heads, jobs, segments, each, start_floats, tiles; // of 64 numbers
+    int32_t heads, jobs, segments, each, start_floats, tiles; // a block's share of a state
     int32_t blocks;                                           // of 32 columns
     int32_t group;                                            // segments of a group
 };
 
-template <int EACH>
+template <int EACH, int GROUPS>
 __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
 {
+    constexpr int ACROSS = 256 / GROUPS;
     using VT = Vec<float, 4>;
-    __shared__ VT ends[kScanGroups][16];
-    __shared__ float powers[kScanGroups];
+    __shared__ VT ends[GROUPS][ACROSS];
+    __shared__ float powers[GROUPS], whole_part[2];
     const int64_t id = a.first + blockIdx.x, line = id / a.tiles / a.jobs;
     const int tile = (int)(id % a.tiles), which = (int)(id / a.tiles % a.jobs);
     const LinearJob &p = a.job[which];
     const int b = (int)(line / a.heads), head = (int)(line - (int64_t)b * a.heads);
-    const int t = (int)threadIdx.x, x = t & 15, group = t >> 4;
-    const int at = (tile * 16 + x) * 4; // its numbers of a state: four rows of a column of StateImage
+    const int t = (int)threadIdx.x, x = t % ACROSS, group = t / ACROSS;
+    const int at = (tile * ACROSS + x) * 4; // its numbers of a state: four rows of a column of StateImage
     const int place = at / 4 / 64, lane = at / 4 & 63, fours = place / a.blocks;
     const int row0 = 32 * (fours >> 2) + state_row(8 * (fours & 3) + 4 * (lane >> 5));
     const int column = 32 * (place % a.blocks) + (lane & 31);
@@ -211,10 +213,16 @@ __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
             if (row0 + i < p.dim_x)
                 run.v[i] = first[(row0 + i) * p.first_stride[2]];
     }
-    const double log_decay = a.log_decay[head];
     const int all = a.lengths ? min(max(a.lengths[b], 0), (int)a.tokens) : (int)a.tokens;
     const auto tokens_of = [&](int k) { return min(max(all - index(k) * a.each, 0), a.each); };
-    const float whole = (float)exp(log_decay * a.each), part = (float)exp(log_decay * (all % a.each));
+    if (t < 64) {
+        const int n = t == 0 ? a.each : all % a.each;
+        const float p = n == 0 ? 1.0f : (float)exp((double)a.log_decay[head] * n);
+        if (t < 2)
+            whole_part[t] = p;
+    }
+    __syncthreads();
+    const float whole = whole_part[0], part = whole_part[1];
     const auto power = [&](int k) {
         const int n = tokens_of(k);
         return n == a.each ? whole : n == 0 ? 1.0f : part;
@@ -266,18 +274,23 @@ int run_scan(const LinearArgs &l, hipStream_t s)
         a.job[i] = l.job[i];
     a.log_decay = l.log_decay, a.lengths = l.lengths, a.tokens = l.tokens;
     a.heads = l.heads, a.jobs = l.jobs, a.segments = l.segments, a.each = l.each, a.start_floats = l.start_floats;
-    a.tiles = l.start_floats / 64;
     a.blocks = (std::max(l.job[0].dim_x, l.job[0].dim_z) + 31) / 32;
-    a.group = (l.segments + kScanGroups - 1) / kScanGroups;
-    in_pieces((int64_t)l.batch * l.heads * l.jobs * a.tiles, 256, [&](int64_t first, uint32_t blocks) {
-        a.first = first;
-        if (a.group == 1)
-            linear_scan<1><<<blocks, 256, 0, s>>>(a);
-        else if (a.group <= 4)
-            linear_scan<4><<<blocks, 256, 0, s>>>(a);
-        else
-            linear_scan<16><<<blocks, 256, 0, s>>>(a);
-    });
+    const auto run = [&](auto kernel, int each, int groups) {
+        a.group = std::min(each, (l.segments + groups - 1) / groups);
+        a.tiles = l.start_floats / (1024 / groups);
+        in_pieces((int64_t)l.batch * l.heads * l.jobs * a.tiles, 256, [&](int64_t first, uint32_t blocks) {
+            a.first = first;
+            kernel<<<blocks, 256, 0, s>>>(a);
+        });
+    };
+    if (l.segments <= 4)
+        run(linear_scan<4, 1>, 4, 1);
+    else if (l.segments <= 16)
+        run(linear_scan<4, 4>, 4, 4);
+    else if (l.segments <= 64)
+        run(linear_scan<4, 16>, 4, 16);
+    else
+        run(linear_scan<16, 16>, 16, 16);
     return launched();
 }
 
