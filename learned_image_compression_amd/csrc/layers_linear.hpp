@@ -526,7 +526,7 @@ __device__ __forceinline__ float *start_of(const LinearArgs &a, const LinearJob 
 
 // PARTS of what a state takes in: all of them where the state leaves the call, with the precision of 32-bit sums.
 template <typename T, int DT, bool VEC, int PARTS>
-__global__ __launch_bounds__(2 * DT, 2) void linear_sweep(LinearArgs a)
+__global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void linear_sweep(LinearArgs a)
 {
     using G = Runs<T, DT, VEC, 3>;
     using RunT = typename G::RunT;
