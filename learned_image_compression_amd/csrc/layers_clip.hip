@@ -8,6 +8,9 @@
 // chunks in 64 bits; then every block adds all sums up itself, in one order, which is cheaper
 // than a launch in between, and scales its chunks, the last ones first, since they are what
 // the caches still hold.  With c = 1 and out = x there is nothing left to do.
+//
+// Measured: 138M bfloat16 values in 56 tensors 51 us for the sums (5.4 TB/s), 90 us to scale them (6.1 TB/s read
+// and written); 410000 float values in 16 tensors 4.3 and 4.9 us, which are launches.
 #include <algorithm>
 #include <utility>
 #include <vector>

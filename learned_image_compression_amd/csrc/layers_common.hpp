@@ -1,5 +1,5 @@
 // layers_common.hpp -- element types and small helpers of the network
-// operators' kernels (group norm, rotary positions, attention).
+// operators' kernels (norms, rotary positions, attention, linear attention, clipping).
 #pragma once
 
 #include <atomic>

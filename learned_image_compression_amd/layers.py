@@ -183,6 +183,19 @@ def _written(tensors):
     torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
 
 
+def _in_place(out, name, inputs):
+    """An output may be an input entry by entry: not one that begins at the same address and lies
+    otherwise."""
+    if out is None or out.numel() == 0:
+        return
+    at = out.data_ptr()
+    for t in inputs:
+        if t is not None and t.data_ptr() == at and \
+                (t.dtype is not out.dtype or any(n > 1 and a != b for n, a, b in
+                                                 zip(out.shape, out.stride(), t.stride()))):
+            raise ValueError(f"{name} overlaps an input and is laid out differently")
+
+
 _NO_WORKSPACE = (None, 0, None)  # address, bytes, owner
 _E_WORKSPACE = NAME_TO_CODE["RANS_E_WORKSPACE"]
 
@@ -489,6 +502,8 @@ def _rms_forward(x, weight, residual, eps, code, y, stat, rstd, sum_out, device,
         else:
             _out_like(sum_out, x, x.dtype, device, "sum_out")
             h = sum_out
+        if h.data_ptr() == y.data_ptr() and h.numel():
+            raise ValueError("out and sum_out must not be one place")
     elif sum_out is not None:
         raise ValueError("sum_out is for calls with a residual")
     c = x.shape[-1]
@@ -523,7 +538,7 @@ def rms_norm_forward(x: torch.Tensor, weight=None, *, residual=None, eps: float 
     the first) evenly spaced, for example tokens [N, S, C] cut out of a wider tensor; ``residual`` is
     like it.  ``h`` is rounded to x's type before the norm (without a residual it is ``x``
     itself), ``y = weight * h * rstd`` and ``rstd = 1 / sqrt(mean(h^2) + eps)``, float32 [...].
-    ``out`` and ``sum_out`` are places for y and h, and may be x or residual.
+    ``out`` and ``sum_out`` are places for y and h, and each may be x or residual.
     """
     device, kind = _rms_params(x, "x", weight, eps)
     given = (out, sum_out)
@@ -532,9 +547,11 @@ def rms_norm_forward(x: torch.Tensor, weight=None, *, residual=None, eps: float 
     else:
         _out_like(out, x, x.dtype, device, "out")
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-    h = _rms_forward(x, weight, residual, eps, 0, out, None, rstd, sum_out, device, kind)
     if given[0] is not None or given[1] is not None:
+        _in_place(given[0], "out", (x, residual))
+        _in_place(given[1], "sum_out", (x, residual))
         _written(given)
+    h = _rms_forward(x, weight, residual, eps, 0, out, None, rstd, sum_out, device, kind)
     return out, h, rstd
 
 
@@ -559,9 +576,11 @@ def rms_norm_8bit(x: torch.Tensor, weight=None, *, residual=None, eps: float = 1
     else:
         _out_like(out, x, dtype, device, "out")
     scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-    h = _rms_forward(x, weight, residual, eps, code, out, scales, None, sum_out, device, kind)
     if given[0] is not None or given[1] is not None:
+        _in_place(given[0], "out", (x, residual))
+        _in_place(given[1], "sum_out", (x, residual))
         _written(given)
+    h = _rms_forward(x, weight, residual, eps, code, out, scales, None, sum_out, device, kind)
     return out, scales, h
 
 
@@ -585,6 +604,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
         out = _dense_like(h)
     else:
         _out_like(out, h, h.dtype, device, "out")
+        _in_place(out, "out", (dy, dsum, h))
         _written((out,))
     c = h.shape[-1]
     dweight = torch.empty(c, dtype=kind, device=device)
@@ -1034,7 +1054,8 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     dim], ``k`` [B, S, kv_heads, dim], ``v`` [B, S, kv_heads, value_dim] (any strides but the last;
     kv_heads divides heads), ``log_decay`` float32 [heads], ``out`` [B, S, heads, value_dim].
     ``state`` and ``state_out``, [B, heads, dim, value_dim], are S before the first token (None:
-    zeros) and behind the last; a decoder that steps passes one tensor as both.  ``lengths``
+    zeros) and behind the last; a decoder that steps passes one tensor as both.  ``out`` must not
+    overlap an input, ``state_out`` none but ``state``.  ``lengths``
     (int32 [B]) are the tokens in use: rows behind them are not read, their out is 0, and the
     state is that behind the last one in use.
     """
@@ -1045,11 +1066,14 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         out = torch.empty(out_shape, dtype=q.dtype, device=device)
     else:
         _out_of(out, out_shape, q.dtype, device, "out")
+        if out.numel() and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+            raise ValueError("out must not be an input")
         _written((out,))
     if state_out is None:
         state_out = torch.empty(shape, dtype=torch.float32, device=device)
     else:
         _out_of(state_out, shape, torch.float32, device, "state_out")
+        _in_place(state_out, "state_out", (state,))
         _written((state_out,))
     last_ptr, ls = _state(state_out, shape, device, "state_out")
     args = _LINEAR.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state_ptr, length_ptr,

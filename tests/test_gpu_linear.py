@@ -3,6 +3,7 @@ where the bounds are derived), at the sizes, lengths, strides and values where i
 from __future__ import annotations
 
 import math
+import threading
 
 import pytest
 import torch
@@ -415,6 +416,77 @@ def test_captured(L, dtype):
         torch.cuda.synchronize()
         for a, b in zip(outs, want):
             assert all(torch.equal(s, t) for s, t in zip(a, b)), turn
+
+
+def test_places(L):
+    """out is no input; state_out is the state's own layout or apart from it."""
+    g = gen(13)
+    q, k, v = (normal(g, 3, 70, 3, 8, dtype=F16) for _ in range(3))
+    log = torch.tensor([-0.1, -0.2, -0.3], device="cuda")
+    state = normal(g, 3, 3, 8, 8)
+    for t in (q, k, v):
+        with pytest.raises(ValueError, match="must not be an input"):
+            L.linear_attention_forward(q, k, v, log, out=t)
+    was = state.clone()
+    for s in (1, 70):
+        with pytest.raises(ValueError, match="laid out differently"):
+            L.linear_attention_forward(q[:, :s], k[:, :s], v[:, :s], log, state=state, state_out=state.transpose(0, 1))
+    assert torch.equal(state, was)
+    for s in (1, 70):
+        a = q[:, :s], k[:, :s], v[:, :s], log
+        want = L.linear_attention_forward(*a, state=state)
+        out, last = L.linear_attention_forward(*a, state=state, state_out=state)
+        assert last is state and torch.equal(out, want[0]) and torch.equal(state, want[1])
+
+
+def test_threads_that_share_a_stream(L):
+    """Each thread's results are the bits that it gets alone."""
+    jobs = [inputs(2, 400 + 100 * i, 4, 2, 32 * (i + 1), 48, dtype, True, False) for i, dtype in enumerate(ALL)]
+
+    def work(i):
+        x, more, grads = jobs[i]
+        y, h, rstd = L.rms_norm_forward(x["q"])
+        both = [x["k"].clone(), x["v"].clone()]
+        return (*L.linear_attention_forward(**x, **more),
+                *L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more),
+                y, *L.rms_norm_backward(h, h, None, rstd), L.clip_gradients(both, 1.0), *both)
+
+    want = [work(i) for i in range(3)]
+    wrong, start = [], threading.Barrier(3)
+
+    def repeat(i):
+        start.wait(60)
+        for _ in range(20):
+            if not all(torch.equal(a, b) for a, b in zip(work(i), want[i])):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=repeat, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not any(t.is_alive() for t in threads) and wrong == []
+
+
+def test_another_stream(L):
+    """The same bits on a stream of the caller's, with scratch memory of its own."""
+    x, more, grads = inputs(2, 700, 4, 2, 64, 64, BF16, True, True)
+
+    def work():
+        y, h, rstd = L.rms_norm_forward(x["q"])
+        return (*L.linear_attention_forward(**x, **more),
+                *L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more),
+                y, *L.rms_norm_backward(h, h, None, rstd), L.gradient_norm([x["k"], x["v"]]))
+
+    want = work()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        got = [work() for _ in range(3)]
+    here = work()  # meanwhile
+    torch.cuda.synchronize()
+    for r in (*got, here):
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
 
 
 def test_results_do_not_depend_on_timing(L):

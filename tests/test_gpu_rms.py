@@ -234,6 +234,31 @@ def test_rms_norm_refusals(L):
         torch.autograd.grad(first.sum(), leaf)
 
 
+def test_rms_norm_places(L):
+    """An output may be an input of the same layout; another layout at its address, and one place for both
+    outputs, are refused before anything is written."""
+    g = gen(12)
+    x, r = normal(g, 6, 6, 16, dtype=BF16), normal(g, 6, 6, 16, dtype=BF16)
+    was = x.clone()
+    turned = x.transpose(0, 1)
+    for call in (
+            lambda: L.rms_norm_forward(x, residual=r, out=turned),
+            lambda: L.rms_norm_forward(x, residual=r, sum_out=turned),
+            lambda: L.rms_norm_forward(r, residual=turned, out=x),
+            lambda: L.rms_norm_8bit(x, out=x.view(torch.float8_e4m3fn)[..., :16]),
+            lambda: L.rms_norm_backward(x, r, None, torch.ones(6, 6, device="cuda"), out=turned),
+            lambda: L.rms_norm_backward(r, r, None, torch.ones(6, 6, device="cuda"), dsum=x, out=turned),
+    ):
+        with pytest.raises(ValueError, match="laid out differently"):
+            call()
+    with pytest.raises(ValueError, match="one place"):
+        L.rms_norm_forward(r, residual=r, out=x, sum_out=x)
+    assert torch.equal(x, was)
+    want = L.rms_norm_forward(x, residual=r)
+    y, h, _ = L.rms_norm_forward(x, residual=r, out=x, sum_out=r)
+    assert y is x and h is r and torch.equal(x, want[0]) and torch.equal(r, want[1])
+
+
 def test_rms_norm_empty(L):
     for shape in ((0, 8), (2, 0, 8), (0, 3, 8)):
         x = torch.zeros(shape, device="cuda")
