@@ -303,7 +303,8 @@ struct Runs {
     static constexpr int kTileBytes = kRun * DT * sizeof(T);
     static constexpr int kPowers = 2 * TILES * kTileBytes;
     static constexpr int kFactors = kPowers + (kRun + 4) * 4; // of a token where the state takes it in
-    static constexpr int kLds = kFactors + 4 * kRun * 4;
+    static constexpr int kSteps = kFactors + 4 * kRun * 4; // of four tiles: what a pair so many tokens apart counts
+    static constexpr int kLds = kSteps + (TILES == 4 ? (2 * kRun + 4) * 4 : 0);
     using RunT = Run<T, kRun, DT, kThreads, VEC>;
     using TileT = Tile<T, kRun, DT>;
 };
@@ -840,11 +841,11 @@ __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(Linear
 //   the others: <T, U> + <S, V>,  U = scale sum_i g^(i+1) q_i dout_i',  V the same with i + 1 in front
 //   T <- g^C (T + C S) + sum_j (C-1-j) g^(C-1-j) k_j v_j'
 // All of these are sums over tokens of an exact operand and one that is split in parts, so nothing is rounded to
-// 16 bits on its way.  (bfloat16: three parts where the registers are there, 4% slower than two; heads wider than
-// 64 take two, with three 16 heads of 128, 8160 tokens take 145 us instead of 75.)  A segment begins with T = 0 and
+// 16 bits on its way.  (bfloat16: three parts, as all states that leave a call; two would leave an error of 2e-6 instead of
+// 4e-7 and save a few percent, with heads of 128, whose registers spill a little, 70 of 115 us.)  A segment begins with T = 0 and
 // counts the steps within it; <T, dS> at its end, dS the gradient of the state there, counts them for the tokens
 // behind it.  Its products and powers bound it (T and S are twice a state's registers, so two waves a SIMD is all there is): 16
-// heads of 128, 8160 tokens 75 us; 32 x 6 heads of 32, 256 tokens, float16 12.
+// heads of 128, 8160 tokens 115 us; 32 x 6 heads of 32, 256 tokens, float16 12.
 struct DecayArgs {
     const void *q, *k, *v, *dout;
     const float *state, *dstate;   // one segment: the call's
@@ -871,7 +872,7 @@ __global__ __launch_bounds__(2 * DT * kDecayWaves<DT>, DT == 128 ? 2 : 1) void l
     using RunT = typename G::RunT;
     using TileT = typename G::TileT;
     constexpr int ND = G::kBlocks, C = kRun, WAVES = kDecayWaves<DT>, MINE = ND / WAVES;
-    constexpr int PARTS = DT <= 64 ? kParts<T> : kFewParts<T>;
+    constexpr int PARTS = kParts<T>;
     extern __shared__ __align__(16) uint8_t lds[];
 
     const uint32_t at = xcd_order(blockIdx.x, a.blocks);
@@ -947,6 +948,9 @@ __global__ __launch_bounds__(2 * DT * kDecayWaves<DT>, DT == 128 ? 2 : 1) void l
     };
     __syncthreads();
     fill(C);
+    float *steps = reinterpret_cast<float *>(lds + G::kSteps) + C;
+    for (int e = t - C; e < C + 4; e += G::kThreads)
+        steps[e] = e > 0 && e < C ? a.scale * (float)e * g[e] : 0.0f;
     double sum = 0.0; // of the runs' sums in 32 bits
     for (int k = 0; k < runs; ++k) {
         const int n = rows_of_run(k), buffer = k & 1;
@@ -973,8 +977,7 @@ __global__ __launch_bounds__(2 * DT * kDecayWaves<DT>, DT == 128 ? 2 : 1) void l
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const int e = c - acc_row(i, h);
-                if (e > 0)
-                    part = fmaf(x[i] * y[i], a.scale * (float)e * g[max(e, 0)], part);
+                part = fmaf(e > 0 ? x[i] * y[i] : 0.0f, steps[e], part);
             }
             sum += part;
         }
