@@ -328,7 +328,7 @@ uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // How the tokens are split: into as many segments as make four blocks a CU, each of at least 64 tokens.  A state's way
 // through scratch memory (written, scanned, read) is as long as that of 4 * dim tokens' rows, so heads wider than
-// 64 take one block a CU.  Measured (us, all kernels, with 256 / 512 / 1024 / 1536 blocks): forward, bfloat16, 2 x
+// 64 take one block a CU.  Measured (us, all kernels as they were, with 256 / 512 / 1024 / 1536 blocks): forward, bfloat16, 2 x
 // 16 heads of 64, 8160 tokens 97 / 68 / 53 / 65; 6 heads of 32, 32640 tokens 64 / 44 / 39 / 41; trained, 16 heads of
 // 128, 8160 tokens 343 / 357 / 480 / 620; float, 4 x 6 heads of 32, 510 tokens in segments of 510 / 128 / 64 / 32: 200 /
 // 120 / 64 / 68.

@@ -842,10 +842,10 @@ __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(Linear
 //   T <- g^C (T + C S) + sum_j (C-1-j) g^(C-1-j) k_j v_j'
 // All of these are sums over tokens of an exact operand and one that is split in parts, so nothing is rounded to
 // 16 bits on its way.  (bfloat16: three parts, as all states that leave a call; two would leave an error of 2e-6 instead of
-// 4e-7 and save a few percent, with heads of 128, whose registers spill a little, 70 of 115 us.)  A segment begins with T = 0 and
+// 4e-7 and save a few percent, with heads of 128, whose registers spill a little, 47 of 117 us.)  A segment begins with T = 0 and
 // counts the steps within it; <T, dS> at its end, dS the gradient of the state there, counts them for the tokens
 // behind it.  Its products and powers bound it (T and S are twice a state's registers, so two waves a SIMD is all there is): 16
-// heads of 128, 8160 tokens 115 us; 32 x 6 heads of 32, 256 tokens, float16 12.
+// heads of 128, 8160 tokens 117 us; 32 x 6 heads of 32, 256 tokens, float16 12.
 struct DecayArgs {
     const void *q, *k, *v, *dout;
     const float *state, *dstate;   // one segment: the call's
