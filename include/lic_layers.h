@@ -95,6 +95,7 @@ int lic_group_norm_backward(const void *dy, int64_t dy_sample, int64_t dy_row, c
  * with xh = h rstd; dx is the gradient of x and of residual alike, dsum the one
  * that comes to h from elsewhere (null: 0).  dweight (param_dtype) may be null.
  * An output may be an input of the same strides (y and sum: x or residual; dx: dy or dsum).
+ * y and sum must not overlap each other, and y in 8 bits no input.
  *
  * format != LIC_FORMAT_NONE (forward only): y has one byte a value, an e4m3 number (up
  * to 448) or a whole number (up to 127), and scales (float [samples][positions]) what
@@ -237,9 +238,9 @@ int lic_attention_backward(const lic_attention_args *args, void *workspace,
  *   S_t = g S_(t-1) + k_t v_t',   out_t = scale q_t S_t
  * that is out_t = scale (sum over s <= t of g^(t-s) (q_t . k_s) v_s + g^(t+1) q_t S_(-1)),
  * where S_(-1) is `state` (null: 0) and state_out (may be null) receives the last S.
- * state_out may be `state` itself; no other output may be an input.  lengths (null: all) are the tokens in use of each
- * batch, held to [0, tokens]: the state stops there, rows behind it are not read,
- * and their out (dq, dk, dv) is 0.
+ * state_out may be `state` itself, with its strides; no other output may be an input.
+ * lengths (null: all) are the tokens in use of each batch, held to [0, tokens]: the state
+ * stops there, rows behind it are not read, and their out (dq, dk, dv) is 0.
  *
  * A token has no part in what comes before it, whatever its values are: a NaN or an
  * infinity shows from its own row on (in gradients: up to it).
