@@ -247,10 +247,11 @@ int lic_attention_backward(const lic_attention_args *args, void *workspace,
  *
  * States are float, [batch][head][dim][value_dim] with strides by batch, head and
  * row of their own.  Sums and states are held in 32 bits, and a state that leaves the call has
- * that precision (16-bit types: an operand that carries a power of g is split into parts);
- * the products that form `out` take the scores and the state rounded to q's type, in half
- * precision as a power of two times them, so their precision does not depend on the size
- * of the inputs.  Products of 32-bit inputs are in 32 bits.
+ * that precision.  16-bit types: an operand that is no input (a power of g times one, a score,
+ * a state) goes into a product as parts of q's type that add up to it: off by 2^-17 in
+ * bfloat16 and 2^-22 in half precision (where it is lifted by a power of two) in what forms
+ * outputs and gradients of q's type, which are rounded once at the end, and by less in
+ * states that leave the call.  Products of 32-bit inputs are in 32 bits.
  *
  * The backward call takes what the forward call took, dout, and dstate, the gradient
  * that comes to state_out (null: 0).  dlog_decay (float [heads], summed over the batch)
