@@ -102,17 +102,12 @@ __device__ __forceinline__ void split(const float (&v)[8], FragV<T> (&part)[PART
 }
 
 // Half precision: a power of two that brings the largest of finite sizes up (or down) to 2^13, so that what
-// is rounded to it for a product keeps its bits; at most 2^MOST.
-template <int MOST>
+// is rounded to it for a product keeps its bits; at most 2^120, whose inverse is a normal number.
 __device__ __forceinline__ float lift_of(float top)
 {
     const int e = (int)(__float_as_uint(top) >> 23);
-    return e == 0 ? 1.0f : __uint_as_float((uint32_t)min(max(127 + 13 + 127 - e, 127 - 100), 127 + MOST) << 23);
+    return e == 0 ? 1.0f : __uint_as_float((uint32_t)min(127 + 13 + 127 - e, 127 + 120) << 23);
 }
-constexpr int kStateLift = 120; // of what is multiplied back at once
-// of scores: the output's other part is multiplied too, and below 2^-51 a score times a value is
-// below half of float16's smallest number
-constexpr int kScoreLift = 64;
 // 1 / a power of two
 __device__ __forceinline__ float inverse_lift(float l) { return __uint_as_float((254u << 23) - __float_as_uint(l)); }
 __device__ __forceinline__ float finite_size(float x) { return not_finite(x) ? 0.0f : fabsf(x); }
@@ -326,7 +321,9 @@ struct Runs {
     static constexpr int kPowers = 2 * TILES * kTileBytes;
     static constexpr int kFactors = kPowers + (kRun + 4) * 4; // of a token where the state takes it in
     static constexpr int kSteps = kFactors + 4 * kRun * 4; // of four tiles: what a pair so many tokens apart counts
-    static constexpr int kLds = kSteps + (TILES == 4 ? (2 * kRun + 4) * 4 : 0);
+    static constexpr int kBacks = kSteps + (TILES == 4 ? (2 * kRun + 4) * 4 : 0); // of three tiles in half precision:
+                                                                                   // a wave's columns'
+    static constexpr int kLds = kBacks + (TILES == 3 && kLifts<T> ? 32 * kBlocks * 4 : 0);
     using RunT = Run<T, kRun, DT, kThreads, VEC>;
     using TileT = Tile<T, kRun, DT>;
 };
@@ -402,7 +399,7 @@ struct Taken {
                     top = fmaxf(top, finite_size(zw[j][e]));
             }
         if constexpr (kLifts<T>) {
-            const float lift = lift_of<kStateLift>(pair_max(top));
+            const float lift = lift_of(pair_max(top));
             back = inverse_lift(lift);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -610,6 +607,7 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
 
     Powers g{reinterpret_cast<float *>(lds + G::kPowers)};
     float *factors = reinterpret_cast<float *>(lds + G::kFactors);
+    float *backs = reinterpret_cast<float *>(lds + G::kBacks) + 32 * w; // half precision: 1 / the columns' powers of two
     const float log_decay = a.log_decay[head];
     g.fill(log_decay, C, t, G::kThreads);
     const Step step(log_decay, C);
@@ -632,7 +630,6 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
     out += (reverse ? (int64_t)max(len - C, 0) + C - 1 - c : (int64_t)c) * out_stride;
     const int64_t out_step = reverse ? -C * out_stride : C * out_stride;
     float16v o;
-    float lift = 1.0f;
     const auto put = [&](int k) {
         const int short_by = C - rows_of_run(k);
         uint8_t *row = out;
@@ -641,11 +638,10 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
             if (c < short_by)
                 return;
         }
-        const float back = kLifts<T> ? inverse_lift(lift) : 1.0f;
         if (part)
-            put_column<float, VEC>(reinterpret_cast<float *>(row), o, back, w, h, dim_z);
+            put_column<float, VEC>(reinterpret_cast<float *>(row), o, 1.0f, w, h, dim_z);
         else
-            put_column<T, VEC>(reinterpret_cast<T *>(row), o, back, w, h, dim_z);
+            put_column<T, VEC>(reinterpret_cast<T *>(row), o, 1.0f, w, h, dim_z);
         out += out_step;
     };
 
@@ -663,9 +659,10 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
         if (k > 0)
             put(k - 1);
 
-        // scores, and x M with the state split into operands
+        // scores, and x M with the state split into operands (in half precision times a power of two of each column,
+        // which is what o's rows are multiplied back by)
         float16v s;
-        float m_lift = 1.0f;
+        float lift = 1.0f; // of this lane's column of the state
         if constexpr (kLifts<T>) {
             float top = 0.0f;
 #pragma unroll
@@ -673,10 +670,10 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     top = fmaxf(top, finite_size(m[d][i]));
-#pragma unroll
-            for (int x = 32; x > 0; x >>= 1)
-                top = fmaxf(top, __shfl_xor(top, x));
-            m_lift = lift_of<kStateLift>(top);
+            lift = lift_of(pair_max(top));
+            if (h == 0)
+                backs[c] = inverse_lift(lift);
+            wave_fence();
         }
         for (bool careful = false;; careful = true) {
             s = zero16();
@@ -689,7 +686,7 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
                     const FragV<T> xf = TileT::row_frag(xt, c, 2 * d + half, h);
                     s = mma(TileT::row_frag(yt, c, 2 * d + half, h), xf, s);
                     FragV<T> mf[FEW];
-                    split_half<T, FEW>(m[d], half, m_lift, mf, careful);
+                    split_half<T, FEW>(m[d], half, lift, mf, careful);
 #pragma unroll
                     for (int n = 0; n < FEW; ++n)
                         o = mma(mf[n], xf, o);
@@ -709,7 +706,8 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
             for (int i = 0; i < 16; ++i)
                 s[i] = acc_row(i, h) < C - n ? 0.0f : s[i];
         }
-        float top = 0.0f, f = n < C ? g[max(c - (C - n), 0) + (reverse ? 0 : 1)] * p.read : come;
+        float top = 0.0f;
+        const float f = n < C ? g[max(c - (C - n), 0) + (reverse ? 0 : 1)] * p.read : come;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             // a later token's score counts for nothing, whatever it is
@@ -718,16 +716,18 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
                 top = fmaxf(top, finite_size(s[i]));
         }
         const bool odd_scores = FEW > 1 && __any(any_odd(s));
+        float score_lift = 1.0f;
         if constexpr (kLifts<T>) {
-            lift = lift_of<kScoreLift>(pair_max(top));
-            f *= lift * inverse_lift(m_lift);
+            score_lift = lift_of(pair_max(top));
+            const Factors back(backs, h);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                s[i] *= lift;
-        }
+                o[i] = o[i] * back.f[i >> 3][i & 7] * f;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            o[i] *= f;
+            for (int i = 0; i < 16; ++i)
+                o[i] *= f;
+        }
         bool careful = false;
         if (odd) { // what is NaN as it is needs no care: a step that overflowed is NaN nearly everywhere
             for (int i = 0; i < 16; ++i)
@@ -759,18 +759,28 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
                 }
             }
         }
+        // in half precision apart from o, so no power of two of one has to fit the other
+        float16v seen = kLifts<T> ? zero16() : o;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             FragV<T> sf[FEW];
-            split_half<T, FEW>(s, half, 1.0f, sf, odd_scores);
+            split_half<T, FEW>(s, half, score_lift, sf, odd_scores);
 #pragma unroll
             for (int n = 0; n < FEW; ++n)
-                o = mma(fine[half], sf[n], o); // settled with the state
+                seen = mma(fine[half], sf[n], seen); // settled with the state
         }
 
         // the state behind the run
         decay(m, n < C ? g[n] : step.at(k));
         add_outer<T, TileT>(m, yt, Taken<T, PARTS>(zf, Factors(factors, h), odd || log_decay > 0.0f), lane);
+        if constexpr (kLifts<T>) {
+            const float back = inverse_lift(score_lift);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[i] = fmaf(seen[i], back, o[i]);
+        } else {
+            o = seen;
+        }
     }
 
     if (works && runs > 0)

@@ -43,3 +43,65 @@ def test_outputs_are_rounded_once(L, b, s, h, kv, d, e, state, ragged, dtype):  
     dq, dk, dv, _, _ = L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more)
     for name, got in (("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
         passes(got, r[name], once(r[name], size[name], dtype), name)
+
+
+def alone(b, s, h, d, e, at, size, dtype=F16):
+    """Tokens of `size` in one component."""
+    t = torch.zeros(b, s, h, e if e else d, device="cuda")
+    t[..., at] = size
+    return t.to(dtype)
+
+
+@pytest.mark.parametrize("s", [2, 40, 700])
+@pytest.mark.parametrize("state,scale", [(2.0 ** 100, None), (2.0 ** 120, None), (2.0 ** 80, 2.0 ** -30), (2.0 ** 60, 2.0 ** -60)])
+def test_half_beside_a_very_large_state(L, s, state, scale):  # noqa: F811
+    """A state's large entry that no token sees leaves what they do see as it is, forward and backward."""
+    d = 32
+    q, v = (normal(gen(i), 1, s, 2, d, dtype=F16) * 2.0 ** -6 for i in (1, 2))
+    k = normal(gen(3), 1, s, 2, d, dtype=F16) * 2.0 ** -6
+    for t in (q, k):
+        t[..., 0] = 0
+    first = torch.zeros(1, 2, d, d, device="cuda")
+    first[:, :, 0, 0] = state
+    log = torch.tensor([-0.01, 0.0], device="cuda")
+    x = {"q": q, "k": k, "v": v, "log_decay": log}
+    more = {"state": first, "lengths": None, "scale": scale}
+    grads = {"dout": normal(gen(4), 1, s, 2, d, dtype=F16) * 2.0 ** -6, "dstate": torch.zeros_like(first)}
+    grads["dout"][..., 0] = 0
+    grads["dstate"][:, :, 0, 0] = state
+    v[..., 0] = 0
+    r, size = both(x, more, grads)
+    out, last = L.linear_attention_forward(**x, **more)
+    passes(out, r["out"], once(r["out"], size["out"], F16), "out")
+    # the large entry stays beside what the tokens add
+    passes(last, r["last"], R.F32 * size["last"], "state")
+    dq, dk, dv, _, _ = L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more)
+    for name, got in (("dq", dq), ("dk", dk), ("dv", dv)):
+        passes(got, r[name], once(r[name], size[name], F16), name)
+
+
+def test_half_tokens_of_one_component_beside_a_very_large_state(L):  # noqa: F811
+    x = {"q": alone(1, 2, 1, 32, 0, 1, 2.0 ** -14), "k": alone(1, 2, 1, 32, 0, 1, 2.0 ** -14),
+         "v": torch.ones(1, 2, 1, 32, dtype=F16, device="cuda"), "log_decay": torch.zeros(1, device="cuda")}
+    state = torch.zeros(1, 1, 32, 32, device="cuda")
+    state[0, 0, 0, 0] = 2.0 ** 100
+    out, last = L.linear_attention_forward(**x, state=state)
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(last).all()) and float(last[0, 0, 0, 0]) == 2.0 ** 100
+
+
+@pytest.mark.parametrize("s", [40, 700])
+def test_half_columns_far_apart_in_size(L, s):  # noqa: F811
+    """One column of v (dout, q, k) twenty-eight powers of two above its neighbours takes none of their bits."""
+    def columns(t):
+        t = t.float() * 2.0 ** -14
+        t[..., 5] *= 2.0 ** 28
+        return t.half()
+
+    x, more, grads = inputs(2, s, 4, 2, 64, 64, F16, False, False, seed=2)
+    x["q"], x["k"] = 4 * x["q"], 4 * x["k"]
+    x["v"], grads["dout"] = columns(x["v"]), columns(grads["dout"])
+    r, size = both(x, more, grads)
+    out, _ = L.linear_attention_forward(**x, **more)
+    passes(out, r["out"], once(r["out"], size["out"], F16), "out")
+    dv = L.linear_attention_backward(grads["dout"], *x.values(), **more)[2]
+    passes(dv, r["dv"], once(r["dv"], size["dv"], F16), "dv")
