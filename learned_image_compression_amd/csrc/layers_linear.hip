@@ -167,7 +167,8 @@ __global__ __launch_bounds__(64) void linear_decay_join(const double *sums, floa
 // start_(k+1) = g^(tokens of k) start_k + what k adds, in place of what the segments add.  A block takes all
 // segments of 1024 / GROUPS numbers of a state, four a thread, in GROUPS groups of up to EACH neighbours.  Each
 // group adds up its own, then what comes from the groups before it, so a thread waits for memory once.  (The
-// powers are formed in 64 bits, by one wave of the block: by all of them they were most of its time.)
+// powers are formed in 64 bits, by one wave of the block: by all of them they were most of its time.  Rounded to 32
+// bits they would be off the same way at every segment: by 5e-6 of the state behind 255 segments of 128 tokens.)
 // Memory bounds it: 16 states of 128 x 128 for each of 16 heads 9 us (33 MB read and written); 32 of 64 x 64 for 32, 10.
 constexpr int kMostSegments = 256;
 
@@ -181,13 +182,28 @@ struct ScanArgs {
     int32_t group;                                            // segments of a group
 };
 
+// g^n in two parts of 32 bits
+struct Power {
+    float whole, rest;
+    static __device__ __forceinline__ Power of(float log_decay, int n)
+    {
+        const double p = n == 0 ? 1.0 : exp((double)log_decay * n);
+        const float whole = (float)p, rest = (float)(p - (double)whole);
+        return {whole, not_finite(rest) ? 0.0f : rest};
+    }
+    __device__ __forceinline__ float times(float v, float add) const
+    {
+        return fmaf(v, whole, fmaf(not_finite(v) ? 0.0f : v, rest, add));
+    }
+};
+
 template <int EACH, int GROUPS>
 __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
 {
     constexpr int ACROSS = 256 / GROUPS;
     using VT = Vec<float, 4>;
     __shared__ VT ends[GROUPS][ACROSS];
-    __shared__ float powers[GROUPS], whole_part[2];
+    __shared__ Power powers[2 + GROUPS]; // of a whole segment, of the last one in use, of each group
     const int64_t id = a.first + blockIdx.x, line = id / a.tiles / a.jobs;
     const int tile = (int)(id % a.tiles), which = (int)(id / a.tiles % a.jobs);
     const LinearJob &p = a.job[which];
@@ -219,47 +235,49 @@ __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
     const int all = a.lengths ? min(max(a.lengths[b], 0), (int)a.tokens) : (int)a.tokens;
     const auto tokens_of = [&](int k) { return min(max(all - index(k) * a.each, 0), a.each); };
     if (t < 64) {
-        const int n = t == 0 ? a.each : all % a.each;
-        const float p = n == 0 ? 1.0f : (float)exp((double)a.log_decay[head] * n);
-        if (t < 2)
-            whole_part[t] = p;
+        int n = t == 0 ? a.each : all % a.each;
+        if (t >= 2) { // a group's, in time
+            const int from = min((t - 2) * a.group, a.segments), to = min(from + a.group, a.segments);
+            n = min(max(all - (p.reverse ? a.segments - to : from) * a.each, 0), (to - from) * a.each);
+        }
+        const Power power = Power::of(a.log_decay[head], n);
+        if (t < 2 + GROUPS)
+            powers[t] = power;
     }
     __syncthreads();
-    const float whole = whole_part[0], part = whole_part[1];
+    const Power whole = powers[0], part = powers[1];
     const auto power = [&](int k) {
         const int n = tokens_of(k);
-        return n == a.each ? whole : n == 0 ? 1.0f : part;
+        return n == a.each ? whole : n == 0 ? Power{1.0f, 0.0f} : part;
     };
     VT sum = run;
-    float all_power = 1.0f;
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
         if (i < a.group && k0 + i < a.segments) {
-            const float g = power(k0 + i);
-            all_power *= g;
+            const Power g = power(k0 + i);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                sum.v[e] = fmaf(sum.v[e], g, add[i].v[e]);
+                sum.v[e] = g.times(sum.v[e], add[i].v[e]);
         }
     ends[group][x] = sum;
-    if (x == 0)
-        powers[group] = all_power;
     __syncthreads();
     if (group > 0) {
         run = ends[0][x];
-        for (int k = 1; k < group; ++k)
+        for (int k = 1; k < group; ++k) {
+            const Power g = powers[2 + k];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                run.v[e] = fmaf(run.v[e], powers[k], ends[k][x].v[e]);
+                run.v[e] = g.times(run.v[e], ends[k][x].v[e]);
+        }
     }
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
         if (i < a.group && k0 + i < a.segments) {
             store_at(starts + (int64_t)index(k0 + i) * a.start_floats, run);
-            const float g = power(k0 + i);
+            const Power g = power(k0 + i);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                run.v[e] = fmaf(run.v[e], g, add[i].v[e]);
+                run.v[e] = g.times(run.v[e], add[i].v[e]);
         }
     if (p.last && k0 < a.segments && k0 + a.group >= a.segments && column < p.dim_z) { // behind the last one
         float *last = p.last + b * p.last_stride[0] + head * p.last_stride[1] + column * p.last_stride[3];

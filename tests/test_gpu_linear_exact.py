@@ -105,3 +105,40 @@ def test_half_columns_far_apart_in_size(L, s):  # noqa: F811
     passes(out, r["out"], once(r["out"], size["out"], F16), "out")
     dv = L.linear_attention_backward(grads["dout"], *x.values(), **more)[2]
     passes(dv, r["dv"], once(r["dv"], size["dv"], F16), "dv")
+
+
+def plain_state(k, v, log_decay, lengths=None):
+    """sum over tokens of g^(n - 1 - j) k_j v_j' in 64 bits, of one kv head a head, and of absolute values."""
+    b, s, h, _ = k.shape
+    n = torch.full((b,), s, device="cuda") if lengths is None else lengths.long()
+    steps = n[:, None] - 1 - torch.arange(s, device="cuda")  # [B, S]
+    w = torch.exp(steps.clamp(min=0)[:, None].double() * log_decay.double()[None, :, None]) * (steps >= 0)[:, None]
+    kd, vd = (t.double().permute(0, 2, 1, 3) for t in (k, v))
+    return ((kd * w[..., None]).transpose(2, 3).contiguous() @ vd.contiguous(),
+            (kd.abs() * w[..., None]).transpose(2, 3).contiguous() @ vd.abs().contiguous())
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("s,lengths", [(32640, None), (16400, (16400, 9001)), (5000, (4999, 37)), (2500, None)])
+def test_long_memories_do_not_drift(L, s, lengths, dtype):  # noqa: F811
+    """States of values of one sign, with memories of a thousand to a million positions, over up to 255 segments: the
+    powers that carry a state on are off by no common part."""
+    h, d, b = 4, 16, 1 if lengths is None else 2
+    g = gen(s)
+    q, k, v, dout = (normal(g, b, s, h, d).abs().to(dtype) for _ in range(4))
+    log = torch.log1p(-torch.tensor([1e-3, 1e-4, 1.3e-5, 1e-6], device="cuda"))
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    state, dstate = (normal(g, b, h, d, d).abs() * 100 for _ in range(2))
+    stay = torch.exp((torch.full((b,), s, device="cuda") if n is None else n)[:, None].double() * log.double())[:, :, None, None]
+    _, last = L.linear_attention_forward(q, k, v, log, state=state, lengths=n)
+    want, size = plain_state(k, v, log, n)
+    passes(last, want + stay * state.double(), SUMS * (size + stay * state.double()), "state")
+    first = L.linear_attention_backward(dout, q, k, v, log, state=state, dstate=dstate, lengths=n)[4]
+    # the gradient of the first state: sum over tokens of g^(i + 1) scale q_i dout_i', the same read from behind
+    i = torch.arange(s, device="cuda")
+    w = torch.exp((i + 1)[None, None].double() * log.double()[None, :, None]) * d ** -0.5
+    if n is not None:
+        w = w * (i < n[:, None].long())[:, None]
+    qd, gd = (t.double().permute(0, 2, 1, 3).contiguous() for t in (q, dout))
+    want = (qd * w[..., None]).transpose(2, 3).contiguous() @ gd + stay * dstate.double()
+    passes(first, want, SUMS * want, "dstate")
