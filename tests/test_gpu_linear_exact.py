@@ -142,3 +142,21 @@ def test_long_memories_do_not_drift(L, s, lengths, dtype):  # noqa: F811
     qd, gd = (t.double().permute(0, 2, 1, 3).contiguous() for t in (q, dout))
     want = (qd * w[..., None]).transpose(2, 3).contiguous() @ gd + stay * dstate.double()
     passes(first, want, SUMS * want, "dstate")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_steps_do_not_drift(L, dtype):  # noqa: F811
+    """A state that a decoder carries through thousands of single tokens, values of one sign."""
+    s, h, d = 3000, 16, 8
+    g = gen(5)
+    q, k, v = (normal(g, 1, s, h, d).abs().to(dtype) for _ in range(3))
+    log = torch.log1p(-torch.logspace(-5, -2, h, device="cuda"))
+    state = torch.zeros(1, h, d, d, device="cuda")
+    outs = [L.linear_attention_forward(q[:, i:i + 1], k[:, i:i + 1], v[:, i:i + 1], log, state=state, state_out=state)[0]
+            for i in range(s)]
+    want, size = plain_state(k, v, log)
+    # two roundings a step, of no common sign: four times the root of their number
+    bound = SUMS + 4 * (2 * s) ** 0.5 * 2.0 ** -24
+    passes(state, want, bound * size, "state")
+    out = (q[:, -1].double()[:, :, None] @ want)[:, :, 0] * d ** -0.5
+    passes(outs[-1][:, 0], out, (R.UNIT[dtype] + bound) * out, "out")
