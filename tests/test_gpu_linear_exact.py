@@ -160,3 +160,56 @@ def test_many_steps_do_not_drift(L, dtype):  # noqa: F811
     passes(state, want, bound * size, "state")
     out = (q[:, -1].double()[:, :, None] @ want)[:, :, 0] * d ** -0.5
     passes(outs[-1][:, 0], out, (R.UNIT[dtype] + bound) * out, "out")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("signs", ["both", "one"])
+@pytest.mark.parametrize("s,d,e", [(2, 1, 1), (3, 2, 1), (5, 1, 2), (33, 1, 1), (40, 8, 8), (70, 3, 40), (300, 64, 64), (130, 128, 96)])
+def test_states_and_the_decays_gradient_keep_32_bits(L, s, d, e, signs, dtype):  # noqa: F811
+    """What leaves a call in 32 bits, where few terms make it up (so errors of the terms do not average out), many heads
+    of them, and values of one sign.  Operands in two parts of bfloat16 are off by up to 2^-17 of a term, eight bounds."""
+    h = 64 if d < 64 else 4
+    x, more, grads = inputs(1, s, h, h, d, e, dtype, True, False, seed=3)
+    if signs == "one":
+        x, more, grads = ({n: t.abs() if isinstance(t, torch.Tensor) and n != "log_decay" else t for n, t in part.items()}
+                          for part in (x, more, grads))
+    for given in (True, False):
+        if not given:  # from nothing: the tokens' terms alone
+            more, grads = {**more, "state": None}, {**grads, "dstate": None}
+        r, size = both(x, more, grads)
+        _, last = L.linear_attention_forward(**x, **more)
+        _, _, _, dlog, first = L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more)
+        passes(last, r["last"], SUMS * size["last"], "state")
+        passes(dlog, r["dlog"], SUMS * size["dlog"], "dlog_decay")
+        if given:
+            passes(first, r["dstate"], SUMS * size["dstate"], "dstate")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("b,s,h,kv,lengths", [(1, 8301, 2, 1, None), (2, 4500, 1, 1, (4133, 4500)), (2, 16390, 1, 1, (5000, 11))])
+def test_gradients_over_many_segments(L, b, s, h, kv, lengths, dtype):  # noqa: F811
+    """More than 64 segments (of 64 and 96 tokens), lengths that end inside one in the middle, state and dstate."""
+    d, e = 24, 16
+    x, more, grads = inputs(b, s, h, kv, d, e, dtype, True, False, seed=4)
+    x["log_decay"] = torch.log1p(-torch.tensor([2e-4, 0.03], device="cuda"))[:h]
+    if lengths is not None:
+        more["lengths"] = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    r, size = both(x, more, grads)
+    out, last = L.linear_attention_forward(**x, **more)
+    dq, dk, dv, dlog, first = L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more)
+    for name, got in (("out", out), ("dq", dq), ("dk", dk), ("dv", dv)):
+        passes(got, r[name], once(r[name], size[name], dtype), name)
+    for name, got in (("last", last), ("dlog", dlog), ("dstate", first)):
+        passes(got, r[name], SUMS * size[name], name)
+
+
+@pytest.mark.parametrize("dtype", ALL)
+def test_decays_gradient_counts_every_step(L, dtype):  # noqa: F811
+    """Ten thousand positions with no decay at all: each pair counts as often as there are positions between."""
+    s, d = 10_000, 16
+    g = gen(3)
+    q, k, v, dout = (normal(g, 1, s, 1, d, dtype=dtype) for _ in range(4))
+    log = torch.zeros(1, device="cuda")
+    r, size = both({"q": q, "k": k, "v": v, "log_decay": log}, {"state": None, "lengths": None}, {"dout": dout, "dstate": None})
+    got = L.linear_attention_backward(dout, q, k, v, log)[3]
+    passes(got, r["dlog"], SUMS * size["dlog"], "dlog_decay")
