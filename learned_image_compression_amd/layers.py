@@ -183,17 +183,70 @@ def _written(tensors):
     torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
 
 
-def _in_place(out, name, inputs):
-    """An output may be an input entry by entry: not one that begins at the same address and lies
-    otherwise."""
-    if out is None or out.numel() == 0:
+def _runs(t):
+    """Where a tensor's values lie: the bytes of its runs without gaps, and the (stride, count) of their
+    repetitions, widest first, in bytes."""
+    run, dims = t.element_size(), []
+    for stride, n in sorted((st * t.element_size(), n) for st, n in zip(t.stride(), t.shape) if n > 1 and st > 0):
+        if dims and stride == dims[0][0] * dims[0][1]:
+            dims[0] = (dims[0][0], dims[0][1] * n)
+        elif not dims and stride == run:
+            run *= n
+        else:
+            dims.insert(0, (stride, n))
+    return run, dims
+
+
+_MANY = 64
+
+
+def _meet(apart, run, dims, other_run, other_dims) -> bool:
+    """Whether runs and others that begin ``apart`` bytes behind them have a byte in common.  Where that would
+    take more than some comparisons (strides that are no multiples of each other), they count as if they had."""
+    end = run + sum(stride * (n - 1) for stride, n in dims)
+    other_end = other_run + sum(stride * (n - 1) for stride, n in other_dims)
+    if apart >= end or apart + other_end <= 0:
+        return False
+    if not dims and not other_dims:
+        return True
+    stride, n = dims[0] if dims else (0, 1)
+    other, m = other_dims[0] if other_dims else (0, 1)
+    # the repetitions of the wider stride, of both where it is the same: only their difference counts
+    wide, first, last = max(stride, other), 0, 0
+    if stride == wide:
+        dims, last, end = dims[1:], n - 1, end - stride * (n - 1)
+    if other == wide:
+        other_dims, first, other_end = other_dims[1:], 1 - m, other_end - other * (m - 1)
+    first, last = max(first, (apart - end) // wide + 1), min(last, -((-apart - other_end) // wide) - 1)
+    return last - first >= _MANY or any(_meet(apart - i * wide, run, dims, other_run, other_dims)
+                                        for i in range(first, last + 1))
+
+
+def _overlapping(out, tensors):
+    """Those that have memory in common with ``out``."""
+    at, found = out.data_ptr(), []
+    end = at + out.untyped_storage().nbytes()
+    for t in tensors:
+        if t is not None:
+            begin = t.data_ptr()
+            # a look at the storages first, which is quick
+            if begin < end and at < begin + t.untyped_storage().nbytes() and t.numel() and out.numel() and \
+                    _meet(begin - at, *_runs(out), *_runs(t)):
+                found.append(t)
+    return found
+
+
+def _in_place(out, name, inputs, others=()):
+    """An output may be one of ``inputs`` entry by entry: not overlap one that is shifted or lies otherwise, and
+    none of ``others``."""
+    if out is None:
         return
-    at = out.data_ptr()
-    for t in inputs:
-        if t is not None and t.data_ptr() == at and \
-                (t.dtype is not out.dtype or any(n > 1 and a != b for n, a, b in
-                                                 zip(out.shape, out.stride(), t.stride()))):
-            raise ValueError(f"{name} overlaps an input and is laid out differently")
+    for t in _overlapping(out, [t for t in inputs if t is not out]):
+        if t.data_ptr() != out.data_ptr() or t.dtype is not out.dtype or \
+                any(n > 1 and a != b for n, a, b in zip(out.shape, out.stride(), t.stride())):
+            raise ValueError(f"{name} overlaps an input and is laid out differently, or shifted")
+    if _overlapping(out, others):
+        raise ValueError(f"{name} overlaps what it must not be")
 
 
 _NO_WORKSPACE = (None, 0, None)  # address, bytes, owner
@@ -502,7 +555,7 @@ def _rms_forward(x, weight, residual, eps, code, y, stat, rstd, sum_out, device,
         else:
             _out_like(sum_out, x, x.dtype, device, "sum_out")
             h = sum_out
-        if h.data_ptr() == y.data_ptr() and h.numel():
+        if sum_out is not None and _overlapping(h, (y,)):
             raise ValueError("out and sum_out must not be one place")
     elif sum_out is not None:
         raise ValueError("sum_out is for calls with a residual")
@@ -538,7 +591,8 @@ def rms_norm_forward(x: torch.Tensor, weight=None, *, residual=None, eps: float 
     the first) evenly spaced, for example tokens [N, S, C] cut out of a wider tensor; ``residual`` is
     like it.  ``h`` is rounded to x's type before the norm (without a residual it is ``x``
     itself), ``y = weight * h * rstd`` and ``rstd = 1 / sqrt(mean(h^2) + eps)``, float32 [...].
-    ``out`` and ``sum_out`` are places for y and h, and each may be x or residual.
+    ``out`` and ``sum_out`` are places for y and h, and each may be x or residual, but not overlap
+    them otherwise.
     """
     device, kind = _rms_params(x, "x", weight, eps)
     given = (out, sum_out)
@@ -548,8 +602,8 @@ def rms_norm_forward(x: torch.Tensor, weight=None, *, residual=None, eps: float 
         _out_like(out, x, x.dtype, device, "out")
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
     if given[0] is not None or given[1] is not None:
-        _in_place(given[0], "out", (x, residual))
-        _in_place(given[1], "sum_out", (x, residual))
+        _in_place(given[0], "out", (x, residual), (weight,))
+        _in_place(given[1], "sum_out", (x, residual), (weight,))
         _written(given)
     h = _rms_forward(x, weight, residual, eps, 0, out, None, rstd, sum_out, device, kind)
     return out, h, rstd
@@ -577,8 +631,8 @@ def rms_norm_8bit(x: torch.Tensor, weight=None, *, residual=None, eps: float = 1
         _out_like(out, x, dtype, device, "out")
     scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
     if given[0] is not None or given[1] is not None:
-        _in_place(given[0], "out", (x, residual))
-        _in_place(given[1], "sum_out", (x, residual))
+        _in_place(given[0], "out", (x, residual), (weight,))
+        _in_place(given[1], "sum_out", (x, residual), (weight,))
         _written(given)
     h = _rms_forward(x, weight, residual, eps, code, out, scales, None, sum_out, device, kind)
     return out, scales, h
@@ -604,7 +658,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
         out = _dense_like(h)
     else:
         _out_like(out, h, h.dtype, device, "out")
-        _in_place(out, "out", (dy, dsum, h))
+        _in_place(out, "out", (dy, dsum, h), (weight, rstd))
         _written((out,))
     c = h.shape[-1]
     dweight = torch.empty(c, dtype=kind, device=device)
@@ -1055,25 +1109,25 @@ def linear_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     kv_heads divides heads), ``log_decay`` float32 [heads], ``out`` [B, S, heads, value_dim].
     ``state`` and ``state_out``, [B, heads, dim, value_dim], are S before the first token (None:
     zeros) and behind the last; a decoder that steps passes one tensor as both.  ``out`` must not
-    overlap an input, ``state_out`` none but ``state``.  ``lengths``
+    overlap an input or ``state_out``, nor that one any input but ``state`` as a whole.  ``lengths``
     (int32 [B]) are the tokens in use: rows behind them are not read, their out is 0, and the
     state is that behind the last one in use.
     """
     device, strides, (state_ptr, ss), length_ptr, shape, sizes = \
         _linear_common(q, k, v, log_decay, state, lengths, scale)
-    out_shape = (*q.shape[:3], shape[3])
+    out_shape, given = (*q.shape[:3], shape[3]), out
     if out is None:
         out = torch.empty(out_shape, dtype=q.dtype, device=device)
     else:
         _out_of(out, out_shape, q.dtype, device, "out")
-        if out.numel() and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+        if _overlapping(out, (q, k, v, log_decay, state, lengths)):
             raise ValueError("out must not be an input")
         _written((out,))
     if state_out is None:
         state_out = torch.empty(shape, dtype=torch.float32, device=device)
     else:
         _out_of(state_out, shape, torch.float32, device, "state_out")
-        _in_place(state_out, "state_out", (state,))
+        _in_place(state_out, "state_out", (state,), (q, k, v, log_decay, lengths, given))
         _written((state_out,))
     last_ptr, ls = _state(state_out, shape, device, "state_out")
     args = _LINEAR.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state_ptr, length_ptr,
