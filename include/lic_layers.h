@@ -297,7 +297,7 @@ int lic_linear_attention_backward(const lic_linear_attention_args *args, void *w
  * (which may be x) are device memory of n values next to each other, each of its own
  * type.  Outputs must not overlap each other, nor an x but their own.  norm is one float on
  * the device.  Squares are summed and the factor is formed in 64 bits, so no size of the values
- * overflows (a norm past 32 bits' range is written as infinity).  An infinity
+ * overflows or leaves the factor without its bits (a norm past 32 bits' range is written as infinity).  An infinity
  * among the values makes the factor 0 (and itself NaN), a NaN makes all outputs NaN.
  * lic_gradient_norm leaves `out` alone (it may be null). */
 typedef struct lic_gradient {

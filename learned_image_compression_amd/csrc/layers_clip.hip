@@ -111,14 +111,14 @@ __device__ __forceinline__ double squares(const T *x, int64_t n)
 }
 
 template <typename T>
-__device__ __forceinline__ void scaled(const T *x, T *out, int64_t n, float c, bool past)
+__device__ __forceinline__ void scaled(const T *x, T *out, int64_t n, float before, float c, bool past)
 {
     constexpr int V = 16 / sizeof(T), EACH = (int)(kChunkBytes / 16 / kClipThreads);
     using VT = Vec<T, V>;
     const auto times = [&](VT v) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            v.v[i] = down_apart<T>(up(v.v[i]) * c);
+            v.v[i] = down_apart<T>(up(v.v[i]) * before * c);
         return v;
     };
     const int t = (int)threadIdx.x;
@@ -136,7 +136,7 @@ __device__ __forceinline__ void scaled(const T *x, T *out, int64_t n, float c, b
     for (int u = t; u < whole; u += kClipThreads)
         store_at(out + u * V, times(load_at<VT>(x + u * V)), past);
     if (t < (int)n - whole * V)
-        out[whole * V + t] = down_apart<T>(up(x[whole * V + t]) * c);
+        out[whole * V + t] = down_apart<T>(up(x[whole * V + t]) * before * c);
 }
 
 // the sum over the block, the same for all of its threads
@@ -187,19 +187,22 @@ __global__ __launch_bounds__(kClipThreads) void clip_norm(ClipArgs a) { total_no
 __global__ __launch_bounds__(kClipThreads) void clip_scale(ClipList l, ClipArgs a)
 {
     const double part = a.max_norm / (total_norm(a) + 1e-6);
-    const float c = part >= 1.0 ? 1.0f : (float)part; // NaN stays
+    // a factor that 32 bits hold in a few bits or not at all takes its power of two first
+    const float before = part < 0x1p-64 ? 0x1p-64f : 1.0f;
+    const float c = part >= 1.0 ? 1.0f : (float)(part / (double)before); // NaN stays
     each_chunk<true>(l, [&](int t, int type, int64_t at, int64_t end) {
         if (c == 1.0f && l.x[t] == l.out[t])
             return;
         switch (type) {
         case LIC_F32:
-            scaled(static_cast<const float *>(l.x[t]) + at, static_cast<float *>(l.out[t]) + at, end - at, c, a.past);
+            scaled(static_cast<const float *>(l.x[t]) + at, static_cast<float *>(l.out[t]) + at, end - at, before, c,
+                   a.past);
             break;
         case LIC_F16:
-            scaled(static_cast<const f16 *>(l.x[t]) + at, static_cast<f16 *>(l.out[t]) + at, end - at, c, a.past);
+            scaled(static_cast<const f16 *>(l.x[t]) + at, static_cast<f16 *>(l.out[t]) + at, end - at, before, c, a.past);
             break;
         default:
-            scaled(static_cast<const bf16 *>(l.x[t]) + at, static_cast<bf16 *>(l.out[t]) + at, end - at, c, a.past);
+            scaled(static_cast<const bf16 *>(l.x[t]) + at, static_cast<bf16 *>(l.out[t]) + at, end - at, before, c, a.past);
             break;
         }
     });
