@@ -251,9 +251,9 @@ int lic_attention_backward(const lic_attention_args *args, void *workspace,
  * a state) goes into a product as parts of q's type that add up to it: off by 2^-17 in
  * bfloat16 and 2^-22 in half precision in what forms outputs and gradients of q's type,
  * which are rounded once at the end, and by less in states that leave the call.  In half
- * precision a power of two lifts each column of a state, and each token's scores, so this holds
- * for values of any size that are not below 2^-16 of the largest beside them (the smaller are
- * off by 2^-38 of that).  Products of 32-bit inputs are in 32 bits.
+ * precision a power of two lifts each column of a state (of what it takes in), and each token's
+ * scores, so this holds for values of any size that are not below 2^-16 of the largest beside them
+ * (the smaller are off by 2^-38 of that).  Products of 32-bit inputs are in 32 bits.
  *
  * The backward call takes what the forward call took, dout, and dstate, the gradient
  * that comes to state_out (null: 0).  dlog_decay (float [heads], summed over the batch)

@@ -282,10 +282,13 @@ __device__ __forceinline__ float tile_value(const uint8_t *lds, int row, int d)
 struct Powers {
     float *at;
     __device__ __forceinline__ float operator[](int n) const { return at[n]; }
+    // (the exponent's rounding would be off by as much of a power as the exponent is of 2^24)
     __device__ __forceinline__ void fill(float log_decay, int n, int t, int threads)
     {
-        for (int e = t; e <= n; e += threads)
-            at[e] = e == 0 ? 1.0f : expf(log_decay * (float)e);
+        for (int e = t; e <= n; e += threads) {
+            const float x = log_decay * (float)e, g = expf(x), rest = fmaf(log_decay, (float)e, -x);
+            at[e] = e == 0 ? 1.0f : not_finite(x) ? g : fmaf(g, rest, g);
+        }
     }
 };
 

@@ -213,3 +213,26 @@ def test_decays_gradient_counts_every_step(L, dtype):  # noqa: F811
     r, size = both({"q": q, "k": k, "v": v, "log_decay": log}, {"state": None, "lengths": None}, {"dout": dout, "dstate": None})
     got = L.linear_attention_backward(dout, q, k, v, log)[3]
     passes(got, r["dlog"], SUMS * size["dlog"], "dlog_decay")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("s", [20, 32])
+def test_powers_of_strong_decays(L, s, dtype):  # noqa: F811
+    """One token far back is all there is: its power of g has 32 bits however small it is."""
+    h, d = 64, 8
+    x, more, grads = inputs(1, s, h, h, d, d, dtype, False, False, seed=6)
+    x["log_decay"] = -torch.linspace(0.1, 2.6, h, device="cuda")
+    x["k"][:, 1:], grads["dout"][:, :-1] = 0, 0
+    r, size = both(x, more, grads)
+    _, last = L.linear_attention_forward(**x, **more)
+    _, _, _, dlog, _ = L.linear_attention_backward(grads["dout"], *x.values(), **more)
+    bound = SUMS * size["last"] + 2.0 ** -126
+    if dtype == F16:
+        # What a state takes in is lifted by a power of two for each column of a run, so that the largest v g^(n-1-j) of
+        # the column's tokens is at least 2^13; its two parts end at float16's last step, 2^-24, so each value
+        # is off by 2^-25 of at least 2^13 of the largest: 2^-38 of it, times k.
+        steps = torch.arange(s - 1, -1, -1, device="cuda")[:, None, None]
+        largest = (x["v"][0].double().abs() * torch.exp(steps * x["log_decay"].double()[:, None])).amax(0)  # [heads, columns]
+        bound = bound + 2.0 ** -38 * x["k"][0, 0].double().abs()[:, :, None] * largest[:, None, :]
+    passes(last, r["last"], bound, "state")
+    passes(dlog, r["dlog"], SUMS * size["dlog"] + 2.0 ** -126, "dlog_decay")
