@@ -236,3 +236,27 @@ def test_powers_of_strong_decays(L, s, dtype):  # noqa: F811
         bound = bound + 2.0 ** -38 * x["k"][0, 0].double().abs()[:, :, None] * largest[:, None, :]
     passes(last, r["last"], bound, "state")
     passes(dlog, r["dlog"], SUMS * size["dlog"] + 2.0 ** -126, "dlog_decay")
+
+
+@pytest.mark.parametrize("dtype", ALL)
+@pytest.mark.parametrize("s", [1, 2, 40, 700])
+def test_an_infinity_of_the_state_stays_one(L, s, dtype):  # noqa: F811
+    """Nothing of it is NaN (a number less itself), and other columns keep their bits."""
+    x, more, grads = inputs(1, s, 2, 2, 32, 32, dtype, True, False, seed=7)
+    x["log_decay"] = torch.tensor([-0.01, -0.02], device="cuda")
+    for n in "qk":
+        x[n][..., 1] = x[n][..., 1].abs() + 0.125
+    clean = L.linear_attention_forward(**x, **more)
+    back = L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more)
+    for t in (more["state"], grads["dstate"]):
+        t[0, 0, 1, 3] = float("inf")
+    out, last = L.linear_attention_forward(**x, **more)
+    _, _, dv, _, first = L.linear_attention_backward(grads["dout"], *x.values(), dstate=grads["dstate"], **more)
+    for got, want in ((out, clean[0]), (dv, back[2])):
+        assert bool((got[0, :, 0, 3] == float("inf")).all())
+        rest = torch.arange(32, device="cuda") != 3
+        assert torch.equal(got[..., rest], want[..., rest]) and torch.equal(got[:, :, 1], want[:, :, 1])
+    for got, want in ((last, clean[1]), (first, back[4])):
+        assert float(got[0, 0, 1, 3]) == float("inf")
+        got[0, 0, 1, 3] = want[0, 0, 1, 3]
+        assert torch.equal(got, want)
