@@ -186,19 +186,21 @@ struct ScanArgs {
     int32_t group;                                            // segments of a group
 };
 
-// g^n in two parts of 32 bits
+// g^n in two parts of 32 bits, the second above 0 where the first is, so an infinity times both is one.
 struct Power {
     float whole, rest;
     static __device__ __forceinline__ Power of(float log_decay, int n)
     {
         const double p = n == 0 ? 1.0 : exp((double)log_decay * n);
-        const float whole = (float)p, rest = (float)(p - (double)whole);
-        return {whole, not_finite(rest) ? 0.0f : rest};
+        float whole = (float)p;
+        if (!(whole > 0.0f) || not_finite(whole)) // 0, NaN, infinity
+            return {whole, whole};
+        whole = (double)whole < p ? whole : __uint_as_float(__float_as_uint(whole) - 1);
+        return {whole, (float)(p - (double)whole)};
     }
-    __device__ __forceinline__ float times(float v, float add) const
-    {
-        return fmaf(v, whole, fmaf(not_finite(v) ? 0.0f : v, rest, add));
-    }
+    static __device__ __forceinline__ Power one() { return {1.0f - 0x1p-24f, 0x1p-24f}; }
+    // v g^n + add
+    __device__ __forceinline__ float times(float v, float add) const { return fmaf(v, whole, fmaf(v, rest, add)); }
 };
 
 template <int EACH, int GROUPS>
@@ -252,7 +254,7 @@ __global__ __launch_bounds__(256) void linear_scan(ScanArgs a)
     const Power whole = powers[0], part = powers[1];
     const auto power = [&](int k) {
         const int n = tokens_of(k);
-        return n == a.each ? whole : n == 0 ? Power{1.0f, 0.0f} : part;
+        return n == a.each ? whole : n == 0 ? Power::one() : part;
     };
     VT sum = run;
 #pragma unroll
