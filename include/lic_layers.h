@@ -249,7 +249,7 @@ int lic_attention_backward(const lic_attention_args *args, void *workspace,
  * row of their own.  Sums and states are held in 32 bits, and a state that leaves the call has
  * that precision.  16-bit types: an operand that is no input (a power of g times one, a score,
  * a state) goes into a product as parts of q's type that add up to it: off by 2^-17 in
- * bfloat16 and 2^-22 in half precision in what forms outputs and gradients of q's type,
+ * bfloat16 and 2^-23 in half precision in what forms outputs and gradients of q's type,
  * which are rounded once at the end, and by less in states that leave the call.  In half
  * precision a power of two lifts each column of a state (of what it takes in), and each token's
  * scores, so this holds for values of any size that are not below 2^-16 of the largest beside them

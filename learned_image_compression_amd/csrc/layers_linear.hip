@@ -10,8 +10,8 @@ namespace {
 // S' = g S + k v',  out = scale q S'.  The state's way through memory bounds it: a block takes a head's
 // state, a thread four of its columns (one where value_dim does not divide) of every R-th row; out is added
 // up over the R threads of a column in LDS, in their order.  A long memory's g is 1 + expm1f(log g) in two parts: its
-// rounding to 32 bits would be the same at every step, 3e-5 of the state after a thousand of them.  16 x 16 heads of 64 on 4, bfloat16: 6.0 us (8.4 MB
-// of states).
+// rounding to 32 bits would be the same at every step, up to 3e-5 of the state after a thousand of them.  16 x 16 heads of
+// 64 on 4, bfloat16: 6.1 us (8.4 MB of states).
 constexpr int kStepThreads = 256;
 
 struct StepArgs {
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(64) void linear_decay_join(const double *sums, floa
 // group adds up its own, then what comes from the groups before it, so a thread waits for memory once.  (The
 // powers are formed in 64 bits, by one wave of the block: by all of them they were most of its time.  Rounded to 32
 // bits they would be off the same way at every segment: by 5e-6 of the state behind 255 segments of 128 tokens.)
-// Memory bounds it: 16 states of 128 x 128 for each of 16 heads 9 us (33 MB read and written); 32 of 64 x 64 for 32, 10.
+// Memory bounds it: 16 states of 128 x 128 for each of 16 heads 10 us (33 MB read and written); 32 of 64 x 64 for 32, 10.
 constexpr int kMostSegments = 256;
 
 struct ScanArgs {
@@ -352,10 +352,9 @@ uint64_t round256(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // How the tokens are split: into as many segments as make four blocks a CU, each of at least 64 tokens.  A state's way
 // through scratch memory (written, scanned, read) is as long as that of 4 * dim tokens' rows, so heads wider than
-// 64 take one block a CU.  Measured (us, all kernels as they were, with 256 / 512 / 1024 / 1536 blocks): forward, bfloat16, 2 x
-// 16 heads of 64, 8160 tokens 97 / 68 / 53 / 65; 6 heads of 32, 32640 tokens 64 / 44 / 39 / 41; trained, 16 heads of
-// 128, 8160 tokens 343 / 357 / 480 / 620; float, 4 x 6 heads of 32, 510 tokens in segments of 510 / 128 / 64 / 32: 200 /
-// 120 / 64 / 68.
+// 64 take one block a CU.  Measured (us, with 256 / 512 / 1024 / 1536 blocks): forward, bfloat16, 2 x 16 heads of 64, 8160
+// tokens 117 / 81 / 62 / 75; 6 heads of 32, 32640 tokens 81 / 52 / 41 / 42; trained, 16 heads of 128, 8160 tokens 409 / 439 /
+// 532 / 607; float, 4 x 6 heads of 32, 510 tokens in segments of 510 / 128 / 64 / 32: 200 / 120 / 64 / 68.
 struct Split {
     int32_t segments, each;
     explicit Split(const lic_linear_attention_args &p)
@@ -392,6 +391,9 @@ struct Layout {
     }
 };
 
+// Whether rows may be fetched 16 bytes at a time.  One tensor that may not be sends all of a call through loads of a value,
+// at about three times the time (bfloat16, 2 x 16 heads of 64, 8160 tokens: 58 us, 190 with v 2 bytes off, 241 with
+// value_dim 65).
 template <typename T>
 bool vector_rows(const lic_linear_attention_args &p, const void *x, const int64_t *stride, int64_t heads)
 {

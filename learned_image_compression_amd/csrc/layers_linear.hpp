@@ -68,14 +68,14 @@ struct Segment {
     }
 };
 
-// Operands of T whose sum is a 32-bit fragment: three of bfloat16 (off by 2^-27 of it; two are by 2^-18, five
-// times what 32-bit sums lose), two of float16 (2^-22).  float is its own operand.
+// Operands of T whose sum is a 32-bit fragment: three of bfloat16 hold its 24 bits (two are off by up to 2^-17 of it,
+// eight times what 32-bit sums are allowed here), two of float16 are off by up to 2^-23.  float is its own operand.
 template <typename T>
 constexpr int kParts = std::is_same<T, float>::value ? 1 : std::is_same<T, f16>::value ? 2 : 3;
 // For what only outputs of T see: the scores and the state on their way into the products that form them, and a
-// state that does not leave the call.  Two parts of bfloat16 are off by 2^-17, a 512th of what the output's own
-// rounding may be (one was as much again: errors of 0.0023 of an output where its rounding alone makes 0.0017; 8160
-// tokens of 2 x 16 heads of 64 take 58 us instead of 51).
+// state that does not leave the call.  Two parts of bfloat16 are off by up to 2^-17, a 512th of what the output's own
+// rounding may be.  (One alone made errors of 0.0023 of an output where its rounding makes 0.0017: 8160 tokens of 2
+// x 16 heads of 64 51 us with one, 58 with two, 63 with three; 8160 trained by 16 heads of 128 370, 410 and 464.)
 template <typename T>
 constexpr int kFewParts = std::is_same<T, float>::value ? 1 : 2;
 
@@ -547,11 +547,12 @@ __device__ __forceinline__ float *start_of(const LinearArgs &a, const LinearJob 
 
 // ---- outputs -------------------------------------------------------------------
 //
-// Latency bounds a run: its tiles arrive in LDS while the run before is computed, and two waves a SIMD (three for
-// heads of 32 in 16 bits: 32 x 256 tokens of 6 heads trained 73 us with two, 67 with three; wider heads spill with
-// three, 16 heads of 128 forward 46 us and 68) fill each other's waits.  Measured, bfloat16: 16 heads of 128 on 4, 8160
-// tokens: out 46 us, dq, dk and dv in one launch 104 (278 MB, 2.7 TB/s); 2 x 16 heads of 64 on 4, 8160 tokens 28 us;
-// 6 heads of 32, 32640 tokens 19.
+// Latency bounds a run: its tiles arrive in LDS while the run before is computed, and where there are blocks enough two
+// waves a SIMD (three for heads of 32 in 16 bits: 32 x 256 tokens of 6 heads trained 72 us with two, 68 with three;
+// wider heads spill with three, 8160 tokens trained by 16 heads of 128 410 us and 502) fill each other's waits; the split
+// into segments leaves few heads of 32 or of 128 one.  Measured, bfloat16: 16 heads of 128 on 4, 8160 tokens: out 66 us, dq, dk
+// and dv in one launch 138 (278 MB, 2.0 TB/s); 2 x 16 heads of 64 on 4, 8160 tokens 35 us; 6 heads of 32, 32640 tokens
+// 20.
 //
 // PARTS of what a state takes in: all of them where the state leaves the call, with the precision of 32-bit sums.
 template <typename T, int DT, bool VEC, int PARTS>
@@ -806,7 +807,7 @@ __global__ __launch_bounds__(2 * DT, sizeof(T) == 2 && DT == 32 ? 3 : 2) void li
 // ---- what segments add to the state ---------------------------------------------
 //
 // M alone, from 0: no scores, no outputs.  Writing the states bounds it as much as its runs do.  Measured, bfloat16: 16
-// heads of 128, 8160 tokens 30 us for one state a segment, 37 for the two gradients; 2 x 16 heads of 64 18 us.
+// heads of 128, 8160 tokens 31 us for one state a segment, 38 for the two gradients; 2 x 16 heads of 64 18 us.
 template <typename T, int DT, bool VEC>
 __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(LinearArgs a)
 {
@@ -883,11 +884,11 @@ __global__ __launch_bounds__(2 * DT, DT <= 64 ? 3 : 2) void linear_states(Linear
 //   the others: <T, U> + <S, V>,  U = scale sum_i g^(i+1) q_i dout_i',  V the same with i + 1 in front
 //   T <- g^C (T + C S) + sum_j (C-1-j) g^(C-1-j) k_j v_j'
 // All of these are sums over tokens of an exact operand and one that is split in parts, so nothing is rounded to
-// 16 bits on its way.  (bfloat16: three parts, as all states that leave a call; two would leave an error of 2e-6 instead of
-// 4e-7 and save a few percent, with heads of 128, whose registers spill a little, 47 of 117 us.)  A segment begins with T = 0 and
+// 16 bits on its way.  (bfloat16: three parts, as all states that leave a call; two would be off by up to 2^-17 of a term
+// and save a few percent, with heads of 128, whose registers spill a little, 45 of 122 us.)  A segment begins with T = 0 and
 // counts the steps within it; <T, dS> at its end, dS the gradient of the state there, counts them for the tokens
 // behind it.  Its products and powers bound it (T and S are twice a state's registers, so two waves a SIMD is all there is): 16
-// heads of 128, 8160 tokens 117 us; 32 x 6 heads of 32, 256 tokens, float16 12.
+// heads of 128, 8160 tokens 122 us; 32 x 6 heads of 32, 256 tokens, float16 11.
 struct DecayArgs {
     const void *q, *k, *v, *dout;
     const float *state, *dstate;   // one segment: the call's

@@ -2,18 +2,17 @@
 the error bounds their tests use (units and the 32-bit share as in `layers_ref`).
 
 Linear attention is a sum of products of inputs with weights that are not negative, so the same
-form of the inputs' absolute values is the sum of the absolute terms: a result is off by its last
-rounding (u times itself), by the rounding of scores and states to operands (u times the absolute
-sum, 16-bit types) and by what 32-bit sums and two-part operands lose (2e-5 of the absolute sum;
-a value in two bfloat16 parts is off by 2^-17 of itself at most, which is 0.8e-5).
+form of the inputs' absolute values is the sum of the absolute terms.  These bounds are wide: a result
+may be off by its last rounding (u times itself), by u times the absolute sum (16-bit types) and by what
+32-bit sums and two-part operands lose (2e-5 of the absolute sum; a value in two bfloat16 parts is off by
+2^-17 of itself at most, which is 0.8e-5).  `test_gpu_linear_exact` holds results to what the arithmetic
+allows, without the second of these.
 """
 from __future__ import annotations
 
 import torch
 
 from layers_ref import F32, STEP, UNIT
-
-SMALL = 1e-6  # of eps, for rows of zeros
 
 
 def rms_norm(x, weight, residual, eps, dy=None, dsum=None):
