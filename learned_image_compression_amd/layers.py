@@ -173,8 +173,11 @@ def _out_of(out, shape, dtype, device, name):
         raise ValueError(f"{name} differs in shape")
     if out.is_contiguous():
         return
-    if any(stride == 0 and size > 1 for stride, size in zip(out.stride(), out.shape)):
-        raise ValueError(f"{name} overlaps itself")
+    end = 1  # of what the narrower strides reach
+    for stride, size in sorted((st, n) for st, n in zip(out.stride(), out.shape) if n > 1):
+        if stride < end:
+            raise ValueError(f"{name} overlaps itself")
+        end += stride * (size - 1)
 
 
 def _written(tensors):

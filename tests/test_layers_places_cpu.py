@@ -120,3 +120,21 @@ def test_linear_attention_places(library, s):
     call(state=ring[:2], state_out=torch.zeros(2, 3, 8, 8))
     call(out=flat[:48 * s].view(2, s, 3, 8), state_out=flat[48 * s:].view(2, 3, 8, 8))
     assert library.calls == 3
+
+
+def test_outputs_that_overlap_themselves(library):
+    """A sliding window's entries are written by several rows, in no order; any other strides are taken."""
+    flat, x = torch.zeros(4096), torch.zeros(6, 16)
+    for out in (flat.as_strided((6, 16), (8, 1)), flat.as_strided((6, 16), (15, 1)), flat.as_strided((6, 16), (0, 1)), flat.unfold(0, 16, 4)[:6]):
+        with pytest.raises(ValueError, match="overlaps itself"):
+            layers.rms_norm_forward(x, out=out)
+    q, state = torch.zeros(2, 1, 3, 8), torch.zeros(2, 3, 8, 8)
+    with pytest.raises(ValueError, match="overlaps itself"):
+        layers.linear_attention_forward(q, q, q, torch.zeros(3), state_out=flat.as_strided((2, 3, 8, 8), (192, 60, 8, 1)))
+    assert library.calls == 0
+    layers.rms_norm_forward(x, out=flat.as_strided((6, 16), (16, 1)))
+    layers.rms_norm_forward(x, out=flat.as_strided((6, 16), (100, 1)))
+    layers.rms_norm_forward(torch.zeros(4, 6, 16), out=flat.as_strided((4, 6, 16), (16, 64, 1)))
+    layers.linear_attention_forward(q, q, q, torch.zeros(3), out=flat.as_strided((2, 1, 3, 8), (8, 4000, 16, 1)),
+                                    state_out=state.transpose(0, 1).contiguous().transpose(0, 1))
+    assert library.calls == 4
